@@ -1,0 +1,328 @@
+// qwm_paged_attend in float32 on the CUDA cores (kernel 1): the kernel of
+// float32 calls, right for every case, and the cross-check of the others.
+//
+//   s_n = q . k_hat_n,  k_hat = zero + code scale;   online softmax in the exp2
+//   domain;   O = sum_n p_n v_hat_n / sum_n p_n.
+//
+// A worker (CTA) walks the tiles of 64 tokens that the partition deals to it.
+// Per tile it dequantises K and V into shared memory (float32, rows padded so
+// that the reads of different keys fall into different banks) and every
+// thread computes RT rows x KT keys of S and RT rows x CT channels of O from
+// registers.  Items have R = 64 rows, or 8 when no request has more than 8
+// (single-token steps: with 64 the arithmetic on absent rows would be 8 times
+// the work on present ones).  Bound by the float32 FMA rate for many rows and
+// by the shared-memory reads of one K element per FMA for few.
+#include "paged_internal.cuh"
+
+namespace qwm {
+namespace paged {
+namespace {
+
+constexpr int kTk = 64, kNt = 256;
+
+template <int D, int R>
+struct Shape {
+  static constexpr int TX = R == 64 ? 16 : 32;   // threads along the keys (and channels) of a row group
+  static constexpr int TY = kNt / TX;
+  static constexpr int RT = R / TY, KT = kTk / TX, CT = D / TX;
+  static constexpr int LD = D + 4, LP = kTk + 4;
+  static constexpr int floats = (R + kTk) * LD + kTk * D + R * LP;
+};
+
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+template <int D, int R, class T>
+__global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs a) {
+  using S = Shape<D, R>;
+  constexpr int G = D / 32;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;                       // [R][LD], scaled by scale * log2(e)
+  float* Ks = Qs + R * S::LD;           // [kTk][LD]
+  float* Vs = Ks + kTk * S::LD;         // [kTk][D]
+  float* Ps = Vs + kTk * D;             // [R][LP]
+  __shared__ int page_of[kTk / 16];
+  const int tid = threadIdx.x, tx = tid % S::TX, ty = tid / S::TX;
+  const int w = blockIdx.x;
+  const Share sh = find_share<R, kTk, kNt>(a, w, (int)gridDim.x);
+  if (tid == 0) a.join[w].last = -1;
+  if (sh.n == 0) return;
+  Walker<R, kTk> it(a);
+  it.start(sh.b, sh.skip, sh.n);
+  do {
+    const int row0 = it.rt * R;
+    __syncthreads();   // the previous item's reads of Qs are done
+    for (int i = tid; i < R * (D / 8); i += kNt) {
+      const int r = i / (D / 8), c = (i % (D / 8)) * 8;
+      float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (r < it.rows) {
+        const int tok = (row0 + r) / a.group, head = it.h * a.group + (row0 + r) % a.group;
+        load8((const T*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row + head * a.q_head + c, x);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) Qs[r * S::LD + c + k] = x[k] * a.scale_log2;
+    }
+    float o[S::RT][S::CT], m[S::RT], l[S::RT];
+    int top[S::RT], bottom[S::RT];      // a row sees bottom <= n < top
+#pragma unroll
+    for (int i = 0; i < S::RT; ++i) {
+      const int r = ty * S::RT + i, tok = (row0 + r) / a.group;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      top[i] = it.hi, bottom[i] = it.lo;
+      if (a.causal) {
+        const int pos = it.rq.n - it.rq.n_new + tok;
+        top[i] = min(it.hi, pos + 1);
+        if (a.window > 0) bottom[i] = max(it.lo, pos - a.window + 1);
+      }
+      if (r >= it.rows) top[i] = 0;
+#pragma unroll
+      for (int j = 0; j < S::CT; ++j) o[i][j] = 0.f;
+    }
+    for (int t = it.from; t < it.to; ++t) {
+      const int n0 = t * kTk;
+      __syncthreads();   // the previous tile's reads are done
+      if (tid < kTk / 16) {
+        const int n = n0 + tid * 16;
+        int pg = -1;
+        if (n < it.hi) {
+          pg = a.table[(int64_t)it.b * a.max_blocks + (n >> a.page_shift)];
+          if (pg < 0 || pg >= a.n_pages) {
+            flag(a.status, QWM_DEV_BOUNDS);
+            pg = -1;
+          }
+        }
+        page_of[tid] = pg;
+      }
+      __syncthreads();
+      for (int i = tid; i < 2 * kTk * (D / 8); i += kNt) {
+        const int half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
+        const int k = rem / (D / 8), wd = rem % (D / 8), n = n0 + k, pg = page_of[k >> 4];
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (pg >= 0 && n >= it.lo && n < it.hi) {
+          const int s = n & (a.page - 1);
+          const uint8_t* blk = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + half * (a.block / 2);
+          const uint32_t code = *reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4);
+          const __half2 par = *reinterpret_cast<const __half2*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4);
+          const float z = __low2float(par), sc = __high2float(par);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = fmaf((float)((code >> (4 * c)) & 15u), sc, z);
+        }
+        float* dst = half ? Vs + k * D + wd * 8 : Ks + k * S::LD + wd * 8;
+        *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      }
+      __syncthreads();
+      float s[S::RT][S::KT];
+#pragma unroll
+      for (int i = 0; i < S::RT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::KT; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 kv[S::KT];
+#pragma unroll
+        for (int j = 0; j < S::KT; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + S::TX * j) * S::LD + c);
+#pragma unroll
+        for (int i = 0; i < S::RT; ++i) {
+          const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * S::RT + i) * S::LD + c);
+#pragma unroll
+          for (int j = 0; j < S::KT; ++j)
+            s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < S::RT; ++i) {
+        float mx = m[i];
+#pragma unroll
+        for (int j = 0; j < S::KT; ++j) {
+          const int n = n0 + tx + S::TX * j;
+          const bool sees = n >= bottom[i] && n < top[i] && page_of[(tx + S::TX * j) >> 4] >= 0;
+          s[i][j] = sees ? s[i][j] : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int d = S::TX / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d, S::TX));
+        const float ref = mx == -INFINITY ? 0.f : mx, corr = exp2f(m[i] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < S::KT; ++j) {
+          const float p = exp2f(s[i][j] - ref);
+          Ps[(ty * S::RT + i) * S::LP + tx + S::TX * j] = p;
+          sum += p;
+        }
+#pragma unroll
+        for (int d = S::TX / 2; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, S::TX);
+        l[i] = fmaf(l[i], corr, sum);
+        m[i] = mx;
+#pragma unroll
+        for (int j = 0; j < S::CT; ++j) o[i][j] *= corr;
+      }
+      __syncwarp();   // a row's P is written and read by the same warp
+#pragma unroll 2
+      for (int n = 0; n < kTk; n += 4) {
+        float4 p[S::RT];
+#pragma unroll
+        for (int i = 0; i < S::RT; ++i) p[i] = *reinterpret_cast<const float4*>(Ps + (ty * S::RT + i) * S::LP + n);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < S::CT; ++j) {
+            const float v = Vs[(n + k) * D + tx + S::TX * j];
+#pragma unroll
+            for (int i = 0; i < S::RT; ++i) {
+              const float pk = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
+              o[i][j] = fmaf(pk, v, o[i][j]);
+            }
+          }
+      }
+    }
+    const bool whole = it.begins() && it.ends();
+    const int slot = it.begins() ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < S::RT; ++i) {
+      const int r = ty * S::RT + i;
+      if (r >= it.rows) continue;
+      if (whole) {
+        const int64_t tok = it.rq.row0 + (row0 + r) / a.group;
+        const int head = it.h * a.group + (row0 + r) % a.group;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        T* dst = (T*)a.out + tok * a.o_row + head * a.o_head;
+#pragma unroll
+        for (int j = 0; j < S::CT; ++j) dst[tx + S::TX * j] = (T)(o[i][j] * inv);
+        if (a.lse && tx == 0) a.lse[tok * a.heads + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+      } else {
+        float* dst = part_row(a, w, slot, R, r, D);
+#pragma unroll
+        for (int j = 0; j < S::CT; ++j) dst[tx + S::TX * j] = o[i][j];
+        if (tx == 0) dst[D] = m[i], dst[D + 1] = l[i];
+      }
+    }
+    if (tid == 0 && it.begins() && !it.ends()) {
+      const int64_t end = sh.first + (sh.n - it.left - (it.to - it.from)) + (it.t1 - it.t0);
+      record_join(a, w, it, last_worker(sh, end), R);
+    }
+  } while (it.next());
+}
+
+// One CTA per cut item and row (rows blockIdx.y, + gridDim.y, ...): groups of
+// D/4 lanes add up the parts, then the groups' results are merged.
+template <int D, class T>
+__global__ void __launch_bounds__(128) paged_attend_join_kernel(const AttendArgs a, int R) {
+  constexpr int L = D / 4, NG = 128 / L;
+  __shared__ __align__(16) float part[NG][D];
+  __shared__ float pm[NG], pl[NG];
+#if __CUDA_ARCH__ >= 900
+  cudaGridDependencySynchronize();
+#endif
+  const int w = blockIdx.x, g = threadIdx.x / L, c = threadIdx.x % L;
+  const Join j = a.join[w];
+  if (j.last < 0) return;
+  for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int x = w + g; x <= j.last; x += NG) {
+      const float* p = part_row(a, x, x == w ? 1 : 0, R, r, D);
+      const float4 v = *reinterpret_cast<const float4*>(p + 4 * c);
+      const float pmx = p[D], plx = p[D + 1];
+      const float mx = fmaxf(m, pmx), ref = mx == -INFINITY ? 0.f : mx;
+      const float f0 = exp2f(m - ref), f1 = exp2f(pmx - ref);
+      o.x = o.x * f0 + v.x * f1;
+      o.y = o.y * f0 + v.y * f1;
+      o.z = o.z * f0 + v.z * f1;
+      o.w = o.w * f0 + v.w * f1;
+      l = l * f0 + plx * f1;
+      m = mx;
+    }
+    *reinterpret_cast<float4*>(&part[g][4 * c]) = o;
+    if (c == 0) pm[g] = m, pl[g] = l;
+    __syncthreads();
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) mx = fmaxf(mx, pm[i]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) sum += pl[i] * exp2f(pm[i] - ref);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t tok = j.q_row0 + (j.row0 + r) / a.group;
+    const int head = j.head * a.group + (j.row0 + r) % a.group;
+    for (int ch = threadIdx.x; ch < D; ch += 128) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) v += part[i][ch] * exp2f(pm[i] - ref);
+      ((T*)a.out)[tok * a.o_row + head * a.o_head + ch] = (T)(v * inv);
+    }
+    if (a.lse && threadIdx.x == 0)
+      a.lse[tok * a.heads + head] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    __syncthreads();
+  }
+}
+
+template <int D, int R, class T>
+cudaError_t launch_simt(const AttendArgs& a, int workers, cudaStream_t st) {
+  constexpr int smem = Shape<D, R>::floats * 4;
+  auto kern = paged_attend_simt_kernel<D, R, T>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<workers, kNt, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_simt_t(const AttendArgs& a, int d, Workers w, cudaStream_t st) {
+  if (w.rows == 64) return d == 64 ? launch_simt<64, 64, T>(a, w.count, st) : launch_simt<128, 64, T>(a, w.count, st);
+  return d == 64 ? launch_simt<64, 8, T>(a, w.count, st) : launch_simt<128, 8, T>(a, w.count, st);
+}
+
+}  // namespace
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 152;
+  return sms;
+}
+
+Workers simt_workers(int64_t max_rows) {
+  const int sms = sm_count();
+  return max_rows <= 8 ? Workers{2 * sms, 8} : Workers{sms, 64};
+}
+
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st) {
+  const Workers w = simt_workers(max_rows);
+  const cudaError_t e = bf16 ? launch_simt_t<__nv_bfloat16>(a, d, w, st) : launch_simt_t<float>(a, d, w, st);
+  return e != cudaSuccess ? e : launch_attend_join(a, d, bf16, w, max_rows, st);
+}
+
+cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w, int64_t max_rows, cudaStream_t st) {
+  const int rows = max_rows < 1 ? 1 : max_rows < w.rows ? (int)max_rows : w.rows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)w.count, (unsigned)(rows < 32 ? rows : 32), 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = bf16 ? (d == 64 ? paged_attend_join_kernel<64, __nv_bfloat16> : paged_attend_join_kernel<128, __nv_bfloat16>)
+                   : (d == 64 ? paged_attend_join_kernel<64, float> : paged_attend_join_kernel<128, float>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, w.rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace qwm

@@ -1,0 +1,359 @@
+// The paged cache's bookkeeping (qwm_paged_plan, qwm_paged_release) and its
+// 4-bit quantiser (qwm_paged_append).
+#include <cooperative_groups.h>
+
+#include "paged_internal.cuh"
+#include "paged_launch.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qwm {
+namespace paged {
+namespace {
+
+constexpr int kPlanNt = 1024;
+
+__device__ __forceinline__ int pages_of(int64_t tokens, int shift) { return (int)((tokens + (1 << shift) - 1) >> shift); }
+
+// Exclusive prefix sums of (x, y) over the CTA's threads; *sx, *sy: the totals.
+__device__ __forceinline__ void scan2(int64_t& x, int64_t& y, int64_t* sx, int64_t* sy) {
+  __shared__ int64_t wx[32], wy[32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int64_t x0 = x, y0 = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x += a, y += b;
+  }
+  __syncthreads();
+  if (lane == 31) wx[wid] = x, wy[wid] = y;
+  __syncthreads();
+  if (wid == 0) {
+    int64_t a = lane < nw ? wx[lane] : 0, b = lane < nw ? wy[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) a += c, b += d;
+    }
+    wx[lane] = a, wy[lane] = b;
+  }
+  __syncthreads();
+  const int64_t bx = wid ? wx[wid - 1] : 0, by = wid ? wy[wid - 1] : 0;
+  *sx = wx[nw - 1], *sy = wy[nw - 1];
+  x += bx - x0, y += by - y0;
+}
+
+// The largest b with first[b] <= i (first ascending, first[0] <= i).
+__device__ __forceinline__ int find(const int32_t* first, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Every CTA of the cluster scans the lengths for itself (a few loads a
+// thread), the cluster meets once all have read what the outputs may
+// overwrite (kv_len_out = kv_len), then all write rows and table entries.
+// The prefix sums stay in shared memory: a row finds its request by bisection.
+__global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_plan_args a, int shift) {
+  extern __shared__ int32_t plan_sm[];
+  int32_t* row_of = plan_sm;                 // first row of each request
+  int32_t* page_of = row_of + a.requests;    // first new page
+  int32_t* len_of = page_of + a.requests;    // cached tokens
+  __shared__ int32_t count_sh;
+  __shared__ int bad_sh, full_sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  if (tid == 0) bad_sh = full_sh = 0, count_sh = *a.free_count;
+  __syncthreads();
+  int64_t rows = 0, pages = 0;
+  for (int b0 = 0; b0 < a.requests; b0 += kPlanNt) {
+    const int b = b0 + tid;
+    int64_t x = 0, y = 0;
+    int len = 0;
+    if (b < a.requests) {
+      len = a.kv_len[b];
+      const int add = a.new_len[b];
+      if (len < 0 || add < 0) {
+        bad_sh = 1;
+      } else {
+        const int64_t total = ((int64_t)len + add + (1 << shift) - 1) >> shift;
+        x = add;
+        y = total - pages_of(len, shift);
+        // a length beyond int32 does not fit its output either
+        if (total > a.max_blocks || (int64_t)len + add > 0x7fffffff) full_sh = 1;
+      }
+    }
+    int64_t sx, sy;
+    scan2(x, y, &sx, &sy);
+    if (b < a.requests) {
+      row_of[b] = (int32_t)(rows + x);
+      page_of[b] = (int32_t)(pages + y);
+      len_of[b] = len;
+    }
+    rows += sx;
+    pages += sy;
+  }
+  __syncthreads();
+  const int count = count_sh;
+  const bool bad = bad_sh != 0 || count < 0 || count > a.n_pages;
+  const bool ok = !bad && !full_sh && rows <= a.rows && pages <= count;
+  if (ctas > 1) cluster.sync();
+  else __syncthreads();
+  if (rank == 0) {
+    for (int b = tid; b < a.requests; b += kPlanNt) {
+      const int next = b + 1 < a.requests ? row_of[b + 1] : (int32_t)rows;
+      a.kv_len_out[b] = len_of[b] + (ok ? next - row_of[b] : 0);
+      a.cu_rows[b] = ok ? row_of[b] : 0;
+    }
+    if (tid == 0) {
+      a.cu_rows[a.requests] = ok ? (int32_t)rows : 0;
+      *a.free_count_out = count - (ok ? (int32_t)pages : 0);
+      if (!ok) flag(a.status, bad ? QWM_DEV_BOUNDS : QWM_DEV_CAPACITY);
+    }
+  }
+  const int first = rank * kPlanNt + tid, step = ctas * kPlanNt;
+  const int used = ok ? (int)rows : 0;
+  if (ok) {
+    for (int i = first; i < (int)pages; i += step) {
+      const int b = find(page_of, a.requests, i);
+      int pg = a.free_pages[count - 1 - i];
+      if (pg < 0 || pg >= a.n_pages) {
+        flag(a.status, QWM_DEV_BOUNDS);
+        pg = -1;
+      }
+      a.block_table[(int64_t)b * a.max_blocks + pages_of(len_of[b], shift) + (i - page_of[b])] = pg;
+    }
+  }
+  for (int64_t t = first; t < a.rows; t += step) {
+    int64_t slot = -1;
+    int pos = -1;
+    if (t < used) {
+      const int b = find(row_of, a.requests, (int)t);
+      pos = len_of[b] + (int)t - row_of[b];
+      const int held = pages_of(len_of[b], shift), j = pos >> shift;
+      // pages held before the call are in the table, the new ones on the stack
+      const int pg = j < held ? a.block_table[(int64_t)b * a.max_blocks + j]
+                              : a.free_pages[count - 1 - (page_of[b] + j - held)];
+      if (pg >= 0 && pg < a.n_pages) slot = ((int64_t)pg << shift) + (pos & ((1 << shift) - 1));
+      else flag(a.status, QWM_DEV_BOUNDS);
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+}
+
+// One CTA: pushes the pages behind keep_len in the order of the requests.
+__global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_release_args a, int shift) {
+  __shared__ int32_t count_sh;
+  const int tid = threadIdx.x;
+  if (tid == 0) count_sh = *a.free_count;
+  __syncthreads();
+  const int count = count_sh;
+  // the pages a request gives up: entries [keep, held) of its table with an id in range
+  auto range = [&](int b, int* keep, int* held) {
+    const int len = a.kv_len[b], want = a.keep_len[b];
+    *keep = *held = 0;
+    if (want < 0 || want > len || pages_of(len, shift) > a.max_blocks) {
+      flag(a.status, QWM_DEV_BOUNDS);
+      return false;
+    }
+    *keep = pages_of(want, shift);
+    *held = pages_of(len, shift);
+    return true;
+  };
+  auto valid = [&](int b, int keep, int held) {
+    int n = 0;
+    for (int j = keep; j < held; ++j) {
+      const int pg = a.block_table[(int64_t)b * a.max_blocks + j];
+      if (pg >= 0 && pg < a.n_pages) ++n;
+      else flag(a.status, QWM_DEV_BOUNDS);
+    }
+    return n;
+  };
+  // first the sum alone: nothing changes unless all of it fits
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.requests; b0 += kPlanNt) {
+    const int b = b0 + tid;
+    int64_t x = 0, y = 0, sx, sy;
+    int keep, held;
+    if (b < a.requests && range(b, &keep, &held)) x = valid(b, keep, held);
+    scan2(x, y, &sx, &sy);
+    total += sx;
+  }
+  if (count < 0 || count > a.n_pages || total + count > a.n_pages) {
+    if (tid == 0) flag(a.status, QWM_DEV_CAPACITY);
+    return;
+  }
+  int64_t at = count;
+  for (int b0 = 0; b0 < a.requests; b0 += kPlanNt) {
+    const int b = b0 + tid;
+    int64_t x = 0, y = 0, sx, sy;
+    int keep = 0, held = 0;
+    const bool ok = b < a.requests && range(b, &keep, &held);
+    if (ok) x = valid(b, keep, held);
+    scan2(x, y, &sx, &sy);
+    if (ok) {
+      int64_t put = at + x;
+      for (int j = keep; j < held; ++j) {
+        int32_t* e = a.block_table + (int64_t)b * a.max_blocks + j;
+        const int pg = *e;
+        if (pg >= 0 && pg < a.n_pages) a.free_pages[put++] = pg;
+        *e = -1;
+      }
+      a.kv_len[b] = a.keep_len[b];
+    }
+    at += sx;
+  }
+  if (tid == 0) *a.free_count = (int32_t)at;
+}
+
+// ---- append
+//
+// A thread takes 8 channels of one (row, head) of k or v (16 or 32 bytes in, 4
+// bytes of codes out), the 4 threads of a group of 32 channels find its range
+// by shuffles.  Bound by HBM: 2 or 4 bytes a channel in, 0.625 out (and 2 or 4
+// more for x_hat).
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kAppendNt = 256;
+constexpr float kClamp = 60000.f;
+
+template <int D, class T>
+__global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged_append_args a, int shift) {
+  constexpr int L = D / 8, G = D / 32;
+  const int64_t i = (int64_t)blockIdx.x * kAppendNt + threadIdx.x;
+  const int wd = (int)(i % L);
+  const int64_t rh = i / L;
+  const bool live = rh < a.rows * a.kv_heads;
+  const int64_t t = live ? rh / a.kv_heads : 0;
+  const int h = (int)(live ? rh % a.kv_heads : 0);
+  const bool value = blockIdx.y != 0;
+  const qwm_rows in = value ? a.v : a.k, hat = value ? a.v_hat : a.k_hat;
+  int64_t slot = live ? a.slots[t] : -1;
+  uint32_t bits = 0;
+  if (slot >= (a.n_pages << shift)) {
+    bits = QWM_DEV_BOUNDS;
+    slot = -1;
+  }
+  float x[8];
+  if (slot >= 0) {
+    load8((const T*)in.ptr + t * in.row_stride + h * in.head_stride + 8 * wd, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (!(x[k] == x[k])) {
+      x[k] = 0.f;
+      bits |= QWM_DEV_NAN;
+    }
+    if (fabsf(x[k]) > kClamp) {
+      x[k] = copysignf(kClamp, x[k]);
+      bits |= QWM_DEV_SATURATED;
+    }
+  }
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) mn = fminf(mn, x[k]), mx = fmaxf(mx, x[k]);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const __half zh = __float2half_rn(mn), sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+  const float z = __half2float(zh), s = __half2float(sh);
+  uint32_t code = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float c = 0.f;
+    if (s > 0.f) c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], z), s)), 0.f), 15.f);
+    code |= (uint32_t)c << (4 * k);
+    x[k] = fmaf(c, s, z);
+  }
+  if (slot >= 0) {
+    const int64_t pg = slot >> shift;
+    const int at = (int)(slot & ((1 << shift) - 1)), page = 1 << shift;
+    uint8_t* half_block = (uint8_t*)a.pool + (pg * a.kv_heads + h) * (int64_t)block_bytes(D, page) +
+                          (value ? block_bytes(D, page) / 2 : 0);
+    *reinterpret_cast<uint32_t*>(half_block + at * (D / 2) + 4 * wd) = code;
+    if ((wd & 3) == 0)
+      *reinterpret_cast<__half2*>(half_block + page * (D / 2) + (at * G + wd / 4) * 4) = __halves2half2(zh, sh);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+  }
+  if (hat.ptr && live) store8((T*)hat.ptr + t * hat.row_stride + h * hat.head_stride + 8 * wd, x);
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if (bits && (threadIdx.x & 31) == 0) flag(a.status, bits);
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st) {
+  const size_t smem = (size_t)a.requests * 12;
+  cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRequests * 12);
+  if (e != cudaSuccess) return e;
+  // one CTA writes ~1024 rows a microsecond
+  const unsigned ctas = a.rows <= 4096 ? 1 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kPlanNt, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {
+  paged_release_kernel<<<1, kPlanNt, 0, st>>>(a, shift);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append(const qwm_paged_append_args& a, int shift, cudaStream_t st) {
+  const int64_t threads = a.rows * a.kv_heads * (a.head_dim / 8);
+  const dim3 grid((unsigned)((threads + kAppendNt - 1) / kAppendNt), 2, 1);
+  const bool bf = a.dtype == QWM_BF16;
+  auto kern = a.head_dim == 64 ? (bf ? paged_append_kernel<64, __nv_bfloat16> : paged_append_kernel<64, float>)
+                               : (bf ? paged_append_kernel<128, __nv_bfloat16> : paged_append_kernel<128, float>);
+  kern<<<grid, kAppendNt, 0, st>>>(a, shift);
+  return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace qwm

@@ -1,0 +1,322 @@
+// Shared declarations of the paged 4-bit cache: the block layout, the work
+// partition of the attention kernels and their partial results.
+#pragma once
+
+#include <math.h>
+
+#include "qwm_internal.cuh"
+
+namespace qwm {
+namespace paged {
+
+constexpr int kMaxRequests = 8192;
+
+inline __host__ __device__ int block_bytes(int d, int page) { return page * (d + d / 4); }
+
+// What every attention kernel reads of a call.
+struct AttendArgs {
+  const void* q;
+  int64_t q_row, q_head;         // element strides
+  void* out;
+  int64_t o_row, o_head;
+  float* lse;
+  const uint8_t* pool;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu;
+  uint32_t* status;
+  float* part;                   // [workers][2][tile rows][part_floats(d)]
+  struct Join* join;             // [workers]
+  int64_t rows;
+  int32_t n_pages;
+  int32_t heads, kv_heads, group;
+  int32_t page, page_shift, block;
+  int32_t requests, max_blocks;
+  int32_t causal, window;
+  float scale_log2;              // softmax scale * log2(e)
+};
+
+// A row of a partial result: O[d] unnormalised, running maximum (log2
+// domain), sum, pad to 16 bytes.
+inline __host__ __device__ constexpr int part_floats(int d) { return d + 4; }
+
+// An item whose tiles are spread over several workers: the worker it starts
+// in records it, the join kernel adds up the parts in the order of the
+// workers (first: the starting worker's part 1, then part 0 of each later
+// one), so the result does not depend on timing.
+struct Join {
+  int32_t last;        // last worker with a part, -1: nothing to join
+  int32_t q_row0;      // first row of q of the request
+  int32_t head;        // kv head
+  int32_t row0, rows;  // first row of the item in its request's problem, its rows
+  int32_t pad[3];
+};
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// One request as the kernels see it, with lengths clamped to what the tables hold.
+struct Request {
+  int32_t row0;     // first row of q
+  int32_t n_new;    // query tokens
+  int32_t n;        // cached tokens
+  int32_t rows;     // n_new * group: rows of one kv head's problem, token-major
+};
+
+__device__ __forceinline__ Request load_request(const AttendArgs& a, int b) {
+  int lo = a.cu[b], hi = a.cu[b + 1], n = a.kv_len[b];
+  const int64_t cap64 = (int64_t)a.max_blocks * a.page;
+  const int cap = cap64 < 0x7fffff00 ? (int)cap64 : 0x7fffff00;
+  const int64_t rows = a.rows;
+  if (lo < 0 || hi < lo || hi > rows || n < 0 || n > cap) {
+    flag(a.status, QWM_DEV_BOUNDS);
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > rows ? (int)rows : hi;
+    hi = hi < lo ? lo : hi;
+    n = n < 0 ? 0 : n > cap ? cap : n;
+  }
+  Request r;
+  r.row0 = lo;
+  r.n_new = hi - lo;
+  r.n = n;
+  r.rows = r.n_new * a.group;
+  return r;
+}
+
+// Token range [lo, hi) that the tokens tok0 .. tok1 of a request's query see
+// between them (empty: lo = hi = 0).
+__device__ __forceinline__ void visible(const AttendArgs& a, const Request& r, int tok0, int tok1, int* lo, int* hi) {
+  int l = 0, h = r.n;
+  if (a.causal) {
+    const int base = r.n - r.n_new;
+    h = min(h, base + tok1 + 1);
+    if (a.window > 0) l = max(0, base + tok0 - a.window + 1);
+  }
+  if (h <= l) l = h = 0;
+  *lo = l;
+  *hi = h;
+}
+
+// ---- the partition of a call's work over `workers` CTAs
+//
+// The work is a list of items (request, kv head, block of R rows), each a run
+// of tiles of TK tokens that its rows see; an item that sees nothing has one
+// tile, so that it is visited and its rows are written.  The list's tiles are
+// dealt to the workers in equal contiguous shares whatever the lengths are:
+// no worker waits for another, and a long request is split exactly as far as
+// the machine needs.  A share cuts at most its first and its last item.
+template <int R, int TK>
+struct Walker {
+  const AttendArgs& a;
+  int64_t left;        // tiles of this worker not yet handed out
+  // the current item
+  int b, h, rt;
+  Request rq;
+  int t0, t1;          // its tiles
+  int lo, hi;          // its visible tokens
+  int from, to;        // the tiles of it that are this worker's
+  int rows;            // valid rows of the item
+
+  __device__ explicit Walker(const AttendArgs& args) : a(args) {}
+
+  __device__ int row_tiles() const { return (rq.rows + R - 1) / R; }
+
+  __device__ static void tiles_of(const AttendArgs& a, const Request& r, int rt, int* lo, int* hi, int* t0, int* t1) {
+    const int first = rt * R, last = min(r.rows, first + R) - 1;
+    visible(a, r, first / a.group, last / a.group, lo, hi);
+    *t0 = *lo / TK;
+    *t1 = *hi > *lo ? (*hi + TK - 1) / TK : *t0 + 1;
+  }
+
+  // tiles of one kv head of a request
+  __device__ static int64_t head_tiles(const AttendArgs& a, const Request& r) {
+    const int nrt = (r.rows + R - 1) / R;
+    if (nrt == 0) return 0;
+    int lo, hi, t0, t1;
+    if (!a.causal) {
+      tiles_of(a, r, 0, &lo, &hi, &t0, &t1);
+      return (int64_t)nrt * (t1 - t0);
+    }
+    int64_t s = 0;
+    for (int i = 0; i < nrt; ++i) {
+      tiles_of(a, r, i, &lo, &hi, &t0, &t1);
+      s += t1 - t0;
+    }
+    return s;
+  }
+
+  __device__ void item(int tile) {
+    tiles_of(a, rq, rt, &lo, &hi, &t0, &t1);
+    from = t0 + tile;
+    rows = min(R, rq.rows - rt * R);
+    const int64_t take = min((int64_t)(t1 - from), left);
+    to = from + (int)take;
+    left -= take;
+  }
+
+  // To the first item of the share that starts `skip` tiles into request b0.
+  __device__ void start(int b0, int64_t skip, int64_t n_tiles) {
+    b = b0;
+    rq = load_request(a, b);
+    left = n_tiles;
+    const int64_t per = head_tiles(a, rq);
+    h = (int)(skip / per);
+    skip -= h * per;
+    rt = 0;
+    if (!a.causal) {
+      int l, u, x0, x1;
+      tiles_of(a, rq, 0, &l, &u, &x0, &x1);
+      rt = (int)(skip / (x1 - x0));
+      skip -= (int64_t)rt * (x1 - x0);
+    } else {
+      while (true) {
+        int l, u, x0, x1;
+        tiles_of(a, rq, rt, &l, &u, &x0, &x1);
+        if (skip < x1 - x0) break;
+        skip -= x1 - x0;
+        ++rt;
+      }
+    }
+    item((int)skip);
+  }
+
+  __device__ bool next() {
+    if (left <= 0) return false;
+    if (++rt >= row_tiles()) {
+      rt = 0;
+      if (++h >= a.kv_heads) {
+        h = 0;
+        do {
+          if (++b >= a.requests) return false;
+          rq = load_request(a, b);
+        } while (rq.rows == 0);
+      }
+    }
+    item(0);
+    return true;
+  }
+
+  __device__ bool begins() const { return from == t0; }
+  __device__ bool ends() const { return to == t1; }
+};
+
+// The share of worker `w` of `workers`: where it starts and how many tiles it
+// has.  Called by all threads of a CTA of NT threads; the sums over the
+// requests are made by every CTA for itself (a few loads per thread).
+struct Share {
+  int b;
+  int workers;         // those with work: no more than there are tiles, so that each has some
+  int64_t skip, n, first, total;
+};
+
+template <int R, int TK, int NT>
+__device__ Share find_share(const AttendArgs& a, int w, int workers) {
+  __shared__ int64_t warp_sum[NT / 32];
+  __shared__ int64_t chunk_base, found_skip;
+  __shared__ int found_b;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  Share s;
+  s.b = s.workers = 0;
+  s.skip = s.n = s.first = s.total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (tid == 0) {
+      chunk_base = 0;
+      found_b = -1;
+    }
+    __syncthreads();
+    const int64_t want = s.first;
+    for (int b0 = 0; b0 < a.requests; b0 += NT) {
+      const int b = b0 + tid;
+      int64_t mine = 0;
+      if (b < a.requests) mine = Walker<R, TK>::head_tiles(a, load_request(a, b)) * a.kv_heads;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[wid] = x;
+      __syncthreads();
+      int64_t before = chunk_base, all = 0;
+      for (int i = 0; i < NT / 32; ++i) {
+        if (i < wid) before += warp_sum[i];
+        all += warp_sum[i];
+      }
+      const int64_t at = before + x - mine;
+      if (pass == 1 && want >= at && want < at + mine) {
+        found_b = b;
+        found_skip = want - at;
+      }
+      // one pass finds both when the requests fit one chunk
+      if (pass == 0 && a.requests <= NT) {
+        const int64_t f = all < workers ? w : all * w / workers;
+        if (f >= at && f < at + mine) {
+          found_b = b;
+          found_skip = f - at;
+        }
+      }
+      __syncthreads();
+      if (tid == 0) chunk_base += all;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      s.total = chunk_base;
+      s.workers = s.total < workers ? (int)s.total : workers;
+      if (w < s.workers) {
+        s.first = s.total * w / s.workers;
+        s.n = s.total * (w + 1) / s.workers - s.first;
+      }
+      if (a.requests <= NT) break;
+      __syncthreads();
+    }
+  }
+  s.b = found_b;
+  s.skip = found_skip;
+  __syncthreads();
+  return s;
+}
+
+// The last worker that has tiles of the item that ends at tile `end` of the
+// whole list (end > the share's first tile).
+__device__ __forceinline__ int last_worker(const Share& s, int64_t end) {
+  // the worker w with first(w) <= end - 1 < first(w + 1), first(w) = floor(total w / workers)
+  int64_t w = ((end - 1) * s.workers + s.workers - 1) / s.total;
+  if (w >= s.workers) w = s.workers - 1;
+  while (w > 0 && s.total * w / s.workers > end - 1) --w;
+  while (w + 1 < s.workers && s.total * (w + 1) / s.workers <= end - 1) ++w;
+  return (int)w;
+}
+
+// What a worker writes for the join kernel: `last` of an item that starts in
+// its share and ends in another's, -1 when there is none.
+template <class W>
+__device__ __forceinline__ void record_join(const AttendArgs& a, int worker, const W& it, int last, int R) {
+  Join j;
+  j.last = last;
+  j.q_row0 = it.rq.row0;
+  j.head = it.h;
+  j.row0 = it.rt * R;
+  j.rows = it.rows;
+  j.pad[0] = j.pad[1] = j.pad[2] = 0;
+  a.join[worker] = j;
+}
+
+__device__ __forceinline__ float* part_row(const AttendArgs& a, int worker, int slot, int R, int r, int d) {
+  return a.part + (((int64_t)worker * 2 + slot) * R + r) * part_floats(d);
+}
+
+// ---- launchers
+struct Workers {
+  int count;   // CTAs that share the work
+  int rows;    // rows of one item
+};
+int sm_count();
+Workers simt_workers(int64_t max_rows);
+cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st);
+// joins the parts of the items that were cut; max_rows: the rows of a
+// request's longest problem as the host knows them (any value is correct)
+cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w, int64_t max_rows, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace qwm

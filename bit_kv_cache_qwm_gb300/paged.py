@@ -1,0 +1,303 @@
+"""Thin Python binding of libqwm's paged 4-bit cache (ctypes).
+
+Argument checks and marshalling only; every step runs in the CUDA library, on
+the device of its tensors and that device's current stream.  Nothing is kept
+between calls: pools, tables and lengths are the caller's tensors, and the
+attention's workspace comes from torch's allocator call by call, so calls on
+different streams and captured graphs share nothing.
+
+A serving step:
+
+    plan = qwm_paged_plan(kv_len, new_len, table, free_pages, free_count, page_tokens, rows)
+    # per layer
+    q, k = qwm_qk_norm_rope(q, k, w_q, w_k, cos_sin, plan.positions)
+    qwm_paged_append(k, v, pool, plan.slots)
+    o = qwm_paged_attend(q, pool, table, plan.kv_len, plan.cu_rows, max_new)
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+from typing import NamedTuple, Optional, Sequence
+
+import torch
+
+from .qwm import QWM_BF16, QWM_F32, _check, lib
+
+PAGE_TOKENS = (16, 32, 64, 128, 256)
+# attention kernels (the `kernel` argument of qwm_paged_attend): automatic
+# choice, float32 CUDA cores, bf16 mma.sync for few rows, bf16 tcgen05
+PAGED_AUTO, PAGED_SIMT, PAGED_MMA, PAGED_TC = 0, 1, 2, 3
+
+# The argument structs of include/qwm.h, packed in one call each: a pointer or
+# 64-bit field is q, a 32-bit one i or f, in the header's order.
+_ROPE = struct.Struct("=19q11if")
+_PLAN = struct.Struct("=13q3i4x")
+_RELEASE = struct.Struct("=7q3i4x")
+_APPEND = struct.Struct("=17q4i")
+_ATTEND = struct.Struct("=17q9ifi4x")
+
+_DTYPES = {torch.bfloat16: QWM_BF16, torch.float32: QWM_F32}
+_workspace_bytes: dict = {}
+
+
+class PagedPlan(NamedTuple):
+    """What qwm_paged_plan writes (see include/qwm.h)."""
+    kv_len: torch.Tensor       # int32 [requests], with the new tokens
+    free_count: torch.Tensor   # int32 [1]
+    cu_rows: torch.Tensor      # int32 [requests + 1]
+    slots: torch.Tensor        # int64 [rows]
+    positions: torch.Tensor    # int32 [rows]
+
+
+def _run(fn, args: bytes, what: str, dev: torch.device):
+    if dev.index == torch.cuda.current_device():
+        st = fn(args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(args, torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _check(st, what)
+
+
+def _rows(x, what: str, like=None):
+    """A CUDA tensor [rows, heads, d] in bf16 or float32 with contiguous heads
+    of 16-byte aligned vectors (any row and head stride), on like's device in
+    like's dtype; returns (pointer, row stride, head stride)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor is expected")
+    if x.dim() != 3 or x.dtype not in _DTYPES:
+        raise ValueError(f"{what}: a bfloat16 or float32 tensor [rows, heads, d] is expected, got {x.dtype} {tuple(x.shape)}")
+    if like is not None and (x.dtype != like.dtype or x.device != like.device):
+        raise ValueError(f"{what}: expected {like.dtype} on {like.device}, got {x.dtype} on {x.device}")
+    s0, s1, s2 = x.stride()
+    n0, n1, n2 = x.shape
+    if s2 != 1 and n2 != 1:
+        raise ValueError(f"{what}: the channels of a head have to be contiguous")
+    align = 8 if x.dtype == torch.bfloat16 else 4
+    if x.data_ptr() % 16 or (n0 > 1 and s0 % align) or (n1 > 1 and s1 % align):
+        raise ValueError(f"{what}: pointer and strides have to be multiples of 16 bytes")
+    return x.data_ptr(), s0 if n0 > 1 else 0, s1 if n1 > 1 else 0
+
+
+def _out_rows(x, what: str, like):
+    r = _rows(x, what, like)
+    if x.shape != like.shape:
+        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(x.shape)}")
+    return r
+
+
+def _array(x, what: str, dtype, shape, dev):
+    """The pointer of a contiguous tensor of `dtype` and `shape` (None: any) on `dev`."""
+    if not isinstance(x, torch.Tensor) or x.device != dev:
+        raise ValueError(f"{what}: a tensor on {dev} is expected")
+    if x.dtype != dtype or x.dim() != len(shape) or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {len(shape)}-d {dtype} tensor is expected, got {x.dtype} {tuple(x.shape)}")
+    for have, want in zip(x.shape, shape):
+        if want is not None and have != want:
+            raise ValueError(f"{what}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _status(x, dev):
+    return 0 if x is None else _array(x, "status", torch.int32, (1,), dev)
+
+
+def _page_tokens(pool, d: int) -> int:
+    """Tokens of a page of `pool` [pages, kv_heads, block] for heads of d channels."""
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != 3 \
+            or not pool.is_contiguous():
+        raise ValueError("pool: a contiguous CUDA uint8 tensor [pages, kv_heads, block bytes] is expected")
+    page, rest = divmod(4 * pool.shape[2], 5 * d)
+    if rest or page not in PAGE_TOKENS:
+        raise ValueError(f"pool: {pool.shape[2]} bytes are no block of a page of {PAGE_TOKENS} tokens at d = {d}")
+    return page
+
+
+def qwm_paged_block_bytes(head_dim: int, page_tokens: int) -> int:
+    """Bytes of one block: page_tokens slots of one key/value head."""
+    n = int(lib().qwm_paged_block_bytes(head_dim, page_tokens))
+    if n == 0:
+        raise ValueError(f"head_dim 64 or 128 and page_tokens of {PAGE_TOKENS} are built, not {head_dim} and {page_tokens}")
+    return n
+
+
+def paged_pool(n_pages: int, kv_heads: int, head_dim: int, page_tokens: int, device=None) -> torch.Tensor:
+    """An uninitialised pool [n_pages, kv_heads, block bytes] (one per layer)."""
+    return torch.empty((n_pages, kv_heads, qwm_paged_block_bytes(head_dim, page_tokens)), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                     k_weight: Optional[torch.Tensor], cos_sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6,
+                     interleaved: bool = False, sections: Optional[Sequence[int]] = None,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
+    """RMS norm of every head of q [rows, heads, d] and k [rows, kv_heads, d]
+    (None: queries alone) and the rotation of their first cos_sin.shape[1]
+    channels, in one pass.  cos_sin: float32 [n_positions, rot]; positions:
+    int32 [rows] or [rows, axes], with `sections` pairs for each axis; a
+    negative position leaves the row of an output given by the caller as it
+    was.  Returns (q_out, k_out), new tensors where none are given; q_out = q
+    works in place."""
+    qr = _rows(q, "q")
+    T, hq, d = q.shape
+    dev, dt = q.device, q.dtype
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=dt, device=dev)
+    qo = _out_rows(q_out, "q_out", q)
+    hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        kr = _rows(k, "k", q)
+        hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != d:
+            raise ValueError(f"k: expected [{T}, kv_heads, {d}], got {tuple(k.shape)}")
+        if k_out is None:
+            k_out = torch.empty((T, hk, d), dtype=dt, device=dev)
+        ko = _out_rows(k_out, "k_out", k)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out, k_weight: given without k")
+    table = _array(cos_sin, "cos_sin", torch.float32, (None, None), dev)
+    n_pos, rot = cos_sin.shape
+    axes = positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 1
+    pos = _array(positions, "positions", torch.int32, (T,) if axes == 1 and positions.dim() == 1 else (T, axes), dev)
+    if not 1 <= axes <= 4:
+        raise ValueError("positions: 1 to 4 axes")
+    if sections is None:
+        if axes > 1:
+            raise ValueError("sections: needed with several axes")
+        sections = (rot // 2,)
+    sections = tuple(int(x) for x in sections)
+    if len(sections) != axes or sum(sections) != rot // 2 or min(sections) < 0:
+        raise ValueError(f"sections: {axes} counts with the sum {rot // 2} are expected, got {sections}")
+    s = sections + (0,) * (4 - axes)
+    wq = 0 if q_weight is None else _array(q_weight, "q_weight", dt, (d,), dev)
+    wk = 0 if k_weight is None else _array(k_weight, "k_weight", dt, (d,), dev)
+    _run(lib().qwm_qk_norm_rope,
+         _ROPE.pack(*qr, *kr, *qo, *ko, wq, wk, table, pos, _status(status, dev), T, n_pos, _DTYPES[dt], d, hq, hk, rot, axes,
+                    *s, 1 if interleaved else 0, eps), "qwm_qk_norm_rope", dev)
+    return q_out, k_out
+
+
+def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                   free_count: torch.Tensor, page_tokens: int, rows: int, out: Optional[PagedPlan] = None,
+                   status: Optional[torch.Tensor] = None) -> PagedPlan:
+    """Pages, slots and positions of a step that adds new_len[b] tokens to each
+    request (int32 tensors on the GPU; `rows` rows of storage, at least the
+    sum of new_len as the host knows it).  block_table is updated in place;
+    the rest is returned, in `out` where given (its kv_len and free_count may
+    be the inputs themselves).  Nothing changes when it does not fit: then
+    cu_rows is 0 throughout, every slot -1, and `status` has DEV_CAPACITY."""
+    dev = kv_len.device if isinstance(kv_len, torch.Tensor) else None
+    if dev is None or not kv_len.is_cuda:
+        raise ValueError("kv_len: a CUDA tensor is expected")
+    i32, i64 = torch.int32, torch.int64
+    a = _array(kv_len, "kv_len", i32, (None,), dev)
+    B = kv_len.shape[0]
+    b = _array(new_len, "new_len", i32, (B,), dev)
+    c = _array(free_pages, "free_pages", i32, (None,), dev)
+    d = _array(free_count, "free_count", i32, (1,), dev)
+    e = _array(block_table, "block_table", i32, (B, None), dev)
+    if out is None:
+        # one allocation for the five (slots first: they are the 8-byte ones)
+        sizes = (2 * rows, rows, B, B + 1, 1)
+        flat = torch.empty(sum(sizes), dtype=i32, device=dev)
+        s, p, kl, cu, fc = flat.split(sizes)
+        out = PagedPlan(kl, fc, cu, s.view(i64), p)
+        base = flat.data_ptr()
+        ptr = (base + 12 * rows, base + 4 * (3 * rows + 2 * B + 1), base + 4 * (3 * rows + B), base, base + 8 * rows)
+    else:
+        ptr = (_array(out.kv_len, "out.kv_len", i32, (B,), dev), _array(out.free_count, "out.free_count", i32, (1,), dev),
+               _array(out.cu_rows, "out.cu_rows", i32, (B + 1,), dev), _array(out.slots, "out.slots", i64, (rows,), dev),
+               _array(out.positions, "out.positions", i32, (rows,), dev))
+    _run(lib().qwm_paged_plan,
+         _PLAN.pack(a, b, c, d, e, *ptr, _status(status, dev), rows, free_pages.shape[0], B, block_table.shape[1],
+                    page_tokens), "qwm_paged_plan", dev)
+    return out
+
+
+def qwm_paged_release(keep_len: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                      free_count: torch.Tensor, page_tokens: int, status: Optional[torch.Tensor] = None):
+    """Cut every request back to keep_len[b] tokens (0: it ends) and push the
+    pages it gives up on the free stack; kv_len, block_table, free_pages and
+    free_count are updated in place."""
+    dev = kv_len.device if isinstance(kv_len, torch.Tensor) else None
+    if dev is None or not kv_len.is_cuda:
+        raise ValueError("kv_len: a CUDA tensor is expected")
+    i32 = torch.int32
+    a = _array(kv_len, "kv_len", i32, (None,), dev)
+    B = kv_len.shape[0]
+    _run(lib().qwm_paged_release,
+         _RELEASE.pack(_array(keep_len, "keep_len", i32, (B,), dev), a, _array(block_table, "block_table", i32, (B, None), dev),
+                       _array(free_pages, "free_pages", i32, (None,), dev), _array(free_count, "free_count", i32, (1,), dev),
+                       _status(status, dev), free_pages.shape[0], B, block_table.shape[1], page_tokens),
+         "qwm_paged_release", dev)
+
+
+def qwm_paged_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, slots: torch.Tensor,
+                     k_hat: Optional[torch.Tensor] = None, v_hat: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
+    """Quantise keys and values [rows, kv_heads, d] to 4 bits into the slots
+    (int64 [rows], -1: no slot) of the pool.  k_hat, v_hat receive the values
+    that the stored bytes stand for (0 in rows without a slot)."""
+    kr, vr = _rows(k, "k"), _rows(v, "v", k)
+    T, hk, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    dev = k.device
+    page = _page_tokens(pool, d)
+    if pool.device != dev or pool.shape[1] != hk:
+        raise ValueError(f"pool: expected [pages, {hk}, block] on {dev}, got {tuple(pool.shape)} on {pool.device}")
+    kh = (0, 0, 0) if k_hat is None else _out_rows(k_hat, "k_hat", k)
+    vh = (0, 0, 0) if v_hat is None else _out_rows(v_hat, "v_hat", v)
+    _run(lib().qwm_paged_append,
+         _APPEND.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), _array(slots, "slots", torch.int64, (T,), dev), _status(status, dev),
+                      T, pool.shape[0], _DTYPES[k.dtype], d, hk, page), "qwm_paged_append", dev)
+
+
+def _workspace(dev: torch.device, d: int) -> torch.Tensor:
+    n = _workspace_bytes.get((dev, d))
+    if n is None:
+        with torch.cuda.device(dev):
+            n = _workspace_bytes[dev, d] = int(lib().qwm_paged_attend_workspace_bytes(d))
+        if n == 0:
+            raise ValueError(f"head_dim 64 or 128 is built, not {d}")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                     cu_rows: torch.Tensor, max_new: Optional[int] = None, causal: bool = True, window: int = 0,
+                     scale: float = 0.0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, kernel: int = PAGED_AUTO) -> torch.Tensor:
+    """Attention of the rows of a plan, q [rows, heads, d], over their
+    requests' pages (kv_len and cu_rows as qwm_paged_plan returns them).
+    max_new: the most rows of one request as the host knows it (chooses the
+    kernel; all rows when absent).  window > 0: only the last `window` tokens
+    up to the row's own.  lse: float32 [rows, heads] to receive the log-sum-
+    exp.  Rows behind the last request are left as they were in `out`."""
+    qr = _rows(q, "q")
+    T, hq, d = q.shape
+    dev = q.device
+    page = _page_tokens(pool, d)
+    hk = pool.shape[1]
+    if pool.device != dev or hk < 1 or hq % hk:
+        raise ValueError(f"pool: kv heads that divide {hq} on {dev} are expected, got {tuple(pool.shape)} on {pool.device}")
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
+    ot = _out_rows(out, "out", q)
+    table = _array(block_table, "block_table", torch.int32, (None, None), dev)
+    B = block_table.shape[0]
+    lens = _array(kv_len, "kv_len", torch.int32, (B,), dev)
+    cu = _array(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
+    ls = 0 if lse is None else _array(lse, "lse", torch.float32, (T, hq), dev)
+    ws = _workspace(dev, d)
+    _run(lib().qwm_paged_attend,
+         _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), ws.numel(), T,
+                      pool.shape[0], T if max_new is None else max_new, _DTYPES[q.dtype], d, hq, hk, page, B,
+                      block_table.shape[1], 1 if causal else 0, window, scale, kernel), "qwm_paged_attend", dev)
+    return out
+
+
+def paged_attend_kernel_for(dtype: torch.dtype, heads: int, kv_heads: int, max_new: int) -> int:
+    """The attention kernel (PAGED_SIMT, PAGED_MMA or PAGED_TC) of the automatic choice."""
+    return int(lib().qwm_paged_attend_kernel_for(_DTYPES[dtype], heads, kv_heads, max_new))

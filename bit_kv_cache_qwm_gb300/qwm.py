@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libqwm_dbg.so" if os.environ.get("QWM_DEBUG_BOUND
 
 QWM_F32, QWM_BF16 = 0, 1
 DEV_NOT_CONVERGED, DEV_SATURATED, DEV_TIMEOUT, DEV_BOUNDS = 0x1, 0x2, 0x4, 0x8
+DEV_NAN, DEV_CAPACITY = 0x10, 0x20
 # attention kernels (qwm_set_attend_kernel): automatic choice, float32 SIMT,
 # bf16 mma.sync, tcgen05 with one query tile per CTA, tcgen05 with two query
 # tiles per CTA, few-row split-KV (M <= 64), tcgen05 with the key split into
@@ -62,7 +63,9 @@ EXPORTS = ["qwm_status_string", "qwm_sizes", "qwm_create", "qwm_destroy", "qwm_s
            "qwm_attend", "qwm_rewind", "qwm_get_status", "qwm_peek_status_bits",
            "qwm_set_attend_kernel", "qwm_resolved_attend_kernel", "qwm_attend_kernel_for", "qwm_set_assignment",
            "qwm_dequantize", "qwm_selftest_wait_timeout", "qwm_num_tokens",
-           "qwm_num_tiles", "qwm_num_segments", "qwm_version"]
+           "qwm_num_tiles", "qwm_num_segments", "qwm_version", "qwm_qk_norm_rope", "qwm_paged_plan",
+           "qwm_paged_release", "qwm_paged_block_bytes", "qwm_paged_append", "qwm_paged_attend",
+           "qwm_paged_attend_workspace_bytes", "qwm_paged_attend_kernel_for"]
 
 _lib = None
 
@@ -97,6 +100,12 @@ def lib() -> ctypes.CDLL:
         "qwm_selftest_wait_timeout": [I64, VP, VP],
         "qwm_calibrate_static": [I32, I32, I32, I32, I32, I32, VP, I64, VP, VP, VP, VP, VP, VP],
         "qwm_kmeans": [I32, I32, I32, I32, VP, I64, VP, I32, VP, VP, VP],
+        # argument structs, packed by paged.py
+        "qwm_qk_norm_rope": [ctypes.c_char_p, VP],
+        "qwm_paged_plan": [ctypes.c_char_p, VP],
+        "qwm_paged_release": [ctypes.c_char_p, VP],
+        "qwm_paged_append": [ctypes.c_char_p, VP],
+        "qwm_paged_attend": [ctypes.c_char_p, VP],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -104,6 +113,12 @@ def lib() -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     L.qwm_kmeans_workspace_bytes.restype = ctypes.c_size_t
     L.qwm_kmeans_workspace_bytes.argtypes = [I32, I32, I32, I64]
+    L.qwm_paged_block_bytes.restype = ctypes.c_size_t
+    L.qwm_paged_block_bytes.argtypes = [I32, I32]
+    L.qwm_paged_attend_workspace_bytes.restype = ctypes.c_size_t
+    L.qwm_paged_attend_workspace_bytes.argtypes = [I32]
+    L.qwm_paged_attend_kernel_for.restype = I32
+    L.qwm_paged_attend_kernel_for.argtypes = [I32, I32, I32, I64]
     L.qwm_attend_kernel_for.restype = I32
     L.qwm_attend_kernel_for.argtypes = [VP, I64]
     for name, rt in [("qwm_resolved_attend_kernel", I32), ("qwm_num_tokens", I64), ("qwm_num_tiles", I64), ("qwm_num_segments", I32),

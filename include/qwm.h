@@ -64,21 +64,28 @@ typedef enum { QWM_F32 = 0, QWM_BF16 = 1 } qwm_dtype;
  *                            checks, before any CUDA call, creating nothing;
  *   QWM_FAULT_INJECT=launch  qwm_set_centroids, qwm_calibrate,
  *                            qwm_set_calibration, qwm_append, qwm_attend,
- *                            qwm_dequantize and qwm_kmeans return QWM_ERR_CUDA
+ *                            qwm_dequantize, qwm_kmeans, qwm_qk_norm_rope and
+ *                            the qwm_paged_ calls return QWM_ERR_CUDA
  *                            after their argument checks and before launching
  *                            anything; the context is left unchanged.
  * A library built with -DQWM_DEBUG_BOUNDS (libqwm_dbg.so) checks every
  * centroid index it reads from the cache against n_centroids; one out of range
  * sets QWM_DEV_BOUNDS in the status word and is read as 0.
- * qwm_calibrate, qwm_append and qwm_attend each open an NVTX range of their
- * own name (recorded only under a profiler). */
+ * qwm_calibrate, qwm_append, qwm_attend, qwm_qk_norm_rope and the qwm_paged_
+ * calls each open an NVTX range of their own name (recorded only under a
+ * profiler). */
 
 /* device status word bits (qwm_get_status / qwm_peek_status_bits) */
 #define QWM_DEV_NOT_CONVERGED 0x1u  /* calibrate: residual above tolerance at max_iter */
 #define QWM_DEV_SATURATED     0x2u  /* append: a float16 zero or scale saturated at 65504 */
 #define QWM_DEV_TIMEOUT       0x4u  /* a bounded device wait ran out; the kernel left early */
 #define QWM_DEV_BOUNDS        0x8u  /* QWM_DEBUG_BOUNDS builds only: a cache slot named a
-                                       centroid index >= n_centroids (read as 0) */
+                                       centroid index >= n_centroids (read as 0); in every
+                                       build: an index, length or position on the device that
+                                       a paged call was handed was out of range (see there) */
+#define QWM_DEV_NAN           0x10u /* paged append: a NaN was stored as 0 */
+#define QWM_DEV_CAPACITY      0x20u /* paged plan or release: the request did not fit; nothing
+                                       was changed */
 
 typedef struct {
   int32_t heads;         /* H >= 1                                              */
@@ -320,6 +327,207 @@ int64_t qwm_num_tokens(const qwm_ctx* ctx);    /* valid tokens cached        */
 int64_t qwm_num_tiles(const qwm_ctx* ctx);     /* tiles in use per head      */
 int32_t qwm_num_segments(const qwm_ctx* ctx);  /* append calls kept          */
 int32_t qwm_version(const qwm_ctx* ctx);       /* current basis version, -1 before any */
+
+/* ------------------------------------------------------------------------
+ * The paged 4-bit cache: many requests of different lengths in one pool of
+ * pages, without calibration or centroids (an extension; the QuantWM pages
+ * describe the 2-bit cache above only).  A serving step is
+ *   qwm_paged_plan      once a step: new pages, slots and positions of its rows;
+ * and in every layer
+ *   qwm_qk_norm_rope    RMS norm of each query and key head, and rotation;
+ *   qwm_paged_append    INT4 quantisation of the new keys and values into pages;
+ *   qwm_paged_attend    attention of the new rows over their requests' pages;
+ * and qwm_paged_release when requests end or are cut back.
+ *
+ * These calls keep nothing between calls and need no context.  Every pointer
+ * in the argument structs is a device address on the current device; all
+ * lengths, tables and counts live on the device, so a step can be captured
+ * into a CUDA graph and replayed with other lengths.  Calls are asynchronous
+ * on `stream`, allocate nothing and write only what is documented, so calls
+ * on different streams (or graphs replayed at the same time) are independent
+ * as long as they share no buffer that one of them writes, workspaces
+ * included.  `status`, where a struct has it, is an optional device word
+ * (caller-zeroed) into which the call ORs QWM_DEV_ bits.
+ *
+ * Pool: [n_pages][kv_heads][block], one pool per layer.  A block holds
+ * page_tokens slots (16, 32, 64, 128 or 256) of one key/value head:
+ *   K codes   [slot][d/2]       4-bit codes, channel c in byte c/2, bits 4 (c mod 2)
+ *   K params  [slot][d/32][2]   fp16 (zero, scale) of each group of 32 channels
+ *   V codes, V params           the same for the value
+ * qwm_paged_block_bytes = page_tokens (d + d/4) bytes.  Token n of request b
+ * is in slot n mod page_tokens of page block_table[b][n / page_tokens]. */
+
+/* Rows of a caller's tensor [rows][heads][head_dim]: element (t, h, c) is at
+ * ptr + t row_stride + h head_stride + c (strides in elements, so views of a
+ * fused projection and [heads][rows][head_dim] tensors both fit).  ptr and
+ * strides must be multiples of 16 bytes (QWM_ERR_INVALID_ARG otherwise);
+ * strides are not negative, and those of an output must not let two elements
+ * share an address. */
+typedef struct {
+  void* ptr;
+  int64_t row_stride, head_stride;
+} qwm_rows;
+
+/* RMS norm of every head of q and k with the rotary position encoding in the
+ * same pass:
+ *   x' = x (mean(x^2) + eps)^(-1/2) w     (float32; w = 1 where a weight is NULL)
+ *   pair j of the rot/2 rotated pairs: (a, b) -> (a cos - b sin, b cos + a sin)
+ * with channels (j, j + rot/2), or (2j, 2j + 1) when interleaved, and cos, sin
+ * = cos_sin[p][j], cos_sin[p][rot/2 + j] at p = positions[t][axis(j)].  Pairs
+ * are dealt to the axes in order: the first sections[0] to axis 0 and so on
+ * (one axis takes all).  Channels from rot on are normed, not rotated.  One
+ * rounding to the dtype at the end.  Outputs may be the inputs (in place; the
+ * same pointer and strides), else must not overlap them.
+ * A row with a negative position on any axis is padding: its outputs are left
+ * as they were.  So is a row with a position >= n_positions, which also sets
+ * QWM_DEV_BOUNDS. */
+typedef struct {
+  qwm_rows q, k, q_out, k_out;   /* dtype; k ignored when k_heads = 0           */
+  const void* q_weight;          /* [head_dim] dtype, or NULL                   */
+  const void* k_weight;
+  const float* cos_sin;          /* [n_positions][rot]: rot/2 cos, rot/2 sin;
+                                    16-byte aligned                             */
+  const int32_t* positions;      /* [rows][axes]                                */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t rows, n_positions;
+  int32_t dtype, head_dim;       /* QWM_F32 or QWM_BF16; 64 or 128              */
+  int32_t q_heads, k_heads;      /* >= 1, >= 0                                  */
+  int32_t rot;                   /* rotated channels: a multiple of 16, <= d    */
+  int32_t axes;                  /* 1 to 4                                      */
+  int32_t sections[4];           /* pairs of each axis; sum rot/2               */
+  int32_t interleaved;
+  float eps;                     /* >= 0                                        */
+} qwm_qk_norm_rope_args;
+qwm_status qwm_qk_norm_rope(const qwm_qk_norm_rope_args* a, void* stream);
+
+/* Block tables, slots and positions of a step from the lengths of its
+ * requests.  Request b holds kv_len[b] tokens in ceil(kv_len[b] / page_tokens)
+ * pages and brings new_len[b] >= 0 tokens.  Pages come off the top of a stack
+ * (free_pages[0 .. free_count)) in the order of the requests: the i-th new
+ * page of the call is free_pages[free_count - 1 - i].  Writes
+ *   kv_len_out[b]   kv_len[b] + new_len[b]
+ *   cu_rows[b]      first row of request b; cu_rows[requests] = rows in use
+ *   block_table     the entries of the new pages, no others
+ *   free_count_out  pages left
+ *   slots[t]        page * page_tokens + slot of row t, -1 for rows not in use
+ *   positions[t]    the row's position in its request, -1 for rows not in use
+ * The call changes all or nothing: when the pages run out, a request would
+ * outgrow max_blocks, the new rows exceed `rows`, or a length is negative, it
+ * sets QWM_DEV_CAPACITY (QWM_DEV_BOUNDS for a negative length or free_count
+ * outside [0, n_pages]), copies kv_len and free_count, sets cu_rows to 0 and
+ * every slot and position to -1, and leaves block_table alone.  A page id
+ * outside [0, n_pages) sets QWM_DEV_BOUNDS and its rows get slot -1.
+ * kv_len_out may be kv_len, free_count_out may be free_count; other outputs
+ * overlap nothing.  At most 8192 requests (QWM_ERR_UNSUPPORTED above). */
+typedef struct {
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* new_len;        /* [requests]                                  */
+  const int32_t* free_pages;     /* [n_pages]                                   */
+  const int32_t* free_count;     /* [1]                                         */
+  int32_t* block_table;          /* [requests][max_blocks]                      */
+  int32_t* kv_len_out;           /* [requests]                                  */
+  int32_t* free_count_out;       /* [1]                                         */
+  int32_t* cu_rows;              /* [requests + 1]                              */
+  int64_t* slots;                /* [rows]                                      */
+  int32_t* positions;            /* [rows]                                      */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t rows, n_pages;         /* rows < 2^31, n_pages < 2^31                 */
+  int32_t requests, max_blocks, page_tokens;
+} qwm_paged_plan_args;
+qwm_status qwm_paged_plan(const qwm_paged_plan_args* a, void* stream);
+
+/* Cut request b back to keep_len[b] tokens (0 ends it) and push the pages it
+ * no longer needs on the free stack, requests in order, a request's pages in
+ * order; their table entries become -1.  kv_len, block_table, free_pages and
+ * free_count are updated in place.  keep_len[b] outside [0, kv_len[b]] keeps
+ * the request as it is and sets QWM_DEV_BOUNDS; a page id outside
+ * [0, n_pages) is not pushed and sets it too.  When the stack would pass
+ * n_pages (a page released twice) nothing is changed and QWM_DEV_CAPACITY is
+ * set.  At most 8192 requests. */
+typedef struct {
+  const int32_t* keep_len;       /* [requests]                                  */
+  int32_t* kv_len;               /* [requests]                                  */
+  int32_t* block_table;          /* [requests][max_blocks]                      */
+  int32_t* free_pages;           /* [n_pages]                                   */
+  int32_t* free_count;           /* [1]                                         */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t n_pages;
+  int32_t requests, max_blocks, page_tokens;
+} qwm_paged_release_args;
+qwm_status qwm_paged_release(const qwm_paged_release_args* a, void* stream);
+
+/* Bytes of one block, or 0 for a head_dim or page_tokens that is not built. */
+size_t qwm_paged_block_bytes(int32_t head_dim, int32_t page_tokens);
+
+/* Quantise keys and values [rows][kv_heads][d] into the slots of a plan.  For
+ * each group of 32 channels, in float32, one IEEE operation at a time:
+ *   NaN -> 0 (QWM_DEV_NAN), then clamped to +-60000 (QWM_DEV_SATURATED), so
+ *   that every value a page stands for is finite in fp16;
+ *   mn, mx = min, max;  zero = f16(mn);  scale = f16(f32(mx - mn) / 15)
+ *   code = 0 if scale = 0, else clamp(rint(f32(f32(x - zero) / scale)), 0, 15)
+ *   x_hat = zero + code scale
+ * k_hat and v_hat (optional; dtype, rows like the inputs) receive x_hat
+ * rounded to the dtype.  A row with slot -1 (any negative slot) stores
+ * nothing, and its k_hat and v_hat are 0; so does a slot >= n_pages
+ * page_tokens, which sets QWM_DEV_BOUNDS.  The slots of one call must differ
+ * (those of a plan do): of two rows with the same slot, which one's bytes end
+ * up there is undefined. */
+typedef struct {
+  qwm_rows k, v;
+  qwm_rows k_hat, v_hat;         /* ptr NULL: not wanted                        */
+  void* pool;                    /* 16-byte aligned                             */
+  const int64_t* slots;          /* [rows]                                      */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t rows, n_pages;
+  int32_t dtype, head_dim, kv_heads, page_tokens;
+} qwm_paged_append_args;
+qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
+
+/* Attention of the rows of a plan over their requests' pages.  Row
+ * cu_rows[b] + i is query i of request b, at position
+ * P = kv_len[b] - (cu_rows[b + 1] - cu_rows[b]) + i (kv_len with the new
+ * tokens, as a plan leaves it), and sees the tokens n < kv_len[b] with n <= P
+ * when causal and n > P - window when window > 0 (window needs causal):
+ *   O = softmax(scale q . k_hat_n) v_hat_n,   lse = log sum exp(scale q . k_hat_n)
+ * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
+ * no token gets O = 0 and lse = -inf.  Tokens that a row does not see have no
+ * effect on it.  Rows outside cu_rows[0 .. requests] are left as they were.
+ * A page id outside [0, n_pages) hides its tokens, a kv_len outside
+ * [0, max_blocks page_tokens] is clamped to it and cu_rows that decrease or
+ * leave [0, rows] are clamped; each sets QWM_DEV_BOUNDS.
+ * max_new is the longest request's row count as the host knows it: it chooses
+ * the kernel and never changes what is computed.
+ * kernel: 0 = automatic; 1 = float32 CUDA-core kernel (the choice for
+ * float32); 2 = bf16 mma.sync kernel that streams the pages once for up to 16
+ * rows (heads / kv_heads times max_new); 3 = bf16 tcgen05 kernel with 256 rows
+ * per CTA.  All split long requests over CTAs and join the parts in a second
+ * kernel, in a fixed order.  QWM_ERR_UNSUPPORTED: 2 and 3 with float32, more
+ * than 2^30 rows times heads / kv_heads, max_blocks page_tokens above 2^30. */
+typedef struct {
+  qwm_rows q, out;               /* out may be q (in place)                     */
+  float* lse;                    /* [rows][heads], or NULL                      */
+  const void* pool;              /* 16-byte aligned                             */
+  const int32_t* block_table;    /* [requests][max_blocks]                      */
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* cu_rows;        /* [requests + 1]                              */
+  uint32_t* status;              /* or NULL                                     */
+  void* workspace;               /* 256-byte aligned                            */
+  size_t workspace_bytes;        /* >= qwm_paged_attend_workspace_bytes         */
+  int64_t rows, n_pages, max_new;
+  int32_t dtype, head_dim, heads, kv_heads, page_tokens;
+  int32_t requests, max_blocks;
+  int32_t causal, window;
+  float scale;                   /* <= 0: 1/sqrt(d)                             */
+  int32_t kernel;
+} qwm_paged_attend_args;
+qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream);
+
+/* Bytes of workspace that any call with this head_dim needs on the current
+ * device, whatever its lengths (0 for a head_dim that is not built). */
+size_t qwm_paged_attend_workspace_bytes(int32_t head_dim);
+
+/* The kernel (1 to 3) that the automatic choice runs. */
+int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new);
 
 #ifdef __cplusplus
 }

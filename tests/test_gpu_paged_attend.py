@@ -1,0 +1,244 @@
+"""qwm_paged_attend on the GPU against the float64 oracle: every kernel, head
+layout, page size and mask, with garbage (NaN bytes) in every slot that holds
+no token."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as P
+from paged_cases import Batch, attend_tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def paged():
+    from bit_kv_cache_qwm_gb300 import build
+    build.build()
+    from bit_kv_cache_qwm_gb300 import paged as p
+    return p
+
+
+def dev(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def check(paged, bt, kernel, causal=True, window=0, scale=0.0, max_new=None, tail=2, **kw):
+    """Run one batch and compare O and lse with the oracle; the `tail` rows
+    behind the last request must stay as they were."""
+    T = bt.rows + tail
+    q = torch.zeros((T, bt.heads, bt.d), dtype=torch.bfloat16 if bt.dtype == "bf16" else torch.float32, device="cuda")
+    q[: bt.rows] = dev(bt.q, bt.dtype)
+    q[bt.rows:] = float("nan")
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((T, bt.heads), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    paged.qwm_paged_attend(q, dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu),
+                           max_new=max(bt.new) if max_new is None else max_new, causal=causal, window=window, scale=scale,
+                           out=out, lse=lse, status=status, kernel=kernel, **kw)
+    torch.cuda.synchronize()
+    sigma = scale if scale > 0 else 1 / np.sqrt(bt.d)
+    O, want_lse, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, causal, window, sigma)
+    got = out[: bt.rows].float().cpu().numpy().astype(np.float64)
+    n = int(bt.kv_len.max())
+    tensor = kernel in (paged.PAGED_MMA, paged.PAGED_TC)
+    tol = attend_tolerance(O, spread, vmax, n, bt.dtype, tensor)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - O) > tol
+    assert not bad.any(), (np.argwhere(bad)[:3], np.abs(got - O).max(), (np.abs(got - O) / tol).max())
+    gl = lse[: bt.rows].cpu().numpy().astype(np.float64)
+    empty = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(gl), empty)
+    ltol = spread * (2.0 ** -11 * 1.01 if tensor else 0) + (spread + np.abs(np.where(empty, 0, want_lse)) + n + 200) * 2.0 ** -22
+    assert (np.abs(gl[~empty] - want_lse[~empty]) <= ltol[~empty]).all()
+    assert (got[empty] == 0).all()
+    assert (out[bt.rows:] == 7).all() and (lse[bt.rows:] == 7).all()
+    return int(status.item())
+
+
+KERNELS = ["simt"]
+
+
+def kid(paged, name):
+    return {"auto": paged.PAGED_AUTO, "simt": paged.PAGED_SIMT, "mma": paged.PAGED_MMA, "tc": paged.PAGED_TC}[name]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 8), (8, 1), (6, 2), (15, 3)])
+def test_single_tokens(paged, kernel, d, heads, kv_heads):
+    """One new token for requests of 1 to a few hundred tokens."""
+    bt = Batch(1, [0, 1, 15, 16, 17, 63, 64, 65, 127, 200, 333], [1] * 11, heads, kv_heads, d, 16)
+    assert check(paged, bt, kid(paged, kernel)) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 33), (True, 100)])
+def test_masks_and_pages(paged, kernel, page, causal, window):
+    """Ragged prompts, requests without new tokens among them, odd sizes."""
+    bt = Batch(2, [0, 5, 100, 260, 31, 0], [7, 0, 33, 3, 1, 129], 4, 2, 128, page)
+    assert check(paged, bt, kid(paged, kernel), causal=causal, window=window) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rows_that_see_nothing(paged, kernel):
+    """More query rows than cached tokens: the first rows stand before the
+    cache and see nothing (O = 0, lse = -inf), also where a request has no
+    token at all."""
+    bt = Batch(3, [0, 0, 40], [5, 0, 20], 4, 2, 128, 16)
+    bt.kv_len = np.array([2, 0, 60], np.int32)
+    assert check(paged, bt, kid(paged, kernel)) == 0
+    bt.kv_len = np.array([0, 0, 60], np.int32)
+    assert check(paged, bt, kid(paged, kernel)) == 0
+    assert check(paged, bt, kid(paged, kernel), causal=False) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_requests_are_split(paged, kernel, d):
+    """One request long enough for every CTA to get a part of it, next to
+    short ones; the result is the same bit for bit on a second run."""
+    bt = Batch(4, [9000, 0, 40], [2, 1, 3], 4, 1, d, 64)
+    k = kid(paged, kernel)
+    assert check(paged, bt, k) == 0
+    a = [paged.qwm_paged_attend(dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu), max_new=3, kernel=k)
+         for _ in range(2)]
+    assert torch.equal(a[0], a[1])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("hint", [0, 1, 2, 5000])
+def test_max_new_is_a_hint(paged, kernel, hint):
+    bt = Batch(5, [50, 3, 700], [3, 40, 1], 4, 2, 128, 32)
+    assert check(paged, bt, kid(paged, kernel), max_new=hint) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scale_and_large_queries(paged, kernel):
+    """Queries beyond float16 with a scale that brings the logits back, and a
+    scale that makes the softmax nearly one-hot."""
+    bt = Batch(6, [100, 30], [20, 1], 4, 2, 128, 16, q_sigma=3e5)
+    assert check(paged, bt, kid(paged, kernel), scale=1e-7) == 0
+    bt = Batch(7, [100, 30], [20, 1], 4, 2, 128, 16)
+    assert check(paged, bt, kid(paged, kernel), scale=0.5) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_strided_rows_in_place_and_head_major(paged, kernel):
+    """q as a view of a fused projection, out = q, and [heads][rows] order."""
+    bt = Batch(8, [77, 12], [9, 2], 6, 2, 128, 16)
+    k = kid(paged, kernel)
+    args = (dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+    ref = paged.qwm_paged_attend(dev(bt.q, "bf16"), *args, max_new=9, kernel=k)
+    fused = torch.zeros((bt.rows, 10, 128), dtype=torch.bfloat16, device="cuda")
+    fused[:, 2:8] = dev(bt.q, "bf16")
+    view = fused[:, 2:8]
+    got = paged.qwm_paged_attend(view, *args, max_new=9, out=view, kernel=k)
+    assert got.data_ptr() == view.data_ptr() and torch.equal(view, ref)
+    assert (fused[:, :2] == 0).all() and (fused[:, 8:] == 0).all()
+    hm = dev(bt.q, "bf16").transpose(0, 1).contiguous()
+    o = torch.empty_like(hm)
+    paged.qwm_paged_attend(hm.transpose(0, 1), *args, max_new=9, out=o.transpose(0, 1), kernel=k)
+    assert torch.equal(o.transpose(0, 1), ref)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_bad_tables_and_lengths_are_masked_and_reported(paged, kernel):
+    """A page id out of range hides its tokens; a length beyond the table and
+    offsets that leave the rows are clamped; each sets the status bit."""
+    bt = Batch(9, [100, 90], [3, 2], 4, 2, 128, 16)
+    k = kid(paged, kernel)
+    for bad in (-1, bt.pool.shape[0], 1 << 30, -(1 << 31)):
+        save = bt.table[0, 2]
+        bt.table[0, 2] = bad
+        assert check(paged, bt, k) == 8
+        bt.table[0, 2] = save
+    bt.table[1, :] = -1
+    assert check(paged, bt, k) == 8          # a request with no valid page at all
+    bt = Batch(9, [100, 90], [3, 2], 4, 2, 128, 16)
+    full = bt.table.shape[1] * 16
+    bt.table[0, : bt.table.shape[1]] = bt.table[0, 0]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table))
+    a = paged.qwm_paged_attend(*args, dev(np.array([full + 5000, 92], np.int32)), dev(bt.cu), max_new=3, status=status, kernel=k)
+    assert int(status.item()) == 8
+    b = paged.qwm_paged_attend(*args, dev(np.array([full, 92], np.int32)), dev(bt.cu), max_new=3, kernel=k)
+    assert torch.equal(a, b)
+    status.zero_()
+    out = torch.full_like(a, 7.0)
+    paged.qwm_paged_attend(*args, dev(bt.kv_len), dev(np.array([0, 3, 900], np.int32)), max_new=3, out=out, status=status, kernel=k)
+    assert int(status.item()) == 8 and torch.isfinite(out.float()).all()
+    status.zero_()
+    paged.qwm_paged_attend(*args, dev(np.array([-4, 92], np.int32)), dev(bt.cu), max_new=3, out=out, status=status, kernel=k)
+    assert int(status.item()) == 8 and (out[:3] == 0).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_float32(paged, kernel):
+    if kernel not in ("simt", "auto"):
+        pytest.skip("bf16 kernel")
+    for d in (64, 128):
+        bt = Batch(10, [0, 5, 100, 700], [7, 0, 70, 1], 6, 2, d, 16, dtype="f32")
+        assert check(paged, bt, kid(paged, kernel)) == 0
+        assert check(paged, bt, kid(paged, kernel), window=20) == 0
+        bt = Batch(11, [1500, 5], [1, 2], 3, 1, d, 32, dtype="f32")
+        assert check(paged, bt, kid(paged, kernel)) == 0
+
+
+def test_offsets_beyond_32_bits(paged):
+    """A pool of more than 2^32 bytes with the request's pages at its end."""
+    bt = Batch(12, [300], [2], 8, 8, 128, 256)
+    n = (1 << 32) // bt.pool[0].size + 10
+    big = torch.zeros((n,) + bt.pool.shape[1:], dtype=torch.uint8, device="cuda")
+    shift = n - bt.pool.shape[0]
+    big[shift:] = dev(bt.pool)
+    args = (dev(bt.kv_len), dev(bt.cu))
+    for k in KERNELS:
+        a = paged.qwm_paged_attend(dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), *args, max_new=2, kernel=kid(paged, k))
+        b = paged.qwm_paged_attend(dev(bt.q, "bf16"), big, dev(np.where(bt.table >= 0, bt.table + shift, -1).astype(np.int32)),
+                                   *args, max_new=2, kernel=kid(paged, k))
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_captured_with_other_lengths_and_on_two_streams(paged, kernel):
+    """Two graphs of different batches, replayed at the same time on two
+    streams, with lengths changed between capture and replay."""
+    k = kid(paged, kernel)
+    bts = [Batch(20, [900, 40], [2, 2], 8, 2, 128, 16), Batch(21, [30, 2000, 7], [1, 3, 2], 8, 2, 128, 64)]
+    graphs = []
+    for bt in bts:
+        st = [dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), dev(np.maximum(bt.kv_len - 5, 0)), dev(bt.cu)]
+        out = torch.zeros_like(st[0])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            paged.qwm_paged_attend(*st, max_new=3, out=out, kernel=k)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            paged.qwm_paged_attend(*st, max_new=3, out=out, kernel=k)
+        st[3].copy_(dev(bt.kv_len))
+        graphs.append((g, s, st, out))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s, _, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (g, s, st, out), bt in zip(graphs, bts):
+        ref = paged.qwm_paged_attend(dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu), max_new=3, kernel=k)
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_many_requests(paged, kernel):
+    """More requests than a CTA has threads, most without rows."""
+    r = np.random.default_rng(0)
+    n = 1300
+    cached = r.integers(0, 20, n)
+    new = (r.random(n) < 0.2).astype(int)
+    bt = Batch(13, cached, new, 2, 2, 64, 16)
+    assert check(paged, bt, kid(paged, kernel)) == 0
