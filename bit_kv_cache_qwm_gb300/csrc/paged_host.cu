@@ -50,7 +50,8 @@ bool dim_ok(int32_t d) { return d == 64 || d == 128; }
 
 constexpr int64_t kInt = 0x7fffffff, kHalf = (int64_t)1 << 30;
 
-// the largest workspace any kernel takes (parts, then one Join per worker)
+// workspace: a word for timeouts, the parts, then one Join per worker
+constexpr size_t kHead = 256;
 size_t part_bytes(Workers w, int d) { return (size_t)w.count * 2 * w.rows * part_floats(d) * 4; }
 
 }  // namespace
@@ -136,17 +137,18 @@ extern "C" qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* str
 extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) {
   if (!dim_ok(head_dim)) return 0;
   size_t n = 0, w = 0;
-  for (const Workers& x : {simt_workers(1), simt_workers(64)}) {
+  for (const Workers& x : {simt_workers(1), simt_workers(64), mma_workers(1), mma_workers(16)}) {
     const size_t b = part_bytes(x, head_dim);
     n = b > n ? b : n;
     w = (size_t)x.count > w ? (size_t)x.count : w;
   }
-  return ((n + 255) & ~(size_t)255) + w * sizeof(Join);
+  return kHead + ((n + 255) & ~(size_t)255) + w * sizeof(Join);
 }
 
 extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new) {
   if (!dtype_ok(dtype) || heads < 1 || kv_heads < 1 || heads % kv_heads || max_new < 0) return -1;
-  return 1;
+  if (dtype == QWM_F32) return 1;
+  return max_new * (heads / kv_heads) <= 16 ? 2 : 1;
 }
 
 extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {
@@ -168,11 +170,11 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
       !aligned(a->workspace, 256) || a->workspace_bytes < qwm_paged_attend_workspace_bytes(d))
     return QWM_ERR_INVALID_ARG;
   const int k = a->kernel ? a->kernel : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
-  if (k != 1) return QWM_ERR_UNSUPPORTED;
+  if (k == 3 || (k != 1 && a->dtype == QWM_F32)) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_attend");
   const int64_t max_rows = (a->max_new < 1 ? 1 : a->max_new > a->rows ? a->rows : a->max_new) * group;
-  const Workers w = simt_workers(max_rows);
+  const Workers w = k == 1 ? simt_workers(max_rows) : mma_workers(max_rows);
   AttendArgs x;
   memset(&x, 0, sizeof(x));
   x.q = a->q.ptr;
@@ -187,8 +189,9 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.kv_len = a->kv_len;
   x.cu = a->cu_rows;
   x.status = a->status;
-  x.part = (float*)a->workspace;
-  x.join = (Join*)((uint8_t*)a->workspace + ((part_bytes(w, d) + 255) & ~(size_t)255));
+  x.timeout = a->status ? a->status : (uint32_t*)a->workspace;
+  x.part = (float*)((uint8_t*)a->workspace + kHead);
+  x.join = (Join*)((uint8_t*)a->workspace + kHead + ((part_bytes(w, d) + 255) & ~(size_t)255));
   x.rows = a->rows;
   x.n_pages = (int32_t)a->n_pages;
   x.heads = a->heads;
@@ -204,5 +207,6 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.window = a->window >= (int64_t)a->max_blocks * a->page_tokens ? 0 : a->window;
   const float scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)d);
   x.scale_log2 = scale * 1.4426950408889634f;
-  return cuda_status(launch_attend_simt(x, d, a->dtype == QWM_BF16, max_rows, S(stream)));
+  return cuda_status(k == 1 ? launch_attend_simt(x, d, a->dtype == QWM_BF16, max_rows, S(stream))
+                            : launch_attend_mma(x, d, max_rows, S(stream)));
 }

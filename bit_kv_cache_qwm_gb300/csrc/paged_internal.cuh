@@ -25,6 +25,7 @@ struct AttendArgs {
   const int32_t* kv_len;
   const int32_t* cu;
   uint32_t* status;
+  uint32_t* timeout;             // word for the bit of a bounded wait that ran out (never null)
   float* part;                   // [workers][2][tile rows][part_floats(d)]
   struct Join* join;             // [workers]
   int64_t rows;
@@ -314,6 +315,8 @@ struct Workers {
 int sm_count();
 Workers simt_workers(int64_t max_rows);
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st);
+Workers mma_workers(int64_t max_rows);
+cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
 // joins the parts of the items that were cut; max_rows: the rows of a
 // request's longest problem as the host knows them (any value is correct)
 cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w, int64_t max_rows, cudaStream_t st);

@@ -57,7 +57,7 @@ def check(paged, bt, kernel, causal=True, window=0, scale=0.0, max_new=None, tai
     return int(status.item())
 
 
-KERNELS = ["simt"]
+KERNELS = ["simt", "mma"]
 
 
 def kid(paged, name):
