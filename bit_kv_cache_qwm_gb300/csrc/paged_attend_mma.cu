@@ -439,12 +439,13 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
 
 template <int D, int NB>
 cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
-  constexpr int smem = Smem<D, NB>::bytes;
-  auto kern = paged_attend_mma_kernel<D, NB>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<workers, kNt, smem, st>>>(a);
-  return cudaGetLastError();
+  static SmemLimit limit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)workers, 1, 1);
+  cfg.blockDim = dim3(kNt, 1, 1);
+  cfg.dynamicSmemBytes = Smem<D, NB>::bytes;
+  cfg.stream = st;
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB>, cfg, a);
 }
 
 }  // namespace

@@ -272,12 +272,13 @@ __global__ void __launch_bounds__(128) paged_attend_join_kernel(const AttendArgs
 
 template <int D, int R, class T>
 cudaError_t launch_simt(const AttendArgs& a, int workers, cudaStream_t st) {
-  constexpr int smem = Shape<D, R>::floats * 4;
-  auto kern = paged_attend_simt_kernel<D, R, T>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<workers, kNt, smem, st>>>(a);
-  return cudaGetLastError();
+  static SmemLimit limit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)workers, 1, 1);
+  cfg.blockDim = dim3(kNt, 1, 1);
+  cfg.dynamicSmemBytes = Shape<D, R>::floats * 4;
+  cfg.stream = st;
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_simt_kernel<D, R, T>, cfg, a);
 }
 
 template <class T>
@@ -289,10 +290,12 @@ cudaError_t launch_simt_t(const AttendArgs& a, int d, Workers w, cudaStream_t st
 }  // namespace
 
 int sm_count() {
+  static std::atomic<int> known[64];   // 0: not asked yet
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 152;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

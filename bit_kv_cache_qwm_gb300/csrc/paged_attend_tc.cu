@@ -1,0 +1,556 @@
+// qwm_paged_attend for many rows (kernel 3, bf16): prompts and chunks, on the
+// 5th-generation tensor cores.
+//
+//   S = Q K_hat^T,  P = exp2(S - m),  O += P V_hat   (float16 operands, float32 sums)
+//
+// A worker (one CTA an SM) walks items of 256 rows (two M = 128 query tiles a,
+// b of one request and key/value head; the rows of a head group follow one
+// another token by token) and tiles of 128 tokens.  Warp roles (13 warps):
+//   warps 0-3 / 4-7  softmax of query tile a / b, thread = row = TMEM lane:
+//                    Q (float16, scaled per row by a power of two) into a SW128
+//                    K-major tile once an item; per tile the online softmax in
+//                    the exp2 domain with O rescaled only when the maximum
+//                    grows by more than 2^8, P in float16 over the first 64
+//                    columns of S; at the item's end O from TMEM to memory.
+//   warps 8-11       producers, thread = token: the packed codes (64 + 64
+//                    bytes at d = 128) and parameters of the next tile are
+//                    loaded into registers one tile ahead, its page id two
+//                    tiles ahead, and dequantised into two-stage K and V tiles
+//                    (one 16-byte store a code word, no bank conflicts: the
+//                    eight rows of a store phase differ in the swizzle).
+//   warp 12          MMA issuer and TMEM owner.
+// Tensor order: S_a(0) S_b(0), then per tile t
+//   PV_a(t) S_a(t+1) PV_b(t) S_b(t+1)
+// so while one query tile's 16 MMAs run (1.25K cycles at d = 128) the other's
+// softmax has the time for P; S_g(t+1) follows PV_g(t) in the pipe, which keeps
+// P_g(t), lying over S_g, until it has been read.  PV_g is issued in three
+// parts as P's keys are written.  K and V are double-buffered so that the
+// producers are never waited for.
+// Handoffs between threads are named barriers (K and V of a stage written, P
+// parts written), which do not queue behind the operand reads in the
+// shared-memory pipe; the tensor pipe's completions arrive on mbarriers.
+// Every mbarrier wait is bounded; after one runs out all roles go on through
+// their loops without waiting or issuing, so that the named barriers stay
+// matched, and the kernel returns with the status bit set.
+// Channel order of all operands within 8 channels: 0 4 1 5 2 6 3 7, the order
+// in which masks of a code word give float16 pairs.
+// TMEM columns: S_a [0,128), S_b [128,256), O_a [256,256+d), O_b [384,384+d).
+// Bound by the tensor pipe and the softmax between its MMAs.
+#include "paged_internal.cuh"
+#include "tcgen05_util.cuh"
+
+namespace qwm {
+namespace paged {
+namespace {
+
+using namespace tcx;
+
+constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12;
+constexpr uint32_t kColO = 256;
+constexpr float kNone = -3.0e38f;
+// float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
+constexpr uint32_t kIdescS = (1u << 4) | (16u << 17) | (8u << 24);
+
+template <int D>
+struct Lay {
+  static constexpr int op = 128 * D * 2;              // one operand tile
+  static constexpr int k = 2 * op, v = k + 2 * op;    // after Q_a, Q_b
+  static constexpr int bytes = v + 2 * op + 1024;     // and room to align
+  static constexpr uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((uint32_t)(D / 8) << 17) | (8u << 24);
+};
+
+// named barriers: K stage s written (1 + s), V stage s written (3 + s), P_g in
+// three parts (5 + g, 7 + g, 9 + g); softmax group g (11 + g)
+constexpr int kNbK = 1, kNbV = 3, kNbP1 = 5, kNbP2 = 7, kNbP3 = 9, kNbS = 11;
+__device__ __forceinline__ void nb_arrive(int id) { asm volatile("bar.arrive %0, 160;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void nb_sync(int id) { asm volatile("bar.sync %0, 160;" ::"r"(id) : "memory"); }
+// the vote of a softmax group: one warp polls, all learn the result
+__device__ __forceinline__ bool group_all(int g, bool v) {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\n"
+               "selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r) : "r"((uint32_t)v), "r"(kNbS + g) : "memory");
+  return r != 0;
+}
+
+// byte offset of 16-byte chunk `chunk` of row `row` in an operand tile of
+// SW128 atoms of 64 elements
+__device__ __forceinline__ int op_off(int row, int chunk) {
+  return (chunk >> 3) * 16384 + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t dq_lo(uint32_t x, __half2 s, __half2 z) {
+  const __half2 c = __hsub2(u2h((x & 0x000f000fu) | 0x64006400u), __float2half2_rn(1024.f));
+  return h2u(__hfma2(c, s, z));
+}
+__device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z) {
+  const __half2 c = __hfma2(u2h((x & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+  return h2u(__hfma2(c, s, z));
+}
+
+// one token's packed codes and parameters of K or V
+template <int D>
+struct Packed {
+  uint4 code[D / 32];
+  uint32_t par[D / 32];
+
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* params) {
+    if (codes) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) code[i] = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+      if constexpr (D == 128) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(params));
+        par[0] = u.x, par[1] = u.y, par[2] = u.z, par[3] = u.w;
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(params));
+        par[0] = u.x, par[1] = u.y;
+      }
+    } else {   // a token outside the request: zeros
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) code[i] = make_uint4(0, 0, 0, 0), par[i] = 0;
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int row) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const __half2 z = __low2half2(u2h(par[i])), s = __high2half2(u2h(par[i]));
+      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(tile + op_off(row, 4 * i + j)) =
+            make_uint4(dq_lo(w[j], s, z), dq_hi(w[j], s, z), dq_lo(w[j] >> 8, s, z), dq_hi(w[j] >> 8, s, z));
+    }
+  }
+};
+
+// P of the 16 Q keys key0 ... of a tile held in v (float16 pairs into TMEM
+// columns key0 / 2 ...); keys outside [lo, hi) give 0 unless FULL.  Returns
+// the sum.
+template <int Q, bool FULL>
+__device__ __forceinline__ float exp_keys(const uint32_t* v, int key0, int lo, int hi, float2 c2, float2 mv, uint32_t taddr) {
+  float2 ps = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int k0 = 16 * q + 2 * k, key = key0 + k0;
+      const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[k0]), __uint_as_float(v[k0 + 1])), c2, mv);
+      float2 pp = make_float2(ex2(arg.x), ex2(arg.y));
+      if (!FULL) {
+        pp.x = key >= lo && key < hi ? pp.x : 0.f;
+        pp.y = key + 1 >= lo && key + 1 < hi ? pp.y : 0.f;
+      }
+      ps = __fadd2_rn(ps, pp);
+      pk[k] = h2u(__floats2half2_rn(pp.x, pp.y));
+    }
+    tmem_st8(taddr + key0 / 2 + 8 * q, pk);
+  }
+  return ps.x + ps.y;
+}
+
+// maximum over v[0 .. 63] = keys key0 ..., those in [lo, hi)
+template <bool FULL>
+__device__ __forceinline__ float max_keys(const uint32_t* v, int key0, int lo, int hi) {
+  float a = -INFINITY, b = -INFINITY;
+  if (FULL) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      a = max3f(a, __uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]));
+      b = max3f(b, __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+      if (key0 + k >= lo && key0 + k < hi) a = fmaxf(a, __uint_as_float(v[k]));
+  }
+  return fmaxf(a, b);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArgs a) {
+  using L = Lay<D>;
+  using W = Walker<kRows, kTk>;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
+  __shared__ __align__(8) uint64_t bars[9];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_sh;
+  // tokens of a tile on a page out of range, a word for each producer warp.
+  // Four tiles deep: a slot is written again after S(u + 2) is complete, which
+  // every softmax thread's P(u + 1) precedes
+  __shared__ __align__(16) uint32_t bad_sh[4][4];
+  uint64_t* s_done = &bars[0];    // [2] S_g complete
+  uint64_t* pv_done = &bars[2];   // [2] O_g of the item complete
+  uint64_t* k_free = &bars[4];    // [2] K stage read by both query tiles
+  uint64_t* v_free = &bars[6];    // [2]
+  uint64_t* q_ready = &bars[8];   // Q_a and Q_b of the item written
+  const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
+
+  if (tid == 0) {
+    abort_sh = 0;
+    for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
+    bar_init(q_ready, kRows);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    a.join[w].last = -1;
+  }
+  const Share sh = find_share<kRows, kTk, kNt>(a, w, (int)gridDim.x);   // has block barriers
+  if (sh.n == 0) return;
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&tmem_base_sh)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  W it(a);
+  it.start(sh.b, sh.skip, sh.n);
+
+  if (warp < kProd) {
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2, i = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
+    uint32_t s_par = 0, pv_par = 0;
+    int u = 0;
+    do {
+      const int r = 128 * g + i, rr = it.rt * kRows + r;
+      const bool live = r < it.rows;
+      const int tok = live ? rr / a.group : 0, head = live ? it.h * a.group + rr % a.group : 0;
+      float c2;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+                                                         head * a.q_head);
+        float mx = 0.f;
+        if (live) {
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = src[c];
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+          }
+        }
+        const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+        const int e = ex > 14 ? ex - 14 : 0;
+        const float qs = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the largest entry below 2^15
+        c2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        uint8_t* qt = sm + g * L::op;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          // channels (0, 4), (1, 5), (2, 6), (3, 7)
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            o[2 * k] = h2u(__floats2half2_rn(__uint_as_float(u[k] << 16) * qs, __uint_as_float(u[2 + k] << 16) * qs));
+            o[2 * k + 1] = h2u(__floats2half2_rn(__uint_as_float(u[k] & 0xffff0000u) * qs,
+                                                 __uint_as_float(u[2 + k] & 0xffff0000u) * qs));
+          }
+          *reinterpret_cast<uint4*>(qt + op_off(i, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_async_smem();
+        bar_arrive(q_ready);
+      }
+      int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
+      if (a.causal) {
+        const int at = it.rq.n - it.rq.n_new;
+        const int first = (it.rt * kRows + 128 * g) / a.group;
+        const int last = (it.rt * kRows + min(it.rows, 128 * g + 128) - 1) / a.group;
+        top = min(it.hi, at + rr / a.group + 1);
+        top_min = min(it.hi, at + first + 1);
+        if (a.window > 0) {
+          bottom = max(it.lo, at + rr / a.group - a.window + 1);
+          bottom_max = max(it.lo, at + last - a.window + 1);
+        }
+      }
+      float m_run = kNone, l_run = 0.f;
+      for (int t = it.from; t < it.to; ++t, ++u) {
+        const int n0 = t * kTk;
+        const int lo = bottom - n0, hi = top - n0;
+        const bool full = n0 + kTk <= top_min && n0 >= bottom_max;
+        // one warp of the group polls the mbarrier, the vote hands the result on
+        group_all(g, (warp & 3) != 0 || bar_wait(&s_done[g], s_par, &abort_sh, a.timeout));
+        s_par ^= 1;
+        fence_after();
+        const uint4 bad = *reinterpret_cast<const uint4*>(bad_sh[u & 3]);
+        if (bad.x | bad.y | bad.z | bad.w) {
+          // rare: their logits become -inf in place
+#pragma unroll 1
+          for (int cb = 0; cb < 8; ++cb) {
+            const uint32_t word = cb < 2 ? bad.x : cb < 4 ? bad.y : cb < 6 ? bad.z : bad.w;
+            const uint32_t bits = word >> (16 * (cb & 1));
+            uint32_t x[16];
+            tmem_ld16(sbase + 16 * cb, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (bits >> k & 1) x[k] = 0xff800000u;
+            tmem_st16(sbase + 16 * cb, x);
+          }
+          tmem_wait_st();
+        }
+        uint32_t v[64];
+        tmem_ld64(sbase + 64, v);
+        tmem_wait_ld();
+        float mx = full ? max_keys<true>(v, 64, lo, hi) : max_keys<false>(v, 64, lo, hi);
+        tmem_ld64(sbase, v);
+        tmem_wait_ld();
+        mx = fmaxf(mx, full ? max_keys<true>(v, 0, lo, hi) : max_keys<false>(v, 0, lo, hi));
+        const float mnew = fmaxf(m_run, mx * c2);
+        const bool need = mnew > m_run + 8.f;
+        // S_g(t) follows PV_g(t-1) in the tensor pipe's order, so O_g is complete
+        if (t > it.from && __any_sync(0xffffffffu, need)) {
+          const float corr = need ? ex2(m_run - mnew) : 1.f;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 16; ++cb) {
+            uint32_t o[16];
+            tmem_ld16(obase + 16 * cb, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+            tmem_st16(obase + 16 * cb, o);
+          }
+          l_run *= corr;
+        }
+        if (need) m_run = mnew;
+        const float2 c2v = make_float2(c2, c2), mv = make_float2(-m_run, -m_run);
+        float ps = full ? exp_keys<4, true>(v, 0, lo, hi, c2v, mv, sbase) : exp_keys<4, false>(v, 0, lo, hi, c2v, mv, sbase);
+        tmem_wait_st();
+        fence_before();
+        nb_arrive(kNbP1 + g);
+#pragma unroll 1
+        for (int hq = 0; hq < 2; ++hq) {
+          uint32_t x[32];
+          tmem_ld32(sbase + 64 + 32 * hq, x);
+          tmem_wait_ld();
+          ps += full ? exp_keys<2, true>(x, 64 + 32 * hq, lo, hi, c2v, mv, sbase)
+                     : exp_keys<2, false>(x, 64 + 32 * hq, lo, hi, c2v, mv, sbase);
+          if (hq == 0) {
+            tmem_wait_st();
+            fence_before();
+            nb_arrive(kNbP2 + g);
+          }
+        }
+        tmem_wait_st();
+        l_run += ps;
+        fence_before();
+        nb_arrive(kNbP3 + g);
+      }
+      group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
+      pv_par ^= 1;
+      fence_after();
+      // ---- O of the item: column p of 8 holds channel (p / 2) + 4 (p % 2)
+      const bool all = it.begins() && it.ends();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      float* part = part_row(a, w, it.begins() ? 1 : 0, kRows, r, D);
+      __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (int64_t)(it.rq.row0 + tok) * a.o_row + head * a.o_head;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t x[32];
+        tmem_ld32(obase + 32 * cb, x);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[(k >> 1) + 4 * (k & 1)] = __uint_as_float(x[8 * q + k]);
+            if (all) {
+              uint32_t u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * k] * inv, y[2 * k + 1] * inv);
+                u[k] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(dst + 32 * cb + 8 * q) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+              *reinterpret_cast<float4*>(part + 32 * cb + 8 * q) = make_float4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<float4*>(part + 32 * cb + 8 * q + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          }
+        }
+      }
+      if (live) {
+        if (!all) {
+          part[D] = m_run, part[D + 1] = l_run;
+        } else if (a.lse) {
+          a.lse[(int64_t)(it.rq.row0 + tok) * a.heads + head] =
+              l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      if (tid == 0 && it.begins() && !it.ends()) {
+        const int64_t end = sh.first + (sh.n - it.left - (it.to - it.from)) + (it.t1 - it.t0);
+        record_join(a, w, it, last_worker(sh, end), kRows);
+      }
+      fence_before();   // the reads of O come before the next item's MMAs
+    } while (it.next());
+  } else if (warp < kMma) {
+    // ------------------------------------------------------------ producers
+    const int p = tid - kProd * 32;
+    constexpr int G = D / 32;
+    Packed<D> kp, vp;
+    int t = it.from;        // the tile whose page id is in flight
+    int pg = -1, n = 0, h = 0;
+    bool in = false, more = true;
+    // the page id of this thread's token of tile t of the current item
+    auto lookup = [&]() {
+      n = t * kTk + p;
+      h = it.h;
+      in = n >= it.lo && n < it.hi;
+      pg = in ? __ldg(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift)) : -1;
+    };
+    auto advance = [&]() {
+      if (++t < it.to) return true;
+      if (!it.next()) return false;
+      t = it.from;
+      return true;
+    };
+    const uint8_t* blk = nullptr;
+    int s = 0;
+    uint32_t bad = 0;
+    auto resolve = [&]() {
+      const bool good = in && pg >= 0 && pg < a.n_pages;
+      if (in && !good) flag(a.status, QWM_DEV_BOUNDS);
+      bad = __ballot_sync(0xffffffffu, in && !good);
+      s = n & (a.page - 1);
+      blk = good ? a.pool + ((int64_t)pg * a.kv_heads + h) * a.block : nullptr;
+    };
+    auto load = [&](Packed<D>& x, int half) {
+      const uint8_t* b = blk ? blk + half * (a.block / 2) : nullptr;
+      x.load(b ? b + s * (D / 2) : nullptr, b ? b + a.page * (D / 2) + s * (G * 4) : nullptr);
+    };
+    lookup();
+    resolve();
+    load(kp, 0);
+    load(vp, 1);
+    more = advance();
+    if (more) lookup();
+    bool ok = true;
+    for (int u = 0;; ++u) {
+      const int st = u & 1;
+      const uint32_t par = (uint32_t)(((u >> 1) - 1) & 1);
+      const bool have = more;
+      if (u >= 2) ok = bar_wait(&k_free[st], par, &abort_sh, a.timeout) && ok;
+      kp.store(sm + L::k + st * L::op, p);
+      if ((p & 31) == 0) bad_sh[u & 3][p >> 5] = bad;
+      fence_async_smem();
+      nb_arrive(kNbK + st);
+      if (have) {
+        resolve();
+        load(kp, 0);
+      }
+      if (u >= 2) ok = bar_wait(&v_free[st], par, &abort_sh, a.timeout) && ok;
+      vp.store(sm + L::v + st * L::op, p);
+      fence_async_smem();
+      nb_arrive(kNbV + st);
+      if (!have) break;
+      load(vp, 1);
+      more = advance();
+      if (more) lookup();
+    }
+  } else {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t q0 = su32(sm), k0 = su32(sm + L::k), v0 = su32(sm + L::v);
+    int u = 0;
+    uint32_t q_par = 0;
+    bool ok = true;
+    auto issue_s = [&](int g, int st) {
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t ko = (j >> 2) * 16384 + (j & 3) * 32;
+          mma_ss(tmem + 128u * g, desc_sw128(q0 + g * L::op + ko), desc_sw128(k0 + st * L::op + ko), kIdescS, j > 0);
+        }
+        commit(&s_done[g]);
+        if (g == 1) commit(&k_free[st]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int g, int st, int j0, int j1, bool first) {
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= j0 && j < j1)
+            mma_ts(tmem + kColO + 128u * g, tmem + 128u * g + 8 * j, desc_sw128_mn(v0 + st * L::op + 2048 * j), L::idesc_pv,
+                   (first && j == 0) ? 0u : 1u);
+      }
+      __syncwarp();
+    };
+    do {
+      ok = warp_all(bar_wait(q_ready, q_par, &abort_sh, a.timeout)) && ok;
+      q_par ^= 1;
+      nb_sync(kNbK + (u & 1));
+      fence_after();
+      if (ok) {
+        issue_s(0, u & 1);
+        issue_s(1, u & 1);
+      }
+      for (int t = it.from; t < it.to; ++t, ++u) {
+        const int st = u & 1;
+        const bool last = t + 1 == it.to;
+        ok = ok && !__any_sync(0xffffffffu, abort_sh != 0);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          nb_sync(kNbP1 + g);
+          if (g == 0) nb_sync(kNbV + st);
+          fence_after();
+          if (ok) issue_pv(g, st, 0, 4, t == it.from);
+          nb_sync(kNbP2 + g);
+          fence_after();
+          if (ok) issue_pv(g, st, 4, 6, false);
+          nb_sync(kNbP3 + g);
+          fence_after();
+          if (ok) {
+            issue_pv(g, st, 6, 8, false);
+            if (elect_one()) {
+              if (last) commit(&pv_done[g]);
+              if (g == 1) commit(&v_free[st]);
+            }
+            __syncwarp();
+          }
+          if (!last) {
+            if (g == 0) {
+              nb_sync(kNbK + (st ^ 1));
+              fence_after();
+            }
+            if (ok) issue_s(g, st ^ 1);
+          }
+        }
+      }
+    } while (it.next());
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D>
+cudaError_t launch_tc(const AttendArgs& a, int workers, cudaStream_t st) {
+  static SmemLimit limit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)workers, 1, 1);
+  cfg.blockDim = dim3(kNt, 1, 1);
+  cfg.dynamicSmemBytes = Lay<D>::bytes;
+  cfg.stream = st;
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_tc_kernel<D>, cfg, a);
+}
+
+}  // namespace
+
+Workers tc_workers() { return Workers{sm_count(), kRows}; }
+
+cudaError_t launch_attend_tc(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
+  const Workers w = tc_workers();
+  const cudaError_t e = d == 64 ? launch_tc<64>(a, w.count, st) : launch_tc<128>(a, w.count, st);
+  return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);
+}
+
+}  // namespace paged
+}  // namespace qwm

@@ -320,24 +320,22 @@ __global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged
 }  // namespace
 
 cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st) {
-  const size_t smem = (size_t)a.requests * 12;
-  cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRequests * 12);
-  if (e != cudaSuccess) return e;
+  static SmemLimit limit;
   // one CTA writes ~1024 rows a microsecond
   const unsigned ctas = a.rows <= 4096 ? 1 : 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kPlanNt, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)a.requests * 12;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return a.requests * 12 <= 48 * 1024 ? cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift)
+                                      : launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift);
 }
 
 cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {

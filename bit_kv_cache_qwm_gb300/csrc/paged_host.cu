@@ -137,7 +137,7 @@ extern "C" qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* str
 extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) {
   if (!dim_ok(head_dim)) return 0;
   size_t n = 0, w = 0;
-  for (const Workers& x : {simt_workers(1), simt_workers(64), mma_workers(1), mma_workers(16)}) {
+  for (const Workers& x : {simt_workers(1), simt_workers(64), mma_workers(1), mma_workers(16), tc_workers()}) {
     const size_t b = part_bytes(x, head_dim);
     n = b > n ? b : n;
     w = (size_t)x.count > w ? (size_t)x.count : w;
@@ -148,7 +148,7 @@ extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) {
 extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new) {
   if (!dtype_ok(dtype) || heads < 1 || kv_heads < 1 || heads % kv_heads || max_new < 0) return -1;
   if (dtype == QWM_F32) return 1;
-  return max_new * (heads / kv_heads) <= 16 ? 2 : 1;
+  return max_new * (heads / kv_heads) <= 16 ? 2 : 3;
 }
 
 extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {
@@ -170,11 +170,11 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
       !aligned(a->workspace, 256) || a->workspace_bytes < qwm_paged_attend_workspace_bytes(d))
     return QWM_ERR_INVALID_ARG;
   const int k = a->kernel ? a->kernel : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
-  if (k == 3 || (k != 1 && a->dtype == QWM_F32)) return QWM_ERR_UNSUPPORTED;
+  if (k != 1 && a->dtype == QWM_F32) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_attend");
   const int64_t max_rows = (a->max_new < 1 ? 1 : a->max_new > a->rows ? a->rows : a->max_new) * group;
-  const Workers w = k == 1 ? simt_workers(max_rows) : mma_workers(max_rows);
+  const Workers w = k == 1 ? simt_workers(max_rows) : k == 2 ? mma_workers(max_rows) : tc_workers();
   AttendArgs x;
   memset(&x, 0, sizeof(x));
   x.q = a->q.ptr;
@@ -208,5 +208,6 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   const float scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)d);
   x.scale_log2 = scale * 1.4426950408889634f;
   return cuda_status(k == 1 ? launch_attend_simt(x, d, a->dtype == QWM_BF16, max_rows, S(stream))
-                            : launch_attend_mma(x, d, max_rows, S(stream)));
+                     : k == 2 ? launch_attend_mma(x, d, max_rows, S(stream))
+                              : launch_attend_tc(x, d, max_rows, S(stream)));
 }

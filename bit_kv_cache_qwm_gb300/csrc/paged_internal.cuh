@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include "qwm_internal.cuh"
 
 namespace qwm {
@@ -312,11 +314,36 @@ struct Workers {
   int count;   // CTAs that share the work
   int rows;    // rows of one item
 };
-int sm_count();
+int sm_count();   // of the current device
+// Launch `kern` with more dynamic shared memory than 48 KB.  The limit (the
+// most the kernel ever asks for) is set on its first launch on a device, and
+// once more if a launch fails: a reset of the device forgets it.
+struct SmemLimit {
+  std::atomic<uint8_t> set[64] = {};
+};
+template <class K, class... A>
+cudaError_t launch_smem(SmemLimit& lim, size_t most, K kern, cudaLaunchConfig_t& cfg, const A&... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    if (dev >= 64 || attempt == 1 || !lim.set[dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) lim.set[dev].store(1, std::memory_order_release);
+    }
+    e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) break;
+    cudaGetLastError();   // a failed first launch is not the error of the second
+  }
+  return e;
+}
 Workers simt_workers(int64_t max_rows);
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st);
 Workers mma_workers(int64_t max_rows);
 cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
+Workers tc_workers();
+cudaError_t launch_attend_tc(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
 // joins the parts of the items that were cut; max_rows: the rows of a
 // request's longest problem as the host knows them (any value is correct)
 cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w, int64_t max_rows, cudaStream_t st);

@@ -50,52 +50,60 @@ class PagedPlan(NamedTuple):
     positions: torch.Tensor    # int32 [rows]
 
 
+# the handle of a device's current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(fn, args: bytes, what: str, dev: torch.device):
-    if dev.index == torch.cuda.current_device():
-        st = fn(args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(args, _raw_stream(index))
     if st:
         _check(st, what)
 
 
-def _rows(x, what: str, like=None):
+def _rows(x, what: str, like=None, shape=None):
     """A CUDA tensor [rows, heads, d] in bf16 or float32 with contiguous heads
     of 16-byte aligned vectors (any row and head stride), on like's device in
-    like's dtype; returns (pointer, row stride, head stride)."""
+    like's dtype (and of `shape`, where given); returns (pointer, row stride,
+    head stride)."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor is expected")
-    if x.dim() != 3 or x.dtype not in _DTYPES:
-        raise ValueError(f"{what}: a bfloat16 or float32 tensor [rows, heads, d] is expected, got {x.dtype} {tuple(x.shape)}")
-    if like is not None and (x.dtype != like.dtype or x.device != like.device):
-        raise ValueError(f"{what}: expected {like.dtype} on {like.device}, got {x.dtype} on {x.device}")
+    dt, have = x.dtype, x.shape
+    if len(have) != 3 or dt not in _DTYPES:
+        raise ValueError(f"{what}: a bfloat16 or float32 tensor [rows, heads, d] is expected, got {dt} {tuple(have)}")
+    if like is not None and (dt != like.dtype or x.device != like.device):
+        raise ValueError(f"{what}: expected {like.dtype} on {like.device}, got {dt} on {x.device}")
+    if shape is not None and have != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(have)}")
     s0, s1, s2 = x.stride()
-    n0, n1, n2 = x.shape
-    if s2 != 1 and n2 != 1:
+    if have[0] <= 1:
+        s0 = 0
+    if have[1] <= 1:
+        s1 = 0
+    if s2 != 1 and have[2] != 1:
         raise ValueError(f"{what}: the channels of a head have to be contiguous")
-    align = 8 if x.dtype == torch.bfloat16 else 4
-    if x.data_ptr() % 16 or (n0 > 1 and s0 % align) or (n1 > 1 and s1 % align):
+    p = x.data_ptr()
+    if (p | (s0 | s1) * x.itemsize) & 15:
         raise ValueError(f"{what}: pointer and strides have to be multiples of 16 bytes")
-    return x.data_ptr(), s0 if n0 > 1 else 0, s1 if n1 > 1 else 0
-
-
-def _out_rows(x, what: str, like):
-    r = _rows(x, what, like)
-    if x.shape != like.shape:
-        raise ValueError(f"{what}: expected shape {tuple(like.shape)}, got {tuple(x.shape)}")
-    return r
+    return p, s0, s1
 
 
 def _array(x, what: str, dtype, shape, dev):
     """The pointer of a contiguous tensor of `dtype` and `shape` (None: any) on `dev`."""
     if not isinstance(x, torch.Tensor) or x.device != dev:
         raise ValueError(f"{what}: a tensor on {dev} is expected")
-    if x.dtype != dtype or x.dim() != len(shape) or not x.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {len(shape)}-d {dtype} tensor is expected, got {x.dtype} {tuple(x.shape)}")
-    for have, want in zip(x.shape, shape):
-        if want is not None and have != want:
-            raise ValueError(f"{what}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(x.shape)}")
+    have = x.shape
+    if x.dtype != dtype or len(have) != len(shape) or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {len(shape)}-d {dtype} tensor is expected, got {x.dtype} {tuple(have)}")
+    if have != shape:
+        for n, want in zip(have, shape):
+            if want is not None and n != want:
+                raise ValueError(f"{what}: expected shape {tuple('any' if w is None else w for w in shape)}, got {tuple(have)}")
     return x.data_ptr()
 
 
@@ -145,7 +153,7 @@ def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     dev, dt = q.device, q.dtype
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=dt, device=dev)
-    qo = _out_rows(q_out, "q_out", q)
+    qo = _rows(q_out, "q_out", q, q.shape)
     hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
         kr = _rows(k, "k", q)
@@ -154,7 +162,7 @@ def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
             raise ValueError(f"k: expected [{T}, kv_heads, {d}], got {tuple(k.shape)}")
         if k_out is None:
             k_out = torch.empty((T, hk, d), dtype=dt, device=dev)
-        ko = _out_rows(k_out, "k_out", k)
+        ko = _rows(k_out, "k_out", k, k.shape)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out, k_weight: given without k")
     table = _array(cos_sin, "cos_sin", torch.float32, (None, None), dev)
@@ -166,11 +174,12 @@ def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     if sections is None:
         if axes > 1:
             raise ValueError("sections: needed with several axes")
-        sections = (rot // 2,)
-    sections = tuple(int(x) for x in sections)
-    if len(sections) != axes or sum(sections) != rot // 2 or min(sections) < 0:
-        raise ValueError(f"sections: {axes} counts with the sum {rot // 2} are expected, got {sections}")
-    s = sections + (0,) * (4 - axes)
+        s = (rot // 2, 0, 0, 0)
+    else:
+        s = tuple(sections)
+        if len(s) != axes or sum(s) != rot // 2 or min(s) < 0:
+            raise ValueError(f"sections: {axes} counts with the sum {rot // 2} are expected, got {s}")
+        s += (0,) * (4 - axes)
     wq = 0 if q_weight is None else _array(q_weight, "q_weight", dt, (d,), dev)
     wk = 0 if k_weight is None else _array(k_weight, "k_weight", dt, (d,), dev)
     _run(lib().qwm_qk_norm_rope,
@@ -199,13 +208,14 @@ def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: tor
     d = _array(free_count, "free_count", i32, (1,), dev)
     e = _array(block_table, "block_table", i32, (B, None), dev)
     if out is None:
-        # one allocation for the five (slots first: they are the 8-byte ones)
-        sizes = (2 * rows, rows, B, B + 1, 1)
-        flat = torch.empty(sum(sizes), dtype=i32, device=dev)
-        s, p, kl, cu, fc = flat.split(sizes)
-        out = PagedPlan(kl, fc, cu, s.view(i64), p)
+        # two allocations for the five
+        flat = torch.empty(rows + 2 * B + 2, dtype=i32, device=dev)
+        slots = torch.empty(rows, dtype=i64, device=dev)
+        view = flat.as_strided
+        out = PagedPlan(view((B,), (1,), rows), view((1,), (1,), rows + 2 * B + 1), view((B + 1,), (1,), rows + B), slots,
+                        view((rows,), (1,), 0))
         base = flat.data_ptr()
-        ptr = (base + 12 * rows, base + 4 * (3 * rows + 2 * B + 1), base + 4 * (3 * rows + B), base, base + 8 * rows)
+        ptr = (base + 4 * rows, base + 4 * (rows + 2 * B + 1), base + 4 * (rows + B), slots.data_ptr(), base)
     else:
         ptr = (_array(out.kv_len, "out.kv_len", i32, (B,), dev), _array(out.free_count, "out.free_count", i32, (1,), dev),
                _array(out.cu_rows, "out.cu_rows", i32, (B + 1,), dev), _array(out.slots, "out.slots", i64, (rows,), dev),
@@ -248,8 +258,8 @@ def qwm_paged_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, slots
     page = _page_tokens(pool, d)
     if pool.device != dev or pool.shape[1] != hk:
         raise ValueError(f"pool: expected [pages, {hk}, block] on {dev}, got {tuple(pool.shape)} on {pool.device}")
-    kh = (0, 0, 0) if k_hat is None else _out_rows(k_hat, "k_hat", k)
-    vh = (0, 0, 0) if v_hat is None else _out_rows(v_hat, "v_hat", v)
+    kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", k, k.shape)
+    vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", v, v.shape)
     _run(lib().qwm_paged_append,
          _APPEND.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), _array(slots, "slots", torch.int64, (T,), dev), _status(status, dev),
                       T, pool.shape[0], _DTYPES[k.dtype], d, hk, page), "qwm_paged_append", dev)
@@ -284,7 +294,7 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
         raise ValueError(f"pool: kv heads that divide {hq} on {dev} are expected, got {tuple(pool.shape)} on {pool.device}")
     if out is None:
         out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
-    ot = _out_rows(out, "out", q)
+    ot = _rows(out, "out", q, q.shape)
     table = _array(block_table, "block_table", torch.int32, (None, None), dev)
     B = block_table.shape[0]
     lens = _array(kv_len, "kv_len", torch.int32, (B,), dev)

@@ -42,7 +42,7 @@ def check(paged, bt, kernel, causal=True, window=0, scale=0.0, max_new=None, tai
     O, want_lse, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, causal, window, sigma)
     got = out[: bt.rows].float().cpu().numpy().astype(np.float64)
     n = int(bt.kv_len.max())
-    tensor = kernel in (paged.PAGED_MMA, paged.PAGED_TC)
+    tensor = bt.dtype == "bf16" and kernel != paged.PAGED_SIMT
     tol = attend_tolerance(O, spread, vmax, n, bt.dtype, tensor)
     assert np.isfinite(got).all()
     bad = np.abs(got - O) > tol
@@ -57,7 +57,7 @@ def check(paged, bt, kernel, causal=True, window=0, scale=0.0, max_new=None, tai
     return int(status.item())
 
 
-KERNELS = ["simt", "mma"]
+KERNELS = ["simt", "mma", "tc", "auto"]
 
 
 def kid(paged, name):
