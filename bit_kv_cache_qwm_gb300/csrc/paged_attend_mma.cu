@@ -39,7 +39,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 64, kCw = 4, kNt = (kCw + 1) * 32, kStages = 4;
+constexpr int kTk = 64, kCw = 4, kNt = (kCw + 1) * 32, kStages = 4, kItem = 2;
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
 
 template <int D>
@@ -103,10 +103,11 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     a.join[w].last = -1;
   }
-  const Share sh = find_share<R, kTk, kNt>(a, w, (int)gridDim.x);   // has block barriers
+  const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);   // has block barriers
+  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
-  Walker<R, kTk> it(a);
-  it.start(sh.b, sh.skip, sh.n);
+  Walker<R, kTk, kItem> it(a);
+  it.start(sh.b, sh.skip, sh.per, sh.n);
   int st = 0;
   uint32_t phase = 0;
 
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
       const bool live = nb * 8 + g < it.rows;
       float x[D / 4];
       float mx = 0.f;
-      const int tok = live ? rr / a.group : 0, head = live ? it.h * a.group + rr % a.group : 0;
+      const int tok = live ? div_group(a, rr) : 0, head = live ? it.h * a.group + rr - div_group(a, rr) * a.group : 0;
       const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
                                                        head * a.q_head + c * (D / 4));
 #pragma unroll
@@ -219,14 +220,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
         const int r2 = it.rt * R + nb * 8 + 2 * c + k;
         top[nb][k] = it.hi, bottom[nb][k] = it.lo;
         if (a.causal) {
-          const int pos = it.rq.n - it.rq.n_new + r2 / a.group;
+          const int pos = it.rq.n - it.rq.n_new + div_group(a, r2);
           top[nb][k] = min(it.hi, pos + 1);
           if (a.window > 0) bottom[nb][k] = max(it.lo, pos - a.window + 1);
         }
       }
     }
     if (a.causal) {
-      const int first = (it.rt * R) / a.group, last = (it.rt * R + it.rows - 1) / a.group, at = it.rq.n - it.rq.n_new;
+      const int first = div_group(a, it.rt * R), last = div_group(a, it.rt * R + it.rows - 1), at = it.rq.n - it.rq.n_new;
       top_min = min(it.hi, at + first + 1);
       if (a.window > 0) bottom_max = max(it.lo, at + last - a.window + 1);
     }
@@ -415,8 +416,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
         }
         if (all) {
           const int rr = it.rt * R + r;
-          const int64_t tok = it.rq.row0 + rr / a.group;
-          const int head = it.h * a.group + rr % a.group;
+          const int64_t tok = it.rq.row0 + div_group(a, rr);
+          const int head = it.h * a.group + rr - div_group(a, rr) * a.group;
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
           *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + tok * a.o_row + head * a.o_head + ch) =
@@ -429,8 +430,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
         }
       }
       if (tid == 0 && it.begins() && !it.ends()) {
-        const int64_t end = sh.first + (sh.n - it.left - (it.to - it.from)) + (it.t1 - it.t0);
-        record_join(a, w, it, last_worker(sh, end), R);
+        record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), R);
       }
     }
     consumers_sync();

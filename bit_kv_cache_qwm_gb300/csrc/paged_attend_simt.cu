@@ -18,7 +18,7 @@ namespace qwm {
 namespace paged {
 namespace {
 
-constexpr int kTk = 64, kNt = 256;
+constexpr int kTk = 64, kNt = 256, kItem = 1;
 
 template <int D, int R>
 struct Shape {
@@ -55,11 +55,12 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
   __shared__ int page_of[kTk / 16];
   const int tid = threadIdx.x, tx = tid % S::TX, ty = tid / S::TX;
   const int w = blockIdx.x;
-  const Share sh = find_share<R, kTk, kNt>(a, w, (int)gridDim.x);
+  const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);
   if (tid == 0) a.join[w].last = -1;
+  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
-  Walker<R, kTk> it(a);
-  it.start(sh.b, sh.skip, sh.n);
+  Walker<R, kTk, kItem> it(a);
+  it.start(sh.b, sh.skip, sh.per, sh.n);
   do {
     const int row0 = it.rt * R;
     __syncthreads();   // the previous item's reads of Qs are done
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       const int r = i / (D / 8), c = (i % (D / 8)) * 8;
       float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (r < it.rows) {
-        const int tok = (row0 + r) / a.group, head = it.h * a.group + (row0 + r) % a.group;
+        const int tok = div_group(a, row0 + r), head = it.h * a.group + (row0 + r) - div_group(a, row0 + r) * a.group;
         load8((const T*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row + head * a.q_head + c, x);
       }
 #pragma unroll
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
     int top[S::RT], bottom[S::RT];      // a row sees bottom <= n < top
 #pragma unroll
     for (int i = 0; i < S::RT; ++i) {
-      const int r = ty * S::RT + i, tok = (row0 + r) / a.group;
+      const int r = ty * S::RT + i, tok = div_group(a, row0 + r);
       m[i] = -INFINITY;
       l[i] = 0.f;
       top[i] = it.hi, bottom[i] = it.lo;
@@ -195,8 +196,8 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       const int r = ty * S::RT + i;
       if (r >= it.rows) continue;
       if (whole) {
-        const int64_t tok = it.rq.row0 + (row0 + r) / a.group;
-        const int head = it.h * a.group + (row0 + r) % a.group;
+        const int64_t tok = it.rq.row0 + div_group(a, row0 + r);
+        const int head = it.h * a.group + (row0 + r) - div_group(a, row0 + r) * a.group;
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T* dst = (T*)a.out + tok * a.o_row + head * a.o_head;
 #pragma unroll
@@ -210,62 +211,123 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       }
     }
     if (tid == 0 && it.begins() && !it.ends()) {
-      const int64_t end = sh.first + (sh.n - it.left - (it.to - it.from)) + (it.t1 - it.t0);
-      record_join(a, w, it, last_worker(sh, end), R);
+      record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), R);
     }
   } while (it.next());
 }
 
-// One CTA per cut item and row (rows blockIdx.y, + gridDim.y, ...): groups of
-// D/4 lanes add up the parts, then the groups' results are merged.
+// Joins the parts of a cut item, in the order of the workers.  With few parts
+// a warp takes a row; with many (one long request over the whole machine) a
+// CTA does: its threads fetch the parts' maxima and sums together, then groups
+// of D/4 lanes add up the parts' O with the factors from shared memory, so
+// that neither waits for one part at a time.  Bound by latency.
+constexpr int kJoinNt = 256, kFewParts = 8, kPartsAtOnce = 256;
+
 template <int D, class T>
-__global__ void __launch_bounds__(128) paged_attend_join_kernel(const AttendArgs a, int R) {
-  constexpr int L = D / 4, NG = 128 / L;
-  __shared__ __align__(16) float part[NG][D];
-  __shared__ float pm[NG], pl[NG];
-#if __CUDA_ARCH__ >= 900
+__device__ __forceinline__ void join_store(const AttendArgs& a, const Join& j, int r, int ch, float4 o, float m, float l) {
+  const int y = j.row0 + r, tok = div_group(a, y);
+  const int head = j.head * a.group + y - tok * a.group;
+  const int64_t row = j.q_row0 + tok;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T* dst = (T*)a.out + row * a.o_row + head * a.o_head + ch;
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  } else {
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+  }
+  if (a.lse && ch == 0) a.lse[row * a.heads + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kJoinNt) paged_attend_join_kernel(const AttendArgs a, int R) {
+  constexpr int L = D / 4, NG = kJoinNt / L;
+  __shared__ __align__(16) float4 sum[NG][L];
+  __shared__ float factor[kPartsAtOnce];
+  __shared__ float red[kJoinNt / 32];
   cudaGridDependencySynchronize();
-#endif
-  const int w = blockIdx.x, g = threadIdx.x / L, c = threadIdx.x % L;
+  const int w = blockIdx.x, tid = threadIdx.x, g = tid / L, c = tid % L;
   const Join j = a.join[w];
   if (j.last < 0) return;
-  for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    for (int x = w + g; x <= j.last; x += NG) {
-      const float* p = part_row(a, x, x == w ? 1 : 0, R, r, D);
-      const float4 v = *reinterpret_cast<const float4*>(p + 4 * c);
-      const float pmx = p[D], plx = p[D + 1];
-      const float mx = fmaxf(m, pmx), ref = mx == -INFINITY ? 0.f : mx;
-      const float f0 = exp2f(m - ref), f1 = exp2f(pmx - ref);
-      o.x = o.x * f0 + v.x * f1;
-      o.y = o.y * f0 + v.y * f1;
-      o.z = o.z * f0 + v.z * f1;
-      o.w = o.w * f0 + v.w * f1;
-      l = l * f0 + plx * f1;
-      m = mx;
+  const int parts = j.last - w + 1;
+  if (parts <= kFewParts) {
+    for (int r = blockIdx.y * NG + g; r < j.rows; r += gridDim.y * NG) {
+      float4 v[kFewParts];
+      float2 ml[kFewParts];
+#pragma unroll
+      for (int x = 0; x < kFewParts; ++x)
+        if (x < parts) {
+          const float* p = part_row(a, w + x, x == 0 ? 1 : 0, R, r, D);
+          v[x] = *reinterpret_cast<const float4*>(p + 4 * c);
+          ml[x] = *reinterpret_cast<const float2*>(p + D);
+        }
+      float m = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kFewParts; ++x)
+        if (x < parts) m = fmaxf(m, ml[x].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+#pragma unroll
+      for (int x = 0; x < kFewParts; ++x)
+        if (x < parts) {
+          const float f = exp2f(ml[x].x - ref);
+          o.x = fmaf(v[x].x, f, o.x), o.y = fmaf(v[x].y, f, o.y), o.z = fmaf(v[x].z, f, o.z), o.w = fmaf(v[x].w, f, o.w);
+          l = fmaf(ml[x].y, f, l);
+        }
+      join_store<D, T>(a, j, r, 4 * c, o, m, l);
     }
-    *reinterpret_cast<float4*>(&part[g][4 * c]) = o;
-    if (c == 0) pm[g] = m, pl[g] = l;
+    return;
+  }
+  // the row's maximum over all parts, then the parts in chunks
+  auto reduce = [&](float v, bool max) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, v, d);
+      v = max ? fmaxf(v, y) : v + y;
+    }
     __syncthreads();
-    float mx = -INFINITY;
+    if ((tid & 31) == 0) red[tid >> 5] = v;
+    __syncthreads();
+    v = red[0];
 #pragma unroll
-    for (int i = 0; i < NG; ++i) mx = fmaxf(mx, pm[i]);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) sum += pl[i] * exp2f(pm[i] - ref);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t tok = j.q_row0 + (j.row0 + r) / a.group;
-    const int head = j.head * a.group + (j.row0 + r) % a.group;
-    for (int ch = threadIdx.x; ch < D; ch += 128) {
-      float v = 0.f;
-#pragma unroll
-      for (int i = 0; i < NG; ++i) v += part[i][ch] * exp2f(pm[i] - ref);
-      ((T*)a.out)[tok * a.o_row + head * a.o_head + ch] = (T)(v * inv);
+    for (int i = 1; i < kJoinNt / 32; ++i) v = max ? fmaxf(v, red[i]) : v + red[i];
+    return v;
+  };
+  for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {
+    float m = -INFINITY;
+    for (int x = tid; x < parts; x += kJoinNt) m = fmaxf(m, part_row(a, w + x, x == 0 ? 1 : 0, R, r, D)[D]);
+    m = reduce(m, true);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int x0 = 0; x0 < parts; x0 += kPartsAtOnce) {
+      const int n = min(kPartsAtOnce, parts - x0);
+      __syncthreads();
+      if (tid < n) {
+        const float2 ml = *reinterpret_cast<const float2*>(part_row(a, w + x0 + tid, x0 + tid == 0 ? 1 : 0, R, r, D) + D);
+        const float f = exp2f(ml.x - ref);
+        factor[tid] = f;
+        l = fmaf(ml.y, f, l);
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int x = g; x < n; x += NG) {
+        const float4 v = *reinterpret_cast<const float4*>(part_row(a, w + x0 + x, x0 + x == 0 ? 1 : 0, R, r, D) + 4 * c);
+        const float f = factor[x];
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      }
     }
-    if (a.lse && threadIdx.x == 0)
-      a.lse[tok * a.heads + head] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    sum[g][c] = o;
+    l = reduce(l, false);   // its barriers publish the groups' sums
+    if (g == 0) {
+#pragma unroll
+      for (int i = 1; i < NG; ++i) {
+        const float4 v = sum[i][c];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      }
+      join_store<D, T>(a, j, r, 4 * c, o, m, l);
+    }
     __syncthreads();
   }
 }
@@ -313,8 +375,8 @@ cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t ma
 cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w, int64_t max_rows, cudaStream_t st) {
   const int rows = max_rows < 1 ? 1 : max_rows < w.rows ? (int)max_rows : w.rows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)w.count, (unsigned)(rows < 32 ? rows : 32), 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3((unsigned)w.count, (unsigned)(rows < 16 ? rows : 16), 1);
+  cfg.blockDim = dim3(kJoinNt, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

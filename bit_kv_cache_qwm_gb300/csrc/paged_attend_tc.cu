@@ -45,7 +45,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12;
+constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 2;
 constexpr uint32_t kColO = 256;
 constexpr float kNone = -3.0e38f;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
@@ -172,10 +172,10 @@ __device__ __forceinline__ float max_keys(const uint32_t* v, int key0, int lo, i
 template <int D>
 __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArgs a) {
   using L = Lay<D>;
-  using W = Walker<kRows, kTk>;
+  using W = Walker<kRows, kTk, kItem>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t bars[9];
+  __shared__ __align__(8) uint64_t bars[10];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
   // tokens of a tile on a page out of range, a word for each producer warp.
@@ -186,17 +186,19 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint64_t* pv_done = &bars[2];   // [2] O_g of the item complete
   uint64_t* k_free = &bars[4];    // [2] K stage read by both query tiles
   uint64_t* v_free = &bars[6];    // [2]
-  uint64_t* q_ready = &bars[8];   // Q_a and Q_b of the item written
+  uint64_t* q_ready = &bars[8];   // [2] Q_g of the item written
   const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
 
   if (tid == 0) {
     abort_sh = 0;
     for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
-    bar_init(q_ready, kRows);
+    bar_init(&q_ready[0], 128);
+    bar_init(&q_ready[1], 128);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     a.join[w].last = -1;
   }
-  const Share sh = find_share<kRows, kTk, kNt>(a, w, (int)gridDim.x);   // has block barriers
+  const Share sh = find_share<kRows, kTk, kItem, kNt>(a, w, (int)gridDim.x);   // has block barriers
+  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
   if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&tmem_base_sh)));
@@ -207,11 +209,12 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   fence_after();
   const uint32_t tmem = tmem_base_sh;
   W it(a);
-  it.start(sh.b, sh.skip, sh.n);
+  it.start(sh.b, sh.skip, sh.per, sh.n);
 
   if (warp < kProd) {
     // ------------------------------------------------------------ softmax
-    const int g = warp >> 2, i = tid & 127;
+    const int g = warp >> 2, i = tid & 127, lane = tid & 31, w32 = 32 * (warp & 3);
+    constexpr int CH = D / 8, RP = 32 / CH, NI = 32 / RP;   // 16-byte chunks a row, rows a load, loads
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
     uint32_t s_par = 0, pv_par = 0;
@@ -219,53 +222,70 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     do {
       const int r = 128 * g + i, rr = it.rt * kRows + r;
       const bool live = r < it.rows;
-      const int tok = live ? rr / a.group : 0, head = live ? it.h * a.group + rr % a.group : 0;
-      float c2;
+      // where the item's row 128 g + x is in a tensor [rows][heads][D]
+      auto place = [&](int x, int64_t row_stride, int64_t head_stride) {
+        const int y = it.rt * kRows + 128 * g + x, tok = div_group(a, y);
+        return (int64_t)(it.rq.row0 + tok) * row_stride + (int64_t)(it.h * a.group + y - tok * a.group) * head_stride;
+      };
+      uint8_t* qt = sm + g * L::op;
+      float c2 = 0.f;
       {
-        const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
-                                                         head * a.q_head);
-        float mx = 0.f;
-        if (live) {
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = src[c];
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        // a warp loads its 32 rows, CH lanes a row
+        uint4 x[NI];
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const int y = w32 + k * RP + lane / CH;
+          x[k] = 128 * g + y < it.rows
+                     ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + place(y, a.q_row, a.q_head) + 8 * (lane % CH))
+                     : make_uint4(0, 0, 0, 0);
+        }
+        // entries of 2^15 and more need the row's scaling; without one it is 1
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+          big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                       __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+        const bool scaled = __any_sync(0xffffffffu, (big & 0xffffu) >= 0x4700u || (big >> 16) >= 0x4700u);
+        c2 = a.scale_log2;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          float qs = 1.f;
+          if (scaled) {
+            float mx = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
+#pragma unroll
+            for (int o = CH / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+            const int e = ex > 14 ? ex - 14 : 0;
+            qs = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the largest entry below 2^15
+            const float f = __shfl_sync(0xffffffffu, a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23), (lane % RP) * CH);
+            if (lane / RP == k) c2 = f;
           }
-        }
-        const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-        const int e = ex > 14 ? ex - 14 : 0;
-        const float qs = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the largest entry below 2^15
-        c2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        uint8_t* qt = sm + g * L::op;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
           // channels (0, 4), (1, 5), (2, 6), (3, 7)
           uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            o[2 * k] = h2u(__floats2half2_rn(__uint_as_float(u[k] << 16) * qs, __uint_as_float(u[2 + k] << 16) * qs));
-            o[2 * k + 1] = h2u(__floats2half2_rn(__uint_as_float(u[k] & 0xffff0000u) * qs,
-                                                 __uint_as_float(u[2 + k] & 0xffff0000u) * qs));
+          for (int j = 0; j < 2; ++j) {
+            o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(u[j] << 16) * qs, __uint_as_float(u[2 + j] << 16) * qs));
+            o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(u[j] & 0xffff0000u) * qs,
+                                                 __uint_as_float(u[2 + j] & 0xffff0000u) * qs));
           }
-          *reinterpret_cast<uint4*>(qt + op_off(i, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(qt + op_off(w32 + k * RP + lane / CH, lane % CH)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_async_smem();
-        bar_arrive(q_ready);
+        bar_arrive(&q_ready[g]);
       }
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
       if (a.causal) {
         const int at = it.rq.n - it.rq.n_new;
-        const int first = (it.rt * kRows + 128 * g) / a.group;
-        const int last = (it.rt * kRows + min(it.rows, 128 * g + 128) - 1) / a.group;
-        top = min(it.hi, at + rr / a.group + 1);
+        const int first = div_group(a, it.rt * kRows + 128 * g);
+        const int last = div_group(a, it.rt * kRows + min(it.rows, 128 * g + 128) - 1);
+        top = min(it.hi, at + div_group(a, rr) + 1);
         top_min = min(it.hi, at + first + 1);
         if (a.window > 0) {
-          bottom = max(it.lo, at + rr / a.group - a.window + 1);
+          bottom = max(it.lo, at + div_group(a, rr) - a.window + 1);
           bottom_max = max(it.lo, at + last - a.window + 1);
         }
       }
@@ -345,48 +365,78 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
       pv_par ^= 1;
       fence_after();
-      // ---- O of the item: column p of 8 holds channel (p / 2) + 4 (p % 2)
+      // ---- O of the item, by way of the warp's rows of the Q tile (its MMAs
+      // are complete), so that a row is stored by neighbouring lanes.  Column
+      // p of 8 holds channel (p / 2) + 4 (p % 2).
       const bool all = it.begins() && it.ends();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      float* part = part_row(a, w, it.begins() ? 1 : 0, kRows, r, D);
-      __nv_bfloat16* dst = (__nv_bfloat16*)a.out + (int64_t)(it.rq.row0 + tok) * a.o_row + head * a.o_head;
+      const int slot = it.begins() ? 1 : 0;
+      if (all) {
+        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t x[32];
-        tmem_ld32(obase + 32 * cb, x);
-        tmem_wait_ld();
-        if (live) {
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t x[32];
+          tmem_ld32(obase + 32 * cb, x);
+          tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float y[8];
+            uint32_t u[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[(k >> 1) + 4 * (k & 1)] = __uint_as_float(x[8 * q + k]);
-            if (all) {
-              uint32_t u[4];
+            for (int k = 0; k < 4; ++k) {
+              // channels 2 k, 2 k + 1 are in columns 2 (2 k % 4) + (k > 1), + 2
+              const int c0 = 8 * q + 2 * ((2 * k) & 3) + (k >> 1);
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[c0]) * inv, __uint_as_float(x[c0 + 2]) * inv);
+              u[k] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(qt + op_off(i, 4 * cb + q)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * k] * inv, y[2 * k + 1] * inv);
-                u[k] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              *reinterpret_cast<uint4*>(dst + 32 * cb + 8 * q) = make_uint4(u[0], u[1], u[2], u[3]);
-            } else {
-              *reinterpret_cast<float4*>(part + 32 * cb + 8 * q) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4*>(part + 32 * cb + 8 * q + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        for (int k = 0; k < NI; ++k) {
+          const int y = w32 + k * RP + lane / CH;
+          if (128 * g + y < it.rows)
+            *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + place(y, a.o_row, a.o_head) + 8 * (lane % CH)) =
+                *reinterpret_cast<const uint4*>(qt + op_off(y, lane % CH));
+        }
+        __syncwarp();
+      } else {
+        // a part in float32: two halves of D / 2 channels
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t x[16];
+            tmem_ld16(obase + hf * (D / 2) + 16 * cb, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int c0 = 8 * (q >> 1) + (q & 1);
+              *reinterpret_cast<uint4*>(qt + op_off(i, 4 * cb + q)) = make_uint4(x[c0], x[c0 + 2], x[c0 + 4], x[c0 + 6]);
             }
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int k = 0; k < NI; ++k) {
+            const int y = w32 + k * RP + lane / CH;
+            if (128 * g + y < it.rows)
+              *reinterpret_cast<uint4*>(part_row(a, w, slot, kRows, 128 * g + y, D) + hf * (D / 2) + 4 * (lane % CH)) =
+                  *reinterpret_cast<const uint4*>(qt + op_off(y, lane % CH));
+          }
+          __syncwarp();
         }
       }
       if (live) {
         if (!all) {
+          float* part = part_row(a, w, slot, kRows, r, D);
           part[D] = m_run, part[D + 1] = l_run;
         } else if (a.lse) {
-          a.lse[(int64_t)(it.rq.row0 + tok) * a.heads + head] =
+          const int tok = div_group(a, rr);
+          a.lse[(int64_t)(it.rq.row0 + tok) * a.heads + it.h * a.group + rr - tok * a.group] =
               l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
         }
       }
       if (tid == 0 && it.begins() && !it.ends()) {
-        const int64_t end = sh.first + (sh.n - it.left - (it.to - it.from)) + (it.t1 - it.t0);
-        record_join(a, w, it, last_worker(sh, end), kRows);
+        record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
       }
       fence_before();   // the reads of O come before the next item's MMAs
     } while (it.next());
@@ -409,6 +459,16 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       if (++t < it.to) return true;
       if (!it.next()) return false;
       t = it.from;
+      // the item's queries on their way to L2 while the one before it is at work
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (128 * g + p < it.rows) {
+          const int y = it.rt * kRows + 128 * g + p, tok = div_group(a, y);
+          const __nv_bfloat16* row = (const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+                                     (int64_t)(it.h * a.group + y - tok * a.group) * a.q_head;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+        }
       return true;
     };
     const uint8_t* blk = nullptr;
@@ -483,14 +543,14 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       __syncwarp();
     };
     do {
-      ok = warp_all(bar_wait(q_ready, q_par, &abort_sh, a.timeout)) && ok;
-      q_par ^= 1;
       nb_sync(kNbK + (u & 1));
-      fence_after();
-      if (ok) {
-        issue_s(0, u & 1);
-        issue_s(1, u & 1);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        ok = warp_all(bar_wait(&q_ready[g], q_par, &abort_sh, a.timeout)) && ok;
+        fence_after();
+        if (ok) issue_s(g, u & 1);
       }
+      q_par ^= 1;
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int st = u & 1;
         const bool last = t + 1 == it.to;

@@ -197,6 +197,11 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.heads = a->heads;
   x.kv_heads = a->kv_heads;
   x.group = group;
+  // ceil(2^(31 + l) / group) with 2^l >= group is exact for every x < 2^31
+  int l = 0;
+  while ((1 << l) < group) ++l;
+  x.group_shift = 31 + l;
+  x.group_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + group - 1) / group);
   x.page = a->page_tokens;
   x.page_shift = shift;
   x.block = block_bytes(d, a->page_tokens);

@@ -33,6 +33,7 @@ struct AttendArgs {
   int64_t rows;
   int32_t n_pages;
   int32_t heads, kv_heads, group;
+  uint32_t group_mul, group_shift;   // x / group = x group_mul >> group_shift for x < 2^31
   int32_t page, page_shift, block;
   int32_t requests, max_blocks;
   int32_t causal, window;
@@ -57,6 +58,10 @@ struct Join {
 
 __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ int div_group(const AttendArgs& a, int x) {
+  return (int)(((uint64_t)(uint32_t)x * a.group_mul) >> a.group_shift);
 }
 
 // One request as the kernels see it, with lengths clamped to what the tables hold.
@@ -105,14 +110,19 @@ __device__ __forceinline__ void visible(const AttendArgs& a, const Request& r, i
 //
 // The work is a list of items (request, kv head, block of R rows), each a run
 // of tiles of TK tokens that its rows see; an item that sees nothing has one
-// tile, so that it is visited and its rows are written.  The list's tiles are
-// dealt to the workers in equal contiguous shares whatever the lengths are:
-// no worker waits for another, and a long request is split exactly as far as
-// the machine needs.  A share cuts at most its first and its last item.
-template <int R, int TK>
+// tile, so that it is visited and its rows are written.  An item weighs its
+// tiles and C more, the cost of starting and ending it in units of a tile
+// (measured for each kernel).  The list's weight is dealt to the workers in
+// equal contiguous shares whatever the lengths are: no worker waits for
+// another, and a long request is split exactly as far as the machine needs.
+// A share cuts at most its first and its last item.  Shares weigh more than C,
+// so every one has a tile; one that ends inside an item's C leaves the item to
+// the next.
+template <int R, int TK, int C>
 struct Walker {
   const AttendArgs& a;
-  int64_t left;        // tiles of this worker not yet handed out
+  int64_t n, done;     // the share's weight, and what of it has been handed out
+  int64_t item_at;     // weight of the current item's start, from the share's
   // the current item
   int b, h, rt;
   Request rq;
@@ -127,21 +137,21 @@ struct Walker {
 
   __device__ static void tiles_of(const AttendArgs& a, const Request& r, int rt, int* lo, int* hi, int* t0, int* t1) {
     const int first = rt * R, last = min(r.rows, first + R) - 1;
-    visible(a, r, first / a.group, last / a.group, lo, hi);
+    visible(a, r, div_group(a, first), div_group(a, last), lo, hi);
     *t0 = *lo / TK;
     *t1 = *hi > *lo ? (*hi + TK - 1) / TK : *t0 + 1;
   }
 
-  // tiles of one kv head of a request
+  // weight of one kv head of a request
   __device__ static int64_t head_tiles(const AttendArgs& a, const Request& r) {
     const int nrt = (r.rows + R - 1) / R;
     if (nrt == 0) return 0;
     int lo, hi, t0, t1;
     if (!a.causal) {
       tiles_of(a, r, 0, &lo, &hi, &t0, &t1);
-      return (int64_t)nrt * (t1 - t0);
+      return (int64_t)nrt * (t1 - t0 + C);
     }
-    int64_t s = 0;
+    int64_t s = (int64_t)nrt * C;
     for (int i = 0; i < nrt; ++i) {
       tiles_of(a, r, i, &lo, &hi, &t0, &t1);
       s += t1 - t0;
@@ -149,43 +159,71 @@ struct Walker {
     return s;
   }
 
-  __device__ void item(int tile) {
+  // The share's piece of the item, which starts `skip` into its weight; false
+  // when it has no tile.
+  __device__ bool item(int skip) {
     tiles_of(a, rq, rt, &lo, &hi, &t0, &t1);
-    from = t0 + tile;
+    item_at = done - skip;
+    const int all = t1 - t0 + C;
+    const int end = (int)min((int64_t)all, n - done + skip);
+    done += end - skip;
+    from = t0 + max(0, skip - C);
+    to = t0 + max(0, end - C);
     rows = min(R, rq.rows - rt * R);
-    const int64_t take = min((int64_t)(t1 - from), left);
-    to = from + (int)take;
-    left -= take;
+    return to > from;
   }
 
-  // To the first item of the share that starts `skip` tiles into request b0.
-  __device__ void start(int b0, int64_t skip, int64_t n_tiles) {
+  // the same by a whole warp
+  __device__ static int64_t head_tiles_warp(const AttendArgs& a, const Request& r) {
+    if (!a.causal) return head_tiles(a, r);
+    const int nrt = (r.rows + R - 1) / R;
+    int64_t s = 0;
+    for (int i = threadIdx.x & 31; i < nrt; i += 32) {
+      s += C;
+      int lo, hi, t0, t1;
+      tiles_of(a, r, i, &lo, &hi, &t0, &t1);
+      s += t1 - t0;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+
+  // To the first item of a share (whole warps call this): it starts `skip`
+  // into the weight of request b0, whose kv heads weigh `per` each.
+  __device__ void start(int b0, int64_t skip, int64_t per, int64_t weight) {
     b = b0;
     rq = load_request(a, b);
-    left = n_tiles;
-    const int64_t per = head_tiles(a, rq);
+    n = weight;
+    done = 0;
     h = (int)(skip / per);
     skip -= h * per;
-    rt = 0;
-    if (!a.causal) {
-      int l, u, x0, x1;
-      tiles_of(a, rq, 0, &l, &u, &x0, &x1);
-      rt = (int)(skip / (x1 - x0));
-      skip -= (int64_t)rt * (x1 - x0);
-    } else {
-      while (true) {
-        int l, u, x0, x1;
-        tiles_of(a, rq, rt, &l, &u, &x0, &x1);
-        if (skip < x1 - x0) break;
-        skip -= x1 - x0;
-        ++rt;
+    const int nrt = row_tiles(), lane = threadIdx.x & 31;
+    for (int base = 0;; base += 32) {
+      int l, u, x0 = 0, x1 = 0;
+      if (base + lane < nrt) tiles_of(a, rq, base + lane, &l, &u, &x0, &x1);
+      const int64_t mine = base + lane < nrt ? x1 - x0 + C : 0;
+      int64_t sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
       }
+      const uint32_t past = __ballot_sync(0xffffffffu, sum > skip);
+      const int64_t before = sum - mine;
+      if (past) {
+        const int f = __ffs(past) - 1;
+        rt = base + f;
+        skip -= __shfl_sync(0xffffffffu, before, f);
+        break;
+      }
+      skip -= __shfl_sync(0xffffffffu, sum, 31);
     }
     item((int)skip);
   }
 
   __device__ bool next() {
-    if (left <= 0) return false;
+    if (done >= n) return false;
     if (++rt >= row_tiles()) {
       rt = 0;
       if (++h >= a.kv_heads) {
@@ -196,32 +234,63 @@ struct Walker {
         } while (rq.rows == 0);
       }
     }
-    item(0);
-    return true;
+    return item(0);
   }
 
   __device__ bool begins() const { return from == t0; }
   __device__ bool ends() const { return to == t1; }
+  // where the item ends in the whole list's weight
+  __device__ int64_t end_of(int64_t share_first) const { return share_first + item_at + (t1 - t0) + C; }
 };
 
-// The share of worker `w` of `workers`: where it starts and how many tiles it
-// has.  Called by all threads of a CTA of NT threads; the sums over the
+// The share of worker `w` of `workers`: where it starts and what it weighs.  Called by all threads of a CTA of NT threads; the sums over the
 // requests are made by every CTA for itself (a few loads per thread).
 struct Share {
   int b;
-  int workers;         // those with work: no more than there are tiles, so that each has some
-  int64_t skip, n, first, total;
+  int workers;         // those with work: no more than have a tile each
+  int64_t skip, per, n, first, total;
 };
 
-template <int R, int TK, int NT>
+template <int R, int TK, int C, int NT>
 __device__ Share find_share(const AttendArgs& a, int w, int workers) {
-  __shared__ int64_t warp_sum[NT / 32];
-  __shared__ int64_t chunk_base, found_skip;
+  constexpr int NW = NT / 32;
+  __shared__ int64_t warp_sum[NW];
+  __shared__ int64_t chunk_base, found_skip, found_per;
   __shared__ int found_b;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   Share s;
   s.b = s.workers = 0;
   s.skip = s.n = s.first = s.total = 0;
+  s.per = 0;
+  auto active = [](int64_t total, int workers) {
+    const int64_t most = total / (C + 1);
+    return most < workers ? (int)most : workers;
+  };
+  if (a.requests <= NW) {
+    // a warp for each request: with few requests these may be long
+    int64_t per = 0;
+    if (wid < a.requests) per = Walker<R, TK, C>::head_tiles_warp(a, load_request(a, wid));
+    if (lane == 0) warp_sum[wid] = per;
+    __syncthreads();
+    for (int b = 0; b < a.requests; ++b) s.total += warp_sum[b] * a.kv_heads;
+    s.workers = active(s.total, workers);
+    if (w < s.workers) {
+      s.first = s.total * w / s.workers;
+      s.n = s.total * (w + 1) / s.workers - s.first;
+      int64_t at = 0;
+      for (int b = 0; b < a.requests; ++b) {
+        const int64_t x = warp_sum[b] * a.kv_heads;
+        if (s.first < at + x) {
+          s.b = b;
+          s.skip = s.first - at;
+          s.per = warp_sum[b];
+          break;
+        }
+        at += x;
+      }
+    }
+    return s;
+  }
   for (int pass = 0; pass < 2; ++pass) {
     if (tid == 0) {
       chunk_base = 0;
@@ -232,7 +301,7 @@ __device__ Share find_share(const AttendArgs& a, int w, int workers) {
     for (int b0 = 0; b0 < a.requests; b0 += NT) {
       const int b = b0 + tid;
       int64_t mine = 0;
-      if (b < a.requests) mine = Walker<R, TK>::head_tiles(a, load_request(a, b)) * a.kv_heads;
+      if (b < a.requests) mine = Walker<R, TK, C>::head_tiles(a, load_request(a, b)) * a.kv_heads;
       int64_t x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -250,13 +319,16 @@ __device__ Share find_share(const AttendArgs& a, int w, int workers) {
       if (pass == 1 && want >= at && want < at + mine) {
         found_b = b;
         found_skip = want - at;
+        found_per = mine / a.kv_heads;
       }
       // one pass finds both when the requests fit one chunk
       if (pass == 0 && a.requests <= NT) {
-        const int64_t f = all < workers ? w : all * w / workers;
+        const int act = active(all, workers);
+        const int64_t f = act ? all * w / act : 0;
         if (f >= at && f < at + mine) {
           found_b = b;
           found_skip = f - at;
+          found_per = mine / a.kv_heads;
         }
       }
       __syncthreads();
@@ -265,7 +337,7 @@ __device__ Share find_share(const AttendArgs& a, int w, int workers) {
     }
     if (pass == 0) {
       s.total = chunk_base;
-      s.workers = s.total < workers ? (int)s.total : workers;
+      s.workers = active(s.total, workers);
       if (w < s.workers) {
         s.first = s.total * w / s.workers;
         s.n = s.total * (w + 1) / s.workers - s.first;
@@ -276,12 +348,13 @@ __device__ Share find_share(const AttendArgs& a, int w, int workers) {
   }
   s.b = found_b;
   s.skip = found_skip;
+  s.per = found_per;
   __syncthreads();
   return s;
 }
 
-// The last worker that has tiles of the item that ends at tile `end` of the
-// whole list (end > the share's first tile).
+// The last worker that has a tile of the item that ends at `end` of the
+// whole list's weight.
 __device__ __forceinline__ int last_worker(const Share& s, int64_t end) {
   // the worker w with first(w) <= end - 1 < first(w + 1), first(w) = floor(total w / workers)
   int64_t w = ((end - 1) * s.workers + s.workers - 1) / s.total;
