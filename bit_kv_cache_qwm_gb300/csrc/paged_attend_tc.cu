@@ -7,17 +7,20 @@
 // b of one request and key/value head; the rows of a head group follow one
 // another token by token) and tiles of 128 tokens.  Warp roles (13 warps):
 //   warps 0-3 / 4-7  softmax of query tile a / b, thread = row = TMEM lane:
-//                    Q (float16, scaled per row by a power of two) into a SW128
-//                    K-major tile once an item; per tile the online softmax in
-//                    the exp2 domain with O rescaled only when the maximum
-//                    grows by more than 2^8, P in float16 over the first 64
-//                    columns of S; at the item's end O from TMEM to memory.
+//                    once an item Q to float16 in place (SW128 K-major, scaled
+//                    per row by a power of two if it has to be); per tile the
+//                    online softmax in the exp2 domain with O rescaled only
+//                    when the maximum grows by more than 2^8, P in float16
+//                    over the first 64 columns of S; at the item's end, after
+//                    the next item's Q, O from TMEM to memory.
 //   warps 8-11       producers, thread = token: the packed codes (64 + 64
 //                    bytes at d = 128) and parameters of the next tile are
 //                    loaded into registers one tile ahead, its page id two
 //                    tiles ahead, and dequantised into two-stage K and V tiles
 //                    (one 16-byte store a code word, no bank conflicts: the
-//                    eight rows of a store phase differ in the swizzle).
+//                    eight rows of a store phase differ in the swizzle); an
+//                    item's query rows are copied as soon as the last S of the
+//                    item before it is complete.
 //   warp 12          MMA issuer and TMEM owner.
 // Tensor order: S_a(0) S_b(0), then per tile t
 //   PV_a(t) S_a(t+1) PV_b(t) S_b(t+1)
@@ -55,7 +58,8 @@ template <int D>
 struct Lay {
   static constexpr int op = 128 * D * 2;              // one operand tile
   static constexpr int k = 2 * op, v = k + 2 * op;    // after Q_a, Q_b
-  static constexpr int bytes = v + 2 * op + 1024;     // and room to align
+  static constexpr int stage = v + 2 * op;            // 32 rows x 128 bytes for each softmax warp
+  static constexpr int bytes = stage + kProd * 4096 + 1024;   // and room to align
   static constexpr uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((uint32_t)(D / 8) << 17) | (8u << 24);
 };
 
@@ -125,24 +129,26 @@ struct Packed {
   }
 };
 
+// keys key0 ... of a tile in v: those from hi on become -inf (P = 0)
+template <int N>
+__device__ __forceinline__ void hide_keys(uint32_t* v, int key0, int hi) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = key0 + k < hi ? v[k] : 0xff800000u;
+}
+
 // P of the 16 Q keys key0 ... of a tile held in v (float16 pairs into TMEM
-// columns key0 / 2 ...); keys outside [lo, hi) give 0 unless FULL.  Returns
-// the sum.
-template <int Q, bool FULL>
-__device__ __forceinline__ float exp_keys(const uint32_t* v, int key0, int lo, int hi, float2 c2, float2 mv, uint32_t taddr) {
+// columns key0 / 2 ...).  Returns the sum.
+template <int Q>
+__device__ __forceinline__ float exp_keys(const uint32_t* v, int key0, float2 c2, float2 mv, uint32_t taddr) {
   float2 ps = make_float2(0.f, 0.f);
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     uint32_t pk[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int k0 = 16 * q + 2 * k, key = key0 + k0;
+      const int k0 = 16 * q + 2 * k;
       const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[k0]), __uint_as_float(v[k0 + 1])), c2, mv);
-      float2 pp = make_float2(ex2(arg.x), ex2(arg.y));
-      if (!FULL) {
-        pp.x = key >= lo && key < hi ? pp.x : 0.f;
-        pp.y = key + 1 >= lo && key + 1 < hi ? pp.y : 0.f;
-      }
+      const float2 pp = make_float2(ex2(arg.x), ex2(arg.y));
       ps = __fadd2_rn(ps, pp);
       pk[k] = h2u(__floats2half2_rn(pp.x, pp.y));
     }
@@ -151,20 +157,12 @@ __device__ __forceinline__ float exp_keys(const uint32_t* v, int key0, int lo, i
   return ps.x + ps.y;
 }
 
-// maximum over v[0 .. 63] = keys key0 ..., those in [lo, hi)
-template <bool FULL>
-__device__ __forceinline__ float max_keys(const uint32_t* v, int key0, int lo, int hi) {
+__device__ __forceinline__ float max64(const uint32_t* v) {
   float a = -INFINITY, b = -INFINITY;
-  if (FULL) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      a = max3f(a, __uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]));
-      b = max3f(b, __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 64; ++k)
-      if (key0 + k >= lo && key0 + k < hi) a = fmaxf(a, __uint_as_float(v[k]));
+  for (int k = 0; k < 16; ++k) {
+    a = max3f(a, __uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]));
+    b = max3f(b, __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
   }
   return fmaxf(a, b);
 }
@@ -175,7 +173,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   using W = Walker<kRows, kTk, kItem>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t bars[10];
+  __shared__ __align__(8) uint64_t bars[11];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
   // tokens of a tile on a page out of range, a word for each producer warp.
@@ -187,6 +185,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint64_t* k_free = &bars[4];    // [2] K stage read by both query tiles
   uint64_t* v_free = &bars[6];    // [2]
   uint64_t* q_ready = &bars[8];   // [2] Q_g of the item written
+  uint64_t* q_raw = &bars[10];    // the item's bf16 rows landed in the Q tiles
   const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
 
   if (tid == 0) {
@@ -194,6 +193,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
     bar_init(&q_ready[0], 128);
     bar_init(&q_ready[1], 128);
+    bar_init(q_raw, 128);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     a.join[w].last = -1;
   }
@@ -213,98 +213,78 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
 
   if (warp < kProd) {
     // ------------------------------------------------------------ softmax
-    const int g = warp >> 2, i = tid & 127, lane = tid & 31, w32 = 32 * (warp & 3);
-    constexpr int CH = D / 8, RP = 32 / CH, NI = 32 / RP;   // 16-byte chunks a row, rows a load, loads
+    const int g = warp >> 2, i = tid & 127, lane = tid & 31;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
-    uint32_t s_par = 0, pv_par = 0;
+    uint8_t* qt = sm + g * L::op;
+    uint8_t* stage = sm + L::stage + warp * 4096;
+    uint32_t s_par = 0, q_par = 0;
     int u = 0;
-    do {
-      const int r = 128 * g + i, rr = it.rt * kRows + r;
-      const bool live = r < it.rows;
-      // where the item's row 128 g + x is in a tensor [rows][heads][D]
-      auto place = [&](int x, int64_t row_stride, int64_t head_stride) {
-        const int y = it.rt * kRows + 128 * g + x, tok = div_group(a, y);
-        return (int64_t)(it.rq.row0 + tok) * row_stride + (int64_t)(it.h * a.group + y - tok * a.group) * head_stride;
-      };
-      uint8_t* qt = sm + g * L::op;
-      float c2 = 0.f;
-      {
-        // a warp loads its 32 rows, CH lanes a row
-        uint4 x[NI];
-        uint32_t big = 0;
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int y = w32 + k * RP + lane / CH;
-          x[k] = 128 * g + y < it.rows
-                     ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + place(y, a.q_row, a.q_head) + 8 * (lane % CH))
-                     : make_uint4(0, 0, 0, 0);
-        }
-        // entries of 2^15 and more need the row's scaling; without one it is 1
-#pragma unroll
-        for (int k = 0; k < NI; ++k)
-          big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                                       __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
-        const bool scaled = __any_sync(0xffffffffu, (big & 0xffffu) >= 0x4700u || (big >> 16) >= 0x4700u);
-        c2 = a.scale_log2;
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          float qs = 1.f;
-          if (scaled) {
-            float mx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx = max3f(mx, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u)));
-#pragma unroll
-            for (int o = CH / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-            const int e = ex > 14 ? ex - 14 : 0;
-            qs = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the largest entry below 2^15
-            const float f = __shfl_sync(0xffffffffu, a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23), (lane % RP) * CH);
-            if (lane / RP == k) c2 = f;
-          }
-          // channels (0, 4), (1, 5), (2, 6), (3, 7)
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(u[j] << 16) * qs, __uint_as_float(u[2 + j] << 16) * qs));
-            o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(u[j] & 0xffff0000u) * qs,
-                                                 __uint_as_float(u[2 + j] & 0xffff0000u) * qs));
-          }
-          *reinterpret_cast<uint4*>(qt + op_off(w32 + k * RP + lane / CH, lane % CH)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        fence_async_smem();
-        bar_arrive(&q_ready[g]);
+    // Q_g of the item: this thread's bf16 row, in place, to float16 in the
+    // order (0, 4), (1, 5), (2, 6), (3, 7), scaled by 2^-e where its largest
+    // entry is 2^15 or more.  Returns the logit factor.
+    auto make_q = [&]() {
+      group_all(g, (warp & 3) != 0 || bar_wait(q_raw, q_par, &abort_sh, a.timeout));
+      q_par ^= 1;
+      uint32_t big = 0;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(qt + op_off(i, c));
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
       }
+      big = max(big & 0xffffu, big >> 16);
+      const int ex = (int)(big >> 7) - 127;
+      const int e = ex > 14 ? ex - 14 : 0;
+      const float qs = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 2
+      for (int c = 0; c < D / 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(qt + op_off(i, c));
+        const uint4 x = *at;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
+          o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
+                                               __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_async_smem();
+      bar_arrive(&q_ready[g]);
+      return a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+    };
+    float c2 = make_q();
+    uint32_t pv_par = 0;
+    while (true) {
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
       if (a.causal) {
-        const int at = it.rq.n - it.rq.n_new;
-        const int first = div_group(a, it.rt * kRows + 128 * g);
-        const int last = div_group(a, it.rt * kRows + min(it.rows, 128 * g + 128) - 1);
-        top = min(it.hi, at + div_group(a, rr) + 1);
-        top_min = min(it.hi, at + first + 1);
+        const int at = it.rq.n - it.rq.n_new, pos = at + div_group(a, it.rt * kRows + 128 * g + i);
+        top = min(it.hi, pos + 1);
+        top_min = min(it.hi, at + div_group(a, it.rt * kRows + 128 * g) + 1);
         if (a.window > 0) {
-          bottom = max(it.lo, at + div_group(a, rr) - a.window + 1);
-          bottom_max = max(it.lo, at + last - a.window + 1);
+          bottom = max(it.lo, pos - a.window + 1);
+          bottom_max = max(it.lo, at + div_group(a, it.rt * kRows + min(it.rows, 128 * g + 128) - 1) - a.window + 1);
         }
       }
       float m_run = kNone, l_run = 0.f;
       for (int t = it.from; t < it.to; ++t, ++u) {
-        const int n0 = t * kTk;
-        const int lo = bottom - n0, hi = top - n0;
-        const bool full = n0 + kTk <= top_min && n0 >= bottom_max;
+        const int n0 = t * kTk, hi = top - n0;
+        const bool full = n0 + kTk <= top_min;
         // one warp of the group polls the mbarrier, the vote hands the result on
         group_all(g, (warp & 3) != 0 || bar_wait(&s_done[g], s_par, &abort_sh, a.timeout));
         s_par ^= 1;
         fence_after();
         const uint4 bad = *reinterpret_cast<const uint4*>(bad_sh[u & 3]);
-        if (bad.x | bad.y | bad.z | bad.w) {
-          // rare: their logits become -inf in place
+        if ((bad.x | bad.y | bad.z | bad.w) != 0 || n0 < bottom_max) {
+          // tokens on a page out of range, or left of a row's window: their
+          // logits become -inf in place
 #pragma unroll 1
           for (int cb = 0; cb < 8; ++cb) {
             const uint32_t word = cb < 2 ? bad.x : cb < 4 ? bad.y : cb < 6 ? bad.z : bad.w;
-            const uint32_t bits = word >> (16 * (cb & 1));
+            const int below = min(max(bottom - n0 - 16 * cb, 0), 16);
+            const uint32_t bits = (word >> (16 * (cb & 1))) | ((1u << below) - 1);
             uint32_t x[16];
             tmem_ld16(sbase + 16 * cb, x);
             tmem_wait_ld();
@@ -318,10 +298,12 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         uint32_t v[64];
         tmem_ld64(sbase + 64, v);
         tmem_wait_ld();
-        float mx = full ? max_keys<true>(v, 64, lo, hi) : max_keys<false>(v, 64, lo, hi);
+        if (!full) hide_keys<64>(v, 64, hi);
+        float mx = max64(v);
         tmem_ld64(sbase, v);
         tmem_wait_ld();
-        mx = fmaxf(mx, full ? max_keys<true>(v, 0, lo, hi) : max_keys<false>(v, 0, lo, hi));
+        if (!full) hide_keys<64>(v, 0, hi);
+        mx = fmaxf(mx, max64(v));
         const float mnew = fmaxf(m_run, mx * c2);
         const bool need = mnew > m_run + 8.f;
         // S_g(t) follows PV_g(t-1) in the tensor pipe's order, so O_g is complete
@@ -340,7 +322,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         }
         if (need) m_run = mnew;
         const float2 c2v = make_float2(c2, c2), mv = make_float2(-m_run, -m_run);
-        float ps = full ? exp_keys<4, true>(v, 0, lo, hi, c2v, mv, sbase) : exp_keys<4, false>(v, 0, lo, hi, c2v, mv, sbase);
+        float ps = exp_keys<4>(v, 0, c2v, mv, sbase);
         tmem_wait_st();
         fence_before();
         nb_arrive(kNbP1 + g);
@@ -349,8 +331,8 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           uint32_t x[32];
           tmem_ld32(sbase + 64 + 32 * hq, x);
           tmem_wait_ld();
-          ps += full ? exp_keys<2, true>(x, 64 + 32 * hq, lo, hi, c2v, mv, sbase)
-                     : exp_keys<2, false>(x, 64 + 32 * hq, lo, hi, c2v, mv, sbase);
+          if (!full) hide_keys<32>(x, 64 + 32 * hq, hi);
+          ps += exp_keys<2>(x, 64 + 32 * hq, c2v, mv, sbase);
           if (hq == 0) {
             tmem_wait_st();
             fence_before();
@@ -362,84 +344,83 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         fence_before();
         nb_arrive(kNbP3 + g);
       }
+      // what the item's end needs, then on to the next item's Q: its S may run
+      // while this one's O is stored
+      const bool all = it.begins() && it.ends();
+      const int slot = it.begins() ? 1 : 0, rows = it.rows - 128 * g, y0 = it.rt * kRows + 128 * g;
+      const int64_t q_row0 = it.rq.row0;
+      const int head0 = it.h * a.group;
+      if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
+      const bool more = it.next();
+      if (more) c2 = make_q();
       group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
       pv_par ^= 1;
       fence_after();
-      // ---- O of the item, by way of the warp's rows of the Q tile (its MMAs
-      // are complete), so that a row is stored by neighbouring lanes.  Column
-      // p of 8 holds channel (p / 2) + 4 (p % 2).
-      const bool all = it.begins() && it.ends();
-      const int slot = it.begins() ? 1 : 0;
-      if (all) {
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      // ---- O of the item by way of shared memory, 128 bytes a row at a time,
+      // so that a row is stored by neighbouring lanes.  Column p of 8 holds
+      // channel (p / 2) + 4 (p % 2).
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const int per = all ? 64 : 32;   // channels of a round: bf16 rows, or float32 parts
 #pragma unroll 1
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t x[32];
-          tmem_ld32(obase + 32 * cb, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t u[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // channels 2 k, 2 k + 1 are in columns 2 (2 k % 4) + (k > 1), + 2
-              const int c0 = 8 * q + 2 * ((2 * k) & 3) + (k >> 1);
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[c0]) * inv, __uint_as_float(x[c0 + 2]) * inv);
-              u[k] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            *reinterpret_cast<uint4*>(qt + op_off(i, 4 * cb + q)) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int y = w32 + k * RP + lane / CH;
-          if (128 * g + y < it.rows)
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + place(y, a.o_row, a.o_head) + 8 * (lane % CH)) =
-                *reinterpret_cast<const uint4*>(qt + op_off(y, lane % CH));
-        }
-        __syncwarp();
-      } else {
-        // a part in float32: two halves of D / 2 channels
+      for (int c0 = 0; c0 < D; c0 += per) {
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
+        for (int q = 0; q < 4; ++q) {
+          if (all) {
             uint32_t x[16];
-            tmem_ld16(obase + hf * (D / 2) + 16 * cb, x);
+            tmem_ld16(obase + c0 + 16 * q, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int c0 = 8 * (q >> 1) + (q & 1);
-              *reinterpret_cast<uint4*>(qt + op_off(i, 4 * cb + q)) = make_uint4(x[c0], x[c0 + 2], x[c0 + 4], x[c0 + 6]);
+            for (int e = 0; e < 2; ++e) {
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                // channels 2 k, 2 k + 1 are in columns 2 (2 k % 4) + (k > 1), + 2
+                const int c = 8 * e + 2 * ((2 * k) & 3) + (k >> 1);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[c]) * inv, __uint_as_float(x[c + 2]) * inv);
+                o[k] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else {
+            uint32_t x[8];
+            tmem_ld8(obase + c0 + 8 * q, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * q + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(x[e], x[e + 2], x[e + 4], x[e + 6]);
+          }
+        }
+        __syncwarp();
+#pragma unroll 2
+        for (int k = 0; k < 8; ++k) {
+          const int y = 4 * k + (lane >> 3), r = 32 * (warp & 3) + y;
+          if (r < rows) {
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+            if (all) {
+              const int tok = div_group(a, y0 + r);
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + (q_row0 + tok) * a.o_row +
+                                        (int64_t)(head0 + y0 + r - tok * a.group) * a.o_head + c0 + 8 * (lane & 7)) = x;
+            } else {
+              *reinterpret_cast<uint4*>(part_row(a, w, slot, kRows, 128 * g + r, D) + c0 + 4 * (lane & 7)) = x;
             }
           }
-          __syncwarp();
-#pragma unroll 4
-          for (int k = 0; k < NI; ++k) {
-            const int y = w32 + k * RP + lane / CH;
-            if (128 * g + y < it.rows)
-              *reinterpret_cast<uint4*>(part_row(a, w, slot, kRows, 128 * g + y, D) + hf * (D / 2) + 4 * (lane % CH)) =
-                  *reinterpret_cast<const uint4*>(qt + op_off(y, lane % CH));
-          }
-          __syncwarp();
         }
+        __syncwarp();
       }
-      if (live) {
+      if (i < rows) {
         if (!all) {
-          float* part = part_row(a, w, slot, kRows, r, D);
+          float* part = part_row(a, w, slot, kRows, 128 * g + i, D);
           part[D] = m_run, part[D + 1] = l_run;
         } else if (a.lse) {
-          const int tok = div_group(a, rr);
-          a.lse[(int64_t)(it.rq.row0 + tok) * a.heads + it.h * a.group + rr - tok * a.group] =
+          const int tok = div_group(a, y0 + i);
+          a.lse[(q_row0 + tok) * a.heads + head0 + y0 + i - tok * a.group] =
               l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
         }
       }
-      if (tid == 0 && it.begins() && !it.ends()) {
-        record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
-      }
       fence_before();   // the reads of O come before the next item's MMAs
-    } while (it.next());
+      if (!more) break;
+    }
   } else if (warp < kMma) {
     // ------------------------------------------------------------ producers
     const int p = tid - kProd * 32;
@@ -459,16 +440,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       if (++t < it.to) return true;
       if (!it.next()) return false;
       t = it.from;
-      // the item's queries on their way to L2 while the one before it is at work
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (128 * g + p < it.rows) {
-          const int y = it.rt * kRows + 128 * g + p, tok = div_group(a, y);
-          const __nv_bfloat16* row = (const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
-                                     (int64_t)(it.h * a.group + y - tok * a.group) * a.q_head;
-#pragma unroll
-          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
-        }
       return true;
     };
     const uint8_t* blk = nullptr;
@@ -485,6 +456,28 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const uint8_t* b = blk ? blk + half * (a.block / 2) : nullptr;
       x.load(b ? b + s * (D / 2) : nullptr, b ? b + a.page * (D / 2) + s * (G * 4) : nullptr);
     };
+    // The queries of an item, bf16, into the Q tiles: asynchronous copies that
+    // arrive on q_raw, rows behind the item's zero.  A walker of its own: the
+    // tiles run ahead of it.
+    W qi = it;
+    int q_u = 0;   // the first tile of its item
+    auto load_q = [&]() {
+      constexpr int CH = D / 8;
+#pragma unroll 4
+      for (int y = p / CH; y < kRows; y += 128 / CH) {
+        const int x = qi.rt * kRows + y, tok = div_group(a, x);
+        const bool live = y < qi.rows;
+        const __nv_bfloat16* src = (const __nv_bfloat16*)a.q;
+        if (live)
+          src += (int64_t)(qi.rq.row0 + tok) * a.q_row + (int64_t)(qi.h * a.group + x - tok * a.group) * a.q_head + 8 * (p % CH);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(sm + (y >> 7) * L::op + op_off(y & 127, p % CH))),
+                     "l"(src), "r"(live ? 16 : 0) : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(q_raw)) : "memory");
+      q_u += qi.to - qi.from;
+      if (!qi.next()) q_u = -2;
+    };
+    load_q();
     lookup();
     resolve();
     load(kp, 0);
@@ -497,6 +490,9 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const uint32_t par = (uint32_t)(((u >> 1) - 1) & 1);
       const bool have = more;
       if (u >= 2) ok = bar_wait(&k_free[st], par, &abort_sh, a.timeout) && ok;
+      // S of tile u - 2 is complete: if the item of tile u - 1 is a new one,
+      // the Q tiles are free for it
+      if (u - 1 == q_u) load_q();
       kp.store(sm + L::k + st * L::op, p);
       if ((p & 31) == 0) bad_sh[u & 3][p >> 5] = bad;
       fence_async_smem();
@@ -509,11 +505,18 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);
-      if (!have) break;
+      if (!have) {
+        if (u == q_u) {   // the last tile is an item of its own
+          ok = bar_wait(&k_free[st ^ 1], (uint32_t)(((u - 1) >> 1) & 1), &abort_sh, a.timeout) && ok;
+          load_q();
+        }
+        break;
+      }
       load(vp, 1);
       more = advance();
       if (more) lookup();
     }
+    cp_async_wait_all();
   } else {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t q0 = su32(sm), k0 = su32(sm + L::k), v0 = su32(sm + L::v);
