@@ -48,7 +48,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 2;
+constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 4;
 constexpr uint32_t kColO = 256;
 constexpr float kNone = -3.0e38f;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
@@ -167,6 +167,25 @@ __device__ __forceinline__ float max64(const uint32_t* v) {
   return fmaxf(a, b);
 }
 
+// The row's logits of tokens below `lo` of the tile, and of those whose bit in
+// `bad` is set, become -inf in place.  Rare and out of line: it must not cost
+// the tile loop its registers.
+__device__ __noinline__ void mend_logits(uint32_t sbase, const uint32_t* bad, int lo) {
+#pragma unroll 1
+  for (int cb = 0; cb < 8; ++cb) {
+    const int below = min(max(lo - 16 * cb, 0), 16);
+    const uint32_t bits = (bad[cb >> 1] >> (16 * (cb & 1))) | ((1u << below) - 1);
+    uint32_t x[16];
+    tmem_ld16(sbase + 16 * cb, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (bits >> k & 1) x[k] = 0xff800000u;
+    tmem_st16(sbase + 16 * cb, x);
+  }
+  tmem_wait_st();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArgs a) {
   using L = Lay<D>;
@@ -268,6 +287,18 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           bottom_max = max(it.lo, at + div_group(a, it.rt * kRows + min(it.rows, 128 * g + 128) - 1) - a.window + 1);
         }
       }
+      // tiles that start below mend_until hold tokens that a row must not see
+      // left of its window, or (any tile of the item) on a page out of range
+      int mend_until = bottom_max;
+      {
+        bool good = true;
+        const int last = (min(it.hi, it.to * kTk) - 1) >> a.page_shift;
+        for (int x = (max(it.lo, it.from * kTk) >> a.page_shift) + i; x <= last; x += 128) {
+          const int pg = __ldg(a.table + (int64_t)it.b * a.max_blocks + x);
+          good = good && pg >= 0 && pg < a.n_pages;
+        }
+        if (!group_all(g, good)) mend_until = 0x7fffffff;
+      }
       float m_run = kNone, l_run = 0.f;
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int n0 = t * kTk, hi = top - n0;
@@ -276,25 +307,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         group_all(g, (warp & 3) != 0 || bar_wait(&s_done[g], s_par, &abort_sh, a.timeout));
         s_par ^= 1;
         fence_after();
-        const uint4 bad = *reinterpret_cast<const uint4*>(bad_sh[u & 3]);
-        if ((bad.x | bad.y | bad.z | bad.w) != 0 || n0 < bottom_max) {
-          // tokens on a page out of range, or left of a row's window: their
-          // logits become -inf in place
-#pragma unroll 1
-          for (int cb = 0; cb < 8; ++cb) {
-            const uint32_t word = cb < 2 ? bad.x : cb < 4 ? bad.y : cb < 6 ? bad.z : bad.w;
-            const int below = min(max(bottom - n0 - 16 * cb, 0), 16);
-            const uint32_t bits = (word >> (16 * (cb & 1))) | ((1u << below) - 1);
-            uint32_t x[16];
-            tmem_ld16(sbase + 16 * cb, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (bits >> k & 1) x[k] = 0xff800000u;
-            tmem_st16(sbase + 16 * cb, x);
-          }
-          tmem_wait_st();
-        }
+        if (n0 < mend_until) mend_logits(sbase, bad_sh[u & 3], bottom - n0);
         uint32_t v[64];
         tmem_ld64(sbase + 64, v);
         tmem_wait_ld();
