@@ -3,33 +3,37 @@
 //
 //   s_n = q . k_hat_n;  O = sum_n exp2(s_n - m) v_hat_n, running maximum m
 //
-// A worker (CTA) walks the tiles of 64 tokens that the partition deals to it.
-// One producer warp copies the packed tiles (160 bytes a token at d = 128)
-// into a ring of shared-memory stages with bulk copies, one mbarrier a stage;
-// it holds the next 64 page ids in registers, so the table's latency is not
-// on the copies' path.  Four consumer warps take 16 tokens of every tile each,
-// with their own running maximum, and meet at the end of an item only.
+// A worker (a CTA of four warps, three on an SM) walks the tiles of 64 tokens
+// that the partition deals to it; a warp takes 16 tokens of each, with its own
+// running maximum, and the warps meet at the end of an item only.  The packed
+// bytes go straight to registers, in the shape of the MMA fragments: a lane
+// loads one run of codes of its token (K) or its channels of a few tokens (V),
+// 12 coalesced loads for 16 tokens.  A block's loads are issued two blocks
+// ahead, into the registers that the block before last has left, and the page
+// ids of 32 tiles are loaded at once, a block before the first is needed, so
+// no load waits for another and 2.5 to 5 KB a warp are always in flight.  (A
+// ring of shared-memory stages filled by bulk copies held 98 us on the batch
+// below without any arithmetic: one thread issues a copy at a time, and pages
+// of 16 tokens make 16 copies a tile.)
 //
-// A consumer keeps everything in registers.  Both products are formed
-// transposed with mma.m16n8k16 (float16 in, float32 out), the 16 tokens or
-// channels on the long side and the 8 query rows on the short one:
+// Both products are formed transposed with mma.m16n8k16 (float16 in, float32
+// out), the 16 tokens or channels on the long side and the 8 query rows on the
+// short one:
 //   S^T[16 tokens][8 rows]  = K_hat[16][d] Q^T      d/16 MMAs
 //   O^T[d][8 rows]         += V_hat^T[d][16] P^T    d/16 MMAs
 // so that a step of 5 or 8 query heads a key/value head does not pay for 16
 // rows.  Channels are contracted in the order in which the codes lie in
-// memory: a lane takes one run of codes of its token in one load, and Q is
-// laid out to match.  P^T is S^T transposed in 8 x 8 blocks (movmatrix).
-// A code c becomes float16 by one mask that puts it into the mantissa of 1024
-// (1024 + c, or 1024 + 16 c for the upper nibble of a byte), one exact
-// subtraction (or fused multiply by 1/16), and c scale + zero by one fused
-// multiply-add: the only rounding of k_hat and v_hat.  Q is float16 scaled per
-// row by a power of two (exact).  The rows' sums and O are float32; O is
-// rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8).
+// memory, and Q is laid out to match.  P^T is S^T transposed in 8 x 8 blocks
+// (movmatrix).  A code c becomes float16 by one mask that puts it into the
+// mantissa of 1024 (1024 + c, or 1024 + 16 c for the upper nibble of a byte),
+// one exact subtraction (or fused multiply by 1/16), and c scale + zero by one
+// fused multiply-add: the only rounding of k_hat and v_hat.  Q is float16
+// scaled per row by a power of two (exact).  The rows' sums and O are float32;
+// O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8).
 // Tokens outside a request (or on a page out of range) have their logits
 // replaced and their value parameters zeroed, so garbage bytes do no harm.
 //
-// Bound by HBM: 1.25 d bytes a token; about 18 instructions a token and warp
-// leave the issue slots about as busy as the memory.
+// Bound by HBM: 1.25 d bytes a token.
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 
@@ -39,22 +43,8 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 64, kCw = 4, kNt = (kCw + 1) * 32, kStages = 4, kItem = 2;
+constexpr int kCw = 4, kCtas = 3, kTk = 16 * kCw, kNt = kCw * 32, kItem = 2;
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
-
-template <int D>
-struct Stage {
-  static constexpr int G = D / 32;
-  static constexpr int kcode = 0, kpar = kTk * D / 2, vcode = kpar + kTk * G * 4, vpar = vcode + kTk * D / 2;
-  static constexpr int bytes = vpar + kTk * G * 4;
-};
-template <int D, int NB>
-struct Smem {
-  static constexpr int LD = D + 4;                          // rows 2 c of a store phase 8 banks apart
-  static constexpr int merge = kStages * Stage<D>::bytes;   // float [kCw][8 NB][LD]
-  static constexpr int stat = merge + kCw * 8 * NB * LD * 4;
-  static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
-};
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -78,100 +68,132 @@ __device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z) {
   const __half2 c = __hfma2(u2h((x & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
   return h2u(__hfma2(c, s, z));
 }
-// the token of a block of 8 that column (or row) n of a fragment holds: the
-// lanes of a load phase then meet even and odd 64-byte rows
-__device__ __forceinline__ int token_of(int n) { return (n & 1) ? 4 + ((n >> 1) ^ 1) : n >> 1; }
+__device__ __forceinline__ uint32_t ldg32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCw * 32) : "memory"); }
+// A lane's share of 16 tokens, as loaded.  Lane (g, c) = (lane / 4, lane % 4):
+// keys g and g + 8, a quarter of their channels; values of tokens 2 c, 2 c + 1
+// (+ 8), an eighth of their channels.
+template <int D>
+struct Block {
+  static constexpr int G = D / 32, KW = D / 32, VW = D / 64;
+  uint32_t k[2][KW], kp[2];
+  uint32_t v[2][2][VW], vp[2][2];
+  bool have;
+
+  // blk: the block of the page and head; at: the first token's slot
+  __device__ __forceinline__ void load(const uint8_t* blk, int at, int page, int half, int g, int c) {
+    const uint8_t* kc = blk + (at + g) * (D / 2) + c * (D / 8);
+    const uint8_t* kq = blk + page * (D / 2) + ((at + g) * G + c * G / 4) * 4;
+    const uint8_t* vc = blk + half + (at + 2 * c) * (D / 2) + g * (D / 16);
+    const uint8_t* vq = blk + half + page * (D / 2) + ((at + 2 * c) * G + g * G / 8) * 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if constexpr (D == 128) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(kc + b * 4 * D));
+        k[b][0] = u.x, k[b][1] = u.y, k[b][2] = u.z, k[b][3] = u.w;
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(kc + b * 4 * D));
+        k[b][0] = u.x, k[b][1] = u.y;
+      }
+      kp[b] = ldg32(kq + b * 32 * G);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (D == 128) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(vc + (8 * b + e) * (D / 2)));
+          v[b][e][0] = u.x, v[b][e][1] = u.y;
+        } else {
+          v[b][e][0] = ldg32(vc + (8 * b + e) * (D / 2));
+        }
+        vp[b][e] = ldg32(vq + (8 * b + e) * (4 * G));
+      }
+    }
+  }
+};
+
+// The blocks of one warp, in order, ahead of the arithmetic.  Its walker is in
+// shared memory: registers hold only what every block needs.
+template <int D, class W>
+struct Ahead {
+  W* walker;
+  int t, to, base;       // next tile; end of the item's; first tile of the ids
+  int lo, hi, ids;
+  const int32_t* row;
+  const uint8_t* head;   // pool + the head's offset in a page
+  bool more;
+
+  __device__ __forceinline__ void fetch_ids(const AttendArgs& a, int warp, int lane) {
+    base = t;
+    const int n = (t + lane) * kTk + 16 * warp;
+    const bool in = t + lane < to && n < hi && n + 16 > lo;
+    ids = in ? __ldg(row + (n >> a.page_shift)) : -2;
+    if (in && (ids < 0 || ids >= a.n_pages)) {
+      flag(a.status, QWM_DEV_BOUNDS);
+      ids = -2;
+    }
+  }
+  __device__ __forceinline__ void open(const AttendArgs& a, const W& w, int warp, int lane) {
+    t = w.from, to = w.to, lo = w.lo, hi = w.hi;
+    row = a.table + (int64_t)w.b * a.max_blocks;
+    head = a.pool + (int64_t)w.h * a.block;
+    fetch_ids(a, warp, lane);
+  }
+  __device__ __forceinline__ void load(const AttendArgs& a, Block<D>& x, int warp, int lane) {
+    const int pg = __shfl_sync(0xffffffffu, ids, t - base);
+    x.have = pg >= 0;
+    if (x.have) {
+      const int n = t * kTk + 16 * warp;
+      x.load(head + (int64_t)pg * a.kv_heads * a.block, n & (a.page - 1), a.page, a.block / 2, lane >> 2, lane & 3);
+    }
+    // on to the next block; its id is on the way before it is asked for
+    if (++t == to) {
+      W w = *walker;
+      more = w.next(a);
+      __syncwarp();
+      if (more) {
+        if (lane == 0) *walker = w;
+        open(a, w, warp, lane);
+      }
+      __syncwarp();
+    } else if (t == base + 32) {
+      fetch_ids(a, warp, lane);
+    }
+  }
+};
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(const AttendArgs a) {
-  constexpr int R = 8 * NB, G = D / 32, KW = D / 32, VW = D / 64, MB = D / 16;
-  using St = Stage<D>;
+struct Smem {
+  static constexpr int LD = D + 4;                          // rows 2 c of a store phase 8 banks apart
+  static constexpr int merge = 0;                           // float [kCw][8 NB][LD]
+  static constexpr int stat = merge + kCw * 8 * NB * LD * 4;
+  static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
+};
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
+  constexpr int R = 8 * NB, KW = D / 32, VW = D / 64, MB = D / 16;
   using Sm = Smem<D, NB>;
+  using W = Walker<R, kTk, kItem>;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
-  __shared__ uint32_t vmask[kStages];
-  __shared__ volatile int abort_sh;
+  __shared__ W ahead_sh[kCw];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x;
-  if (tid == 0) {
-    abort_sh = 0;
-    for (int i = 0; i < kStages; ++i) {
-      bar_init(&full[i], 1);
-      bar_init(&empty[i], kCw);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    a.join[w].last = -1;
-  }
+  if (tid == 0) a.join[w].last = -1;
   const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);   // has block barriers
   cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
-  Walker<R, kTk, kItem> it(a);
-  it.start(sh.b, sh.skip, sh.per, sh.n);
-  int st = 0;
-  uint32_t phase = 0;
+  W it;
+  it.start(a, sh.b, sh.skip, sh.per, sh.n);
+  if (lane == 0) ahead_sh[warp] = it;
+  __syncwarp();
+  Ahead<D, W> ahead;
+  ahead.walker = &ahead_sh[warp];
+  ahead.more = true;
+  ahead.open(a, it, warp, lane);
+  Block<D> buf0, buf1;
+  ahead.load(a, buf0, warp, lane);
+  if (ahead.more) ahead.load(a, buf1, warp, lane);
+  bool odd = false;      // the next block is in buf1
 
-  if (warp == kCw) {
-    // ------------------------------------------------------------ producer
-    const int run = a.page < kTk ? a.page : kTk;        // tokens of one copy
-    const int r = lane >> 2, sec = lane & 3;
-    const bool code = (sec & 1) == 0;
-    const int per = code ? D / 2 : G * 4;               // bytes a token in this section
-    const int src_off = (sec & 2 ? a.block / 2 : 0) + (code ? 0 : a.page * (D / 2));
-    const int dst_off = (sec == 0 ? St::kcode : sec == 1 ? St::kpar : sec == 2 ? St::vcode : St::vpar) + r * run * per;
-    const uint32_t bytes = (uint32_t)(run * per);
-    int issued = 0;
-    bool ok = true;
-    do {
-      const int32_t* row = a.table + (int64_t)it.b * a.max_blocks;
-      int base = (it.from * kTk) >> a.page_shift;
-      auto ids = [&](int p) { return p + lane < a.max_blocks ? row[p + lane] : -1; };
-      int cur = ids(base), nxt = ids(base + 32);
-      for (int t = it.from; t < it.to && ok; ++t) {
-        const int n = t * kTk + r * run, p = (t * kTk) >> a.page_shift;
-        if (p >= base + 32) {
-          base += 32;
-          cur = nxt;
-          nxt = ids(base + 32);
-        }
-        const bool need = r * run < kTk && n < it.hi && n + run > it.lo;
-        const int pg = __shfl_sync(0xffffffffu, cur, ((n >> a.page_shift) - base) & 31);
-        const bool good = need && pg >= 0 && pg < a.n_pages;
-        if (need && !good && sec == 0) flag(a.status, QWM_DEV_BOUNDS);
-        const uint32_t who = __ballot_sync(0xffffffffu, good);
-        if (issued >= kStages) ok = warp_all(bar_wait(&empty[st], phase ^ 1, &abort_sh, a.timeout));
-        if (!ok) break;
-        if (lane == 0) {
-          uint32_t m = 0;      // a bit for every 16 tokens
-          for (int s = 0; s < 4; ++s)
-            if (who >> ((s * 16 / run) * 4) & 1) m |= 1u << s;
-          vmask[st] = m;
-          bar_expect_tx(&full[st], (uint32_t)(__popc(who) / 4) * (uint32_t)(run * (D + D / 4)));
-        }
-        __syncwarp();
-        if (good) {
-          const uint8_t* src = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + src_off + (n & (a.page - 1)) * per;
-          bulk_g2s(sm + st * St::bytes + dst_off, src, bytes, &full[st]);
-        }
-        ++issued;
-        if (++st == kStages) st = 0, phase ^= 1;
-      }
-    } while (ok && it.next());
-    // after a timeout: no copy of ours may land in memory that is given back
-    if (!ok && lane == 0)
-      for (int i = 0; i < (issued < kStages ? issued : kStages); ++i) {
-        const int s = (st + kStages - 1 - i) % kStages;
-        const uint32_t ph = (uint32_t)(((issued - 1 - i) / kStages) & 1);
-        const long long t0 = clock64();
-        while (!bar_test(&full[s], ph) && clock64() - t0 < kWaitCycles) {}
-      }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
-  const int tok0 = token_of(g);                  // this lane's key of a block of 8
-  const int ta = token_of(2 * c), tb = token_of(2 * c + 1);   // its value tokens
   float* merge = reinterpret_cast<float*>(sm + Sm::merge);
   float2* stat = reinterpret_cast<float2*>(sm + Sm::stat);
   do {
@@ -241,79 +263,57 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
 #pragma unroll
       for (int k = 0; k < 2; ++k) m[nb][k] = kNone, l[nb][k] = 0.f;
     }
-    for (int t = it.from; t < it.to; ++t) {
-      bar_wait(&full[st], phase, &abort_sh, a.timeout);
-      const uint8_t* tile = sm + st * St::bytes;
-      const int n0 = t * kTk + 16 * warp;
-      const bool have = (vmask[st] >> warp) & 1;
-      if (have && n0 < it.hi && n0 + 16 > it.lo) {
-        const bool whole = n0 + 16 <= top_min && n0 >= bottom_max;
-        // ---- S^T
-        float s[NB][4];
+    // the 16 tokens of a block that start at n0
+    auto step = [&](Block<D>& x, int n0) {
+      const bool live = x.have && n0 < it.hi && n0 + 16 > it.lo;
+      const bool whole = n0 + 16 <= top_min && n0 >= bottom_max;   // every row sees all of them
+      // ---- S^T
+      float s[NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
-        {
-          uint32_t kw[2][KW];
-          __half2 ks[2], kz[2];
+      for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+      if (live) {
+        const __half2 kz[2] = {__low2half2(u2h(x.kp[0])), __low2half2(u2h(x.kp[1]))};
+        const __half2 ks[2] = {__high2half2(u2h(x.kp[0])), __high2half2(u2h(x.kp[1]))};
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          uint32_t f[4], f2[4];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const int row = 16 * warp + 8 * b + tok0;
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4*>(tile + St::kcode + row * 64 + 16 * c);
-              kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(tile + St::kcode + row * 32 + 8 * c);
-              kw[b][0] = u.x, kw[b][1] = u.y;
-            }
-            const __half2 par = *reinterpret_cast<const __half2*>(tile + St::kpar + (row * G + c * G / 4) * 4);
-            kz[b] = __low2half2(par);
-            ks[b] = __high2half2(par);
+            f[b] = dq_lo(x.k[b][i], ks[b], kz[b]);
+            f[2 + b] = dq_hi(x.k[b][i], ks[b], kz[b]);
+            const uint32_t up = x.k[b][i] >> 8;
+            f2[b] = dq_lo(up, ks[b], kz[b]);
+            f2[2 + b] = dq_hi(up, ks[b], kz[b]);
           }
 #pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            uint32_t f[4], f2[4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              f[b] = dq_lo(kw[b][i], ks[b], kz[b]);
-              f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b]);
-              const uint32_t up = kw[b][i] >> 8;
-              f2[b] = dq_lo(up, ks[b], kz[b]);
-              f2[2 + b] = dq_hi(up, ks[b], kz[b]);
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma(s[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-              mma(s[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
-            }
+          for (int nb = 0; nb < NB; ++nb) {
+            mma(s[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+            mma(s[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
           }
         }
-        // ---- softmax: s[nb][2 b + k] is token 8 b + token_of(g), row 2 c + k
+        // ---- softmax: s[nb][2 b + k] is token 8 b + g, row 2 c + k
         uint32_t pf[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = s[nb][i] * c2[nb][i & 1];
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int n = n0 + 8 * (i >> 1) + tok0;
-              if (n < bottom[nb][i & 1] || n >= top[nb][i & 1]) x[i] = -INFINITY;
+              const int n = n0 + 8 * (i >> 1) + g;
+              if (n < bottom[nb][i & 1] || n >= top[nb][i & 1]) s[nb][i] = -INFINITY;
             }
           }
-          const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+          float mx0 = fmaxf(s[nb][0], s[nb][2]) * c2[nb][0], mx1 = fmaxf(s[nb][1], s[nb][3]) * c2[nb][1];
           if (__any_sync(0xffffffffu, mx0 > m[nb][0] + 8.f || mx1 > m[nb][1] + 8.f)) {
             // rare: the rows' maxima over the 16 tokens, and O rescaled
-            float u0 = mx0, u1 = mx1;
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
-              u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, d));
-              u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, d));
+              mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+              mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
             }
-            u0 = fmaxf(u0, m[nb][0]);
-            u1 = fmaxf(u1, m[nb][1]);
-            const float f0 = ex2(m[nb][0] - u0), f1 = ex2(m[nb][1] - u1);
-            m[nb][0] = u0, m[nb][1] = u1;
+            mx0 = fmaxf(mx0, m[nb][0]);
+            mx1 = fmaxf(mx1, m[nb][1]);
+            const float f0 = ex2(m[nb][0] - mx0), f1 = ex2(m[nb][1] - mx1);
+            m[nb][0] = mx0, m[nb][1] = mx1;
             l[nb][0] *= f0, l[nb][1] *= f1;
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
@@ -323,33 +323,22 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
           }
           float p[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = ex2(x[i] - m[nb][i & 1]);
+          for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[nb][i], c2[nb][i & 1], -m[nb][i & 1]));
           l[nb][0] += p[0] + p[2];
           l[nb][1] += p[1] + p[3];
           pf[nb][0] = transpose8(h2u(__floats2half2_rn(p[0], p[1])));
           pf[nb][1] = transpose8(h2u(__floats2half2_rn(p[2], p[3])));
         }
-        // ---- O^T: tokens ta, tb (columns 2 c, 2 c + 1) of both blocks of 8
+        // ---- O^T: tokens 2 c, 2 c + 1 of both blocks of 8
         uint32_t f[MB][4];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int r0 = 16 * warp + 8 * b + ta, r1 = 16 * warp + 8 * b + tb;
-          uint32_t v0[VW], v1[VW];
-          if constexpr (D == 128) {
-            const uint2 u0 = *reinterpret_cast<const uint2*>(tile + St::vcode + r0 * 64 + 8 * g);
-            const uint2 u1 = *reinterpret_cast<const uint2*>(tile + St::vcode + r1 * 64 + 8 * g);
-            v0[0] = u0.x, v0[1] = u0.y, v1[0] = u1.x, v1[1] = u1.y;
-          } else {
-            v0[0] = *reinterpret_cast<const uint32_t*>(tile + St::vcode + r0 * 32 + 4 * g);
-            v1[0] = *reinterpret_cast<const uint32_t*>(tile + St::vcode + r1 * 32 + 4 * g);
-          }
-          uint32_t p0 = *reinterpret_cast<const uint32_t*>(tile + St::vpar + (r0 * G + g * G / 8) * 4);
-          uint32_t p1 = *reinterpret_cast<const uint32_t*>(tile + St::vpar + (r1 * G + g * G / 8) * 4);
+          uint32_t p0 = x.vp[b][0], p1 = x.vp[b][1];
           if (!whole) {
             // tokens outside the request: their bytes may be anything
-            const int x0 = n0 + 8 * b + ta, x1 = n0 + 8 * b + tb;
-            if (x0 < it.lo || x0 >= it.hi) p0 = 0;
-            if (x1 < it.lo || x1 >= it.hi) p1 = 0;
+            const int n = n0 + 8 * b + 2 * c;
+            if (n < it.lo || n >= it.hi) p0 = 0;
+            if (n + 1 < it.lo || n + 1 >= it.hi) p1 = 0;
           }
           const __half2 z = u2h(__byte_perm(p0, p1, 0x5410)), sc = u2h(__byte_perm(p0, p1, 0x7632));
           // f[j][2 b]: channel row g, f[j][2 b + 1]: channel row g + 8 of block j
@@ -358,8 +347,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               // byte y of both tokens into bytes 0 and 2
-              const uint32_t x = __byte_perm(v0[q], v1[q], y * 0x0011 + (4 + y) * 0x1100);
-              const uint32_t lo = dq_lo(x, sc, z), hi = dq_hi(x, sc, z);
+              const uint32_t v = __byte_perm(x.v[b][0][q], x.v[b][1][q], y * 0x0011 + (4 + y) * 0x1100);
+              const uint32_t lo = dq_lo(v, sc, z), hi = dq_hi(v, sc, z);
               if constexpr (D == 128) {
                 f[2 * y][2 * b + q] = lo;
                 f[2 * y + 1][2 * b + q] = hi;
@@ -374,9 +363,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma(o[nb][j], f[j], pf[nb][0], pf[nb][1]);
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(&empty[st]);
-      if (++st == kStages) st = 0, phase ^= 1;
+      // the block's registers are free for the one after next
+      if (ahead.more) ahead.load(a, x, warp, lane);
+    };
+    for (int t = it.from; t < it.to; ++t) {
+      const int n0 = t * kTk + 16 * warp;
+      if (odd) step(buf1, n0);
+      else step(buf0, n0);
+      odd = !odd;
     }
     // ---- the warps' parts of the item meet
 #pragma unroll
@@ -395,7 +389,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
           *reinterpret_cast<float2*>(row + 16 * j + 2 * g) = make_float2(o[nb][j][k], o[nb][j][2 + k]);
       }
     }
-    consumers_sync();
+    __syncthreads();
     {
       const bool all = it.begins() && it.ends();
       const int slot = it.begins() ? 1 : 0;
@@ -433,8 +427,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? 3 : 2) paged_attend_mma_kernel(
         record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), R);
       }
     }
-    consumers_sync();
-  } while (it.next());
+    __syncthreads();
+  } while (it.next(a));
 }
 
 template <int D, int NB>
@@ -452,7 +446,7 @@ cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
 
 Workers mma_workers(int64_t max_rows) {
   const int sms = sm_count();
-  return max_rows <= 8 ? Workers{3 * sms, 8} : Workers{2 * sms, 16};
+  return max_rows <= 8 ? Workers{kCtas * sms, 8} : Workers{2 * sms, 16};
 }
 
 cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {

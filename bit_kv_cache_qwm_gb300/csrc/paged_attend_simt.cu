@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
   if (tid == 0) a.join[w].last = -1;
   cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
-  Walker<R, kTk, kItem> it(a);
-  it.start(sh.b, sh.skip, sh.per, sh.n);
+  Walker<R, kTk, kItem> it;
+  it.start(a, sh.b, sh.skip, sh.per, sh.n);
   do {
     const int row0 = it.rt * R;
     __syncthreads();   // the previous item's reads of Qs are done
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
     if (tid == 0 && it.begins() && !it.ends()) {
       record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), R);
     }
-  } while (it.next());
+  } while (it.next(a));
 }
 
 // Joins the parts of a cut item, in the order of the workers.  With few parts

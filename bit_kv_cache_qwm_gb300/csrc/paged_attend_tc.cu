@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base_sh;
-  W it(a);
-  it.start(sh.b, sh.skip, sh.per, sh.n);
+  W it;
+  it.start(a, sh.b, sh.skip, sh.per, sh.n);
 
   if (warp < kProd) {
     // ------------------------------------------------------------ softmax
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const int64_t q_row0 = it.rq.row0;
       const int head0 = it.h * a.group;
       if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
-      const bool more = it.next();
+      const bool more = it.next(a);
       if (more) c2 = make_q();
       group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
       pv_par ^= 1;
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     };
     auto advance = [&]() {
       if (++t < it.to) return true;
-      if (!it.next()) return false;
+      if (!it.next(a)) return false;
       t = it.from;
       return true;
     };
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(q_raw)) : "memory");
       q_u += qi.to - qi.from;
-      if (!qi.next()) q_u = -2;
+      if (!qi.next(a)) q_u = -2;
     };
     load_q();
     lookup();
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           }
         }
       }
-    } while (it.next());
+    } while (it.next(a));
   }
   fence_before();
   __syncthreads();

@@ -120,7 +120,6 @@ __device__ __forceinline__ void visible(const AttendArgs& a, const Request& r, i
 // the next.
 template <int R, int TK, int C>
 struct Walker {
-  const AttendArgs& a;
   int64_t n, done;     // the share's weight, and what of it has been handed out
   int64_t item_at;     // weight of the current item's start, from the share's
   // the current item
@@ -130,8 +129,6 @@ struct Walker {
   int lo, hi;          // its visible tokens
   int from, to;        // the tiles of it that are this worker's
   int rows;            // valid rows of the item
-
-  __device__ explicit Walker(const AttendArgs& args) : a(args) {}
 
   __device__ int row_tiles() const { return (rq.rows + R - 1) / R; }
 
@@ -161,7 +158,7 @@ struct Walker {
 
   // The share's piece of the item, which starts `skip` into its weight; false
   // when it has no tile.
-  __device__ bool item(int skip) {
+  __device__ bool item(const AttendArgs& a, int skip) {
     tiles_of(a, rq, rt, &lo, &hi, &t0, &t1);
     item_at = done - skip;
     const int all = t1 - t0 + C;
@@ -191,7 +188,7 @@ struct Walker {
 
   // To the first item of a share (whole warps call this): it starts `skip`
   // into the weight of request b0, whose kv heads weigh `per` each.
-  __device__ void start(int b0, int64_t skip, int64_t per, int64_t weight) {
+  __device__ void start(const AttendArgs& a, int b0, int64_t skip, int64_t per, int64_t weight) {
     b = b0;
     rq = load_request(a, b);
     n = weight;
@@ -219,10 +216,10 @@ struct Walker {
       }
       skip -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    item((int)skip);
+    item(a, (int)skip);
   }
 
-  __device__ bool next() {
+  __device__ bool next(const AttendArgs& a) {
     if (done >= n) return false;
     if (++rt >= row_tiles()) {
       rt = 0;
@@ -234,7 +231,7 @@ struct Walker {
         } while (rq.rows == 0);
       }
     }
-    return item(0);
+    return item(a, 0);
   }
 
   __device__ bool begins() const { return from == t0; }
