@@ -3,18 +3,17 @@
 //
 //   s_n = q . k_hat_n;  O = sum_n exp2(s_n - m) v_hat_n, running maximum m
 //
-// A worker (a CTA of four warps, three on an SM) walks the tiles of 64 tokens
-// that the partition deals to it; a warp takes 16 tokens of each, with its own
-// running maximum, and the warps meet at the end of an item only.  The packed
-// bytes go straight to registers, in the shape of the MMA fragments: a lane
-// loads one run of codes of its token (K) or its channels of a few tokens (V),
-// 12 coalesced loads for 16 tokens.  A block's loads are issued two blocks
-// ahead, into the registers that the block before last has left, and the page
-// ids of 32 tiles are loaded at once, a block before the first is needed, so
-// no load waits for another and 2.5 to 5 KB a warp are always in flight.  (A
-// ring of shared-memory stages filled by bulk copies held 98 us on the batch
-// below without any arithmetic: one thread issues a copy at a time, and pages
-// of 16 tokens make 16 copies a tile.)
+// A worker (a CTA of four warps) walks the tiles of 64 tokens that the
+// partition deals to it; a warp takes 16 tokens of each, with its own running
+// maximum, and the warps meet at the end of an item only.  Every warp copies
+// its own packed bytes (2.5 KB a block of 16 tokens at d = 128, five 16-byte
+// asynchronous copies a lane) into its own ring of shared memory, so that no
+// barrier stands between the copies and the arithmetic; the page ids of 32
+// tiles are loaded at once, a block before the first is needed.  (Measured on
+// the ragged batch of 48 requests: one producer warp a CTA with bulk copies
+// 155 us, where a thread issues one copy at a time and pages of 16 tokens make
+// 16 a tile; loads to registers two blocks ahead 143 us, too few bytes in
+// flight.)
 //
 // Both products are formed transposed with mma.m16n8k16 (float16 in, float32
 // out), the 16 tokens or channels on the long side and the 8 query rows on the
@@ -43,7 +42,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kCw = 4, kCtas = 3, kTk = 16 * kCw, kNt = kCw * 32, kItem = 2;
+constexpr int kCw = 4, kCtas = 3, kStages = 4, kTk = 16 * kCw, kNt = kCw * 32, kItem = 2;
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -59,53 +58,40 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
-// c scale + zero for the lower (upper) nibbles of bytes 0 and 2 of x
-__device__ __forceinline__ uint32_t dq_lo(uint32_t x, __half2 s, __half2 z) {
-  const __half2 c = __hsub2(u2h((x & 0x000f000fu) | 0x64006400u), __float2half2_rn(1024.f));
+// c scale + zero for the lower (upper) nibbles of bytes 0 and 2 of x.  `magic`
+// (1024 twice in float16) comes from the call's arguments: with a mask and a
+// register one instruction puts the codes into place, with two constants known
+// to the compiler it takes two.
+__device__ __forceinline__ uint32_t dq_lo(uint32_t x, __half2 s, __half2 z, uint32_t magic) {
+  const __half2 c = __hsub2(u2h((x & 0x000f000fu) | magic), __float2half2_rn(1024.f));
   return h2u(__hfma2(c, s, z));
 }
-__device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z) {
-  const __half2 c = __hfma2(u2h((x & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+__device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z, uint32_t magic) {
+  const __half2 c = __hfma2(u2h((x & 0x00f000f0u) | magic), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
   return h2u(__hfma2(c, s, z));
 }
-__device__ __forceinline__ uint32_t ldg32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
+// the token of a block of 8 that column (or row) n of a fragment holds: the
+// lanes of a load phase then meet even and odd rows of codes
+__device__ __forceinline__ int token_of(int n) { return (n & 1) ? 4 + ((n >> 1) ^ 1) : n >> 1; }
 
-// A lane's share of 16 tokens, as loaded.  Lane (g, c) = (lane / 4, lane % 4):
-// keys g and g + 8, a quarter of their channels; values of tokens 2 c, 2 c + 1
-// (+ 8), an eighth of their channels.
+// 16 tokens of one head as they lie in a ring stage
 template <int D>
-struct Block {
-  static constexpr int G = D / 32, KW = D / 32, VW = D / 64;
-  uint32_t k[2][KW], kp[2];
-  uint32_t v[2][2][VW], vp[2][2];
-  bool have;
+struct Stage {
+  static constexpr int G = D / 32;
+  static constexpr int kcode = 0, kpar = 8 * D, vcode = kpar + 64 * G, vpar = vcode + 8 * D, bytes = vpar + 64 * G;
+  static constexpr int copies = (bytes / 16 + 31) / 32;   // of 16 bytes, a lane
 
   // blk: the block of the page and head; at: the first token's slot
-  __device__ __forceinline__ void load(const uint8_t* blk, int at, int page, int half, int g, int c) {
-    const uint8_t* kc = blk + (at + g) * (D / 2) + c * (D / 8);
-    const uint8_t* kq = blk + page * (D / 2) + ((at + g) * G + c * G / 4) * 4;
-    const uint8_t* vc = blk + half + (at + 2 * c) * (D / 2) + g * (D / 16);
-    const uint8_t* vq = blk + half + page * (D / 2) + ((at + 2 * c) * G + g * G / 8) * 4;
+  __device__ __forceinline__ static void copy(uint8_t* stage, const uint8_t* blk, int at, int page, int half, int lane) {
+    const uint8_t* codes = blk + at * (D / 2);
+    const uint8_t* pars = blk + page * (D / 2) + at * (4 * G);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if constexpr (D == 128) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(kc + b * 4 * D));
-        k[b][0] = u.x, k[b][1] = u.y, k[b][2] = u.z, k[b][3] = u.w;
-      } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(kc + b * 4 * D));
-        k[b][0] = u.x, k[b][1] = u.y;
-      }
-      kp[b] = ldg32(kq + b * 32 * G);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (D == 128) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(vc + (8 * b + e) * (D / 2)));
-          v[b][e][0] = u.x, v[b][e][1] = u.y;
-        } else {
-          v[b][e][0] = ldg32(vc + (8 * b + e) * (D / 2));
-        }
-        vp[b][e] = ldg32(vq + (8 * b + e) * (4 * G));
-      }
+    for (int k = 0; k < copies; ++k) {
+      const int i = 32 * k + lane, o = 16 * i;
+      const bool value = o >= vcode;
+      const int x = value ? o - vcode : o;
+      const uint8_t* src = (x < kpar ? codes + x : pars + (x - kpar)) + (value ? half : 0);
+      if (32 * k + 32 <= bytes / 16 || i < bytes / 16) cp_async16(stage + o, src);
     }
   }
 };
@@ -137,40 +123,47 @@ struct Ahead {
     head = a.pool + (int64_t)w.h * a.block;
     fetch_ids(a, warp, lane);
   }
-  __device__ __forceinline__ void load(const AttendArgs& a, Block<D>& x, int warp, int lane) {
-    const int pg = __shfl_sync(0xffffffffu, ids, t - base);
-    x.have = pg >= 0;
-    if (x.have) {
-      const int n = t * kTk + 16 * warp;
-      x.load(head + (int64_t)pg * a.kv_heads * a.block, n & (a.page - 1), a.page, a.block / 2, lane >> 2, lane & 3);
-    }
-    // on to the next block; its id is on the way before it is asked for
-    if (++t == to) {
-      W w = *walker;
-      more = w.next(a);
-      __syncwarp();
-      if (more) {
-        if (lane == 0) *walker = w;
-        open(a, w, warp, lane);
+  // Copies the next block into a stage (one commit group, also when there is
+  // nothing to copy); returns whether the block has tokens.
+  __device__ __forceinline__ bool copy(const AttendArgs& a, uint8_t* stage, int warp, int lane) {
+    bool have = false;
+    if (more) {
+      const int pg = __shfl_sync(0xffffffffu, ids, t - base);
+      have = pg >= 0;
+      if (have) {
+        const int n = t * kTk + 16 * warp;
+        Stage<D>::copy(stage, head + (int64_t)pg * a.kv_heads * a.block, n & (a.page - 1), a.page, a.block / 2, lane);
       }
-      __syncwarp();
-    } else if (t == base + 32) {
-      fetch_ids(a, warp, lane);
+      // on to the next block; its id is on the way before it is asked for
+      if (++t == to) {
+        W w = *walker;
+        more = w.next(a);
+        __syncwarp();
+        if (more) {
+          if (lane == 0) *walker = w;
+          open(a, w, warp, lane);
+        }
+        __syncwarp();
+      } else if (t == base + 32) {
+        fetch_ids(a, warp, lane);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return have;
   }
 };
 
 template <int D, int NB>
 struct Smem {
   static constexpr int LD = D + 4;                          // rows 2 c of a store phase 8 banks apart
-  static constexpr int merge = 0;                           // float [kCw][8 NB][LD]
+  static constexpr int merge = kCw * kStages * Stage<D>::bytes;   // float [kCw][8 NB][LD]
   static constexpr int stat = merge + kCw * 8 * NB * LD * 4;
   static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
 };
 
 template <int D, int NB>
 __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
-  constexpr int R = 8 * NB, KW = D / 32, VW = D / 64, MB = D / 16;
+  constexpr int R = 8 * NB, KW = D / 32, MB = D / 16;
   using Sm = Smem<D, NB>;
   using W = Walker<R, kTk, kItem>;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -188,12 +181,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   ahead.walker = &ahead_sh[warp];
   ahead.more = true;
   ahead.open(a, it, warp, lane);
-  Block<D> buf0, buf1;
-  ahead.load(a, buf0, warp, lane);
-  if (ahead.more) ahead.load(a, buf1, warp, lane);
-  bool odd = false;      // the next block is in buf1
+  uint8_t* ring = sm + warp * kStages * Stage<D>::bytes;
+  uint32_t have = 0;     // a bit for each stage: its block has tokens
+  for (int i = 0; i < kStages; ++i) have |= (uint32_t)ahead.copy(a, ring + i * Stage<D>::bytes, warp, lane) << i;
+  int st = 0;
 
   const int g = lane >> 2, c = lane & 3;
+  const int tok0 = token_of(g), ta = token_of(2 * c), tb = token_of(2 * c + 1);   // this lane's key, its values
+  const uint32_t magic = a.magic;
   float* merge = reinterpret_cast<float*>(sm + Sm::merge);
   float2* stat = reinterpret_cast<float2*>(sm + Sm::stat);
   do {
@@ -263,27 +258,45 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
 #pragma unroll
       for (int k = 0; k < 2; ++k) m[nb][k] = kNone, l[nb][k] = 0.f;
     }
-    // the 16 tokens of a block that start at n0
-    auto step = [&](Block<D>& x, int n0) {
-      const bool live = x.have && n0 < it.hi && n0 + 16 > it.lo;
+    for (int t = it.from; t < it.to; ++t) {
+      const int n0 = t * kTk + 16 * warp;                          // the block's 16 tokens
+      const bool live = (have >> st & 1) != 0;
       const bool whole = n0 + 16 <= top_min && n0 >= bottom_max;   // every row sees all of them
-      // ---- S^T
-      float s[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+      uint8_t* x = ring + st * Stage<D>::bytes;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
       if (live) {
-        const __half2 kz[2] = {__low2half2(u2h(x.kp[0])), __low2half2(u2h(x.kp[1]))};
-        const __half2 ks[2] = {__high2half2(u2h(x.kp[0])), __high2half2(u2h(x.kp[1]))};
+        using St = Stage<D>;
+        // ---- S^T
+        float s[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+        uint32_t kw[2][KW];
+        __half2 ks[2], kz[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int row = 8 * b + tok0;
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(x + St::kcode + row * 64 + 16 * c);
+            kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(x + St::kcode + row * 32 + 8 * c);
+            kw[b][0] = u.x, kw[b][1] = u.y;
+          }
+          const __half2 par = *reinterpret_cast<const __half2*>(x + St::kpar + (row * St::G + c * St::G / 4) * 4);
+          kz[b] = __low2half2(par);
+          ks[b] = __high2half2(par);
+        }
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           uint32_t f[4], f2[4];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            f[b] = dq_lo(x.k[b][i], ks[b], kz[b]);
-            f[2 + b] = dq_hi(x.k[b][i], ks[b], kz[b]);
-            const uint32_t up = x.k[b][i] >> 8;
-            f2[b] = dq_lo(up, ks[b], kz[b]);
-            f2[2 + b] = dq_hi(up, ks[b], kz[b]);
+            f[b] = dq_lo(kw[b][i], ks[b], kz[b], magic);
+            f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b], magic);
+            const uint32_t up = kw[b][i] >> 8;
+            f2[b] = dq_lo(up, ks[b], kz[b], magic);
+            f2[2 + b] = dq_hi(up, ks[b], kz[b], magic);
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -291,14 +304,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
             mma(s[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
           }
         }
-        // ---- softmax: s[nb][2 b + k] is token 8 b + g, row 2 c + k
+        // ---- softmax: s[nb][2 b + k] is token 8 b + tok0, row 2 c + k
         uint32_t pf[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int n = n0 + 8 * (i >> 1) + g;
+              const int n = n0 + 8 * (i >> 1) + tok0;
               if (n < bottom[nb][i & 1] || n >= top[nb][i & 1]) s[nb][i] = -INFINITY;
             }
           }
@@ -329,48 +342,56 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
           pf[nb][0] = transpose8(h2u(__floats2half2_rn(p[0], p[1])));
           pf[nb][1] = transpose8(h2u(__floats2half2_rn(p[2], p[3])));
         }
-        // ---- O^T: tokens 2 c, 2 c + 1 of both blocks of 8
-        uint32_t f[MB][4];
+        // ---- O^T: tokens ta, tb (columns 2 c, 2 c + 1) of both blocks of 8
+        uint32_t v0[2][D / 64], v1[2][D / 64];
+        __half2 vz[2], vs[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          uint32_t p0 = x.vp[b][0], p1 = x.vp[b][1];
+          const int r0 = 8 * b + ta, r1 = 8 * b + tb;
+          if constexpr (D == 128) {
+            const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::vcode + r0 * 64 + 8 * g);
+            const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::vcode + r1 * 64 + 8 * g);
+            v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
+          } else {
+            v0[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r0 * 32 + 4 * g);
+            v1[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r1 * 32 + 4 * g);
+          }
+          uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
+          uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
           if (!whole) {
             // tokens outside the request: their bytes may be anything
-            const int n = n0 + 8 * b + 2 * c;
-            if (n < it.lo || n >= it.hi) p0 = 0;
-            if (n + 1 < it.lo || n + 1 >= it.hi) p1 = 0;
+            if (n0 + r0 < it.lo || n0 + r0 >= it.hi) p0 = 0;
+            if (n0 + r1 < it.lo || n0 + r1 >= it.hi) p1 = 0;
           }
-          const __half2 z = u2h(__byte_perm(p0, p1, 0x5410)), sc = u2h(__byte_perm(p0, p1, 0x7632));
-          // f[j][2 b]: channel row g, f[j][2 b + 1]: channel row g + 8 of block j
-#pragma unroll
-          for (int q = 0; q < VW; ++q)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              // byte y of both tokens into bytes 0 and 2
-              const uint32_t v = __byte_perm(x.v[b][0][q], x.v[b][1][q], y * 0x0011 + (4 + y) * 0x1100);
-              const uint32_t lo = dq_lo(v, sc, z), hi = dq_hi(v, sc, z);
-              if constexpr (D == 128) {
-                f[2 * y][2 * b + q] = lo;
-                f[2 * y + 1][2 * b + q] = hi;
-              } else {
-                f[(2 * y) & 3][2 * b + (y >> 1)] = lo;
-                f[(2 * y + 1) & 3][2 * b + (y >> 1)] = hi;
-              }
-            }
+          vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
+          vs[b] = u2h(__byte_perm(p0, p1, 0x7632));
         }
+        // two blocks j of 16 channels at a time: f[.][2 b] is channel row g,
+        // f[.][2 b + 1] row g + 8 (d = 128: of the two words; d = 64: of the
+        // two halves of the one)
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
+        for (int y = 0; y < MB / 2; ++y) {
+          uint32_t f[2][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma(o[nb][j], f[j], pf[nb][0], pf[nb][1]);
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              // byte y (or y + 2) of both tokens into bytes 0 and 2
+              const int word = D == 128 ? q : 0, byte = D == 128 ? y : y + 2 * q;
+              const uint32_t v = __byte_perm(v0[b][word], v1[b][word], byte * 0x0011 + (4 + byte) * 0x1100);
+              f[0][2 * b + q] = dq_lo(v, vs[b], vz[b], magic);
+              f[1][2 * b + q] = dq_hi(v, vs[b], vz[b], magic);
+            }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][0], pf[nb][1]);
+        }
       }
-      // the block's registers are free for the one after next
-      if (ahead.more) ahead.load(a, x, warp, lane);
-    };
-    for (int t = it.from; t < it.to; ++t) {
-      const int n0 = t * kTk + 16 * warp;
-      if (odd) step(buf1, n0);
-      else step(buf0, n0);
-      odd = !odd;
+      // the stage is read: the block kStages on takes it
+      __syncwarp();
+      have = (have & ~(1u << st)) | ((uint32_t)ahead.copy(a, x, warp, lane) << st);
+      if (++st == kStages) st = 0;
     }
     // ---- the warps' parts of the item meet
 #pragma unroll

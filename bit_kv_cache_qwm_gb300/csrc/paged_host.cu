@@ -212,6 +212,7 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.window = a->window >= (int64_t)a->max_blocks * a->page_tokens ? 0 : a->window;
   const float scale = a->scale > 0.f ? a->scale : 1.0f / sqrtf((float)d);
   x.scale_log2 = scale * 1.4426950408889634f;
+  x.magic = 0x64006400u;
   return cuda_status(k == 1 ? launch_attend_simt(x, d, a->dtype == QWM_BF16, max_rows, S(stream))
                      : k == 2 ? launch_attend_mma(x, d, max_rows, S(stream))
                               : launch_attend_tc(x, d, max_rows, S(stream)));

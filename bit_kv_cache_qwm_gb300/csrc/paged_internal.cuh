@@ -38,6 +38,7 @@ struct AttendArgs {
   int32_t requests, max_blocks;
   int32_t causal, window;
   float scale_log2;              // softmax scale * log2(e)
+  uint32_t magic;                // 1024 twice in float16
 };
 
 // A row of a partial result: O[d] unnormalised, running maximum (log2
