@@ -50,6 +50,12 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same from a zero sum
+__device__ __forceinline__ void mma0(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -81,18 +87,28 @@ struct Stage {
   static constexpr int kcode = 0, kpar = 8 * D, vcode = kpar + 64 * G, vpar = vcode + 8 * D, bytes = vpar + 64 * G;
   static constexpr int copies = (bytes / 16 + 31) / 32;   // of 16 bytes, a lane
 
-  // blk: the block of the page and head; at: the first token's slot
-  __device__ __forceinline__ static void copy(uint8_t* stage, const uint8_t* blk, int at, int page, int half, int lane) {
-    const uint8_t* codes = blk + at * (D / 2);
-    const uint8_t* pars = blk + page * (D / 2) + at * (4 * G);
+  // Where a lane's copies come from: byte cst + mul x (first token's slot) of
+  // the page's block, for 16-byte piece 32 k + lane of the stage.
+  struct Source {
+    int cst[copies], mul[copies];
+    __device__ __forceinline__ void init(int page, int half, int lane) {
 #pragma unroll
-    for (int k = 0; k < copies; ++k) {
-      const int i = 32 * k + lane, o = 16 * i;
-      const bool value = o >= vcode;
-      const int x = value ? o - vcode : o;
-      const uint8_t* src = (x < kpar ? codes + x : pars + (x - kpar)) + (value ? half : 0);
-      if (32 * k + 32 <= bytes / 16 || i < bytes / 16) cp_async16(stage + o, src);
+      for (int k = 0; k < copies; ++k) {
+        const int o = 16 * (32 * k + lane);
+        const bool value = o >= vcode;
+        const int x = value ? o - vcode : o;
+        const bool code = x < kpar;
+        cst[k] = (code ? x : page * (D / 2) + x - kpar) + (value ? half : 0);
+        mul[k] = code ? D / 2 : 4 * G;
+      }
     }
+  };
+  __device__ __forceinline__ static void copy(uint32_t stage, const uint8_t* blk, int at, const Source& src, int lane) {
+#pragma unroll
+    for (int k = 0; k < copies; ++k)
+      if (32 * k + 32 <= bytes / 16 || 32 * k + lane < bytes / 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage + 512 * k),
+                     "l"(blk + (uint32_t)(src.cst[k] + at * src.mul[k])) : "memory");
   }
 };
 
@@ -105,6 +121,8 @@ struct Ahead {
   int lo, hi, ids;
   const int32_t* row;
   const uint8_t* head;   // pool + the head's offset in a page
+  uint32_t page_bytes;   // of all heads
+  typename Stage<D>::Source src;
   bool more;
 
   __device__ __forceinline__ void fetch_ids(const AttendArgs& a, int warp, int lane) {
@@ -125,14 +143,13 @@ struct Ahead {
   }
   // Copies the next block into a stage (one commit group, also when there is
   // nothing to copy); returns whether the block has tokens.
-  __device__ __forceinline__ bool copy(const AttendArgs& a, uint8_t* stage, int warp, int lane) {
+  __device__ __forceinline__ bool copy(const AttendArgs& a, uint32_t stage, int warp, int lane) {
     bool have = false;
     if (more) {
       const int pg = __shfl_sync(0xffffffffu, ids, t - base);
       have = pg >= 0;
       if (have) {
-        const int n = t * kTk + 16 * warp;
-        Stage<D>::copy(stage, head + (int64_t)pg * a.kv_heads * a.block, n & (a.page - 1), a.page, a.block / 2, lane);
+        Stage<D>::copy(stage, head + (uint64_t)(uint32_t)pg * page_bytes, (t * kTk + 16 * warp) & (a.page - 1), src, lane);
       }
       // on to the next block; its id is on the way before it is asked for
       if (++t == to) {
@@ -180,10 +197,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   Ahead<D, W> ahead;
   ahead.walker = &ahead_sh[warp];
   ahead.more = true;
+  ahead.page_bytes = (uint32_t)(a.kv_heads * a.block);
+  ahead.src.init(a.page, a.block / 2, lane);
   ahead.open(a, it, warp, lane);
-  uint8_t* ring = sm + warp * kStages * Stage<D>::bytes;
+  // the warp's stages; copies of a lane start 16 bytes a lane into one
+  const uint8_t* ring = sm + warp * kStages * Stage<D>::bytes;
+  const uint32_t ring_at = su32(ring) + 16 * lane;
   uint32_t have = 0;     // a bit for each stage: its block has tokens
-  for (int i = 0; i < kStages; ++i) have |= (uint32_t)ahead.copy(a, ring + i * Stage<D>::bytes, warp, lane) << i;
+  for (int i = 0; i < kStages; ++i) have |= (uint32_t)ahead.copy(a, ring_at + i * Stage<D>::bytes, warp, lane) << i;
   int st = 0;
 
   const int g = lane >> 2, c = lane & 3;
@@ -262,15 +283,13 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
       const int n0 = t * kTk + 16 * warp;                          // the block's 16 tokens
       const bool live = (have >> st & 1) != 0;
       const bool whole = n0 + 16 <= top_min && n0 >= bottom_max;   // every row sees all of them
-      uint8_t* x = ring + st * Stage<D>::bytes;
+      const uint8_t* x = ring + st * Stage<D>::bytes;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
       if (live) {
         using St = Stage<D>;
         // ---- S^T
-        float s[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+        float s[NB][4], s2[NB][4];   // two sums: half the chain of dependent MMAs
         uint32_t kw[2][KW];
         __half2 ks[2], kz[2];
 #pragma unroll
@@ -300,10 +319,19 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            mma(s[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-            mma(s[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+            if (i == 0) {
+              mma0(s[nb], f, qf[nb][0][0], qf[nb][0][1]);
+              mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
+            } else {
+              mma(s[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+              mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+            }
           }
         }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nb][i] += s2[nb][i];
         // ---- softmax: s[nb][2 b + k] is token 8 b + tok0, row 2 c + k
         uint32_t pf[NB][2];
 #pragma unroll
@@ -390,7 +418,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
       }
       // the stage is read: the block kStages on takes it
       __syncwarp();
-      have = (have & ~(1u << st)) | ((uint32_t)ahead.copy(a, x, warp, lane) << st);
+      have = (have & ~(1u << st)) | ((uint32_t)ahead.copy(a, ring_at + st * Stage<D>::bytes, warp, lane) << st);
       if (++st == kStages) st = 0;
     }
     // ---- the warps' parts of the item meet

@@ -161,7 +161,7 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   if (!dim_ok(d) || shift < 0) return QWM_ERR_UNSUPPORTED;
   const int group = a->heads / a->kv_heads;
   // positions and the rows of one kv head's problem are kept in 32 bits
-  if (a->rows * group > kHalf || (int64_t)a->max_blocks * a->page_tokens > kHalf) return QWM_ERR_UNSUPPORTED;
+  if ((int64_t)a->kv_heads * block_bytes(d, a->page_tokens) > kInt || a->rows * group > kHalf || (int64_t)a->max_blocks * a->page_tokens > kHalf) return QWM_ERR_UNSUPPORTED;
   if (a->rows == 0 || a->requests == 0) return QWM_OK;
   const int e = esize(a->dtype);
   if (!rows_ok(a->q, a->rows, a->heads, d, e, false) || !rows_ok(a->out, a->rows, a->heads, d, e, true))
