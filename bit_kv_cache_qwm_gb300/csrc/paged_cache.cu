@@ -213,23 +213,15 @@ __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_
 
 // ---- append
 //
-// A thread takes 8 channels of one (row, head) of k or v (16 or 32 bytes in, 4
-// bytes of codes out), the 4 threads of a group of 32 channels find its range
-// by shuffles.  Bound by HBM: 2 or 4 bytes a channel in, 0.625 out (and 2 or 4
-// more for x_hat).
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
+// A thread takes 8 channels of one row and head, of k and of v (16 or 32 bytes
+// each, both loads in flight; 4 bytes of codes out); the 4 threads of a group
+// of 32 channels find its range by shuffles.  The definition divides once a
+// channel: the quotient is formed with the reciprocal instead, and where it
+// comes within 2^-14 of a tie between two codes, farther than its error of
+// 2^-18 (15 times three roundings), the thread divides after all, so the codes
+// are those of the definition.  Adding 1.5 2^23 rounds to the nearest even
+// integer and leaves the code in the low bits.  Bound by HBM: 2 or 4 bytes a
+// channel in, 0.625 out (and 2 or 4 more for x_hat).
 __device__ __forceinline__ void store8(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -245,76 +237,131 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
 }
 
 constexpr int kAppendNt = 256;
-constexpr float kClamp = 60000.f;
+constexpr float kClamp = 60000.f, kRound = 12582912.f;
 
-template <int D, class T>
-__global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged_append_args a, int shift) {
-  constexpr int L = D / 8, G = D / 32;
-  const int64_t i = (int64_t)blockIdx.x * kAppendNt + threadIdx.x;
-  const int wd = (int)(i % L);
-  const int64_t rh = i / L;
-  const bool live = rh < a.rows * a.kv_heads;
-  const int64_t t = live ? rh / a.kv_heads : 0;
-  const int h = (int)(live ? rh % a.kv_heads : 0);
-  const bool value = blockIdx.y != 0;
-  const qwm_rows in = value ? a.v : a.k, hat = value ? a.v_hat : a.k_hat;
-  int64_t slot = live ? a.slots[t] : -1;
-  uint32_t bits = 0;
-  if (slot >= (a.n_pages << shift)) {
-    bits = QWM_DEV_BOUNDS;
-    slot = -1;
+// 8 channels as loaded; large: one may be NaN or beyond the clamp
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p + 4));
   }
-  float x[8];
-  if (slot >= 0) {
-    load8((const T*)in.ptr + t * in.row_stride + h * in.head_stride + 8 * wd, x);
-  } else {
+  __device__ __forceinline__ bool get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
+    return m > 0x476a6000u;   // 60000
   }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ bool get(float* x) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (!(x[k] == x[k])) {
-      x[k] = 0.f;
-      bits |= QWM_DEV_NAN;
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      m = __vmaxu2(m, w[i] & 0x7fff7fffu);
     }
-    if (fabsf(x[k]) > kClamp) {
-      x[k] = copysignf(kClamp, x[k]);
-      bits |= QWM_DEV_SATURATED;
+    return max(m & 0xffffu, m >> 16) > 0x476au;   // 59904, the largest below 60000
+  }
+};
+
+// Quantises the thread's 8 channels x of its group; x becomes x_hat.  Whole
+// warps call this.
+__device__ __forceinline__ uint32_t quantise8(float* x, bool large, __half2* par, uint32_t* bits) {
+  if (large) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (!(x[k] == x[k])) {
+        x[k] = 0.f;
+        *bits |= QWM_DEV_NAN;
+      }
+      if (fabsf(x[k]) > kClamp) {
+        x[k] = copysignf(kClamp, x[k]);
+        *bits |= QWM_DEV_SATURATED;
+      }
     }
   }
-  float mn = x[0], mx = x[0];
-#pragma unroll
-  for (int k = 1; k < 8; ++k) mn = fminf(mn, x[k]), mx = fmaxf(mx, x[k]);
+  float mn = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   const __half zh = __float2half_rn(mn), sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+  *par = __halves2half2(zh, sh);
   const float z = __half2float(zh), s = __half2float(sh);
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;   // scale 0: every quotient and code 0
   uint32_t code = 0;
+  float far = 0.f;
+  float c[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    float c = 0.f;
-    if (s > 0.f) c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], z), s)), 0.f), 15.f);
-    code |= (uint32_t)c << (4 * k);
-    x[k] = fmaf(c, s, z);
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k], z), r), 0.f), 15.f), y = __fadd_rn(q, kRound);
+    c[k] = __fsub_rn(y, kRound);
+    far = fmaxf(far, fabsf(q - c[k]));
+    code |= (__float_as_uint(y) & 15u) << (4 * k);
   }
-  if (slot >= 0) {
-    const int64_t pg = slot >> shift;
-    const int at = (int)(slot & ((1 << shift) - 1)), page = 1 << shift;
-    uint8_t* half_block = (uint8_t*)a.pool + (pg * a.kv_heads + h) * (int64_t)block_bytes(D, page) +
-                          (value ? block_bytes(D, page) / 2 : 0);
-    *reinterpret_cast<uint32_t*>(half_block + at * (D / 2) + 4 * wd) = code;
-    if ((wd & 3) == 0)
-      *reinterpret_cast<__half2*>(half_block + page * (D / 2) + (at * G + wd / 4) * 4) = __halves2half2(zh, sh);
-  } else {
+  if (far > 0.5f - 6.1035e-5f) {
+    code = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+    for (int k = 0; k < 8; ++k) {
+      c[k] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], z), s)), 0.f), 15.f);
+      code |= (uint32_t)c[k] << (4 * k);
+    }
   }
-  if (hat.ptr && live) store8((T*)hat.ptr + t * hat.row_stride + h * hat.head_stride + 8 * wd, x);
-  bits = __reduce_or_sync(0xffffffffu, bits);
-  if (bits && (threadIdx.x & 31) == 0) flag(a.status, bits);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = fmaf(c[k], s, z);
+  return code;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged_append_args a, int shift, uint32_t heads_mul,
+                                                                 uint32_t heads_shift) {
+  constexpr int L = D / 8, G = D / 32;
+  const uint32_t unit = blockIdx.x * (kAppendNt / L) + threadIdx.x / L;
+  const int wd = threadIdx.x % L;
+  const bool live = unit < (uint32_t)(a.rows * a.kv_heads);
+  const uint32_t t = live ? (uint32_t)(((uint64_t)unit * heads_mul) >> heads_shift) : 0;
+  const int h = live ? (int)(unit - t * a.kv_heads) : 0;
+  int64_t slot = live ? __ldg(reinterpret_cast<const long long*>(a.slots) + t) : -1;
+  uint32_t bits = 0;
+  if (slot >= (a.n_pages << shift)) {
+    bits = QWM_DEV_BOUNDS;
+    slot = -1;
+  }
+  Raw8<T> raw[2];
+  if (slot >= 0) {
+    raw[0].load((const T*)a.k.ptr + t * a.k.row_stride + h * a.k.head_stride + 8 * wd);
+    raw[1].load((const T*)a.v.ptr + t * a.v.row_stride + h * a.v.head_stride + 8 * wd);
+  }
+  const int at = (int)(slot & ((1 << shift) - 1)), page = 1 << shift;
+  uint8_t* block = (uint8_t*)a.pool + ((slot >> shift) * a.kv_heads + h) * (int64_t)block_bytes(D, page);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    bool large = false;
+    if (slot >= 0) large = raw[half].get(x);
+    __half2 par;
+    const uint32_t code = quantise8(x, large, &par, &bits);
+    if (slot >= 0) {
+      uint8_t* dst = block + half * (block_bytes(D, page) / 2);
+      *reinterpret_cast<uint32_t*>(dst + at * (D / 2) + 4 * wd) = code;
+      if ((wd & 3) == 0) *reinterpret_cast<__half2*>(dst + page * (D / 2) + (at * G + wd / 4) * 4) = par;
+    }
+    const qwm_rows& hat = half ? a.v_hat : a.k_hat;
+    if (hat.ptr && live) store8((T*)hat.ptr + t * hat.row_stride + h * hat.head_stride + 8 * wd, x);
+  }
+  if (bits) flag(a.status, bits);
 }
 
 }  // namespace
@@ -344,12 +391,14 @@ cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStrea
 }
 
 cudaError_t launch_append(const qwm_paged_append_args& a, int shift, cudaStream_t st) {
-  const int64_t threads = a.rows * a.kv_heads * (a.head_dim / 8);
-  const dim3 grid((unsigned)((threads + kAppendNt - 1) / kAppendNt), 2, 1);
+  const int per = kAppendNt / (a.head_dim / 8);
+  const dim3 grid((unsigned)((a.rows * a.kv_heads + per - 1) / per), 1, 1);
+  uint32_t mul, by;
+  fast_division(a.kv_heads, &mul, &by);
   const bool bf = a.dtype == QWM_BF16;
   auto kern = a.head_dim == 64 ? (bf ? paged_append_kernel<64, __nv_bfloat16> : paged_append_kernel<64, float>)
                                : (bf ? paged_append_kernel<128, __nv_bfloat16> : paged_append_kernel<128, float>);
-  kern<<<grid, kAppendNt, 0, st>>>(a, shift);
+  kern<<<grid, kAppendNt, 0, st>>>(a, shift, mul, by);
   return cudaGetLastError();
 }
 

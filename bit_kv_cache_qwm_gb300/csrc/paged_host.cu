@@ -128,7 +128,7 @@ extern "C" qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* str
       (a->v_hat.ptr && !rows_ok(a->v_hat, a->rows, a->kv_heads, a->head_dim, e, true)))
     return QWM_ERR_INVALID_ARG;
   if (!a->pool || !aligned(a->pool, 16) || !a->slots || !aligned(a->slots, 8)) return QWM_ERR_INVALID_ARG;
-  if (a->rows * a->kv_heads > ((int64_t)1 << 34)) return QWM_ERR_UNSUPPORTED;   // the grid
+  if (a->rows * a->kv_heads > kInt) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_append");
   return cuda_status(launch_append(*a, shift, S(stream)));
@@ -161,7 +161,9 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   if (!dim_ok(d) || shift < 0) return QWM_ERR_UNSUPPORTED;
   const int group = a->heads / a->kv_heads;
   // positions and the rows of one kv head's problem are kept in 32 bits
-  if ((int64_t)a->kv_heads * block_bytes(d, a->page_tokens) > kInt || a->rows * group > kHalf || (int64_t)a->max_blocks * a->page_tokens > kHalf) return QWM_ERR_UNSUPPORTED;
+  if (a->rows * group > kHalf || (int64_t)a->max_blocks * a->page_tokens > kHalf ||
+      (int64_t)a->kv_heads * block_bytes(d, a->page_tokens) > kInt)
+    return QWM_ERR_UNSUPPORTED;
   if (a->rows == 0 || a->requests == 0) return QWM_OK;
   const int e = esize(a->dtype);
   if (!rows_ok(a->q, a->rows, a->heads, d, e, false) || !rows_ok(a->out, a->rows, a->heads, d, e, true))
@@ -197,11 +199,7 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.heads = a->heads;
   x.kv_heads = a->kv_heads;
   x.group = group;
-  // ceil(2^(31 + l) / group) with 2^l >= group is exact for every x < 2^31
-  int l = 0;
-  while ((1 << l) < group) ++l;
-  x.group_shift = 31 + l;
-  x.group_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + group - 1) / group);
+  fast_division(group, &x.group_mul, &x.group_shift);
   x.page = a->page_tokens;
   x.page_shift = shift;
   x.block = block_bytes(d, a->page_tokens);

@@ -15,6 +15,14 @@ constexpr int kMaxRequests = 8192;
 
 inline __host__ __device__ int block_bytes(int d, int page) { return page * (d + d / 4); }
 
+// x / d = x mul >> shift for every x < 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d
+inline void fast_division(int d, uint32_t* mul, uint32_t* shift) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  *shift = 31 + l;
+  *mul = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+}
+
 // What every attention kernel reads of a call.
 struct AttendArgs {
   const void* q;
