@@ -3,15 +3,20 @@
 //
 //   x' = x (mean(x^2) + eps)^(-1/2) w;   (a, b) -> (a cos - b sin, b cos + a sin)
 //
-// A warp takes one row and some or all of its heads: D/8 lanes hold a head, 8
-// channels each (16 bytes of bf16), 2 or 4 heads a step, four steps' loads in
-// flight.  A lane keeps its cos and sin for all heads of the row, so the table
-// is read once a row (a group of lanes for each head read it 16 times, more
-// bytes from L1 than the data: 64 us on the chunk below); its loads follow the
-// first heads' loads, which do not depend on the position.  The mean square is
-// a shuffle sum.  Pairs half the rotated width apart sit in lanes R/16 apart
-// and meet by one shuffle a channel; adjacent pairs sit in the same lane.
-// Bound by HBM: every element is read and written once.
+// A warp takes one row and some or all of its heads: D/8 lanes hold a head, 2
+// or 4 heads a step.  A rotating lane holds both channels of four pairs (two
+// pieces of four channels, rot/2 apart or, for adjacent pairs, side by side),
+// so no channel has to travel between lanes; the others hold eight channels
+// behind the rotated ones and turn by cos 1, sin 0.  A lane keeps four cos and
+// sin for all heads of the row, multiplied by the weight once for the queries
+// and once for the keys:
+//   out_a = inv (a (w_a c) - b (w_b s)),  out_b = inv (b (w_b c) + a (w_a s))
+// in two-wide float32 arithmetic; the mean square is a shuffle sum.  The table
+// is read once a row; its loads do not hold up the first heads' loads.
+// Bound by HBM (every element is read and written once) and, in bf16, by the
+// ~60 instructions of a step: with pairs in lanes apart (8 shuffles), per-head
+// addresses from the strides and scalar arithmetic a step took 215 and the
+// chunk below 34 us.
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
 
@@ -19,171 +24,180 @@ namespace qwm {
 namespace paged {
 namespace {
 
-constexpr int kRopeNt = 256;
+constexpr int kRopeNt = 128;
 
+// four channels as loaded
 template <class T>
-struct Vec8;
+struct Vec4;
 template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
-  }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+struct Vec4<float> {
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float2* x) const { x[0] = make_float2(u.x, u.y), x[1] = make_float2(u.z, u.w); }
+  __device__ __forceinline__ static void store(float* p, float2 a, float2 b) {
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
   }
 };
 template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+struct Vec4<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float2* x) const {
+    x[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    x[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, float2 a, float2 b) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(b.x, b.y);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
 };
-__device__ __forceinline__ void store8(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // steps whose loads are in flight together
 constexpr int kAhead = 4;
 
-template <int D, class T>
-__global__ void __launch_bounds__(kRopeNt) qk_norm_rope_kernel(const qwm_qk_norm_rope_args a, int splits, int per_split) {
+// ADJ: pairs are adjacent channels
+template <int D, bool ADJ, class T>
+__global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 8 : 6) qk_norm_rope_kernel(const qwm_qk_norm_rope_args a, int splits,
+                                                                                     int per_split) {
   constexpr int L = D / 8, PER = 32 / L;
   const int lane = threadIdx.x % L, sub = (threadIdx.x & 31) / L, heads = a.q_heads + a.k_heads;
   const int64_t unit = (int64_t)blockIdx.x * (kRopeNt / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / splits;
+  const int64_t t = splits == 1 ? unit : unit / splits;
   if (t >= a.rows) return;
   const int h0 = (int)(unit - t * splits) * per_split, h1 = min(heads, h0 + per_split);
-  const int half = a.rot / 2, ch = 8 * lane;
+  // this lane's two pieces of four channels
+  const int half = a.rot / 2;
+  const bool turned = 4 * lane < half;
+  const int o0 = ADJ || !turned ? 8 * lane : 4 * lane, o1 = ADJ || !turned ? o0 + 4 : o0 + half;
   // the row's positions: one negative or beyond the table leaves the row alone
   int pos[4] = {0, 0, 0, 0};
-  bool skip = false, out = false;
 #pragma unroll
   for (int x = 0; x < 4; ++x)
     if (x < a.axes) pos[x] = __ldg(a.positions + t * a.axes + x);
-  Vec8<T> v[kAhead];
-  auto load = [&](int hb) {
+  float2 co[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, si[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  bool first = true, dead = false;
+  auto run = [&](const qwm_rows& in, const qwm_rows& out, const T* weight, int n0, int n1) {
+    const T* src = (const T*)in.ptr + t * in.row_stride + (int64_t)(n0 + sub) * in.head_stride;
+    T* dst = (T*)out.ptr + t * out.row_stride + (int64_t)(n0 + sub) * out.head_stride;
+    const int64_t src_step = PER * in.head_stride, dst_step = PER * out.head_stride;
+    float2 ca[2], sa[2], cb[2], sb[2];   // w_a c, w_a s, w_b c, -w_b s
+    bool ready = false;
+    for (int n = n0; n < n1; n += kAhead * PER) {
+      Vec4<T> v[kAhead][2];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = hb + u * PER + sub;
-      if (h < h1) {
-        const bool key = h >= a.q_heads;
-        v[u].load((const T*)(key ? a.k.ptr : a.q.ptr) + t * (key ? a.k.row_stride : a.q.row_stride) +
-                  (key ? (h - a.q_heads) * a.k.head_stride : h * a.q.head_stride) + ch);
-      }
-    }
-  };
-  load(h0);
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (x < a.axes) {
-      skip |= pos[x] < 0;
-      out |= pos[x] >= a.n_positions;
-    }
-  if (skip || out) {
-    if (!skip && h0 == 0 && (threadIdx.x & 31) == 0) flag(a.status, QWM_DEV_BOUNDS);
-    return;
-  }
-  // the cos and sin of this lane's channels: 4 pairs (interleaved) or 8
-  const bool turned = ch < a.rot, low = ch < half;
-  float co[8], si[8];
-  if (turned) {
-    const int p0 = a.interleaved ? ch / 2 : low ? ch : ch - half;
-    const int e0 = a.sections[0], e1 = e0 + a.sections[1], e2 = e1 + a.sections[2];
-    auto axis = [&](int p) { return a.axes == 1 || p < e0 ? 0 : p < e1 ? 1 : p < e2 ? 2 : 3; };
-    auto row = [&](int x) {
-      return a.cos_sin + (int64_t)(x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3]) * a.rot;
-    };
-    const int last = a.interleaved ? 3 : 7, x0 = axis(p0);
-    if (x0 == axis(p0 + last)) {
-      // rot is a multiple of 16, so the vectors are aligned
-      const float* r = row(x0) + p0;
-      const float4 c0 = __ldg(reinterpret_cast<const float4*>(r)), s0 = __ldg(reinterpret_cast<const float4*>(r + half));
-      co[0] = c0.x, co[1] = c0.y, co[2] = c0.z, co[3] = c0.w, si[0] = s0.x, si[1] = s0.y, si[2] = s0.z, si[3] = s0.w;
-      if (!a.interleaved) {
-        const float4 c1 = __ldg(reinterpret_cast<const float4*>(r + 4)), s1 = __ldg(reinterpret_cast<const float4*>(r + half + 4));
-        co[4] = c1.x, co[5] = c1.y, co[6] = c1.z, co[7] = c1.w, si[4] = s1.x, si[5] = s1.y, si[6] = s1.z, si[7] = s1.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k <= last) {
-          const float* r = row(axis(p0 + k)) + p0 + k;
-          co[k] = __ldg(r);
-          si[k] = __ldg(r + half);
+      for (int u = 0; u < kAhead; ++u)
+        if (n + u * PER + sub < n1) {
+          v[u][0].load(src + u * src_step + o0);
+          v[u][1].load(src + u * src_step + o1);
         }
-    }
-  }
-  // lane of a pair's other half: half / 8 lanes away
-  const int mate = !turned ? lane : low ? lane + half / 8 : lane - half / 8;
-  const float sign = low ? -1.f : 1.f;
-  Vec8<T> wq, wk;
-  if (a.q_weight) wq.load((const T*)a.q_weight + ch);
-  if (a.k_weight && h1 > a.q_heads) wk.load((const T*)a.k_weight + ch);
-  for (int hb = h0; hb < h1; hb += kAhead * PER) {
-    if (hb > h0) load(hb);
+      if (first) {
+        first = false;
+        bool skip = false, over = false;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = hb + u * PER + sub;
-      if (hb + u * PER >= h1) break;   // the whole warp
-      const bool key = h >= a.q_heads;
-      float x[8], y[8];
-      v[u].get(x);
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-      for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
-      const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-      if (key ? a.k_weight : a.q_weight) {
-        if (key) wk.get(y);
-        else wq.get(y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= inv * y[k];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= inv;
-      }
-      if (a.interleaved) {
+        for (int x = 0; x < 4; ++x)
+          if (x < a.axes) {
+            skip |= pos[x] < 0;
+            over |= pos[x] >= a.n_positions;
+          }
+        if (skip || over) {
+          if (!skip && h0 == 0 && (threadIdx.x & 31) == 0) flag(a.status, QWM_DEV_BOUNDS);
+          dead = true;
+          return;
+        }
         if (turned) {
+          const int p0 = 4 * lane, e0 = a.sections[0], e1 = e0 + a.sections[1], e2 = e1 + a.sections[2];
+          auto axis = [&](int p) { return a.axes == 1 || p < e0 ? 0 : p < e1 ? 1 : p < e2 ? 2 : 3; };
+          auto row = [&](int x) {
+            return a.cos_sin + (int64_t)(x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3]) * a.rot;
+          };
+          const int x0 = axis(p0);
+          if (x0 == axis(p0 + 3)) {
+            // rot is a multiple of 16, so the vectors are aligned
+            const float* r = row(x0) + p0;
+            const float4 c = __ldg(reinterpret_cast<const float4*>(r)), z = __ldg(reinterpret_cast<const float4*>(r + half));
+            co[0] = make_float2(c.x, c.y), co[1] = make_float2(c.z, c.w);
+            si[0] = make_float2(z.x, z.y), si[1] = make_float2(z.z, z.w);
+          } else {
+            float c[4], z[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float p = x[2 * k], q = x[2 * k + 1];
-            x[2 * k] = p * co[k] - q * si[k];
-            x[2 * k + 1] = q * co[k] + p * si[k];
+            for (int k = 0; k < 4; ++k) {
+              const float* r = row(axis(p0 + k)) + p0 + k;
+              c[k] = __ldg(r);
+              z[k] = __ldg(r + half);
+            }
+            co[0] = make_float2(c[0], c[1]), co[1] = make_float2(c[2], c[3]);
+            si[0] = make_float2(z[0], z[1]), si[1] = make_float2(z[2], z[3]);
           }
         }
-      } else {
+      }
+      if (!ready) {
+        ready = true;
+        float2 w0[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, w1[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+        if (weight) {
+          Vec4<T> x;
+          x.load(weight + o0);
+          x.get(w0);
+          x.load(weight + o1);
+          x.get(w1);
+        }
+        if (ADJ) {
+          // pairs (x0, x1), (x2, x3) of both pieces: a = (0, 2 | 4, 6), b = (1, 3 | 5, 7)
+          const float2 p[2] = {w0[0], w0[1]}, q[2] = {w1[0], w1[1]};
+          w0[0] = make_float2(p[0].x, p[1].x), w0[1] = make_float2(q[0].x, q[1].x);
+          w1[0] = make_float2(p[0].y, p[1].y), w1[1] = make_float2(q[0].y, q[1].y);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, x[k], mate, L);
-        if (turned) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = fmaf(x[k], co[k], sign * (y[k] * si[k]));
+        for (int k = 0; k < 2; ++k) {
+          ca[k] = __fmul2_rn(w0[k], co[k]);
+          sa[k] = __fmul2_rn(w0[k], si[k]);
+          cb[k] = __fmul2_rn(w1[k], co[k]);
+          sb[k] = __fmul2_rn(make_float2(-w1[k].x, -w1[k].y), si[k]);
         }
       }
-      if (h < h1)
-        store8((T*)(key ? a.k_out.ptr : a.q_out.ptr) + t * (key ? a.k_out.row_stride : a.q_out.row_stride) +
-                   (key ? (h - a.q_heads) * a.k_out.head_stride : h * a.q_out.head_stride) + ch, x);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (n + u * PER >= n1) break;   // the whole warp
+        float2 x[2], y[2];
+        v[u][0].get(x);
+        v[u][1].get(y);
+        float2 s2 = __fmul2_rn(x[0], x[0]);
+        s2 = __ffma2_rn(x[1], x[1], s2);
+        s2 = __ffma2_rn(y[0], y[0], s2);
+        s2 = __ffma2_rn(y[1], y[1], s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
+        const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+        const float2 i2 = make_float2(inv, inv);
+        if (ADJ) {
+          const float2 p[2] = {x[0], x[1]}, q[2] = {y[0], y[1]};
+          x[0] = make_float2(p[0].x, p[1].x), x[1] = make_float2(q[0].x, q[1].x);
+          y[0] = make_float2(p[0].y, p[1].y), y[1] = make_float2(q[0].y, q[1].y);
+        }
+        float2 r[2], z[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          x[k] = __fmul2_rn(x[k], i2);
+          y[k] = __fmul2_rn(y[k], i2);
+          r[k] = __ffma2_rn(x[k], ca[k], __fmul2_rn(y[k], sb[k]));
+          z[k] = __ffma2_rn(y[k], cb[k], __fmul2_rn(x[k], sa[k]));
+        }
+        if (ADJ) {
+          const float2 p[2] = {r[0], r[1]}, q[2] = {z[0], z[1]};
+          r[0] = make_float2(p[0].x, q[0].x), r[1] = make_float2(p[0].y, q[0].y);
+          z[0] = make_float2(p[1].x, q[1].x), z[1] = make_float2(p[1].y, q[1].y);
+        }
+        if (n + u * PER + sub < n1) {
+          Vec4<T>::store(dst + u * dst_step + o0, r[0], r[1]);
+          Vec4<T>::store(dst + u * dst_step + o1, z[0], z[1]);
+        }
+      }
+      src += kAhead * src_step;
+      dst += kAhead * dst_step;
     }
-  }
+  };
+  if (h0 < a.q_heads) run(a.q, a.q_out, (const T*)a.q_weight, h0, min(h1, a.q_heads));
+  if (h1 > a.q_heads && !dead) run(a.k, a.k_out, (const T*)a.k_weight, max(h0, a.q_heads) - a.q_heads, h1 - a.q_heads);
 }
 
 }  // namespace
@@ -197,8 +211,11 @@ cudaError_t launch_qk_norm_rope(const qwm_qk_norm_rope_args& a, cudaStream_t st)
   const int splits = (heads + per - 1) / per;
   const dim3 grid((unsigned)((a.rows * splits + kRopeNt / 32 - 1) / (kRopeNt / 32)), 1, 1);
   const bool bf = a.dtype == QWM_BF16;
-  auto kern = a.head_dim == 64 ? (bf ? qk_norm_rope_kernel<64, __nv_bfloat16> : qk_norm_rope_kernel<64, float>)
-                               : (bf ? qk_norm_rope_kernel<128, __nv_bfloat16> : qk_norm_rope_kernel<128, float>);
+  auto kern = a.head_dim == 64
+                  ? (a.interleaved ? (bf ? qk_norm_rope_kernel<64, true, __nv_bfloat16> : qk_norm_rope_kernel<64, true, float>)
+                                   : (bf ? qk_norm_rope_kernel<64, false, __nv_bfloat16> : qk_norm_rope_kernel<64, false, float>))
+                  : (a.interleaved ? (bf ? qk_norm_rope_kernel<128, true, __nv_bfloat16> : qk_norm_rope_kernel<128, true, float>)
+                                   : (bf ? qk_norm_rope_kernel<128, false, __nv_bfloat16> : qk_norm_rope_kernel<128, false, float>));
   kern<<<grid, kRopeNt, 0, st>>>(a, splits, per);
   return cudaGetLastError();
 }
