@@ -215,22 +215,25 @@ __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_
 //
 // A thread takes 8 channels of one row and head, of k and of v (16 or 32 bytes
 // each, both loads in flight; 4 bytes of codes out); the 4 threads of a group
-// of 32 channels find its range by shuffles.  The definition divides once a
-// channel: the quotient is formed with the reciprocal instead, and where it
-// comes within 2^-14 of a tie between two codes, farther than its error of
-// 2^-18 (15 times three roundings), the thread divides after all, so the codes
-// are those of the definition.  Adding 1.5 2^23 rounds to the nearest even
-// integer and leaves the code in the low bits.  Bound by HBM: 2 or 4 bytes a
-// channel in, 0.625 out (and 2 or 4 more for x_hat).
-__device__ __forceinline__ void store8(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+// of 32 channels find its range by shuffles (bf16: minimum and negated maximum
+// in one register).  The definition divides once a channel: here the quotient
+// over 15 is formed with a reciprocal and saturated to [0, 1], which is the
+// clamp; where 15 times it comes within 2^-14 of a tie between two codes,
+// farther than its error of 2^-17 (15 times four roundings and the
+// reciprocal's), the thread divides after all, so the codes are those of the
+// definition.  Adding 1.5 2^23 rounds to the nearest even integer and leaves
+// the code in the low bits.  Bound by HBM (2 or 4 bytes a channel in, 0.625
+// out, 2 or 4 more for x_hat) and by the instructions: one division a channel
+// made 71 us of the chunk below, scalar clamps and ranges 35 us.
+__device__ __forceinline__ void store8(float* p, const float2* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -239,7 +242,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
 constexpr int kAppendNt = 256;
 constexpr float kClamp = 60000.f, kRound = 12582912.f;
 
-// 8 channels as loaded; large: one may be NaN or beyond the clamp
+// 8 channels as loaded, and the range of the group's 32 (4 lanes): mn, mx,
+// NaN when a channel is NaN
 template <class T>
 struct Raw8;
 template <>
@@ -249,78 +253,125 @@ struct Raw8<float> {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p + 4));
   }
-  __device__ __forceinline__ bool get(float* x) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    uint32_t m = 0;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float2* x) const {
+    x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w), x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
+  }
+  __device__ __forceinline__ static float min_nan(float x, float y) {
+    float z;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+  }
+  __device__ __forceinline__ static float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+  }
+  __device__ __forceinline__ void range(float* mn, float* mx) const {
+    float l = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
+    float h = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
-    return m > 0x476a6000u;   // 60000
+    for (int o = 1; o < 4; o <<= 1) {
+      l = min_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+      h = max_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
+    }
+    *mn = l, *mx = h;
   }
 };
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ bool get(float* x) const {
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float2* x) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    }
-    return max(m & 0xffffu, m >> 16) > 0x476au;   // 59904, the largest below 60000
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ void range(float* mn, float* mx) const {
+    auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    __nv_bfloat162 l = __hmin2_nan(__hmin2_nan(b(u.x), b(u.y)), __hmin2_nan(b(u.z), b(u.w)));
+    const __nv_bfloat162 h = __hmax2_nan(__hmax2_nan(b(u.x), b(u.y)), __hmax2_nan(b(u.z), b(u.w)));
+    // (minimum, -maximum): one minimum serves both
+    l = __halves2bfloat162(__hmin_nan(__low2bfloat16(l), __high2bfloat16(l)),
+                           __hneg(__hmax_nan(__low2bfloat16(h), __high2bfloat16(h))));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) l = __hmin2_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+    *mn = __low2float(l), *mx = -__high2float(l);
   }
 };
 
-// Quantises the thread's 8 channels x of its group; x becomes x_hat.  Whole
+// Quantises the thread's 8 channels of its group; x receives x_hat.  Whole
 // warps call this.
-__device__ __forceinline__ uint32_t quantise8(float* x, bool large, __half2* par, uint32_t* bits) {
-  if (large) {
+template <class T>
+__device__ __forceinline__ uint32_t quantise8(const Raw8<T>& raw, float2* x, __half2* par, uint32_t* bits) {
+  float mn, mx;
+  raw.range(&mn, &mx);
+  raw.get(x);
+  // NaN, infinite or beyond the clamp: the group starts again from mended channels
+  if (__any_sync(0xffffffffu, !(mn >= -kClamp && mx <= kClamp))) {
+    float lo = kClamp, hi = -kClamp;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (!(x[k] == x[k])) {
-        x[k] = 0.f;
+      float& v = (k & 1) ? x[k >> 1].y : x[k >> 1].x;
+      if (!(v == v)) {
+        v = 0.f;
         *bits |= QWM_DEV_NAN;
       }
-      if (fabsf(x[k]) > kClamp) {
-        x[k] = copysignf(kClamp, x[k]);
+      if (fabsf(v) > kClamp) {
+        v = copysignf(kClamp, v);
         *bits |= QWM_DEV_SATURATED;
       }
+      lo = fminf(lo, v), hi = fmaxf(hi, v);
     }
-  }
-  float mn = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 1; o < 4; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    mn = lo, mx = hi;
   }
   const __half zh = __float2half_rn(mn), sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
   *par = __halves2half2(zh, sh);
   const float z = __half2float(zh), s = __half2float(sh);
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;   // scale 0: every quotient and code 0
-  uint32_t code = 0;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = s > 0.f ? r * (1.0f / 15.0f) : 0.f;   // scale 0: every quotient and code 0
+  const float2 z2 = make_float2(-z, -z), k15 = make_float2(15.f, 15.f), round2 = make_float2(kRound, kRound);
+  const float2 back2 = make_float2(-kRound, -kRound), s2 = make_float2(s, s), zz = make_float2(z, z);
+  float2 c[4];
+  uint32_t y[8];
   float far = 0.f;
-  float c[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k], z), r), 0.f), 15.f), y = __fadd_rn(q, kRound);
-    c[k] = __fsub_rn(y, kRound);
-    far = fmaxf(far, fabsf(q - c[k]));
-    code |= (__float_as_uint(y) & 15u) << (4 * k);
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = __fadd2_rn(x[k], z2);
+    const float2 q = make_float2(__saturatef(t.x * r), __saturatef(t.y * r));
+    const float2 v = __ffma2_rn(q, k15, round2);
+    c[k] = __fadd2_rn(v, back2);
+    const float2 d = __ffma2_rn(q, k15, make_float2(-c[k].x, -c[k].y));
+    far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+    y[2 * k] = __float_as_uint(v.x), y[2 * k + 1] = __float_as_uint(v.y);
   }
+  // y = bits of 1.5 2^23 + code: their sum with weights 16^k, less the constant's
+  uint32_t code = y[7];
+#pragma unroll
+  for (int k = 6; k >= 0; --k) code = (code << 4) + y[k];
+  code -= 0x4b400000u;   // 16^k 0x4b400000 leaves 32 bits for k >= 3; those of k = 1, 2 are:
+  code -= 0xb4000000u;
+  code -= 0x40000000u;
   if (far > 0.5f - 6.1035e-5f) {
     code = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      c[k] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[k], z), s)), 0.f), 15.f);
-      code |= (uint32_t)c[k] << (4 * k);
+      const float v = (k & 1) ? x[k >> 1].y : x[k >> 1].x;
+      const float e = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, z), s)), 0.f), 15.f);
+      if (k & 1) c[k >> 1].y = e;
+      else c[k >> 1].x = e;
+      code |= (uint32_t)e << (4 * k);
     }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = fmaf(c[k], s, z);
+  for (int k = 0; k < 4; ++k) x[k] = __ffma2_rn(c[k], s2, zz);
   return code;
 }
 
@@ -340,6 +391,8 @@ __global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged
     slot = -1;
   }
   Raw8<T> raw[2];
+  raw[0].zero();
+  raw[1].zero();
   if (slot >= 0) {
     raw[0].load((const T*)a.k.ptr + t * a.k.row_stride + h * a.k.head_stride + 8 * wd);
     raw[1].load((const T*)a.v.ptr + t * a.v.row_stride + h * a.v.head_stride + 8 * wd);
@@ -348,11 +401,9 @@ __global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged
   uint8_t* block = (uint8_t*)a.pool + ((slot >> shift) * a.kv_heads + h) * (int64_t)block_bytes(D, page);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    bool large = false;
-    if (slot >= 0) large = raw[half].get(x);
+    float2 x[4];
     __half2 par;
-    const uint32_t code = quantise8(x, large, &par, &bits);
+    const uint32_t code = quantise8(raw[half], x, &par, &bits);   // a row without a slot: zeros
     if (slot >= 0) {
       uint8_t* dst = block + half * (block_bytes(D, page) / 2);
       *reinterpret_cast<uint32_t*>(dst + at * (D / 2) + 4 * wd) = code;

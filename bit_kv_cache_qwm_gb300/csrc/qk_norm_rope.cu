@@ -53,11 +53,11 @@ struct Vec4<__nv_bfloat16> {
 };
 
 // steps whose loads are in flight together
-constexpr int kAhead = 4;
+constexpr int kAhead = 3;
 
 // ADJ: pairs are adjacent channels
 template <int D, bool ADJ, class T>
-__global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 8 : 6) qk_norm_rope_kernel(const qwm_qk_norm_rope_args a, int splits,
+__global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_kernel(const qwm_qk_norm_rope_args a, int splits,
                                                                                      int per_split) {
   constexpr int L = D / 8, PER = 32 / L;
   const int lane = threadIdx.x % L, sub = (threadIdx.x & 31) / L, heads = a.q_heads + a.k_heads;
