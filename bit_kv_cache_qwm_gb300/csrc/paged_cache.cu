@@ -54,19 +54,20 @@ __device__ __forceinline__ int find(const int32_t* first, int n, int i) {
   return lo;
 }
 
-// Every CTA of the cluster scans the lengths for itself (a few loads a
-// thread), the cluster meets once all have read what the outputs may
-// overwrite (kv_len_out = kv_len), then all write rows and table entries.
-// The prefix sums stay in shared memory: a row finds its request by bisection.
-__global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_plan_args a, int shift) {
+// Every CTA scans the lengths for itself (a few loads a thread), then all
+// write rows and table entries, CTA 0 the rest.  Where an output is an input
+// (kv_len_out = kv_len) the CTAs are one cluster that meets once all have read
+// it; otherwise nothing joins them and there is one for every 1024 rows.  The
+// prefix sums stay in shared memory: a row finds its request by bisection.
+// Bound by latency: the loads of the lengths, the scan, the page ids.
+__global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_plan_args a, int shift, bool in_place) {
   extern __shared__ int32_t plan_sm[];
   int32_t* row_of = plan_sm;                 // first row of each request
   int32_t* page_of = row_of + a.requests;    // first new page
   int32_t* len_of = page_of + a.requests;    // cached tokens
   __shared__ int32_t count_sh;
   __shared__ int bad_sh, full_sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) bad_sh = full_sh = 0, count_sh = *a.free_count;
   __syncthreads();
   int64_t rows = 0, pages = 0;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_pla
   const int count = count_sh;
   const bool bad = bad_sh != 0 || count < 0 || count > a.n_pages;
   const bool ok = !bad && !full_sh && rows <= a.rows && pages <= count;
-  if (ctas > 1) cluster.sync();
+  if (in_place && ctas > 1) cg::this_cluster().sync();
   else __syncthreads();
   if (rank == 0) {
     for (int b = tid; b < a.requests; b += kPlanNt) {
@@ -213,18 +214,21 @@ __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_
 
 // ---- append
 //
-// A thread takes 8 channels of one row and head, of k and of v (16 or 32 bytes
-// each, both loads in flight; 4 bytes of codes out); the 4 threads of a group
-// of 32 channels find its range by shuffles (bf16: minimum and negated maximum
-// in one register).  The definition divides once a channel: here the quotient
-// over 15 is formed with a reciprocal and saturated to [0, 1], which is the
-// clamp; where 15 times it comes within 2^-14 of a tie between two codes,
-// farther than its error of 2^-17 (15 times four roundings and the
+// A thread takes 16 channels of one row and head, of k and then of v (32 or 64
+// bytes each, loaded together; 8 bytes of codes out); the 2 threads of a group
+// of 32 channels share its range by a shuffle (bf16: minimum and negated
+// maximum in one register).  The definition divides once a channel: here the
+// quotient over 15 is formed with a reciprocal and saturated to [0, 1], which
+// is the clamp; where 15 times it comes within 2^-14 of a tie between two
+// codes, farther than its error of 2^-17 (15 times four roundings and the
 // reciprocal's), the thread divides after all, so the codes are those of the
 // definition.  Adding 1.5 2^23 rounds to the nearest even integer and leaves
-// the code in the low bits.  Bound by HBM (2 or 4 bytes a channel in, 0.625
-// out, 2 or 4 more for x_hat) and by the instructions: one division a channel
-// made 71 us of the chunk below, scalar clamps and ranges 35 us.
+// the code in the low bits.  A group's range over 15 is Markstein's corrected
+// quotient (IBM J. Res. Dev. 34, 1990): q = R c, q + (R - 15 q) c with
+// c = f32(1/15) and fused multiply-adds, the correctly rounded R / 15.
+// Bound by HBM (2 or 4 bytes a channel in, 0.625 out, 2 or 4 more for x_hat)
+// and by the instructions: a division a channel made 71 us of the chunk below,
+// 8 channels a thread with scalar ranges 35 us.
 __device__ __forceinline__ void store8(float* p, const float2* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
@@ -239,23 +243,27 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float2* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kAppendNt = 256;
+constexpr int kAppendNt = 128, kAppendCtas = 8, kCh = 16;
 constexpr float kClamp = 60000.f, kRound = 12582912.f;
 
-// 8 channels as loaded, and the range of the group's 32 (4 lanes): mn, mx,
-// NaN when a channel is NaN
+// kCh channels as loaded, and the range of the group's 32 (2 lanes): NaN when
+// a channel is NaN
 template <class T>
-struct Raw8;
+struct Raw;
 template <>
-struct Raw8<float> {
-  float4 a, b;
+struct Raw<float> {
+  float4 u[4];
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p + 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   __device__ __forceinline__ void get(float2* x) const {
-    x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w), x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = make_float2(u[i].x, u[i].y), x[2 * i + 1] = make_float2(u[i].z, u[i].w);
   }
   __device__ __forceinline__ static float min_nan(float x, float y) {
     float z;
@@ -268,43 +276,47 @@ struct Raw8<float> {
     return z;
   }
   __device__ __forceinline__ void range(float* mn, float* mx) const {
-    float l = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
-    float h = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+    float l = u[0].x, h = u[0].x;
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      l = min_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
-      h = max_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
+    for (int i = 0; i < 4; ++i) {
+      l = min_nan(l, min_nan(min_nan(u[i].x, u[i].y), min_nan(u[i].z, u[i].w)));
+      h = max_nan(h, max_nan(max_nan(u[i].x, u[i].y), max_nan(u[i].z, u[i].w)));
     }
-    *mn = l, *mx = h;
+    *mn = min_nan(l, __shfl_xor_sync(0xffffffffu, l, 1));
+    *mx = max_nan(h, __shfl_xor_sync(0xffffffffu, h, 1));
   }
 };
 template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+struct Raw<__nv_bfloat16> {
+  uint4 u[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float2* x) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   __device__ __forceinline__ void range(float* mn, float* mx) const {
     auto b = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    __nv_bfloat162 l = __hmin2_nan(__hmin2_nan(b(u.x), b(u.y)), __hmin2_nan(b(u.z), b(u.w)));
-    const __nv_bfloat162 h = __hmax2_nan(__hmax2_nan(b(u.x), b(u.y)), __hmax2_nan(b(u.z), b(u.w)));
+    __nv_bfloat162 l = b(u[0].x), h = l;
+    const uint32_t w[7] = {u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) l = __hmin2_nan(l, b(w[i])), h = __hmax2_nan(h, b(w[i]));
     // (minimum, -maximum): one minimum serves both
     l = __halves2bfloat162(__hmin_nan(__low2bfloat16(l), __high2bfloat16(l)),
                            __hneg(__hmax_nan(__low2bfloat16(h), __high2bfloat16(h))));
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) l = __hmin2_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+    l = __hmin2_nan(l, __shfl_xor_sync(0xffffffffu, l, 1));
     *mn = __low2float(l), *mx = -__high2float(l);
   }
 };
 
-// Quantises the thread's 8 channels of its group; x receives x_hat.  Whole
-// warps call this.
+// Quantises the thread's channels of its group; x receives x_hat.  Whole warps
+// call this.
 template <class T>
-__device__ __forceinline__ uint32_t quantise8(const Raw8<T>& raw, float2* x, __half2* par, uint32_t* bits) {
+__device__ __forceinline__ uint2 quantise(const Raw<T>& raw, float2* x, __half2* par, uint32_t* bits) {
   float mn, mx;
   raw.range(&mn, &mx);
   raw.get(x);
@@ -312,7 +324,7 @@ __device__ __forceinline__ uint32_t quantise8(const Raw8<T>& raw, float2* x, __h
   if (__any_sync(0xffffffffu, !(mn >= -kClamp && mx <= kClamp))) {
     float lo = kClamp, hi = -kClamp;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kCh; ++k) {
       float& v = (k & 1) ? x[k >> 1].y : x[k >> 1].x;
       if (!(v == v)) {
         v = 0.f;
@@ -324,93 +336,92 @@ __device__ __forceinline__ uint32_t quantise8(const Raw8<T>& raw, float2* x, __h
       }
       lo = fminf(lo, v), hi = fmaxf(hi, v);
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    mn = lo, mx = hi;
+    mn = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    mx = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
   }
-  const __half zh = __float2half_rn(mn), sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
+  constexpr float k15th = 1.0f / 15.0f;
+  const float span = __fsub_rn(mx, mn), part = __fmul_rn(span, k15th);
+  const __half zh = __float2half_rn(mn), sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, part, span), k15th, part));
   *par = __halves2half2(zh, sh);
   const float z = __half2float(zh), s = __half2float(sh);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  r = s > 0.f ? r * (1.0f / 15.0f) : 0.f;   // scale 0: every quotient and code 0
+  r = s > 0.f ? r * k15th : 0.f;   // scale 0: every quotient and code 0
   const float2 z2 = make_float2(-z, -z), k15 = make_float2(15.f, 15.f), round2 = make_float2(kRound, kRound);
-  const float2 back2 = make_float2(-kRound, -kRound), s2 = make_float2(s, s), zz = make_float2(z, z);
-  float2 c[4];
-  uint32_t y[8];
+  const float2 minus2 = make_float2(-1.f, -1.f), s2 = make_float2(-s, -s), zz = make_float2(z, z);
+  float2 c[kCh / 2];   // minus the codes
+  uint32_t y[kCh];
   float far = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kCh / 2; ++k) {
     const float2 t = __fadd2_rn(x[k], z2);
     const float2 q = make_float2(__saturatef(t.x * r), __saturatef(t.y * r));
     const float2 v = __ffma2_rn(q, k15, round2);
-    c[k] = __fadd2_rn(v, back2);
-    const float2 d = __ffma2_rn(q, k15, make_float2(-c[k].x, -c[k].y));
+    c[k] = __ffma2_rn(v, minus2, round2);
+    const float2 d = __ffma2_rn(q, k15, c[k]);
     far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
     y[2 * k] = __float_as_uint(v.x), y[2 * k + 1] = __float_as_uint(v.y);
   }
-  // y = bits of 1.5 2^23 + code: their sum with weights 16^k, less the constant's
-  uint32_t code = y[7];
+  // y = bits of 1.5 2^23 + code, 0x4b400000 + code: their sums with weights
+  // 16^k, less that of the constant
+  uint2 code = make_uint2(y[7], y[15]);
 #pragma unroll
-  for (int k = 6; k >= 0; --k) code = (code << 4) + y[k];
-  code -= 0x4b400000u;   // 16^k 0x4b400000 leaves 32 bits for k >= 3; those of k = 1, 2 are:
-  code -= 0xb4000000u;
-  code -= 0x40000000u;
+  for (int k = 6; k >= 0; --k) code.x = (code.x << 4) + y[k], code.y = (code.y << 4) + y[8 + k];
+  code.x -= 0x3f400000u, code.y -= 0x3f400000u;
   if (far > 0.5f - 6.1035e-5f) {
-    code = 0;
+    code = make_uint2(0, 0);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kCh; ++k) {
       const float v = (k & 1) ? x[k >> 1].y : x[k >> 1].x;
       const float e = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, z), s)), 0.f), 15.f);
-      if (k & 1) c[k >> 1].y = e;
-      else c[k >> 1].x = e;
-      code |= (uint32_t)e << (4 * k);
+      if (k & 1) c[k >> 1].y = -e;
+      else c[k >> 1].x = -e;
+      (k < 8 ? code.x : code.y) |= (uint32_t)e << (4 * (k & 7));
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = __ffma2_rn(c[k], s2, zz);
+  for (int k = 0; k < kCh / 2; ++k) x[k] = __ffma2_rn(c[k], s2, zz);
   return code;
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged_append_args a, int shift, uint32_t heads_mul,
+__global__ void __launch_bounds__(kAppendNt, kAppendCtas) paged_append_kernel(const qwm_paged_append_args a, int shift, uint32_t heads_mul,
                                                                  uint32_t heads_shift) {
-  constexpr int L = D / 8, G = D / 32;
+  constexpr int L = D / kCh, G = D / 32;
   const uint32_t unit = blockIdx.x * (kAppendNt / L) + threadIdx.x / L;
-  const int wd = threadIdx.x % L;
+  const int wd = threadIdx.x % L, page = 1 << shift;
   const bool live = unit < (uint32_t)(a.rows * a.kv_heads);
   const uint32_t t = live ? (uint32_t)(((uint64_t)unit * heads_mul) >> heads_shift) : 0;
   const int h = live ? (int)(unit - t * a.kv_heads) : 0;
+  // the channels do not wait for the slot: every row may be read
+  Raw<T> raw[2];
+  raw[0].load((const T*)a.k.ptr + t * a.k.row_stride + h * a.k.head_stride + kCh * wd);
+  raw[1].load((const T*)a.v.ptr + t * a.v.row_stride + h * a.v.head_stride + kCh * wd);
   int64_t slot = live ? __ldg(reinterpret_cast<const long long*>(a.slots) + t) : -1;
   uint32_t bits = 0;
   if (slot >= (a.n_pages << shift)) {
     bits = QWM_DEV_BOUNDS;
     slot = -1;
   }
-  Raw8<T> raw[2];
-  raw[0].zero();
-  raw[1].zero();
-  if (slot >= 0) {
-    raw[0].load((const T*)a.k.ptr + t * a.k.row_stride + h * a.k.head_stride + 8 * wd);
-    raw[1].load((const T*)a.v.ptr + t * a.v.row_stride + h * a.v.head_stride + 8 * wd);
-  }
-  const int at = (int)(slot & ((1 << shift) - 1)), page = 1 << shift;
+  if (slot < 0) raw[0].zero(), raw[1].zero();   // a row without a slot: zeros
+  const int at = (int)(slot & (page - 1));
   uint8_t* block = (uint8_t*)a.pool + ((slot >> shift) * a.kv_heads + h) * (int64_t)block_bytes(D, page);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float2 x[4];
+    float2 x[kCh / 2];
     __half2 par;
-    const uint32_t code = quantise8(raw[half], x, &par, &bits);   // a row without a slot: zeros
+    const uint2 code = quantise(raw[half], x, &par, &bits);
     if (slot >= 0) {
       uint8_t* dst = block + half * (block_bytes(D, page) / 2);
-      *reinterpret_cast<uint32_t*>(dst + at * (D / 2) + 4 * wd) = code;
-      if ((wd & 3) == 0) *reinterpret_cast<__half2*>(dst + page * (D / 2) + (at * G + wd / 4) * 4) = par;
+      *reinterpret_cast<uint2*>(dst + at * (D / 2) + 8 * wd) = code;
+      if ((wd & 1) == 0) *reinterpret_cast<__half2*>(dst + page * (D / 2) + (at * G + wd / 2) * 4) = par;
     }
     const qwm_rows& hat = half ? a.v_hat : a.k_hat;
-    if (hat.ptr && live) store8((T*)hat.ptr + t * hat.row_stride + h * hat.head_stride + 8 * wd, x);
+    if (hat.ptr && live) {
+      T* p = (T*)hat.ptr + t * hat.row_stride + h * hat.head_stride + kCh * wd;
+      store8(p, x);
+      store8(p + 8, x + 4);
+    }
   }
   if (bits) flag(a.status, bits);
 }
@@ -419,8 +430,9 @@ __global__ void __launch_bounds__(kAppendNt) paged_append_kernel(const qwm_paged
 
 cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st) {
   static SmemLimit limit;
-  // one CTA writes ~1024 rows a microsecond
-  const unsigned ctas = a.rows <= 4096 ? 1 : 8;
+  const bool in_place = a.kv_len_out == a.kv_len || a.free_count_out == a.free_count;
+  const int64_t want = (a.rows + kPlanNt - 1) / kPlanNt, most = in_place ? 8 : 2 * sm_count();
+  const unsigned ctas = (unsigned)(want < 1 ? 1 : want < most ? want : most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kPlanNt, 1, 1);
@@ -431,9 +443,9 @@ cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return a.requests * 12 <= 48 * 1024 ? cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift)
-                                      : launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift);
+  cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
+  return a.requests * 12 <= 48 * 1024 ? cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift, in_place)
+                                      : launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift, in_place);
 }
 
 cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {
@@ -442,7 +454,7 @@ cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStrea
 }
 
 cudaError_t launch_append(const qwm_paged_append_args& a, int shift, cudaStream_t st) {
-  const int per = kAppendNt / (a.head_dim / 8);
+  const int per = kAppendNt / (a.head_dim / kCh);
   const dim3 grid((unsigned)((a.rows * a.kv_heads + per - 1) / per), 1, 1);
   uint32_t mul, by;
   fast_division(a.kv_heads, &mul, &by);
