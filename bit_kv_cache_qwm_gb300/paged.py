@@ -55,9 +55,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _run(fn, args: bytes, what: str, dev: torch.device):
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -153,23 +156,28 @@ def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     dev, dt = q.device, q.dtype
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=dt, device=dev)
-    qo = _rows(q_out, "q_out", q, q.shape)
+        qo = (q_out.data_ptr(), hq * d, d)
+    else:
+        qo = _rows(q_out, "q_out", q, q.shape)
     hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
         kr = _rows(k, "k", q)
-        hk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != d:
+        tk, hk, dk = k.shape
+        if tk != T or dk != d:
             raise ValueError(f"k: expected [{T}, kv_heads, {d}], got {tuple(k.shape)}")
         if k_out is None:
             k_out = torch.empty((T, hk, d), dtype=dt, device=dev)
-        ko = _rows(k_out, "k_out", k, k.shape)
+            ko = (k_out.data_ptr(), hk * d, d)
+        else:
+            ko = _rows(k_out, "k_out", k, k.shape)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out, k_weight: given without k")
     table = _array(cos_sin, "cos_sin", torch.float32, (None, None), dev)
     n_pos, rot = cos_sin.shape
-    axes = positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 1
-    pos = _array(positions, "positions", torch.int32, (T,) if axes == 1 and positions.dim() == 1 else (T, axes), dev)
-    if not 1 <= axes <= 4:
+    axes = positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
+    pos = _array(positions, "positions", torch.int32, (T, axes) if axes else (T,), dev)
+    axes = axes or 1
+    if axes > 4:
         raise ValueError("positions: 1 to 4 axes")
     if sections is None:
         if axes > 1:
@@ -265,14 +273,13 @@ def qwm_paged_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, slots
                       T, pool.shape[0], _DTYPES[k.dtype], d, hk, page), "qwm_paged_append", dev)
 
 
-def _workspace(dev: torch.device, d: int) -> torch.Tensor:
-    n = _workspace_bytes.get((dev, d))
-    if n is None:
-        with torch.cuda.device(dev):
-            n = _workspace_bytes[dev, d] = int(lib().qwm_paged_attend_workspace_bytes(d))
-        if n == 0:
-            raise ValueError(f"head_dim 64 or 128 is built, not {d}")
-    return torch.empty(n, dtype=torch.uint8, device=dev)
+def _workspace_size(dev: torch.device, d: int) -> int:
+    with torch.cuda.device(dev):
+        n = int(lib().qwm_paged_attend_workspace_bytes(d))
+    if n == 0:
+        raise ValueError(f"head_dim 64 or 128 is built, not {d}")
+    _workspace_bytes[dev, d] = n
+    return n
 
 
 def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -289,22 +296,25 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     T, hq, d = q.shape
     dev = q.device
     page = _page_tokens(pool, d)
-    hk = pool.shape[1]
+    n_pages, hk, _ = pool.shape
     if pool.device != dev or hk < 1 or hq % hk:
         raise ValueError(f"pool: kv heads that divide {hq} on {dev} are expected, got {tuple(pool.shape)} on {pool.device}")
     if out is None:
         out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
-    ot = _rows(out, "out", q, q.shape)
+        ot = (out.data_ptr(), hq * d, d)
+    else:
+        ot = _rows(out, "out", q, q.shape)
     table = _array(block_table, "block_table", torch.int32, (None, None), dev)
-    B = block_table.shape[0]
+    B, width = block_table.shape
     lens = _array(kv_len, "kv_len", torch.int32, (B,), dev)
     cu = _array(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
     ls = 0 if lse is None else _array(lse, "lse", torch.float32, (T, hq), dev)
-    ws = _workspace(dev, d)
+    n_ws = _workspace_bytes.get((dev, d)) or _workspace_size(dev, d)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev)
     _run(lib().qwm_paged_attend,
-         _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), ws.numel(), T,
-                      pool.shape[0], T if max_new is None else max_new, _DTYPES[q.dtype], d, hq, hk, page, B,
-                      block_table.shape[1], 1 if causal else 0, window, scale, kernel), "qwm_paged_attend", dev)
+         _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
+                      T if max_new is None else max_new, _DTYPES[q.dtype], d, hq, hk, page, B, width, 1 if causal else 0,
+                      window, scale, kernel), "qwm_paged_attend", dev)
     return out
 
 
