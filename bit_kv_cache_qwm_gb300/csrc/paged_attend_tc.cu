@@ -240,35 +240,42 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     uint32_t s_par = 0, q_par = 0;
     int u = 0;
     // Q_g of the item: this thread's bf16 row, in place, to float16 in the
-    // order (0, 4), (1, 5), (2, 6), (3, 7), scaled by 2^-e where its largest
-    // entry is 2^15 or more.  Returns the logit factor.
+    // order (0, 4), (1, 5), (2, 6), (3, 7).  A row with an entry of 2^15 or more
+    // is read again and scaled by the power of two that brings it below.
+    // Returns the logit factor.
+    auto to_half = [&](uint4 x, float qs) {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
+        o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
+                                             __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
+      }
+      return make_uint4(o[0], o[1], o[2], o[3]);
+    };
     auto make_q = [&]() {
       group_all(g, (warp & 3) != 0 || bar_wait(q_raw, q_par, &abort_sh, a.timeout));
       q_par ^= 1;
       uint32_t big = 0;
 #pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(qt + op_off(i, c));
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-      }
-      big = max(big & 0xffffu, big >> 16);
-      const int ex = (int)(big >> 7) - 127;
-      const int e = ex > 14 ? ex - 14 : 0;
-      const float qs = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
-      for (int c = 0; c < D / 8; ++c) {
         uint4* at = reinterpret_cast<uint4*>(qt + op_off(i, c));
         const uint4 x = *at;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
-          o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
-                                               __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
-        }
-        *at = make_uint4(o[0], o[1], o[2], o[3]);
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        *at = to_half(x, 1.f);
+      }
+      big = max(big & 0xffffu, big >> 16);
+      int e = 0;
+      if (big >= 0x4700u) {   // 2^15; only a row of the item holds anything
+        e = (int)(big >> 7) - 127 - 14;
+        const int y = it.rt * kRows + 128 * g + i, tok = div_group(a, y);
+        const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+                                                         (int64_t)(it.h * a.group + y - tok * a.group) * a.q_head);
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(qt + op_off(i, c)) = to_half(src[c], __uint_as_float((uint32_t)(127 - e) << 23));
       }
       fence_async_smem();
       bar_arrive(&q_ready[g]);
@@ -405,11 +412,17 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           }
         }
         __syncwarp();
-#pragma unroll 2
+        uint4 piece[8];
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int y = 4 * k + (lane >> 3), r = 32 * (warp & 3) + y;
+          const int y = 4 * k + (lane >> 3);
+          piece[k] = *reinterpret_cast<const uint4*>(stage + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 32 * (warp & 3) + 4 * k + (lane >> 3);
           if (r < rows) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+            const uint4 x = piece[k];
             if (all) {
               const int tok = div_group(a, y0 + r);
               *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + (q_row0 + tok) * a.o_row +
@@ -453,6 +466,16 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       if (++t < it.to) return true;
       if (!it.next(a)) return false;
       t = it.from;
+      // the item's queries on their way to L2 while the one before it is at work
+#pragma unroll
+      for (int y = p; y < kRows; y += 128)
+        if (y < it.rows) {
+          const int x = it.rt * kRows + y, tok = div_group(a, x);
+          const __nv_bfloat16* row = (const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+                                     (int64_t)(it.h * a.group + x - tok * a.group) * a.q_head;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+        }
       return true;
     };
     const uint8_t* blk = nullptr;
