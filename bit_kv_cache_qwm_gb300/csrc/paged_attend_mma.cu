@@ -3,17 +3,18 @@
 //
 //   s_n = q . k_hat_n;  O = sum_n exp2(s_n - m) v_hat_n, running maximum m
 //
-// A worker (a CTA of four warps) walks the tiles of 64 tokens that the
-// partition deals to it; a warp takes 16 tokens of each, with its own running
+// A worker (a CTA of four warps) walks the tiles of 128 tokens that the
+// partition deals to it; a warp takes 32 tokens of each, with its own running
 // maximum, and the warps meet at the end of an item only.  Every warp copies
 // its own packed bytes (2.5 KB a block of 16 tokens at d = 128, five 16-byte
 // asynchronous copies a lane) into its own ring of shared memory, so that no
 // barrier stands between the copies and the arithmetic; the page ids of 32
-// tiles are loaded at once, a block before the first is needed.  (Measured on
+// tiles are loaded at once, a step before the first is needed.  (Measured on
 // the ragged batch of 48 requests: one producer warp a CTA with bulk copies
 // 155 us, where a thread issues one copy at a time and pages of 16 tokens make
 // 16 a tile; loads to registers two blocks ahead 143 us, too few bytes in
-// flight.)
+// flight; this with 16 tokens a step 118 us, with 32 109 us: half the control
+// and address instructions, two independent chains of MMAs.)
 //
 // Both products are formed transposed with mma.m16n8k16 (float16 in, float32
 // out), the 16 tokens or channels on the long side and the 8 query rows on the
@@ -32,7 +33,9 @@
 // Tokens outside a request (or on a page out of range) have their logits
 // replaced and their value parameters zeroed, so garbage bytes do no harm.
 //
-// Bound by HBM: 1.25 d bytes a token.
+// Bound by HBM (1.25 d bytes a token) and the ~26 instructions a token and
+// warp, half of them the codes' way to float16; without arithmetic the same
+// copies take 84 us.
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 
@@ -42,7 +45,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kCw = 4, kCtas = 3, kStages = 4, kTk = 16 * kCw, kNt = kCw * 32, kItem = 2;
+constexpr int kCw = 4, kCtas = 3, kStages = 2, kSub = 2, kTk = 16 * kSub * kCw, kNt = kCw * 32, kItem = 2;
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -118,7 +121,7 @@ template <int D, class W>
 struct Ahead {
   W* walker;
   int t, to, base;       // next tile; end of the item's; first tile of the ids
-  int lo, hi, ids;
+  int lo, hi, ids[kSub];
   const int32_t* row;
   const uint8_t* head;   // pool + the head's offset in a page
   uint32_t page_bytes;   // of all heads
@@ -127,12 +130,15 @@ struct Ahead {
 
   __device__ __forceinline__ void fetch_ids(const AttendArgs& a, int warp, int lane) {
     base = t;
-    const int n = (t + lane) * kTk + 16 * warp;
-    const bool in = t + lane < to && n < hi && n + 16 > lo;
-    ids = in ? __ldg(row + (n >> a.page_shift)) : -2;
-    if (in && (ids < 0 || ids >= a.n_pages)) {
-      flag(a.status, QWM_DEV_BOUNDS);
-      ids = -2;
+#pragma unroll
+    for (int x = 0; x < kSub; ++x) {
+      const int n = (t + lane) * kTk + 16 * (kSub * warp + x);
+      const bool in = t + lane < to && n < hi && n + 16 > lo;
+      ids[x] = in ? __ldg(row + (n >> a.page_shift)) : -2;
+      if (in && (ids[x] < 0 || ids[x] >= a.n_pages)) {
+        flag(a.status, QWM_DEV_BOUNDS);
+        ids[x] = -2;
+      }
     }
   }
   __device__ __forceinline__ void open(const AttendArgs& a, const W& w, int warp, int lane) {
@@ -142,14 +148,18 @@ struct Ahead {
     fetch_ids(a, warp, lane);
   }
   // Copies the next block into a stage (one commit group, also when there is
-  // nothing to copy); returns whether the block has tokens.
-  __device__ __forceinline__ bool copy(const AttendArgs& a, uint32_t stage, int warp, int lane) {
-    bool have = false;
+  // nothing to copy); returns a bit for each 16 tokens that there are.
+  __device__ __forceinline__ uint32_t copy(const AttendArgs& a, uint32_t stage, int warp, int lane) {
+    uint32_t have = 0;
     if (more) {
-      const int pg = __shfl_sync(0xffffffffu, ids, t - base);
-      have = pg >= 0;
-      if (have) {
-        Stage<D>::copy(stage, head + (uint64_t)(uint32_t)pg * page_bytes, (t * kTk + 16 * warp) & (a.page - 1), src, lane);
+#pragma unroll
+      for (int x = 0; x < kSub; ++x) {
+        const int pg = __shfl_sync(0xffffffffu, ids[x], t - base);
+        if (pg >= 0) {
+          have |= 1u << x;
+          Stage<D>::copy(stage + x * Stage<D>::bytes, head + (uint64_t)(uint32_t)pg * page_bytes,
+                         (t * kTk + 16 * (kSub * warp + x)) & (a.page - 1), src, lane);
+        }
       }
       // on to the next block; its id is on the way before it is asked for
       if (++t == to) {
@@ -173,7 +183,7 @@ struct Ahead {
 template <int D, int NB>
 struct Smem {
   static constexpr int LD = D + 4;                          // rows 2 c of a store phase 8 banks apart
-  static constexpr int merge = kCw * kStages * Stage<D>::bytes;   // float [kCw][8 NB][LD]
+  static constexpr int merge = kCw * kStages * kSub * Stage<D>::bytes;   // float [kCw][8 NB][LD]
   static constexpr int stat = merge + kCw * 8 * NB * LD * 4;
   static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
 };
@@ -201,10 +211,10 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   ahead.src.init(a.page, a.block / 2, lane);
   ahead.open(a, it, warp, lane);
   // the warp's stages; copies of a lane start 16 bytes a lane into one
-  const uint8_t* ring = sm + warp * kStages * Stage<D>::bytes;
+  const uint8_t* ring = sm + warp * kStages * kSub * Stage<D>::bytes;
   const uint32_t ring_at = su32(ring) + 16 * lane;
-  uint32_t have = 0;     // a bit for each stage: its block has tokens
-  for (int i = 0; i < kStages; ++i) have |= (uint32_t)ahead.copy(a, ring_at + i * Stage<D>::bytes, warp, lane) << i;
+  uint32_t have = 0;     // kSub bits for each stage: which 16 tokens there are
+  for (int i = 0; i < kStages; ++i) have |= ahead.copy(a, ring_at + i * kSub * Stage<D>::bytes, warp, lane) << (kSub * i);
   int st = 0;
 
   const int g = lane >> 2, c = lane & 3;
@@ -280,72 +290,87 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
       for (int k = 0; k < 2; ++k) m[nb][k] = kNone, l[nb][k] = 0.f;
     }
     for (int t = it.from; t < it.to; ++t) {
-      const int n0 = t * kTk + 16 * warp;                          // the block's 16 tokens
-      const bool live = (have >> st & 1) != 0;
-      const bool whole = n0 + 16 <= top_min && n0 >= bottom_max;   // every row sees all of them
-      const uint8_t* x = ring + st * Stage<D>::bytes;
+      using St = Stage<D>;
+      const int n0 = t * kTk + 16 * kSub * warp;                   // the step's first token
+      const uint32_t live = (have >> (kSub * st)) & ((1u << kSub) - 1);
+      // every row sees all of them
+      const bool whole = live == (1u << kSub) - 1 && n0 + 16 * kSub <= top_min && n0 >= bottom_max;
+      const uint8_t* x0 = ring + st * kSub * St::bytes;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
       if (live) {
-        using St = Stage<D>;
         // ---- S^T
-        float s[NB][4], s2[NB][4];   // two sums: half the chain of dependent MMAs
-        uint32_t kw[2][KW];
-        __half2 ks[2], kz[2];
+        float s[NB][kSub][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int row = 8 * b + tok0;
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(x + St::kcode + row * 64 + 16 * c);
-            kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(x + St::kcode + row * 32 + 8 * c);
-            kw[b][0] = u.x, kw[b][1] = u.y;
-          }
-          const __half2 par = *reinterpret_cast<const __half2*>(x + St::kpar + (row * St::G + c * St::G / 4) * 4);
-          kz[b] = __low2half2(par);
-          ks[b] = __high2half2(par);
-        }
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          uint32_t f[4], f2[4];
+        for (int e = 0; e < kSub; ++e) {
+          const uint8_t* x = x0 + e * St::bytes;
+          float s2[NB][4];   // two sums: half the chain of dependent MMAs
+          uint32_t kw[2][KW];
+          __half2 ks[2], kz[2];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            f[b] = dq_lo(kw[b][i], ks[b], kz[b], magic);
-            f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b], magic);
-            const uint32_t up = kw[b][i] >> 8;
-            f2[b] = dq_lo(up, ks[b], kz[b], magic);
-            f2[2 + b] = dq_hi(up, ks[b], kz[b], magic);
+            const int row = 8 * b + tok0;
+            if constexpr (D == 128) {
+              const uint4 u = *reinterpret_cast<const uint4*>(x + St::kcode + row * 64 + 16 * c);
+              kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(x + St::kcode + row * 32 + 8 * c);
+              kw[b][0] = u.x, kw[b][1] = u.y;
+            }
+            const __half2 par = *reinterpret_cast<const __half2*>(x + St::kpar + (row * St::G + c * St::G / 4) * 4);
+            kz[b] = __low2half2(par);
+            ks[b] = __high2half2(par);
           }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (i == 0) {
-              mma0(s[nb], f, qf[nb][0][0], qf[nb][0][1]);
-              mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
-            } else {
-              mma(s[nb], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-              mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+          for (int i = 0; i < KW; ++i) {
+            uint32_t f[4], f2[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              f[b] = dq_lo(kw[b][i], ks[b], kz[b], magic);
+              f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b], magic);
+              const uint32_t up = kw[b][i] >> 8;
+              f2[b] = dq_lo(up, ks[b], kz[b], magic);
+              f2[2 + b] = dq_hi(up, ks[b], kz[b], magic);
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              if (i == 0) {
+                mma0(s[nb][e], f, qf[nb][0][0], qf[nb][0][1]);
+                mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
+              } else {
+                mma(s[nb][e], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+                mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+              }
             }
           }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nb][e][i] += s2[nb][i];
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nb][i] += s2[nb][i];
-        // ---- softmax: s[nb][2 b + k] is token 8 b + tok0, row 2 c + k
-        uint32_t pf[NB][2];
+        // ---- softmax: s[nb][e][2 b + k] is token 16 e + 8 b + tok0, row 2 c + k
+        uint32_t pf[NB][kSub][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = n0 + 8 * (i >> 1) + tok0;
-              if (n < bottom[nb][i & 1] || n >= top[nb][i & 1]) s[nb][i] = -INFINITY;
-            }
+            for (int e = 0; e < kSub; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int n = n0 + 16 * e + 8 * (i >> 1) + tok0;
+                if (n < bottom[nb][i & 1] || n >= top[nb][i & 1] || !(live >> e & 1)) s[nb][e][i] = -INFINITY;
+              }
           }
-          float mx0 = fmaxf(s[nb][0], s[nb][2]) * c2[nb][0], mx1 = fmaxf(s[nb][1], s[nb][3]) * c2[nb][1];
+          float mx0 = fmaxf(s[nb][0][0], s[nb][0][2]), mx1 = fmaxf(s[nb][0][1], s[nb][0][3]);
+#pragma unroll
+          for (int e = 1; e < kSub; ++e) {
+            mx0 = max3f(mx0, s[nb][e][0], s[nb][e][2]);
+            mx1 = max3f(mx1, s[nb][e][1], s[nb][e][3]);
+          }
+          mx0 *= c2[nb][0];
+          mx1 *= c2[nb][1];
           if (__any_sync(0xffffffffu, mx0 > m[nb][0] + 8.f || mx1 > m[nb][1] + 8.f)) {
-            // rare: the rows' maxima over the 16 tokens, and O rescaled
+            // rare: the rows' maxima over the tokens, and O rescaled
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
@@ -362,63 +387,73 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
               o[nb][j][2] *= f0, o[nb][j][3] *= f1;
             }
           }
-          float p[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[nb][i], c2[nb][i & 1], -m[nb][i & 1]));
-          l[nb][0] += p[0] + p[2];
-          l[nb][1] += p[1] + p[3];
-          pf[nb][0] = transpose8(h2u(__floats2half2_rn(p[0], p[1])));
-          pf[nb][1] = transpose8(h2u(__floats2half2_rn(p[2], p[3])));
+          for (int e = 0; e < kSub; ++e) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[nb][e][i], c2[nb][i & 1], -m[nb][i & 1]));
+            l[nb][0] += p[0] + p[2];
+            l[nb][1] += p[1] + p[3];
+            pf[nb][e][0] = transpose8(h2u(__floats2half2_rn(p[0], p[1])));
+            pf[nb][e][1] = transpose8(h2u(__floats2half2_rn(p[2], p[3])));
+          }
         }
         // ---- O^T: tokens ta, tb (columns 2 c, 2 c + 1) of both blocks of 8
-        uint32_t v0[2][D / 64], v1[2][D / 64];
-        __half2 vz[2], vs[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int r0 = 8 * b + ta, r1 = 8 * b + tb;
-          if constexpr (D == 128) {
-            const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::vcode + r0 * 64 + 8 * g);
-            const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::vcode + r1 * 64 + 8 * g);
-            v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
-          } else {
-            v0[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r0 * 32 + 4 * g);
-            v1[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r1 * 32 + 4 * g);
-          }
-          uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
-          uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
-          if (!whole) {
-            // tokens outside the request: their bytes may be anything
-            if (n0 + r0 < it.lo || n0 + r0 >= it.hi) p0 = 0;
-            if (n0 + r1 < it.lo || n0 + r1 >= it.hi) p1 = 0;
-          }
-          vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
-          vs[b] = u2h(__byte_perm(p0, p1, 0x7632));
-        }
-        // two blocks j of 16 channels at a time: f[.][2 b] is channel row g,
-        // f[.][2 b + 1] row g + 8 (d = 128: of the two words; d = 64: of the
-        // two halves of the one)
+        for (int e = 0; e < kSub; ++e) {
+          const uint8_t* x = x0 + e * St::bytes;
+          uint32_t v0[2][D / 64], v1[2][D / 64];
+          __half2 vz[2], vs[2];
 #pragma unroll
-        for (int y = 0; y < MB / 2; ++y) {
-          uint32_t f[2][4];
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              // byte y (or y + 2) of both tokens into bytes 0 and 2
-              const int word = D == 128 ? q : 0, byte = D == 128 ? y : y + 2 * q;
-              const uint32_t v = __byte_perm(v0[b][word], v1[b][word], byte * 0x0011 + (4 + byte) * 0x1100);
-              f[0][2 * b + q] = dq_lo(v, vs[b], vz[b], magic);
-              f[1][2 * b + q] = dq_hi(v, vs[b], vz[b], magic);
+          for (int b = 0; b < 2; ++b) {
+            const int r0 = 8 * b + ta, r1 = 8 * b + tb;
+            if constexpr (D == 128) {
+              const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::vcode + r0 * 64 + 8 * g);
+              const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::vcode + r1 * 64 + 8 * g);
+              v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
+            } else {
+              v0[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r0 * 32 + 4 * g);
+              v1[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r1 * 32 + 4 * g);
             }
+            uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
+            uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
+            if (!whole) {
+              // tokens outside the request, or on no page: their bytes may be anything
+              const int y0 = n0 + 16 * e + r0, y1 = n0 + 16 * e + r1;
+              const bool got = live >> e & 1;
+              if (!got || y0 < it.lo || y0 >= it.hi) p0 = 0;
+              if (!got || y1 < it.lo || y1 >= it.hi) p1 = 0;
+            }
+            vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
+            vs[b] = u2h(__byte_perm(p0, p1, 0x7632));
+          }
+          // two blocks j of 16 channels at a time: f[.][2 b] is channel row g,
+          // f[.][2 b + 1] row g + 8 (d = 128: of the two words; d = 64: of the
+          // two halves of the one)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int y = 0; y < MB / 2; ++y) {
+            uint32_t f[2][4];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][0], pf[nb][1]);
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                // byte y (or y + 2) of both tokens into bytes 0 and 2
+                const int word = D == 128 ? q : 0, byte = D == 128 ? y : y + 2 * q;
+                const uint32_t v = __byte_perm(v0[b][word], v1[b][word], byte * 0x0011 + (4 + byte) * 0x1100);
+                f[0][2 * b + q] = dq_lo(v, vs[b], vz[b], magic);
+                f[1][2 * b + q] = dq_hi(v, vs[b], vz[b], magic);
+              }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+          }
         }
       }
-      // the stage is read: the block kStages on takes it
+      // the stage is read: the step kStages on takes it
       __syncwarp();
-      have = (have & ~(1u << st)) | ((uint32_t)ahead.copy(a, ring_at + st * Stage<D>::bytes, warp, lane) << st);
+      have = (have & ~(((1u << kSub) - 1) << (kSub * st))) |
+             (ahead.copy(a, ring_at + st * kSub * Stage<D>::bytes, warp, lane) << (kSub * st));
       if (++st == kStages) st = 0;
     }
     // ---- the warps' parts of the item meet

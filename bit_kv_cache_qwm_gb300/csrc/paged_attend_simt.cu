@@ -18,7 +18,7 @@ namespace qwm {
 namespace paged {
 namespace {
 
-constexpr int kTk = 64, kNt = 256, kItem = 1;
+constexpr int kTk = 64, kNt = 256, kItem = 1, kCtas64 = 1;
 
 template <int D, int R>
 struct Shape {
@@ -363,7 +363,7 @@ int sm_count() {
 
 Workers simt_workers(int64_t max_rows) {
   const int sms = sm_count();
-  return max_rows <= 8 ? Workers{2 * sms, 8} : Workers{sms, 64};
+  return max_rows <= 8 ? Workers{2 * sms, 8} : Workers{kCtas64 * sms, 64};
 }
 
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st) {

@@ -48,7 +48,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 4;
+constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 6;
 constexpr uint32_t kColO = 256;
 constexpr float kNone = -3.0e38f;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
