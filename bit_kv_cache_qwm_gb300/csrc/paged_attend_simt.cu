@@ -6,7 +6,9 @@
 //
 // A worker (CTA) walks the tiles of 64 tokens that the partition deals to it.
 // Per tile it dequantises K and V into shared memory (float32, rows padded so
-// that the reads of different keys fall into different banks) and every
+// that the reads of different keys fall into different banks), sends for the
+// next tile's packed bytes (without that the page ids' and the codes' latency
+// lay between every two tiles: 38 us of the windowed batch below), and every
 // thread computes RT rows x KT keys of S and RT rows x CT channels of O from
 // registers.  Items have R = 64 rows, or 8 when no request has more than 8
 // (single-token steps: with 64 the arithmetic on absent rows would be 8 times
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
   float* Ks = Qs + R * S::LD;           // [kTk][LD]
   float* Vs = Ks + kTk * S::LD;         // [kTk][D]
   float* Ps = Vs + kTk * D;             // [R][LP]
-  __shared__ int page_of[kTk / 16];
+  __shared__ uint8_t live_sh[kTk];      // the tile's tokens that are there
   const int tid = threadIdx.x, tx = tid % S::TX, ty = tid / S::TX;
   const int w = blockIdx.x;
   const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);
@@ -91,40 +93,50 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 #pragma unroll
       for (int j = 0; j < S::CT; ++j) o[i][j] = 0.f;
     }
+    // the next tile's packed bytes, on their way during this one's arithmetic:
+    // thread's code words i = tid, tid + 256, ... of [half][token][word]
+    constexpr int IT = 2 * kTk * (D / 8) / kNt;
+    uint32_t code[IT], par[IT], live = 0;
+    auto fetch = [&](int n0) {
+      live = 0;
+#pragma unroll
+      for (int x = 0; x < IT; ++x) {
+        const int i = tid + x * kNt, half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
+        const int k = rem / (D / 8), wd = rem % (D / 8), n = n0 + k;
+        code[x] = par[x] = 0;
+        if (n < it.lo || n >= it.hi) continue;
+        const int pg = __ldg(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift));
+        if (pg < 0 || pg >= a.n_pages) {
+          if (half == 0 && wd == 0) flag(a.status, QWM_DEV_BOUNDS);
+          continue;
+        }
+        live |= 1u << x;
+        const int s = n & (a.page - 1);
+        const uint8_t* blk = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + half * (a.block / 2);
+        code[x] = __ldg(reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4));
+        par[x] = __ldg(reinterpret_cast<const uint32_t*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4));
+      }
+    };
+    fetch(it.from * kTk);
     for (int t = it.from; t < it.to; ++t) {
       const int n0 = t * kTk;
       __syncthreads();   // the previous tile's reads are done
-      if (tid < kTk / 16) {
-        const int n = n0 + tid * 16;
-        int pg = -1;
-        if (n < it.hi) {
-          pg = a.table[(int64_t)it.b * a.max_blocks + (n >> a.page_shift)];
-          if (pg < 0 || pg >= a.n_pages) {
-            flag(a.status, QWM_DEV_BOUNDS);
-            pg = -1;
-          }
-        }
-        page_of[tid] = pg;
-      }
-      __syncthreads();
-      for (int i = tid; i < 2 * kTk * (D / 8); i += kNt) {
-        const int half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
-        const int k = rem / (D / 8), wd = rem % (D / 8), n = n0 + k, pg = page_of[k >> 4];
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (pg >= 0 && n >= it.lo && n < it.hi) {
-          const int s = n & (a.page - 1);
-          const uint8_t* blk = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + half * (a.block / 2);
-          const uint32_t code = *reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4);
-          const __half2 par = *reinterpret_cast<const __half2*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4);
-          const float z = __low2float(par), sc = __high2float(par);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = fmaf((float)((code >> (4 * c)) & 15u), sc, z);
-        }
+      for (int x = 0; x < IT; ++x) {
+        const int i = tid + x * kNt, half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
+        const int k = rem / (D / 8), wd = rem % (D / 8);
+        const __half2 p = *reinterpret_cast<const __half2*>(&par[x]);
+        const float z = __low2float(p), sc = __high2float(p);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = fmaf((float)((code[x] >> (4 * c)) & 15u), sc, z);
         float* dst = half ? Vs + k * D + wd * 8 : Ks + k * S::LD + wd * 8;
-        *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        if (half == 0 && wd == 0) live_sh[k] = (live >> x) & 1;
       }
       __syncthreads();
+      if (t + 1 < it.to) fetch(n0 + kTk);
       float s[S::RT][S::KT];
 #pragma unroll
       for (int i = 0; i < S::RT; ++i)
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 #pragma unroll
         for (int j = 0; j < S::KT; ++j) {
           const int n = n0 + tx + S::TX * j;
-          const bool sees = n >= bottom[i] && n < top[i] && page_of[(tx + S::TX * j) >> 4] >= 0;
+          const bool sees = n >= bottom[i] && n < top[i] && live_sh[tx + S::TX * j];
           s[i][j] = sees ? s[i][j] : -INFINITY;
           mx = fmaxf(mx, s[i][j]);
         }
