@@ -376,8 +376,10 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
               mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
               mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
             }
-            mx0 = fmaxf(mx0, m[nb][0]);
-            mx1 = fmaxf(mx1, m[nb][1]);
+            // a row that does not need it keeps its maximum, so its bits do
+            // not depend on its neighbours
+            mx0 = mx0 > m[nb][0] + 8.f ? mx0 : m[nb][0];
+            mx1 = mx1 > m[nb][1] + 8.f ? mx1 : m[nb][1];
             const float f0 = ex2(m[nb][0] - mx0), f1 = ex2(m[nb][1] - mx1);
             m[nb][0] = mx0, m[nb][1] = mx1;
             l[nb][0] *= f0, l[nb][1] *= f1;

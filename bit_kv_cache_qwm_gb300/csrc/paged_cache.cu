@@ -147,69 +147,68 @@ __global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_pla
   }
 }
 
-// One CTA: pushes the pages behind keep_len in the order of the requests.
+// One CTA, a warp a request: the pages behind keep_len are counted (ids in
+// range), the counts summed up in the order of the requests, and if the stack
+// holds them all, pushed.  Bound by latency.
 __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_release_args a, int shift) {
+  extern __shared__ int32_t first_sm[];   // pages given up by each request, then their first place
   __shared__ int32_t count_sh;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) count_sh = *a.free_count;
-  __syncthreads();
-  const int count = count_sh;
-  // the pages a request gives up: entries [keep, held) of its table with an id in range
+  // entries [keep, held) of a request's table; false where keep_len is out of range
   auto range = [&](int b, int* keep, int* held) {
     const int len = a.kv_len[b], want = a.keep_len[b];
-    *keep = *held = 0;
-    if (want < 0 || want > len || pages_of(len, shift) > a.max_blocks) {
-      flag(a.status, QWM_DEV_BOUNDS);
-      return false;
-    }
+    if (want < 0 || want > len || pages_of(len, shift) > a.max_blocks) return false;
     *keep = pages_of(want, shift);
     *held = pages_of(len, shift);
     return true;
   };
-  auto valid = [&](int b, int keep, int held) {
-    int n = 0;
-    for (int j = keep; j < held; ++j) {
+  for (int b = warp; b < a.requests; b += kPlanNt / 32) {
+    int keep = 0, held = 0, n = 0;
+    const bool ok = range(b, &keep, &held);
+    if (!ok && lane == 0) flag(a.status, QWM_DEV_BOUNDS);
+    for (int j = keep + lane; ok && j < held; j += 32) {
       const int pg = a.block_table[(int64_t)b * a.max_blocks + j];
       if (pg >= 0 && pg < a.n_pages) ++n;
       else flag(a.status, QWM_DEV_BOUNDS);
     }
-    return n;
-  };
-  // first the sum alone: nothing changes unless all of it fits
+    n = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    if (lane == 0) first_sm[b] = n;
+  }
+  __syncthreads();
+  const int count = count_sh;
   int64_t total = 0;
   for (int b0 = 0; b0 < a.requests; b0 += kPlanNt) {
     const int b = b0 + tid;
-    int64_t x = 0, y = 0, sx, sy;
-    int keep, held;
-    if (b < a.requests && range(b, &keep, &held)) x = valid(b, keep, held);
+    int64_t x = b < a.requests ? first_sm[b] : 0, y = 0, sx, sy;
     scan2(x, y, &sx, &sy);
+    // beyond int32 only where it does not fit, and is not used
+    if (b < a.requests) first_sm[b] = (int32_t)(total + x);
     total += sx;
   }
+  __syncthreads();
   if (count < 0 || count > a.n_pages || total + count > a.n_pages) {
     if (tid == 0) flag(a.status, QWM_DEV_CAPACITY);
     return;
   }
-  int64_t at = count;
-  for (int b0 = 0; b0 < a.requests; b0 += kPlanNt) {
-    const int b = b0 + tid;
-    int64_t x = 0, y = 0, sx, sy;
+  for (int b = warp; b < a.requests; b += kPlanNt / 32) {
     int keep = 0, held = 0;
-    const bool ok = b < a.requests && range(b, &keep, &held);
-    if (ok) x = valid(b, keep, held);
-    scan2(x, y, &sx, &sy);
-    if (ok) {
-      int64_t put = at + x;
-      for (int j = keep; j < held; ++j) {
-        int32_t* e = a.block_table + (int64_t)b * a.max_blocks + j;
-        const int pg = *e;
-        if (pg >= 0 && pg < a.n_pages) a.free_pages[put++] = pg;
-        *e = -1;
-      }
-      a.kv_len[b] = a.keep_len[b];
+    if (!range(b, &keep, &held)) continue;
+    int put = count + first_sm[b];
+    for (int j0 = keep; j0 < held; j0 += 32) {
+      const int j = j0 + lane;
+      int32_t* e = a.block_table + (int64_t)b * a.max_blocks + j;
+      const int pg = j < held ? *e : -1;
+      const bool good = pg >= 0 && pg < a.n_pages;
+      const uint32_t who = __ballot_sync(0xffffffffu, good);
+      if (good) a.free_pages[put + __popc(who & ((1u << lane) - 1))] = pg;
+      if (j < held) *e = -1;
+      put += __popc(who);
     }
-    at += sx;
+    __syncwarp();
+    if (lane == 0) a.kv_len[b] = a.keep_len[b];
   }
-  if (tid == 0) *a.free_count = (int32_t)at;
+  if (tid == 0) *a.free_count = (int32_t)(count + total);
 }
 
 // ---- append
@@ -449,7 +448,7 @@ cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st
 }
 
 cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {
-  paged_release_kernel<<<1, kPlanNt, 0, st>>>(a, shift);
+  paged_release_kernel<<<1, kPlanNt, (size_t)a.requests * 4, st>>>(a, shift);   // 32 KB at most
   return cudaGetLastError();
 }
 

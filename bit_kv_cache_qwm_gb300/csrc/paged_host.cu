@@ -155,7 +155,7 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 ||
       a->kv_heads < 1 || a->kv_heads > a->heads || a->heads % a->kv_heads || a->requests < 0 || a->max_blocks < 1 ||
       a->n_pages < 1 || a->n_pages > kInt || a->window < 0 || (a->window > 0 && !a->causal) || a->max_new < 0 ||
-      a->kernel < 0 || a->kernel > 3 || a->scale != a->scale)
+      a->kernel < 0 || a->kernel > 3 || !(fabsf(a->scale) < INFINITY))
     return QWM_ERR_INVALID_ARG;
   const int shift = page_shift(a->page_tokens), d = a->head_dim;
   if (!dim_ok(d) || shift < 0) return QWM_ERR_UNSUPPORTED;

@@ -242,3 +242,43 @@ def test_many_requests(paged, kernel):
     new = (r.random(n) < 0.2).astype(int)
     bt = Batch(13, cached, new, 2, 2, 64, 16)
     assert check(paged, bt, kid(paged, kernel)) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_row_of_nan_or_infinity_stays_alone(paged, kernel, new):
+    """Rows of q that hold NaN or infinity change no other row, of their own
+    head group, token or request."""
+    bt = Batch(14, [70, 300], [new, new], 6, 2, 128, 16)
+    k = kid(paged, kernel)
+    args = (dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+    q = dev(bt.q, "bf16")
+    ref = paged.qwm_paged_attend(q, *args, max_new=new, kernel=k)
+    bad = q.clone()
+    bad[0, 1, 5] = float("nan")
+    bad[-1, 4, 100] = float("inf")
+    got = paged.qwm_paged_attend(bad, *args, max_new=new, kernel=k)
+    same = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+    same[0, 1] = same[-1, 4] = False
+    assert torch.equal(got[same], ref[same])
+    assert not torch.isfinite(got[0, 1].float()).any()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_on_another_stream(paged, kernel):
+    """The call runs on the current stream, after what is ahead of it there."""
+    bt = Batch(15, [200, 3000], [2, 2], 8, 2, 128, 32)
+    k = kid(paged, kernel)
+    args = [dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu)]
+    ref = paged.qwm_paged_attend(dev(bt.q, "bf16"), *args, max_new=2, kernel=k)
+    q = torch.zeros_like(dev(bt.q, "bf16"))
+    want = dev(bt.q, "bf16")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        q.copy_(want)
+        got = paged.qwm_paged_attend(q, *args, max_new=2, kernel=k)
+        after = got.clone()
+    s.synchronize()
+    assert torch.equal(after, ref)

@@ -42,7 +42,8 @@ def layout(seed, cached, page, width, spare):
 
 
 @pytest.mark.parametrize("requests,page,most,pad", [(1, 16, 1, 0), (1, 64, 700, 3), (48, 16, 1, 16), (48, 128, 300, 0),
-                                                    (240, 32, 60, 100), (1025, 16, 9, 7), (3000, 256, 4, 1)])
+                                                    (240, 32, 60, 100), (1025, 16, 9, 7), (3000, 256, 4, 1),
+                                                    (8192, 16, 3, 5)])
 def test_plan_matches_the_oracle(paged, requests, page, most, pad):
     r = np.random.default_rng(requests)
     cached, new = r.integers(0, 500, requests), r.integers(0, most + 1, requests)
@@ -106,7 +107,7 @@ def test_plan_with_a_bad_page_gives_its_rows_no_slot(paged):
     assert np.array_equal(host(got.positions), [*range(20, 40), 3, 4])
 
 
-@pytest.mark.parametrize("requests,page", [(1, 16), (7, 64), (1300, 16)])
+@pytest.mark.parametrize("requests,page", [(1, 16), (7, 64), (1300, 16), (8192, 32)])
 def test_release_and_plan_again(paged, requests, page):
     r = np.random.default_rng(requests)
     cached = r.integers(0, 300, requests).astype(np.int32)

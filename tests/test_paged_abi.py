@@ -132,7 +132,7 @@ def attend_args(paged, **kw):
 @pytest.mark.parametrize("kw,status", [
     ({}, 6), (dict(rows=0), 0), (dict(requests=0), 0), (dict(rows=-1), 1), (dict(dtype=2), 1), (dict(d=256), 2), (dict(page=8), 2),
     (dict(hq=7), 1), (dict(hk=0), 1), (dict(hk=12), 1), (dict(window=-1), 1), (dict(window=5, causal=0), 1),
-    (dict(scale=float("nan")), 1), (dict(kernel=4), 1), (dict(kernel=-1), 1), (dict(max_new=-1), 1), (dict(max_blocks=0), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(kernel=4), 1), (dict(kernel=-1), 1), (dict(max_new=-1), 1), (dict(max_blocks=0), 1),
     (dict(max_blocks=1 << 27), 2), (dict(n_pages=0), 1), (dict(pool=0), 1), (dict(pool=FAKE + 8), 1), (dict(table=0), 1),
     (dict(lens=0), 1), (dict(cu=0), 1), (dict(ws=0), 1), (dict(ws=FAKE + 64), 1), (dict(ws_bytes=100), 1),
     (dict(q=(FAKE + 4, 768, 128)), 1), (dict(out=(FAKE, 768, 64)), 1), (dict(out=(FAKE, 512, 128)), 1),
