@@ -12,8 +12,9 @@ encodings of the same keys and values: nearest-centroid assignment without
 compensation (the QVG-style baseline the pages compare with), QSAC without
 compensation, and QSAC with PSAC (rank r); `qwm_dequantize` gives their
 keys, values and coefficients in float32, and the comparisons against the
-unquantised keys and values run here in torch (float32).  Measured per
-encoding:
+unquantised keys and values run here in torch (float32).  The paged cache's
+INT4 quantiser (`qwm_paged_append`, no calibration) is measured next to them
+on the same keys, values and queries.  Measured per encoding:
   top1_change        fraction of (head, query) pairs whose argmax token differs
   logit_rel_error    RMS(q.k - l_quant) / RMS(q.k) over all (query, token) pairs
   key_rel_error      ||K - K_hat|| / ||K||  (Frobenius, all heads)
@@ -47,15 +48,33 @@ def measure(ctx, K, V, q, sigma: float) -> dict:
     """The diagnostics of one cache (a qwm.Qwm context holding exactly the
     keys K and values V [H, N, d], in cache order) for query rows q [H, M, d]
     (float32 tensors on the context's device)."""
-    L = q @ K.transpose(1, 2)                                   # exact logits [H, M, N]
-    P = torch.softmax(sigma * L, dim=-1)
-    O = P @ V
     kh, vh, e, valid = ctx.dequantize()
     kh, vh, e = kh[:, valid], vh[:, valid], e[:, valid]
     Lq = q @ kh.transpose(1, 2)
     if ctx.cfg.rank > 0:
         U = torch.from_numpy(ctx.get_calibration()["U"]).to(q.device).float()   # [H, r, d]
         Lq = Lq + (q @ U.transpose(1, 2)) @ e.transpose(1, 2)
+    return compare(K, V, q, sigma, kh, vh, Lq)
+
+
+def measure_paged(K, V, q, sigma: float, page_tokens: int = 64) -> dict:
+    """The same diagnostics of the paged cache's INT4 encoding of K and V
+    [H, N, d] (bfloat16 or float32), for query rows q [H, M, d] float32."""
+    from . import paged
+    H, N, d = K.shape
+    pool = paged.paged_pool((N + page_tokens - 1) // page_tokens, H, d, page_tokens, device=K.device)
+    kh, vh = torch.empty_like(K, dtype=torch.float32), torch.empty_like(V, dtype=torch.float32)
+    paged.qwm_paged_append(K.float().transpose(0, 1), V.float().transpose(0, 1), pool, torch.arange(N, device=K.device),
+                           k_hat=kh.transpose(0, 1), v_hat=vh.transpose(0, 1))
+    return compare(K.float(), V.float(), q, sigma, kh, vh, q @ kh.transpose(1, 2))
+
+
+def compare(K, V, q, sigma: float, kh, vh, Lq) -> dict:
+    """The diagnostics of quantised keys kh, values vh and logits Lq against
+    the exact ones (all float32)."""
+    L = q @ K.transpose(1, 2)                                   # exact logits [H, M, N]
+    P = torch.softmax(sigma * L, dim=-1)
+    O = P @ V
     Pq = torch.softmax(sigma * Lq, dim=-1)
     return {
         "top1_change": float((Lq.argmax(dim=-1) != L.argmax(dim=-1)).float().mean()),
@@ -103,6 +122,7 @@ def run(workload: str, heads=None, rows: int = 256, n_chunks=None, device=None) 
         assert ctx.status() == 0
         out["encodings"][f"{assign}{'+psac' if psac else ''}"] = res
         ctx.close()
+    out["paged_int4"] = measure_paged(K, V, q, 1.0 / np.sqrt(d))
     return out
 
 

@@ -386,3 +386,23 @@ def test_step_captured_into_a_graph(paged):
         for key in ("pool", "t", "kl", "fc", "out"):
             assert torch.equal(a[key], b[key]), key
     assert host(a["kl"]).tolist() == [40, 40, 0, 40]
+
+
+def test_diagnostics_measure_the_paged_encoding(paged):
+    """The attention-shift diagnostics' INT4 entry against the oracle's own
+    quantiser on the same keys, values and queries."""
+    from bit_kv_cache_qwm_gb300 import diagnostics
+    r = np.random.default_rng(8)
+    K, V = (rounded(r.standard_normal((2, 300, 128)), "bf16") for _ in "kv")
+    q = r.standard_normal((2, 20, 128)).astype(np.float32)
+    got = diagnostics.measure_paged(dev(K), dev(V), dev(q), 128 ** -0.5)
+    k64, v64, q64 = K.astype(np.float64), V.astype(np.float64), q.astype(np.float64)
+    kh, vh = (P.dequantize_int4(*P.quantize_int4(x)) for x in (K, V))
+    rel = lambda a, b: np.sqrt(((a - b) ** 2).sum() / (b ** 2).sum())  # noqa: E731
+    L, Lq = q64 @ k64.swapaxes(1, 2), q64 @ kh.swapaxes(1, 2)
+    soft = lambda x: np.exp(x - x.max(-1, keepdims=True)) / np.exp(x - x.max(-1, keepdims=True)).sum(-1, keepdims=True)  # noqa: E731
+    O, Oq = soft(L / 128 ** 0.5) @ v64, soft(Lq / 128 ** 0.5) @ vh
+    for key, want in (("key_rel_error", rel(kh, k64)), ("value_rel_error", rel(vh, v64)), ("logit_rel_error", rel(Lq, L)),
+                      ("output_rel_error", rel(Oq, O))):
+        assert got[key] == pytest.approx(want, rel=1e-3), key
+    assert abs(got["top1_change"] - (L.argmax(-1) != Lq.argmax(-1)).mean()) <= 1 / 40
