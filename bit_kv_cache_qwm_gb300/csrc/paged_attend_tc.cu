@@ -5,23 +5,22 @@
 //
 // A worker (one CTA an SM) walks items of 256 rows (two M = 128 query tiles a,
 // b of one request and key/value head; the rows of a head group follow one
-// another token by token) and tiles of 128 tokens.  Warp roles (13 warps):
+// another token by token) and tiles of 128 tokens.  Warp roles (16 warps):
 //   warps 0-3 / 4-7  softmax of query tile a / b, thread = row = TMEM lane:
-//                    once an item Q to float16 in place (SW128 K-major, scaled
-//                    per row by a power of two if it has to be); per tile the
-//                    online softmax in the exp2 domain with O rescaled only
-//                    when the maximum grows by more than 2^8, P in float16
-//                    over the first 64 columns of S; at the item's end, after
-//                    the next item's Q, O from TMEM to memory.
+//                    per tile the online softmax in the exp2 domain with O
+//                    rescaled only when the maximum grows by more than 2^8, P
+//                    in float16 over the first 64 columns of S; at the item's
+//                    end O from TMEM to memory.
 //   warps 8-11       producers, thread = token: the packed codes (64 + 64
 //                    bytes at d = 128) and parameters of the next tile are
 //                    loaded into registers one tile ahead, its page id two
 //                    tiles ahead, and dequantised into two-stage K and V tiles
 //                    (one 16-byte store a code word, no bank conflicts: the
-//                    eight rows of a store phase differ in the swizzle); an
-//                    item's query rows are copied as soon as the last S of the
-//                    item before it is complete.
+//                    eight rows of a store phase differ in the swizzle).
 //   warp 12          MMA issuer and TMEM owner.
+//   warps 13-15      query loaders: an item's queries (float16, SW128 K-major)
+//                    as soon as the last S of the item before is complete, so
+//                    its first S runs while that one's O is stored.
 // Tensor order: S_a(0) S_b(0), then per tile t
 //   PV_a(t) S_a(t+1) PV_b(t) S_b(t+1)
 // so while one query tile's 16 MMAs run (1.25K cycles at d = 128) the other's
@@ -38,7 +37,17 @@
 // Channel order of all operands within 8 channels: 0 4 1 5 2 6 3 7, the order
 // in which masks of a code word give float16 pairs.
 // TMEM columns: S_a [0,128), S_b [128,256), O_a [256,256+d), O_b [384,384+d).
-// Bound by the tensor pipe and the softmax between its MMAs.
+// Bound by the tensor pipe and the softmax between its MMAs.  Measured at d =
+// 128: 4,680 queries over 32,760 tokens, 24 heads, not causal, 1.34 ms (1.40
+// PFLOP/s); four ragged prompts of 900 to 4,096 tokens, 32 heads over 8,
+// causal, 0.41 ms (0.97 PFLOP/s of the visible products), where an item has
+// some 18 tiles and its first S, its end and its causal edge cost about 5 more.
+// The first without the producers' stores takes 1.22 ms, without exponentials
+// 1.30 and without either 1.18 (these three with the queries loaded by the
+// softmax warps, then 1.43 in all: the loads shared their registers); with the
+// producers loading the queries 1.55, the prompts 0.51.  What an item weighs in
+// tiles when work is dealt out (kItem): the prompts take 0.57 ms at 0, 0.45 at
+// 3, 0.42 at 4 to 6.
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 
@@ -48,7 +57,7 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTk = 128, kRows = 256, kNt = 13 * 32, kProd = 8, kMma = 12, kItem = 6;
+constexpr int kTk = 128, kRows = 256, kNt = 16 * 32, kProd = 8, kMma = 12, kLoad = 13, kItem = 6;
 constexpr uint32_t kColO = 256;
 constexpr float kNone = -3.0e38f;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
@@ -64,8 +73,10 @@ struct Lay {
 };
 
 // named barriers: K stage s written (1 + s), V stage s written (3 + s), P_g in
-// three parts (5 + g, 7 + g, 9 + g); softmax group g (11 + g)
-constexpr int kNbK = 1, kNbV = 3, kNbP1 = 5, kNbP2 = 7, kNbP3 = 9, kNbS = 11;
+// three parts (5 + g, 7 + g, 9 + g); softmax group g (11 + g), query
+// loaders (13)
+constexpr int kNbK = 1, kNbV = 3, kNbP1 = 5, kNbP2 = 7, kNbP3 = 9, kNbS = 11, kNbQ = 13;
+constexpr int kLoaders = (kNt / 32 - kLoad) * 32;   // threads
 __device__ __forceinline__ void nb_arrive(int id) { asm volatile("bar.arrive %0, 160;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void nb_sync(int id) { asm volatile("bar.sync %0, 160;" ::"r"(id) : "memory"); }
 // the vote of a softmax group: one warp polls, all learn the result
@@ -74,6 +85,14 @@ __device__ __forceinline__ bool group_all(int g, bool v) {
   asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\n"
                "selp.u32 %0, 1, 0, q;\n}"
                : "=r"(r) : "r"((uint32_t)v), "r"(kNbS + g) : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ bool loaders_all(bool v) {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, %3, p;\n"
+               "selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r) : "r"((uint32_t)v), "n"(kNbQ), "n"(kLoaders) : "memory");
   return r != 0;
 }
 
@@ -192,7 +211,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   using W = Walker<kRows, kTk, kItem>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t bars[11];
+  __shared__ __align__(8) uint64_t bars[10];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
   // tokens of a tile on a page out of range, a word for each producer warp.
@@ -203,16 +222,19 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint64_t* pv_done = &bars[2];   // [2] O_g of the item complete
   uint64_t* k_free = &bars[4];    // [2] K stage read by both query tiles
   uint64_t* v_free = &bars[6];    // [2]
-  uint64_t* q_ready = &bars[8];   // [2] Q_g of the item written
-  uint64_t* q_raw = &bars[10];    // the item's bf16 rows landed in the Q tiles
+  uint64_t* q_ready = &bars[8];   // Q_a and Q_b of the item written
+  uint64_t* q_free = &bars[9];    // all S of the item complete
+  // what the softmax needs of an item besides its logits, two items deep (a
+  // slot is written again when all S of the item in between are complete)
+  __shared__ uint8_t row_exp_sh[2][kRows];   // Q was scaled by 2^-this
+  __shared__ uint32_t bad_item_sh[2];        // some page of the item is out of range
   const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
 
   if (tid == 0) {
     abort_sh = 0;
     for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
-    bar_init(&q_ready[0], 128);
-    bar_init(&q_ready[1], 128);
-    bar_init(q_raw, 128);
+    bar_init(q_ready, kLoaders);
+    bar_init(q_free, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     a.join[w].last = -1;
   }
@@ -235,53 +257,9 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     const int g = warp >> 2, i = tid & 127, lane = tid & 31;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
-    uint8_t* qt = sm + g * L::op;
     uint8_t* stage = sm + L::stage + warp * 4096;
-    uint32_t s_par = 0, q_par = 0;
-    int u = 0;
-    // Q_g of the item: this thread's bf16 row, in place, to float16 in the
-    // order (0, 4), (1, 5), (2, 6), (3, 7).  A row with an entry of 2^15 or more
-    // is read again and scaled by the power of two that brings it below.
-    // Returns the logit factor.
-    auto to_half = [&](uint4 x, float qs) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
-        o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
-                                             __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
-      }
-      return make_uint4(o[0], o[1], o[2], o[3]);
-    };
-    auto make_q = [&]() {
-      group_all(g, (warp & 3) != 0 || bar_wait(q_raw, q_par, &abort_sh, a.timeout));
-      q_par ^= 1;
-      uint32_t big = 0;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint4* at = reinterpret_cast<uint4*>(qt + op_off(i, c));
-        const uint4 x = *at;
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-        *at = to_half(x, 1.f);
-      }
-      big = max(big & 0xffffu, big >> 16);
-      int e = 0;
-      if (big >= 0x4700u) {   // 2^15; only a row of the item holds anything
-        e = (int)(big >> 7) - 127 - 14;
-        const int y = it.rt * kRows + 128 * g + i, tok = div_group(a, y);
-        const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
-                                                         (int64_t)(it.h * a.group + y - tok * a.group) * a.q_head);
-#pragma unroll 1
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(qt + op_off(i, c)) = to_half(src[c], __uint_as_float((uint32_t)(127 - e) << 23));
-      }
-      fence_async_smem();
-      bar_arrive(&q_ready[g]);
-      return a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-    };
-    float c2 = make_q();
+    uint32_t s_par = 0;
+    int u = 0, slot_in = 0;
     uint32_t pv_par = 0;
     while (true) {
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
@@ -297,15 +275,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       // tiles that start below mend_until hold tokens that a row must not see
       // left of its window, or (any tile of the item) on a page out of range
       int mend_until = bottom_max;
-      {
-        bool good = true;
-        const int last = (min(it.hi, it.to * kTk) - 1) >> a.page_shift;
-        for (int x = (max(it.lo, it.from * kTk) >> a.page_shift) + i; x <= last; x += 128) {
-          const int pg = __ldg(a.table + (int64_t)it.b * a.max_blocks + x);
-          good = good && pg >= 0 && pg < a.n_pages;
-        }
-        if (!group_all(g, good)) mend_until = 0x7fffffff;
-      }
+      float c2 = 0.f;
       float m_run = kNone, l_run = 0.f;
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int n0 = t * kTk, hi = top - n0;
@@ -314,6 +284,11 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         group_all(g, (warp & 3) != 0 || bar_wait(&s_done[g], s_par, &abort_sh, a.timeout));
         s_par ^= 1;
         fence_after();
+        if (t == it.from) {
+          c2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + row_exp_sh[slot_in][128 * g + i]) << 23);
+          if (bad_item_sh[slot_in]) mend_until = 0x7fffffff;
+          slot_in ^= 1;
+        }
         if (n0 < mend_until) mend_logits(sbase, bad_sh[u & 3], bottom - n0);
         uint32_t v[64];
         tmem_ld64(sbase + 64, v);
@@ -364,15 +339,13 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         fence_before();
         nb_arrive(kNbP3 + g);
       }
-      // what the item's end needs, then on to the next item's Q: its S may run
-      // while this one's O is stored
+      // what the item's end needs
       const bool all = it.begins() && it.ends();
       const int slot = it.begins() ? 1 : 0, rows = it.rows - 128 * g, y0 = it.rt * kRows + 128 * g;
       const int64_t q_row0 = it.rq.row0;
       const int head0 = it.h * a.group;
       if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
       const bool more = it.next(a);
-      if (more) c2 = make_q();
       group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
       pv_par ^= 1;
       fence_after();
@@ -466,16 +439,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       if (++t < it.to) return true;
       if (!it.next(a)) return false;
       t = it.from;
-      // the item's queries on their way to L2 while the one before it is at work
-#pragma unroll
-      for (int y = p; y < kRows; y += 128)
-        if (y < it.rows) {
-          const int x = it.rt * kRows + y, tok = div_group(a, x);
-          const __nv_bfloat16* row = (const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
-                                     (int64_t)(it.h * a.group + x - tok * a.group) * a.q_head;
-#pragma unroll
-          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
-        }
       return true;
     };
     const uint8_t* blk = nullptr;
@@ -492,28 +455,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const uint8_t* b = blk ? blk + half * (a.block / 2) : nullptr;
       x.load(b ? b + s * (D / 2) : nullptr, b ? b + a.page * (D / 2) + s * (G * 4) : nullptr);
     };
-    // The queries of an item, bf16, into the Q tiles: asynchronous copies that
-    // arrive on q_raw, rows behind the item's zero.  A walker of its own: the
-    // tiles run ahead of it.
-    W qi = it;
-    int q_u = 0;   // the first tile of its item
-    auto load_q = [&]() {
-      constexpr int CH = D / 8;
-#pragma unroll 4
-      for (int y = p / CH; y < kRows; y += 128 / CH) {
-        const int x = qi.rt * kRows + y, tok = div_group(a, x);
-        const bool live = y < qi.rows;
-        const __nv_bfloat16* src = (const __nv_bfloat16*)a.q;
-        if (live)
-          src += (int64_t)(qi.rq.row0 + tok) * a.q_row + (int64_t)(qi.h * a.group + x - tok * a.group) * a.q_head + 8 * (p % CH);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(sm + (y >> 7) * L::op + op_off(y & 127, p % CH))),
-                     "l"(src), "r"(live ? 16 : 0) : "memory");
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(q_raw)) : "memory");
-      q_u += qi.to - qi.from;
-      if (!qi.next(a)) q_u = -2;
-    };
-    load_q();
     lookup();
     resolve();
     load(kp, 0);
@@ -526,9 +467,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const uint32_t par = (uint32_t)(((u >> 1) - 1) & 1);
       const bool have = more;
       if (u >= 2) ok = bar_wait(&k_free[st], par, &abort_sh, a.timeout) && ok;
-      // S of tile u - 2 is complete: if the item of tile u - 1 is a new one,
-      // the Q tiles are free for it
-      if (u - 1 == q_u) load_q();
       kp.store(sm + L::k + st * L::op, p);
       if ((p & 31) == 0) bad_sh[u & 3][p >> 5] = bad;
       fence_async_smem();
@@ -541,25 +479,18 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);
-      if (!have) {
-        if (u == q_u) {   // the last tile is an item of its own
-          ok = bar_wait(&k_free[st ^ 1], (uint32_t)(((u - 1) >> 1) & 1), &abort_sh, a.timeout) && ok;
-          load_q();
-        }
-        break;
-      }
+      if (!have) break;
       load(vp, 1);
       more = advance();
       if (more) lookup();
     }
-    cp_async_wait_all();
-  } else {
+  } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t q0 = su32(sm), k0 = su32(sm + L::k), v0 = su32(sm + L::v);
     int u = 0;
     uint32_t q_par = 0;
     bool ok = true;
-    auto issue_s = [&](int g, int st) {
+    auto issue_s = [&](int g, int st, bool last) {
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -568,6 +499,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         }
         commit(&s_done[g]);
         if (g == 1) commit(&k_free[st]);
+        if (g == 1 && last) commit(q_free);
       }
       __syncwarp();
     };
@@ -583,13 +515,13 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     };
     do {
       nb_sync(kNbK + (u & 1));
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        ok = warp_all(bar_wait(&q_ready[g], q_par, &abort_sh, a.timeout)) && ok;
-        fence_after();
-        if (ok) issue_s(g, u & 1);
-      }
+      ok = warp_all(bar_wait(q_ready, q_par, &abort_sh, a.timeout)) && ok;
       q_par ^= 1;
+      fence_after();
+      if (ok) {
+        issue_s(0, u & 1, false);
+        issue_s(1, u & 1, it.from + 1 == it.to);
+      }
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int st = u & 1;
         const bool last = t + 1 == it.to;
@@ -618,11 +550,100 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
               nb_sync(kNbK + (st ^ 1));
               fence_after();
             }
-            if (ok) issue_s(g, st ^ 1);
+            if (ok) issue_s(g, st ^ 1, t + 2 == it.to);
           }
         }
       }
     } while (it.next(a));
+  } else {
+    // ------------------------------------------------------------ query loaders
+    // The queries of an item to float16 in the order (0, 4), (1, 5), (2, 6),
+    // (3, 7) into the Q tiles, CH lanes a row, rows behind the item's zero, as
+    // soon as all S of the item before are complete.  If an entry is 2^15 or
+    // more the rows are read again and each scaled by the power of two that
+    // brings it below; the softmax is told which.  Also: whether any page of
+    // the item is out of range.
+    constexpr int CH = D / 8, STEP = kLoaders / CH;
+    const int p = tid - kLoad * 32, cl = p % CH;
+    int slot_out = 0;
+    uint32_t free_par = 0;
+    bool more = true, first = true;
+    while (more) {
+      auto row_of = [&](int y) {
+        const int x = it.rt * kRows + y, tok = div_group(a, x);
+        return (const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row + (int64_t)(it.h * a.group + x - tok * a.group) * a.q_head;
+      };
+      auto place = [&](int y) { return sm + (y >> 7) * L::op + op_off(y & 127, cl); };
+      bool good = true;
+      const int last = (min(it.hi, it.to * kTk) - 1) >> a.page_shift;
+#pragma unroll 1
+      for (int x = (max(it.lo, it.from * kTk) >> a.page_shift) + p; x <= last; x += kLoaders) {
+        const int id = __ldg(a.table + (int64_t)it.b * a.max_blocks + x);
+        good = good && id >= 0 && id < a.n_pages;
+      }
+      // on their way to L2 before the tiles are free
+#pragma unroll 1
+      for (int y = p >> 1; y < it.rows; y += kLoaders / 2)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(y) + (D / 2) * (p & 1)));
+      if (!first) {
+        bar_wait(q_free, free_par, &abort_sh, a.timeout);
+        free_par ^= 1;
+      }
+      first = false;
+      for (int y = p; y < kRows; y += kLoaders) row_exp_sh[slot_out][y] = 0;
+#pragma unroll 2
+      for (int y = p / CH; y < kRows; y += STEP) {
+        const bool live = y < it.rows;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(place(y))),
+                     "l"(live ? row_of(y) + 8 * cl : (const __nv_bfloat16*)a.q), "r"(live ? 16 : 0) : "memory");
+      }
+      cp_async_wait_all();
+      // a thread converts the pieces it has copied
+      auto convert = [&](int y, float qs) {
+        uint4* at = reinterpret_cast<uint4*>(place(y));
+        const uint4 x = *at;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
+          o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
+                                               __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+        return max(m & 0xffffu, m >> 16);   // the largest magnitude's bits
+      };
+      uint32_t big = 0;
+#pragma unroll 4
+      for (int y = p / CH; y < kRows; y += STEP) big = max(big, convert(y, 1.f));
+      const bool all_fit = loaders_all(big < 0x4700u), all_good = loaders_all(good);   // 0x4700: 2^15
+      if (!all_fit) {
+        // CH lanes share a row; the rows of a step need not divide 256
+#pragma unroll 1
+        for (int y0 = 0; y0 < kRows; y0 += STEP) {
+          const int y = y0 + p / CH;
+          const bool live = y < it.rows;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(row_of(y) + 8 * cl);
+          uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (int o = CH / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const int ex = (int)(m >> 7) - 127, e = ex > 14 ? ex - 14 : 0;
+          if (live) {
+            *reinterpret_cast<uint4*>(place(y)) = v;
+            convert(y, __uint_as_float((uint32_t)(127 - e) << 23));
+            if (cl == 0) row_exp_sh[slot_out][y] = (uint8_t)e;
+          }
+        }
+      }
+      if (p == 0) bad_item_sh[slot_out] = !all_good;
+      slot_out ^= 1;
+      fence_async_smem();
+      bar_arrive(q_ready);
+      more = it.next(a);
+    }
   }
   fence_before();
   __syncthreads();
