@@ -37,6 +37,7 @@ _RELEASE = struct.Struct("=7q3i4x")
 _APPEND = struct.Struct("=17q4i")
 _ATTEND = struct.Struct("=17q9ifi4x")
 
+_Tensor, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
 _DTYPES = {torch.bfloat16: QWM_BF16, torch.float32: QWM_F32}
 _workspace_bytes: dict = {}
 
@@ -58,29 +59,33 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _run(fn, args: bytes, what: str, dev: torch.device):
-    index = dev.index
+def _run(fn, args: bytes, what: str, index: int):
+    """fn(args) on device `index` and its current stream."""
     if index == _current_device():
         st = fn(args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             st = fn(args, _raw_stream(index))
     if st:
         _check(st, what)
 
 
-def _rows(x, what: str, like=None, shape=None):
+# The checks read each attribute of a tensor once, and the number of its device
+# (-1: the CPU) for the device itself: a small step costs the host more than
+# the GPU.
+
+def _rows(x, what: str, dtype=None, index=None, shape=None):
     """A CUDA tensor [rows, heads, d] in bf16 or float32 with contiguous heads
-    of 16-byte aligned vectors (any row and head stride), on like's device in
-    like's dtype (and of `shape`, where given); returns (pointer, row stride,
+    of 16-byte aligned vectors (any row and head stride), and where given of
+    `dtype` on device `index` and of `shape`; returns (pointer, row stride,
     head stride)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+    if not isinstance(x, _Tensor) or not x.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor is expected")
     dt, have = x.dtype, x.shape
     if len(have) != 3 or dt not in _DTYPES:
         raise ValueError(f"{what}: a bfloat16 or float32 tensor [rows, heads, d] is expected, got {dt} {tuple(have)}")
-    if like is not None and (dt != like.dtype or x.device != like.device):
-        raise ValueError(f"{what}: expected {like.dtype} on {like.device}, got {dt} on {x.device}")
+    if dtype is not None and (dt is not dtype or x.get_device() != index):
+        raise ValueError(f"{what}: expected {dtype} on cuda:{index}, got {dt} on {x.device}")
     if shape is not None and have != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(have)}")
     s0, s1, s2 = x.stride()
@@ -91,17 +96,24 @@ def _rows(x, what: str, like=None, shape=None):
     if s2 != 1 and have[2] != 1:
         raise ValueError(f"{what}: the channels of a head have to be contiguous")
     p = x.data_ptr()
-    if (p | (s0 | s1) * x.itemsize) & 15:
+    if (p | (s0 | s1) * (2 if dt is _BF16 else 4)) & 15:
         raise ValueError(f"{what}: pointer and strides have to be multiples of 16 bytes")
     return p, s0, s1
 
 
-def _array(x, what: str, dtype, shape, dev):
-    """The pointer of a contiguous tensor of `dtype` and `shape` (None: any) on `dev`."""
-    if not isinstance(x, torch.Tensor) or x.device != dev:
-        raise ValueError(f"{what}: a tensor on {dev} is expected")
+def _like(x):
+    """An uninitialised contiguous tensor like x, and its pointer and strides."""
+    T, h, d = x.shape
+    y = torch.empty_like(x) if x.is_contiguous() else torch.empty((T, h, d), dtype=x.dtype, device=x.device)
+    return y, (y.data_ptr(), h * d, d)
+
+
+def _array(x, what: str, dtype, shape, index: int):
+    """The pointer of a contiguous tensor of `dtype` and `shape` (None: any) on device `index`."""
+    if not isinstance(x, _Tensor) or x.get_device() != index:
+        raise ValueError(f"{what}: a tensor on cuda:{index} is expected")
     have = x.shape
-    if x.dtype != dtype or len(have) != len(shape) or not x.is_contiguous():
+    if x.dtype is not dtype or len(have) != len(shape) or not x.is_contiguous():
         raise ValueError(f"{what}: a contiguous {len(shape)}-d {dtype} tensor is expected, got {x.dtype} {tuple(have)}")
     if have != shape:
         for n, want in zip(have, shape):
@@ -110,13 +122,13 @@ def _array(x, what: str, dtype, shape, dev):
     return x.data_ptr()
 
 
-def _status(x, dev):
-    return 0 if x is None else _array(x, "status", torch.int32, (1,), dev)
+def _status(x, index: int):
+    return 0 if x is None else _array(x, "status", _I32, (1,), index)
 
 
 def _page_tokens(pool, d: int) -> int:
     """Tokens of a page of `pool` [pages, kv_heads, block] for heads of d channels."""
-    if not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != 3 \
+    if not isinstance(pool, _Tensor) or not pool.is_cuda or pool.dtype is not torch.uint8 or pool.dim() != 3 \
             or not pool.is_contiguous():
         raise ValueError("pool: a contiguous CUDA uint8 tensor [pages, kv_heads, block bytes] is expected")
     page, rest = divmod(4 * pool.shape[2], 5 * d)
@@ -153,29 +165,27 @@ def qwm_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     works in place."""
     qr = _rows(q, "q")
     T, hq, d = q.shape
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=dt, device=dev)
-        qo = (q_out.data_ptr(), hq * d, d)
+        q_out, qo = _like(q)
     else:
-        qo = _rows(q_out, "q_out", q, q.shape)
+        qo = _rows(q_out, "q_out", dt, dev, q.shape)
     hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
-        kr = _rows(k, "k", q)
+        kr = _rows(k, "k", dt, dev)
         tk, hk, dk = k.shape
         if tk != T or dk != d:
             raise ValueError(f"k: expected [{T}, kv_heads, {d}], got {tuple(k.shape)}")
         if k_out is None:
-            k_out = torch.empty((T, hk, d), dtype=dt, device=dev)
-            ko = (k_out.data_ptr(), hk * d, d)
+            k_out, ko = _like(k)
         else:
-            ko = _rows(k_out, "k_out", k, k.shape)
+            ko = _rows(k_out, "k_out", dt, dev, k.shape)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out, k_weight: given without k")
-    table = _array(cos_sin, "cos_sin", torch.float32, (None, None), dev)
+    table = _array(cos_sin, "cos_sin", _F32, (None, None), dev)
     n_pos, rot = cos_sin.shape
-    axes = positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
-    pos = _array(positions, "positions", torch.int32, (T, axes) if axes else (T,), dev)
+    axes = positions.shape[1] if isinstance(positions, _Tensor) and positions.dim() == 2 else 0
+    pos = _array(positions, "positions", _I32, (T, axes) if axes else (T,), dev)
     axes = axes or 1
     if axes > 4:
         raise ValueError("positions: 1 to 4 axes")
@@ -205,10 +215,9 @@ def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: tor
     the rest is returned, in `out` where given (its kv_len and free_count may
     be the inputs themselves).  Nothing changes when it does not fit: then
     cu_rows is 0 throughout, every slot -1, and `status` has DEV_CAPACITY."""
-    dev = kv_len.device if isinstance(kv_len, torch.Tensor) else None
-    if dev is None or not kv_len.is_cuda:
+    if not isinstance(kv_len, _Tensor) or not kv_len.is_cuda:
         raise ValueError("kv_len: a CUDA tensor is expected")
-    i32, i64 = torch.int32, torch.int64
+    dev, i32 = kv_len.get_device(), _I32
     a = _array(kv_len, "kv_len", i32, (None,), dev)
     B = kv_len.shape[0]
     b = _array(new_len, "new_len", i32, (B,), dev)
@@ -217,16 +226,15 @@ def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: tor
     e = _array(block_table, "block_table", i32, (B, None), dev)
     if out is None:
         # two allocations for the five
-        flat = torch.empty(rows + 2 * B + 2, dtype=i32, device=dev)
-        slots = torch.empty(rows, dtype=i64, device=dev)
-        view = flat.as_strided
-        out = PagedPlan(view((B,), (1,), rows), view((1,), (1,), rows + 2 * B + 1), view((B + 1,), (1,), rows + B), slots,
-                        view((rows,), (1,), 0))
+        flat = kv_len.new_empty(rows + 2 * B + 2)
+        slots = kv_len.new_empty(rows, dtype=_I64)
+        positions, lens, cu, count = flat.split_with_sizes((rows, B, B + 1, 1))
+        out = PagedPlan(lens, count, cu, slots, positions)
         base = flat.data_ptr()
         ptr = (base + 4 * rows, base + 4 * (rows + 2 * B + 1), base + 4 * (rows + B), slots.data_ptr(), base)
     else:
         ptr = (_array(out.kv_len, "out.kv_len", i32, (B,), dev), _array(out.free_count, "out.free_count", i32, (1,), dev),
-               _array(out.cu_rows, "out.cu_rows", i32, (B + 1,), dev), _array(out.slots, "out.slots", i64, (rows,), dev),
+               _array(out.cu_rows, "out.cu_rows", i32, (B + 1,), dev), _array(out.slots, "out.slots", _I64, (rows,), dev),
                _array(out.positions, "out.positions", i32, (rows,), dev))
     _run(lib().qwm_paged_plan,
          _PLAN.pack(a, b, c, d, e, *ptr, _status(status, dev), rows, free_pages.shape[0], B, block_table.shape[1],
@@ -239,10 +247,9 @@ def qwm_paged_release(keep_len: torch.Tensor, kv_len: torch.Tensor, block_table:
     """Cut every request back to keep_len[b] tokens (0: it ends) and push the
     pages it gives up on the free stack; kv_len, block_table, free_pages and
     free_count are updated in place."""
-    dev = kv_len.device if isinstance(kv_len, torch.Tensor) else None
-    if dev is None or not kv_len.is_cuda:
+    if not isinstance(kv_len, _Tensor) or not kv_len.is_cuda:
         raise ValueError("kv_len: a CUDA tensor is expected")
-    i32 = torch.int32
+    dev, i32 = kv_len.get_device(), _I32
     a = _array(kv_len, "kv_len", i32, (None,), dev)
     B = kv_len.shape[0]
     _run(lib().qwm_paged_release,
@@ -258,22 +265,22 @@ def qwm_paged_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, slots
     """Quantise keys and values [rows, kv_heads, d] to 4 bits into the slots
     (int64 [rows], -1: no slot) of the pool.  k_hat, v_hat receive the values
     that the stored bytes stand for (0 in rows without a slot)."""
-    kr, vr = _rows(k, "k"), _rows(v, "v", k)
-    T, hk, d = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    dev = k.device
+    kr = _rows(k, "k")
+    shape, dt, dev = k.shape, k.dtype, k.get_device()
+    T, hk, d = shape
+    vr = _rows(v, "v", dt, dev, shape)
     page = _page_tokens(pool, d)
-    if pool.device != dev or pool.shape[1] != hk:
-        raise ValueError(f"pool: expected [pages, {hk}, block] on {dev}, got {tuple(pool.shape)} on {pool.device}")
-    kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", k, k.shape)
-    vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", v, v.shape)
+    n_pages, hp, _ = pool.shape
+    if pool.get_device() != dev or hp != hk:
+        raise ValueError(f"pool: expected [pages, {hk}, block] on {k.device}, got {tuple(pool.shape)} on {pool.device}")
+    kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", dt, dev, shape)
+    vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", dt, dev, shape)
     _run(lib().qwm_paged_append,
-         _APPEND.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), _array(slots, "slots", torch.int64, (T,), dev), _status(status, dev),
-                      T, pool.shape[0], _DTYPES[k.dtype], d, hk, page), "qwm_paged_append", dev)
+         _APPEND.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), _array(slots, "slots", _I64, (T,), dev), _status(status, dev),
+                      T, n_pages, _DTYPES[dt], d, hk, page), "qwm_paged_append", dev)
 
 
-def _workspace_size(dev: torch.device, d: int) -> int:
+def _workspace_size(dev: int, d: int) -> int:
     with torch.cuda.device(dev):
         n = int(lib().qwm_paged_attend_workspace_bytes(d))
     if n == 0:
@@ -294,26 +301,25 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     exp.  Rows behind the last request are left as they were in `out`."""
     qr = _rows(q, "q")
     T, hq, d = q.shape
-    dev = q.device
+    dev, dt = q.get_device(), q.dtype
     page = _page_tokens(pool, d)
     n_pages, hk, _ = pool.shape
-    if pool.device != dev or hk < 1 or hq % hk:
-        raise ValueError(f"pool: kv heads that divide {hq} on {dev} are expected, got {tuple(pool.shape)} on {pool.device}")
+    if pool.get_device() != dev or hk < 1 or hq % hk:
+        raise ValueError(f"pool: kv heads that divide {hq} on {q.device} are expected, got {tuple(pool.shape)} on {pool.device}")
     if out is None:
-        out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
-        ot = (out.data_ptr(), hq * d, d)
+        out, ot = _like(q)
     else:
-        ot = _rows(out, "out", q, q.shape)
-    table = _array(block_table, "block_table", torch.int32, (None, None), dev)
+        ot = _rows(out, "out", dt, dev, q.shape)
+    table = _array(block_table, "block_table", _I32, (None, None), dev)
     B, width = block_table.shape
-    lens = _array(kv_len, "kv_len", torch.int32, (B,), dev)
-    cu = _array(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
-    ls = 0 if lse is None else _array(lse, "lse", torch.float32, (T, hq), dev)
+    lens = _array(kv_len, "kv_len", _I32, (B,), dev)
+    cu = _array(cu_rows, "cu_rows", _I32, (B + 1,), dev)
+    ls = 0 if lse is None else _array(lse, "lse", _F32, (T, hq), dev)
     n_ws = _workspace_bytes.get((dev, d)) or _workspace_size(dev, d)
-    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev)
+    ws = pool.new_empty(n_ws)
     _run(lib().qwm_paged_attend,
          _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
-                      T if max_new is None else max_new, _DTYPES[q.dtype], d, hq, hk, page, B, width, 1 if causal else 0,
+                      T if max_new is None else max_new, _DTYPES[dt], d, hq, hk, page, B, width, 1 if causal else 0,
                       window, scale, kernel), "qwm_paged_attend", dev)
     return out
 
