@@ -10,10 +10,17 @@
 // next tile's packed bytes (without that the page ids' and the codes' latency
 // lay between every two tiles: 38 us of the windowed batch below), and every
 // thread computes RT rows x KT keys of S and RT rows x CT channels of O from
-// registers.  Items have R = 64 rows, or 8 when no request has more than 8
-// (single-token steps: with 64 the arithmetic on absent rows would be 8 times
-// the work on present ones).  Bound by the float32 FMA rate for many rows and
-// by the shared-memory reads of one K element per FMA for few.
+// registers, two float32 multiply-adds an instruction (S: even and odd channels
+// apart, O: neighbouring channels).  Items have R = 64 rows, or 8 when no
+// request has more than 8 (single-token steps: with 64 the arithmetic on absent
+// rows would be 8 times the work on present ones).  Bound by the float32 FMA
+// rate and the shared-memory reads beside it (96 wavefronts to 128 cycles of
+// FMA a step of 4 channels), with two warps a scheduler to overlap them.
+// Measured: three windowed requests (30 to 260 rows, 1,001 tokens visible, 8
+// heads over 4, d = 64) 32 us, of one-wide multiply-adds and scalar reads of V
+// 35 us; 2,048 rows over 10,240 tokens 1.22 ms (32 TFLOP/s), at d = 128 2.08 ms
+// (37).  Two CTAs an SM (128 registers) bring the long d = 64 case to 1.09 ms,
+// but the short one to 37.5 us and d = 128, which spills, to 2.46 ms.
 #include "paged_internal.cuh"
 
 namespace qwm {
@@ -27,6 +34,7 @@ struct Shape {
   static constexpr int TX = R == 64 ? 16 : 32;   // threads along the keys (and channels) of a row group
   static constexpr int TY = kNt / TX;
   static constexpr int RT = R / TY, KT = kTk / TX, CT = D / TX;
+  static constexpr int CW = CT < 4 ? CT : 4;     // channels of a thread that are neighbours
   static constexpr int LD = D + 4, LP = kTk + 4;
   static constexpr int floats = (R + kTk) * LD + kTk * D + R * LP;
 };
@@ -43,6 +51,20 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+
+// channel j of a thread
+template <class S>
+__device__ __forceinline__ int channel(int tx, int j) { return (j / S::CW) * S::TX * S::CW + tx * S::CW + j % S::CW; }
+
+__device__ __forceinline__ void load_run(const float* p, float2 (&x)[2]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
+}
+__device__ __forceinline__ void load_run(const float* p, float2 (&x)[1]) { x[0] = *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store_pair(float* p, float2 x) { *reinterpret_cast<float2*>(p) = x; }
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 x) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x.x, x.y);
 }
 
 template <int D, int R, class T>
@@ -76,7 +98,8 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 #pragma unroll
       for (int k = 0; k < 8; ++k) Qs[r * S::LD + c + k] = x[k] * a.scale_log2;
     }
-    float o[S::RT][S::CT], m[S::RT], l[S::RT];
+    float2 o[S::RT][S::CT / 2];
+    float m[S::RT], l[S::RT];
     int top[S::RT], bottom[S::RT];      // a row sees bottom <= n < top
 #pragma unroll
     for (int i = 0; i < S::RT; ++i) {
@@ -91,7 +114,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       }
       if (r >= it.rows) top[i] = 0;
 #pragma unroll
-      for (int j = 0; j < S::CT; ++j) o[i][j] = 0.f;
+      for (int j = 0; j < S::CT / 2; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
     // the next tile's packed bytes, on their way during this one's arithmetic:
     // thread's code words i = tid, tid + 256, ... of [half][token][word]
@@ -138,10 +161,11 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       __syncthreads();
       if (t + 1 < it.to) fetch(n0 + kTk);
       float s[S::RT][S::KT];
+      float2 s2[S::RT][S::KT];   // even and odd channels
 #pragma unroll
       for (int i = 0; i < S::RT; ++i)
 #pragma unroll
-        for (int j = 0; j < S::KT; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < S::KT; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
         float4 kv[S::KT];
@@ -152,9 +176,14 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
           const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * S::RT + i) * S::LD + c);
 #pragma unroll
           for (int j = 0; j < S::KT; ++j)
-            s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
+            s2[i][j] = __ffma2_rn(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y),
+                                  __ffma2_rn(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), s2[i][j]));
         }
       }
+#pragma unroll
+      for (int i = 0; i < S::RT; ++i)
+#pragma unroll
+        for (int j = 0; j < S::KT; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
 #pragma unroll
       for (int i = 0; i < S::RT; ++i) {
         float mx = m[i];
@@ -180,7 +209,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
         l[i] = fmaf(l[i], corr, sum);
         m[i] = mx;
 #pragma unroll
-        for (int j = 0; j < S::CT; ++j) o[i][j] *= corr;
+        for (int j = 0; j < S::CT / 2; ++j) o[i][j] = __fmul2_rn(o[i][j], make_float2(corr, corr));
       }
       __syncwarp();   // a row's P is written and read by the same warp
 #pragma unroll 2
@@ -191,12 +220,14 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int j = 0; j < S::CT; ++j) {
-            const float v = Vs[(n + k) * D + tx + S::TX * j];
+          for (int j = 0; j < S::CT; j += S::CW) {
+            float2 v[S::CW / 2];
+            load_run(Vs + (n + k) * D + channel<S>(tx, j), v);
 #pragma unroll
             for (int i = 0; i < S::RT; ++i) {
               const float pk = k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w;
-              o[i][j] = fmaf(pk, v, o[i][j]);
+#pragma unroll
+              for (int x = 0; x < S::CW / 2; ++x) o[i][j / 2 + x] = __ffma2_rn(make_float2(pk, pk), v[x], o[i][j / 2 + x]);
             }
           }
       }
@@ -213,12 +244,15 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
         const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T* dst = (T*)a.out + tok * a.o_row + head * a.o_head;
 #pragma unroll
-        for (int j = 0; j < S::CT; ++j) dst[tx + S::TX * j] = (T)(o[i][j] * inv);
+        for (int j = 0; j < S::CT; j += 2) {
+          const float2 y = __fmul2_rn(o[i][j / 2], make_float2(inv, inv));
+          store_pair(dst + channel<S>(tx, j), y);
+        }
         if (a.lse && tx == 0) a.lse[tok * a.heads + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
       } else {
         float* dst = part_row(a, w, slot, R, r, D);
 #pragma unroll
-        for (int j = 0; j < S::CT; ++j) dst[tx + S::TX * j] = o[i][j];
+        for (int j = 0; j < S::CT; j += 2) store_pair(dst + channel<S>(tx, j), o[i][j / 2]);
         if (tx == 0) dst[D] = m[i], dst[D + 1] = l[i];
       }
     }
