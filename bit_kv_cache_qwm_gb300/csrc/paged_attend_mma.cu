@@ -29,7 +29,7 @@
 // one exact subtraction (or fused multiply by 1/16), and c scale + zero by one
 // fused multiply-add: the only rounding of k_hat and v_hat.  Q is float16
 // scaled per row by a power of two (exact).  The rows' sums and O are float32;
-// O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8).
+// O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^15).
 // Tokens outside a request (or on a page out of range) have their logits
 // replaced and their value parameters zeroed, so garbage bytes do no harm.
 //
@@ -47,6 +47,10 @@ using namespace tcx;
 
 constexpr int kCw = 4, kCtas = 3, kStages = 2, kSub = 2, kTk = 16 * kSub * kCw, kNt = kCw * 32, kItem = 2;
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
+// Where a row's maximum is x0 when it is taken, m = x0 - 7, and it is taken again
+// when a logit passes x0 + 8: P <= 2^15 stays inside float16, and a token of a
+// long cache is lost only below 2^-25 / 2^7 of the largest weight
+constexpr float kBelow = 7.f, kGrow = 8.f;
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -367,9 +371,9 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
             mx0 = max3f(mx0, s[nb][e][0], s[nb][e][2]);
             mx1 = max3f(mx1, s[nb][e][1], s[nb][e][3]);
           }
-          mx0 *= c2[nb][0];
-          mx1 *= c2[nb][1];
-          if (__any_sync(0xffffffffu, mx0 > m[nb][0] + 8.f || mx1 > m[nb][1] + 8.f)) {
+          mx0 = fmaf(mx0, c2[nb][0], -kBelow);
+          mx1 = fmaf(mx1, c2[nb][1], -kBelow);
+          if (__any_sync(0xffffffffu, mx0 > m[nb][0] + kGrow || mx1 > m[nb][1] + kGrow)) {
             // rare: the rows' maxima over the tokens, and O rescaled
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
@@ -378,8 +382,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
             }
             // a row that does not need it keeps its maximum, so its bits do
             // not depend on its neighbours
-            mx0 = mx0 > m[nb][0] + 8.f ? mx0 : m[nb][0];
-            mx1 = mx1 > m[nb][1] + 8.f ? mx1 : m[nb][1];
+            mx0 = mx0 > m[nb][0] + kGrow ? mx0 : m[nb][0];
+            mx1 = mx1 > m[nb][1] + kGrow ? mx1 : m[nb][1];
             const float f0 = ex2(m[nb][0] - mx0), f1 = ex2(m[nb][1] - mx1);
             m[nb][0] = mx0, m[nb][1] = mx1;
             l[nb][0] *= f0, l[nb][1] *= f1;

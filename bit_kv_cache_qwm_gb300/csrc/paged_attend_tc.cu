@@ -8,7 +8,8 @@
 // another token by token) and tiles of 128 tokens.  Warp roles (16 warps):
 //   warps 0-3 / 4-7  softmax of query tile a / b, thread = row = TMEM lane:
 //                    per tile the online softmax in the exp2 domain with O
-//                    rescaled only when the maximum grows by more than 2^8, P
+//                    rescaled only when the maximum grows by more than 2^8 (P <=
+//                    2^15), P
 //                    in float16 over the first 64 columns of S; at the item's
 //                    end O from TMEM to memory.
 //   warps 8-11       producers, thread = token: the packed codes (64 + 64
@@ -60,6 +61,10 @@ using namespace tcx;
 constexpr int kTk = 128, kRows = 256, kNt = 16 * 32, kProd = 8, kMma = 12, kLoad = 13, kItem = 6;
 constexpr uint32_t kColO = 256;
 constexpr float kNone = -3.0e38f;
+// Where a row's maximum is x0 when it is taken, m = x0 - 7, and it is taken again
+// when a logit passes x0 + 8: P <= 2^15 stays inside float16, and a token of a
+// long cache is lost only below 2^-25 / 2^7 of the largest weight
+constexpr float kBelow = 7.f, kGrow = 8.f;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
 constexpr uint32_t kIdescS = (1u << 4) | (16u << 17) | (8u << 24);
 
@@ -299,8 +304,8 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         tmem_wait_ld();
         if (!full) hide_keys<64>(v, 0, hi);
         mx = fmaxf(mx, max64(v));
-        const float mnew = fmaxf(m_run, mx * c2);
-        const bool need = mnew > m_run + 8.f;
+        const float mnew = mx * c2 - kBelow;
+        const bool need = mnew > m_run + kGrow;
         // S_g(t) follows PV_g(t-1) in the tensor pipe's order, so O_g is complete
         if (t > it.from && __any_sync(0xffffffffu, need)) {
           const float corr = need ? ex2(m_run - mnew) : 1.f;

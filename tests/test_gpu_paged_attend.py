@@ -282,3 +282,43 @@ def test_on_another_stream(paged, kernel):
         after = got.clone()
     s.synchronize()
     assert torch.equal(after, ref)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d, key", [(64, 2.203125), (128, 1.5625)])
+def test_small_weights_beside_a_large_one(paged, kernel, d, key):
+    """One token outweighs each of the others by about 2^25.5 and has the value
+    0, the others the value 1: O is what the small weights add up to.  All
+    codes, logits and values are exact.  P is float16 with the maximum at 2^7
+    or more, so a small weight w keeps an error of half its smallest step, 2^-25
+    / 2^7, relative to w = 2^-diff; the exponential, the sums of 200 tokens and
+    the logit (float32, below 2^5) make less than 2^-16; O is rounded to bf16."""
+    page, n = 16, 200
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    k[0], v[0] = key, 0
+    width = -(-n // page)
+    pool = paged.paged_pool(width, 1, d, page)
+    table = torch.arange(width, dtype=torch.int32, device="cuda")[None].contiguous()
+    paged.qwm_paged_append(k, v, pool, torch.arange(n, device="cuda"))
+    q = torch.ones(2, 1, d, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = paged.qwm_paged_attend(q, pool, table, torch.tensor([n], **i32), torch.tensor([0, 2], **i32), max_new=2,
+                                 causal=False, kernel=kid(paged, kernel))
+    diff = np.sqrt(d) * key / np.log(2)
+    want = (n - 1) * 2.0 ** -diff / (1 + (n - 1) * 2.0 ** -diff)
+    rel = 2.0 ** (diff - 32) + 2.0 ** -16 + 2.0 ** -8
+    assert ((out.double().cpu() - want).abs() <= rel * want).all(), out[0, 0, :4]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("new", [1, 300])
+def test_in_place(paged, kernel, new):
+    """out may be q: every row is read by those who need it before it is
+    written, whole items and cut ones alike."""
+    bt = Batch(16, [40, 5000, 0, 700], [new] * 4, 8, 2, 64, 16)
+    args = (dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+    q = dev(bt.q, "bf16")
+    ref = paged.qwm_paged_attend(q, *args, max_new=new, kernel=kid(paged, kernel))
+    got = paged.qwm_paged_attend(q, *args, max_new=new, kernel=kid(paged, kernel), out=q)
+    assert got is q and torch.equal(q, ref)
