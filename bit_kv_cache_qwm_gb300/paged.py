@@ -104,7 +104,7 @@ def _rows(x, what: str, dtype=None, index=None, shape=None):
 def _like(x):
     """An uninitialised contiguous tensor like x, and its pointer and strides."""
     T, h, d = x.shape
-    y = torch.empty_like(x) if x.is_contiguous() else torch.empty((T, h, d), dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x) if x.is_contiguous() else x.new_empty((T, h, d))
     return y, (y.data_ptr(), h * d, d)
 
 
