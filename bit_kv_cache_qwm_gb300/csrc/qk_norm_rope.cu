@@ -15,8 +15,11 @@
 // is read once a row; its loads do not hold up the first heads' loads.
 // Bound by HBM (every element is read and written once) and, in bf16, by the
 // ~60 instructions of a step: with pairs in lanes apart (8 shuffles), per-head
-// addresses from the strides and scalar arithmetic a step took 215 and the
-// chunk below 34 us.
+// addresses from the strides and scalar arithmetic a step took 215.  4,680 rows
+// of 48 heads, d = 128, bf16: 25.5 us (4.6 TB/s; 34 us with those 215), 32,760
+// rows of 16 heads, d = 64, float32: 48 us (5.7 TB/s).  Fewer heads a warp, so
+// that the last wave of warps is full, took 27.6 us: the table and the weights
+// are read once more for each.
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
 
