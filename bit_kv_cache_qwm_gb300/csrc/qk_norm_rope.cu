@@ -16,10 +16,8 @@
 // Bound by HBM (every element is read and written once) and, in bf16, by the
 // ~60 instructions of a step: with pairs in lanes apart (8 shuffles), per-head
 // addresses from the strides and scalar arithmetic a step took 215.  4,680 rows
-// of 48 heads, d = 128, bf16: 25.5 us (4.6 TB/s; 34 us with those 215), 32,760
-// rows of 16 heads, d = 64, float32: 48 us (5.7 TB/s).  Fewer heads a warp, so
-// that the last wave of warps is full, took 27.6 us: the table and the weights
-// are read once more for each.
+// of 48 heads, d = 128, bf16: 23.6 us (5.0 TB/s; 34 us with those 215), 32,760
+// rows of 16 heads, d = 64, float32: 48 us (5.7 TB/s).
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
 
@@ -55,8 +53,12 @@ struct Vec4<__nv_bfloat16> {
   }
 };
 
-// steps whose loads are in flight together
+// steps whose loads are in flight together, and whether the next ones are sent
+// for before these are worked on: in bf16 the chunk takes 25.5 us without, in
+// float32, where they are twice the registers, 48 us without and 55 us with
 constexpr int kAhead = 3;
+template <class T>
+constexpr bool kEarly = sizeof(T) == 2;
 
 // ADJ: pairs are adjacent channels
 template <int D, bool ADJ, class T>
@@ -85,14 +87,19 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
     const int64_t src_step = PER * in.head_stride, dst_step = PER * out.head_stride;
     float2 ca[2], sa[2], cb[2], sb[2];   // w_a c, w_a s, w_b c, -w_b s
     bool ready = false;
-    for (int n = n0; n < n1; n += kAhead * PER) {
-      Vec4<T> v[kAhead][2];
+    Vec4<T> next[kAhead][2];
+    auto fetch = [&](int n) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (n + u * PER + sub < n1) {
-          v[u][0].load(src + u * src_step + o0);
-          v[u][1].load(src + u * src_step + o1);
+          next[u][0].load(src + u * src_step + o0);
+          next[u][1].load(src + u * src_step + o1);
         }
+      src += kAhead * src_step;
+    };
+    if (kEarly<T>) fetch(n0);
+    for (int n = n0; n < n1; n += kAhead * PER) {
+      if (!kEarly<T>) fetch(n);
       if (first) {
         first = false;
         bool skip = false, over = false;
@@ -157,6 +164,10 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
           sb[k] = __fmul2_rn(make_float2(-w1[k].x, -w1[k].y), si[k]);
         }
       }
+      Vec4<T> v[kAhead][2];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) v[u][0] = next[u][0], v[u][1] = next[u][1];
+      if (kEarly<T>) fetch(n + kAhead * PER);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (n + u * PER >= n1) break;   // the whole warp
@@ -195,7 +206,6 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
           Vec4<T>::store(dst + u * dst_step + o1, z[0], z[1]);
         }
       }
-      src += kAhead * src_step;
       dst += kAhead * dst_step;
     }
   };
@@ -207,7 +217,9 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
 
 cudaError_t launch_qk_norm_rope(const qwm_qk_norm_rope_args& a, cudaStream_t st) {
   // a warp takes a whole row when the rows alone fill the machine with 32
-  // warps an SM, else fewer heads, down to one step
+  // warps an SM, else fewer heads, down to one step (4,680 rows: one warp a row
+  // 25.5 us, two, as here, 23.6, three 27.7, which read the table and the
+  // weights once more each)
   const int step = 32 / (a.head_dim / 8), heads = a.q_heads + a.k_heads, steps = (heads + step - 1) / step;
   const int64_t want = ((int64_t)sm_count() * 32 + a.rows - 1) / a.rows;
   const int split = (int)(want < steps ? want : steps), per = (steps + split - 1) / split * step;
