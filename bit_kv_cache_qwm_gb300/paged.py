@@ -40,6 +40,7 @@ _ATTEND = struct.Struct("=17q9ifi4x")
 _Tensor, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
 _DTYPES = {torch.bfloat16: QWM_BF16, torch.float32: QWM_F32}
 _workspace_bytes: dict = {}
+_INT_MAX = 2 ** 31 - 1   # a window beyond it is one as well
 
 
 class PagedPlan(NamedTuple):
@@ -103,8 +104,8 @@ def _rows(x, what: str, dtype=None, index=None, shape=None):
 
 def _like(x):
     """An uninitialised contiguous tensor like x, and its pointer and strides."""
-    T, h, d = x.shape
-    y = torch.empty_like(x) if x.is_contiguous() else x.new_empty((T, h, d))
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _, h, d = x.shape
     return y, (y.data_ptr(), h * d, d)
 
 
@@ -226,8 +227,9 @@ def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: tor
     e = _array(block_table, "block_table", i32, (B, None), dev)
     if out is None:
         # two allocations for the five
-        flat = kv_len.new_empty(rows + 2 * B + 2)
-        slots = kv_len.new_empty(rows, dtype=_I64)
+        at = kv_len.device
+        flat = torch.empty(rows + 2 * B + 2, dtype=i32, device=at)
+        slots = torch.empty(rows, dtype=_I64, device=at)
         positions, lens, cu, count = flat.split_with_sizes((rows, B, B + 1, 1))
         out = PagedPlan(lens, count, cu, slots, positions)
         base = flat.data_ptr()
@@ -320,7 +322,7 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     _run(lib().qwm_paged_attend,
          _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
                       T if max_new is None else max_new, _DTYPES[dt], d, hq, hk, page, B, width, 1 if causal else 0,
-                      window, scale, kernel), "qwm_paged_attend", dev)
+                      min(window, _INT_MAX), scale, kernel), "qwm_paged_attend", dev)
     return out
 
 

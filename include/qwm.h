@@ -443,7 +443,9 @@ qwm_status qwm_paged_plan(const qwm_paged_plan_args* a, void* stream);
  * the request as it is and sets QWM_DEV_BOUNDS; a page id outside
  * [0, n_pages) is not pushed and sets it too.  When the stack would pass
  * n_pages (a page released twice) nothing is changed and QWM_DEV_CAPACITY is
- * set.  At most 8192 requests. */
+ * set.  No references are counted: a page that several tables name (a shared
+ * prefix, which the attention reads like any other) would be pushed once for
+ * each, so such pages stay out of this call.  At most 8192 requests. */
 typedef struct {
   const int32_t* keep_len;       /* [requests]                                  */
   int32_t* kv_len;               /* [requests]                                  */
@@ -467,9 +469,9 @@ size_t qwm_paged_block_bytes(int32_t head_dim, int32_t page_tokens);
  *   code = 0 if scale = 0, else clamp(rint(f32(f32(x - zero) / scale)), 0, 15)
  *   x_hat = zero + code scale
  * k_hat and v_hat (optional; dtype, rows like the inputs) receive x_hat
- * rounded to the dtype.  A row with slot -1 (any negative slot) stores
- * nothing, and its k_hat and v_hat are 0; so does a slot >= n_pages
- * page_tokens, which sets QWM_DEV_BOUNDS.  The slots of one call must differ
+ * rounded to the dtype; they overlap neither the inputs nor each other.  A row
+ * with slot -1 (any negative slot) stores nothing, and its k_hat and v_hat are
+ * 0; so does a slot >= n_pages page_tokens, which sets QWM_DEV_BOUNDS.  The slots of one call must differ
  * (those of a plan do): of two rows with the same slot, which one's bytes end
  * up there is undefined. */
 typedef struct {

@@ -322,3 +322,19 @@ def test_in_place(paged, kernel, new):
     ref = paged.qwm_paged_attend(q, *args, max_new=new, kernel=kid(paged, kernel))
     got = paged.qwm_paged_attend(q, *args, max_new=new, kernel=kid(paged, kernel), out=q)
     assert got is q and torch.equal(q, ref)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_shared_prefix_and_endless_window(paged, kernel):
+    """Two requests whose tables name the same pages read the same tokens (not
+    to the same bits: the partition may cut one of them and not the other), and
+    a window longer than any cache hides none."""
+    bt = Batch(17, [200, 200], [2, 2], 4, 2, 128, 32)
+    bt.table[1] = bt.table[0]
+    bt.q[2:] = bt.q[:2]
+    args = (dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+    q = dev(bt.q, "bf16")
+    k = kid(paged, kernel)
+    got = paged.qwm_paged_attend(q, *args, max_new=2, kernel=k)
+    assert check(paged, bt, k) == 0
+    assert torch.equal(paged.qwm_paged_attend(q, *args, max_new=2, window=2 ** 40, kernel=k), got)
