@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 // CTA does: its threads fetch the parts' maxima and sums together, then groups
 // of D/4 lanes add up the parts' O with the factors from shared memory, so
 // that neither waits for one part at a time.  Bound by latency.
-constexpr int kJoinNt = 256, kFewParts = 8, kPartsAtOnce = 256;
+constexpr int kJoinNt = 256, kFewParts = 8, kPartsAtOnce = 256, kEarlyParts = 8;
+static_assert(kPartsAtOnce == kJoinNt, "a thread has a part");
 
 template <int D, class T>
 __device__ __forceinline__ void join_store(const AttendArgs& a, const Join& j, int r, int ch, float4 o, float m, float l) {
@@ -341,28 +342,42 @@ __global__ void __launch_bounds__(kJoinNt) paged_attend_join_kernel(const Attend
     return v;
   };
   for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {
-    float m = -INFINITY;
-    for (int x = tid; x < parts; x += kJoinNt) m = fmaxf(m, part_row(a, w + x, x == 0 ? 1 : 0, R, r, D)[D]);
+    auto part = [&](int x) { return part_row(a, w + x, x == 0 ? 1 : 0, R, r, D); };
+    // the first parts' O, maxima and sums are on their way together
+    float4 early[kEarlyParts];
+#pragma unroll
+    for (int u = 0; u < kEarlyParts; ++u)
+      if (g + u * NG < parts) early[u] = *reinterpret_cast<const float4*>(part(g + u * NG) + 4 * c);
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (tid < parts) mine = *reinterpret_cast<const float2*>(part(tid) + D);
+    float m = mine.x;
+    for (int x = tid + kJoinNt; x < parts; x += kJoinNt) m = fmaxf(m, part(x)[D]);
     m = reduce(m, true);
     const float ref = m == -INFINITY ? 0.f : m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
+    auto add = [&](const float4& v, float f) {
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    };
     for (int x0 = 0; x0 < parts; x0 += kPartsAtOnce) {
       const int n = min(kPartsAtOnce, parts - x0);
       __syncthreads();
       if (tid < n) {
-        const float2 ml = *reinterpret_cast<const float2*>(part_row(a, w + x0 + tid, x0 + tid == 0 ? 1 : 0, R, r, D) + D);
+        const float2 ml = x0 == 0 ? mine : *reinterpret_cast<const float2*>(part(x0 + tid) + D);
         const float f = exp2f(ml.x - ref);
         factor[tid] = f;
         l = fmaf(ml.y, f, l);
       }
       __syncthreads();
-#pragma unroll 8
-      for (int x = g; x < n; x += NG) {
-        const float4 v = *reinterpret_cast<const float4*>(part_row(a, w + x0 + x, x0 + x == 0 ? 1 : 0, R, r, D) + 4 * c);
-        const float f = factor[x];
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      int x = g;
+      if (x0 == 0) {
+#pragma unroll
+        for (int u = 0; u < kEarlyParts; ++u)
+          if (g + u * NG < n) add(early[u], factor[g + u * NG]);
+        x += kEarlyParts * NG;
       }
+#pragma unroll 8
+      for (; x < n; x += NG) add(*reinterpret_cast<const float4*>(part(x0 + x) + 4 * c), factor[x]);
     }
     sum[g][c] = o;
     l = reduce(l, false);   // its barriers publish the groups' sums
