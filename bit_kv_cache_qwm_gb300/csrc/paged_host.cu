@@ -148,7 +148,14 @@ extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) {
 extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new) {
   if (!dtype_ok(dtype) || heads < 1 || kv_heads < 1 || heads % kv_heads || max_new < 0) return -1;
   if (dtype == QWM_F32) return 1;
-  return max_new * (heads / kv_heads) <= 16 ? 2 : 3;
+  // Kernel 2 reads the pages once for 16 rows of a key/value head, kernel 3 once
+  // for 256, of which few rows leave most of its tensor work and softmax empty.
+  // Measured, kernel 2 against 3 in us, d = 128: 48 ragged requests (200 to 16,380
+  // tokens, 32 heads over 8) 105 and 305 at 4 rows, 149 and 309 at 16, 272 and
+  // 312 at 20, 277 and 313 at 32, where it reads twice; four requests of up to
+  // 1,000 tokens 19 and 29 at 32; one of 98,280 tokens 85 and 96 at 30.  A third
+  // pass from 33 rows on costs more than kernel 3.
+  return max_new * (heads / kv_heads) <= 32 ? 2 : 3;
 }
 
 extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {

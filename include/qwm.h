@@ -498,11 +498,14 @@ qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
  * [0, max_blocks page_tokens] is clamped to it and cu_rows that decrease or
  * leave [0, rows] are clamped; each sets QWM_DEV_BOUNDS.
  * max_new is the longest request's row count as the host knows it: it chooses
- * the kernel and never changes what is computed.
+ * the kernel and never changes what is computed.  A step of single tokens and
+ * prompts is better made in two calls, each over its range of requests
+ * (block_table, kv_len and cu_rows from the range's first entry on, q and out
+ * whole), so that either gets its kernel.
  * kernel: 0 = automatic; 1 = float32 CUDA-core kernel (the choice for
- * float32); 2 = bf16 mma.sync kernel that streams the pages once for up to 16
- * rows (heads / kv_heads times max_new); 3 = bf16 tcgen05 kernel with 256 rows
- * per CTA.  All split long requests over CTAs and join the parts in a second
+ * float32); 2 = bf16 mma.sync kernel that streams the pages once for every 16
+ * rows (the choice for heads / kv_heads times max_new up to 32); 3 = bf16
+ * tcgen05 kernel with 256 rows per CTA.  All split long requests over CTAs and join the parts in a second
  * kernel, in a fixed order.  QWM_ERR_UNSUPPORTED: 2 and 3 with float32, more
  * than 2^30 rows times heads / kv_heads, max_blocks page_tokens above 2^30. */
 typedef struct {

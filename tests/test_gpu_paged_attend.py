@@ -338,3 +338,16 @@ def test_shared_prefix_and_endless_window(paged, kernel):
     got = paged.qwm_paged_attend(q, *args, max_new=2, kernel=k)
     assert check(paged, bt, k) == 0
     assert torch.equal(paged.qwm_paged_attend(q, *args, max_new=2, window=2 ** 40, kernel=k), got)
+
+
+def test_a_mixed_step_in_two_calls(paged):
+    """Single tokens and prompts of one plan, each range of requests in a call
+    of its own over the same rows."""
+    bt = Batch(18, [300, 5000, 17, 0, 900], [1, 1, 1, 200, 70], 8, 2, 128, 16)
+    q, pool, table, lens, cu = dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu)
+    out = torch.full_like(q, float("nan"))
+    for a, b in ((0, 3), (3, 5)):
+        paged.qwm_paged_attend(q, pool, table[a:b], lens[a:b], cu[a:b + 1], max_new=max(bt.new[a:b]), out=out)
+    O, _, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, True, 0, 128 ** -0.5)
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert (np.abs(got - O) <= attend_tolerance(O, spread, vmax, int(bt.kv_len.max()), "bf16", True)).all()

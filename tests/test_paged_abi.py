@@ -148,6 +148,7 @@ def test_null_arguments(paged):
         assert fn(None, None) == 1
     assert L.qwm_paged_attend_workspace_bytes(96) == 0
     assert L.qwm_paged_attend_kernel_for(0, 8, 2, 1) == 1
+    assert [L.qwm_paged_attend_kernel_for(1, 8, 2, n) for n in (0, 1, 8, 9, 4096)] == [2, 2, 2, 3, 3]
     assert L.qwm_paged_attend_kernel_for(1, 8, 3, 1) == -1
 
 
