@@ -287,7 +287,7 @@ __device__ __forceinline__ void join_store(const AttendArgs& a, const Join& j, i
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kJoinNt) paged_attend_join_kernel(const AttendArgs a, int R) {
+__global__ void __launch_bounds__(kJoinNt, 3) paged_attend_join_kernel(const AttendArgs a, int R) {
   constexpr int L = D / 4, NG = kJoinNt / L;
   __shared__ __align__(16) float4 sum[NG][L];
   __shared__ float factor[kPartsAtOnce];
