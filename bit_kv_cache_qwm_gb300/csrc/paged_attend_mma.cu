@@ -13,7 +13,7 @@
 // the ragged batch of 48 requests: one producer warp a CTA with bulk copies
 // 155 us, where a thread issues one copy at a time and pages of 16 tokens make
 // 16 a tile; loads to registers two blocks ahead 143 us, too few bytes in
-// flight; this with 16 tokens a step 118 us, with 32 104 us: half the control
+// flight; this with 16 tokens a step 118 us, with 32 103 us: half the control
 // and address instructions, two independent chains of MMAs.)
 //
 // Both products are formed transposed with mma.m16n8k16 (float16 in, float32
@@ -37,7 +37,7 @@
 // warp, half of them the codes' way to float16: that batch (8 K tokens on
 // average, 32 query heads over 8, d = 128, pages of 16) runs at 4.6 TB/s with
 // 61% of the issue slots taken; without arithmetic the same copies take 84 us.
-// One request of 98,280 tokens (40 heads over 8) takes 38 us, 8 to 10 of them
+// One request of 98,280 tokens (40 heads over 8) takes 35 us, 8 to 10 of them
 // the start, the first ids and copies, and the join.
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
@@ -220,9 +220,24 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   // the warp's stages; copies of a lane start 16 bytes a lane into one
   const uint8_t* ring = sm + warp * kStages * kSub * Stage<D>::bytes;
   const uint32_t ring_at = su32(ring) + 16 * lane;
+  // the item's queries, sent for ahead of the copies, which they would queue
+  // behind (2 to 3 us of a first item)
+  uint4 qraw[NB][KW];
+  auto load_q = [&]() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = nb * 8 + (lane >> 2), rr = it.rt * R + r, tok = div_group(a, rr);
+      const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+                                                       (int64_t)(it.h * a.group + rr - tok * a.group) * a.q_head + (lane & 3) * (D / 4));
+#pragma unroll
+      for (int i = 0; i < KW; ++i) qraw[nb][i] = r < it.rows ? src[i] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_q();
   uint32_t have = 0;     // kSub bits for each stage: which 16 tokens there are
   for (int i = 0; i < kStages; ++i) have |= ahead.copy(a, ring_at + i * kSub * Stage<D>::bytes, warp, lane) << (kSub * i);
   int st = 0;
+  bool more = true;
 
   const int g = lane >> 2, c = lane & 3;
   const int tok0 = token_of(g), ta = token_of(2 * c), tb = token_of(2 * c + 1);   // this lane's key, its values
@@ -237,16 +252,11 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
     int top_min = it.hi, bottom_max = it.lo;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int rr = it.rt * R + nb * 8 + g;
-      const bool live = nb * 8 + g < it.rows;
       float x[D / 4];
       float mx = 0.f;
-      const int tok = live ? div_group(a, rr) : 0, head = live ? it.h * a.group + rr - div_group(a, rr) * a.group : 0;
-      const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
-                                                       head * a.q_head + c * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = live ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint4 u = qraw[nb][i];
         const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -520,8 +530,10 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
         record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), R);
       }
     }
+    more = it.next(a);
     __syncthreads();
-  } while (it.next(a));
+    if (more) load_q();
+  } while (more);
 }
 
 template <int D, int NB>
