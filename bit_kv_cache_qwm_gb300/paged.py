@@ -226,14 +226,12 @@ def qwm_paged_plan(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: tor
     d = _array(free_count, "free_count", i32, (1,), dev)
     e = _array(block_table, "block_table", i32, (B, None), dev)
     if out is None:
-        # two allocations for the five
-        at = kv_len.device
-        flat = torch.empty(rows + 2 * B + 2, dtype=i32, device=at)
-        slots = torch.empty(rows, dtype=_I64, device=at)
-        positions, lens, cu, count = flat.split_with_sizes((rows, B, B + 1, 1))
-        out = PagedPlan(lens, count, cu, slots, positions)
-        base = flat.data_ptr()
-        ptr = (base + 4 * rows, base + 4 * (rows + 2 * B + 1), base + 4 * (rows + B), slots.data_ptr(), base)
+        # an allocation each: views of a common one cost more
+        at, new = kv_len.device, torch.empty
+        lens, left, cu = torch.empty_like(kv_len), torch.empty_like(free_count), new(B + 1, dtype=i32, device=at)
+        slots, positions = new(rows, dtype=_I64, device=at), new(rows, dtype=i32, device=at)
+        out = PagedPlan(lens, left, cu, slots, positions)
+        ptr = (lens.data_ptr(), left.data_ptr(), cu.data_ptr(), slots.data_ptr(), positions.data_ptr())
     else:
         ptr = (_array(out.kv_len, "out.kv_len", i32, (B,), dev), _array(out.free_count, "out.free_count", i32, (1,), dev),
                _array(out.cu_rows, "out.cu_rows", i32, (B + 1,), dev), _array(out.slots, "out.slots", _I64, (rows,), dev),
