@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import paged_oracle as P
-from paged_cases import Batch, attend_tolerance
+from paged_cases import Batch, attend_tolerance, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -351,3 +351,37 @@ def test_a_mixed_step_in_two_calls(paged):
     O, _, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, True, 0, 128 ** -0.5)
     got = out.float().cpu().numpy().astype(np.float64)
     assert (np.abs(got - O) <= attend_tolerance(O, spread, vmax, int(bt.kv_len.max()), "bf16", True)).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("heads,kv_heads,new", [(32, 1, 1), (71, 1, 1), (24, 1, 2), (9, 3, 6)])
+def test_more_rows_than_a_few_row_item(paged, kernel, heads, kv_heads, new):
+    """Wide head groups and drafts: a key/value head's rows fill one to three
+    items of 16."""
+    bt = Batch(19, [0, 31, 500, 2049], [new, new, 1, new], heads, kv_heads, 64, 16)
+    assert check(paged, bt, kid(paged, kernel)) == 0
+
+
+@pytest.mark.parametrize("kernel", ["tc", "auto"])
+def test_items_of_one_cta_differ(paged, kernel):
+    """Several items follow one another in a CTA, with queries beyond float16
+    in some of them, a page out of range in others, and ragged ends: what an
+    item needs must not reach the next."""
+    bt = Batch(22, [100, 0, 300, 20], [300, 513, 257, 700], 24, 24, 64, 32)
+    large = np.zeros((bt.rows, 1, 1))
+    for b in (1, 3):
+        large[bt.cu[b]: bt.cu[b + 1]] = 1
+    large[bt.cu[0] + 100: bt.cu[0] + 130] = 1     # some rows of an item
+    bt.q = rounded(bt.q * np.where(large > 0, 3e5, 1.0), "bf16")
+    assert check(paged, bt, kid(paged, kernel), scale=1e-7) == 0
+    q, args = dev(bt.q, "bf16"), (dev(bt.pool), dev(bt.kv_len), dev(bt.cu))
+    ref = paged.qwm_paged_attend(q, args[0], dev(bt.table), *args[1:], max_new=700, scale=1e-7, kernel=kid(paged, kernel))
+    bt.table[2, 3] = bt.pool.shape[0]             # tokens 96 to 127 of request 2
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = paged.qwm_paged_attend(q, args[0], dev(bt.table), *args[1:], max_new=700, scale=1e-7, status=status,
+                                 kernel=kid(paged, kernel))
+    assert int(status.item()) == 8
+    other = np.ones(bt.rows, bool)
+    other[bt.cu[2]: bt.cu[3]] = False
+    keep = torch.from_numpy(other).cuda()
+    assert torch.equal(got[keep], ref[keep]) and not torch.equal(got[~keep], ref[~keep])
