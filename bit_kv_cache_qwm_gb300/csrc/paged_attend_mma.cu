@@ -141,7 +141,7 @@ struct Ahead {
     for (int x = 0; x < kSub; ++x) {
       const int n = (t + lane) * kTk + 16 * (kSub * warp + x);
       const bool in = t + lane < to && n < hi && n + 16 > lo;
-      ids[x] = in ? __ldg(row + (n >> a.page_shift)) : -2;
+      ids[x] = in ? load_global(row + (n >> a.page_shift)) : -2;
       if (in && (ids[x] < 0 || ids[x] >= a.n_pages)) {
         flag(a.status, QWM_DEV_BOUNDS);
         ids[x] = -2;
@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ W ahead_sh[kCw];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x;
+  wait_for_kernel_ahead();
   if (tid == 0) a.join[w].last = -1;
   const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);   // has block barriers
-  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
   W it;
   it.start(a, sh.b, sh.skip, sh.per, sh.n);
@@ -544,6 +544,9 @@ cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
   cfg.blockDim = dim3(kNt, 1, 1);
   cfg.dynamicSmemBytes = Smem<D, NB>::bytes;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB>, cfg, a);
 }
 

@@ -79,9 +79,9 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
   __shared__ uint8_t live_sh[kTk];      // the tile's tokens that are there
   const int tid = threadIdx.x, tx = tid % S::TX, ty = tid / S::TX;
   const int w = blockIdx.x;
+  wait_for_kernel_ahead();
   const Share sh = find_share<R, kTk, kItem, kNt>(a, w, (int)gridDim.x);
   if (tid == 0) a.join[w].last = -1;
-  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
   Walker<R, kTk, kItem> it;
   it.start(a, sh.b, sh.skip, sh.per, sh.n);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
         const int k = rem / (D / 8), wd = rem % (D / 8), n = n0 + k;
         code[x] = par[x] = 0;
         if (n < it.lo || n >= it.hi) continue;
-        const int pg = __ldg(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift));
+        const int pg = load_global(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift));
         if (pg < 0 || pg >= a.n_pages) {
           if (half == 0 && wd == 0) flag(a.status, QWM_DEV_BOUNDS);
           continue;
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
         live |= 1u << x;
         const int s = n & (a.page - 1);
         const uint8_t* blk = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + half * (a.block / 2);
-        code[x] = __ldg(reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4));
-        par[x] = __ldg(reinterpret_cast<const uint32_t*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4));
+        code[x] = load_global(reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4));
+        par[x] = load_global(reinterpret_cast<const uint32_t*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4));
       }
     };
     fetch(it.from * kTk);
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kJoinNt, 3) paged_attend_join_kernel(const Att
   __shared__ __align__(16) float4 sum[NG][L];
   __shared__ float factor[kPartsAtOnce];
   __shared__ float red[kJoinNt / 32];
-  cudaGridDependencySynchronize();
+  wait_for_kernel_ahead();
   const int w = blockIdx.x, tid = threadIdx.x, g = tid / L, c = tid % L;
   const Join j = a.join[w];
   if (j.last < 0) return;
@@ -401,6 +401,9 @@ cudaError_t launch_simt(const AttendArgs& a, int workers, cudaStream_t st) {
   cfg.blockDim = dim3(kNt, 1, 1);
   cfg.dynamicSmemBytes = Shape<D, R>::floats * 4;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_simt_kernel<D, R, T>, cfg, a);
 }
 
@@ -439,9 +442,7 @@ cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w,
   cfg.gridDim = dim3((unsigned)w.count, (unsigned)(rows < 16 ? rows : 16), 1);
   cfg.blockDim = dim3(kJoinNt, 1, 1);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto kern = bf16 ? (d == 64 ? paged_attend_join_kernel<64, __nv_bfloat16> : paged_attend_join_kernel<128, __nv_bfloat16>)

@@ -127,12 +127,12 @@ struct Packed {
   __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* params) {
     if (codes) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) code[i] = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+      for (int i = 0; i < D / 32; ++i) code[i] = load_global(reinterpret_cast<const uint4*>(codes) + i);
       if constexpr (D == 128) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(params));
+        const uint4 u = load_global(reinterpret_cast<const uint4*>(params));
         par[0] = u.x, par[1] = u.y, par[2] = u.z, par[3] = u.w;
       } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(params));
+        const uint2 u = load_global(reinterpret_cast<const uint2*>(params));
         par[0] = u.x, par[1] = u.y;
       }
     } else {   // a token outside the request: zeros
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   __shared__ uint8_t row_exp_sh[2][kRows];   // Q was scaled by 2^-this
   __shared__ uint32_t bad_item_sh[2];        // some page of the item is out of range
   const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
+  wait_for_kernel_ahead();
 
   if (tid == 0) {
     abort_sh = 0;
@@ -244,7 +245,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     a.join[w].last = -1;
   }
   const Share sh = find_share<kRows, kTk, kItem, kNt>(a, w, (int)gridDim.x);   // has block barriers
-  cudaTriggerProgrammaticLaunchCompletion();   // the join kernel may be made ready
   if (sh.n == 0) return;
   if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&tmem_base_sh)));
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       n = t * kTk + p;
       h = it.h;
       in = n >= it.lo && n < it.hi;
-      pg = in ? __ldg(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift)) : -1;
+      pg = in ? load_global(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift)) : -1;
     };
     auto advance = [&]() {
       if (++t < it.to) return true;
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const int last = (min(it.hi, it.to * kTk) - 1) >> a.page_shift;
 #pragma unroll 1
       for (int x = (max(it.lo, it.from * kTk) >> a.page_shift) + p; x <= last; x += kLoaders) {
-        const int id = __ldg(a.table + (int64_t)it.b * a.max_blocks + x);
+        const int id = load_global(a.table + (int64_t)it.b * a.max_blocks + x);
         good = good && id >= 0 && id < a.n_pages;
       }
       // on their way to L2 before the tiles are free
@@ -664,6 +664,9 @@ cudaError_t launch_tc(const AttendArgs& a, int workers, cudaStream_t st) {
   cfg.blockDim = dim3(kNt, 1, 1);
   cfg.dynamicSmemBytes = Lay<D>::bytes;
   cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_tc_kernel<D>, cfg, a);
 }
 

@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kPlanNt) paged_plan_kernel(const qwm_paged_pla
   __shared__ int32_t count_sh;
   __shared__ int bad_sh, full_sh;
   const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
+  wait_for_kernel_ahead();
   if (tid == 0) bad_sh = full_sh = 0, count_sh = *a.free_count;
   __syncthreads();
   int64_t rows = 0, pages = 0;
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_
   extern __shared__ int32_t first_sm[];   // pages given up by each request, then their first place
   __shared__ int32_t count_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  wait_for_kernel_ahead();
   if (tid == 0) count_sh = *a.free_count;
   // entries [keep, held) of a request's table; false where keep_len is out of range
   auto range = [&](int b, int* keep, int* held) {
@@ -228,8 +230,8 @@ __global__ void __launch_bounds__(kPlanNt) paged_release_kernel(const qwm_paged_
 // c = f32(1/15) and fused multiply-adds, the correctly rounded R / 15.
 // Bound by HBM (2 or 4 bytes a channel in, 0.625 out, 2 or 4 more for x_hat)
 // and by the instructions (69% of the issue slots): 4,680 rows of 24 heads, d =
-// 128, bf16 with x_hat, 26.3 us (5.1 TB/s); with a division a channel 71 us, with
-// 8 channels a thread and scalar ranges 35 us.  A step of 48 rows takes 3.8 us.
+// 128, bf16 with x_hat, 25.6 us (5.2 TB/s); with a division a channel 71 us, with
+// 8 channels a thread and scalar ranges 35 us.  A step of 48 rows takes 3.5 us.
 __device__ __forceinline__ void store8(float* p, const float2* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
@@ -256,7 +258,7 @@ struct Raw<float> {
   float4 u[4];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 4; ++i) u[i] = load_global(reinterpret_cast<const float4*>(p) + i);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -291,8 +293,8 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint4 u[2];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    u[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    u[0] = load_global(reinterpret_cast<const uint4*>(p));
+    u[1] = load_global(reinterpret_cast<const uint4*>(p) + 1);
   }
   __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float2* x) const {
@@ -389,6 +391,7 @@ template <int D, class T>
 __global__ void __launch_bounds__(kAppendNt, kAppendCtas) paged_append_kernel(const qwm_paged_append_args a, int shift, uint32_t heads_mul,
                                                                  uint32_t heads_shift) {
   constexpr int L = D / kCh, G = D / 32;
+  wait_for_kernel_ahead();
   const uint32_t unit = blockIdx.x * (kAppendNt / L) + threadIdx.x / L;
   const int wd = threadIdx.x % L, page = 1 << shift;
   const bool live = unit < (uint32_t)(a.rows * a.kv_heads);
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kAppendNt, kAppendCtas) paged_append_kernel(co
   Raw<T> raw[2];
   raw[0].load((const T*)a.k.ptr + t * a.k.row_stride + h * a.k.head_stride + kCh * wd);
   raw[1].load((const T*)a.v.ptr + t * a.v.row_stride + h * a.v.head_stride + kCh * wd);
-  int64_t slot = live ? __ldg(reinterpret_cast<const long long*>(a.slots) + t) : -1;
+  int64_t slot = live ? load_global(reinterpret_cast<const long long*>(a.slots) + t) : -1;
   uint32_t bits = 0;
   if (slot >= (a.n_pages << shift)) {
     bits = QWM_DEV_BOUNDS;
@@ -439,19 +442,18 @@ cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st
   cfg.blockDim = dim3(kPlanNt, 1, 1);
   cfg.dynamicSmemBytes = (size_t)a.requests * 12;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {early_launch()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = in_place && ctas > 1 ? 1 : 0;
+  cfg.numAttrs = in_place && ctas > 1 ? 2 : 1;
   return a.requests * 12 <= 48 * 1024 ? cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift, in_place)
                                       : launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift, in_place);
 }
 
 cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {
-  paged_release_kernel<<<1, kPlanNt, (size_t)a.requests * 4, st>>>(a, shift);   // 32 KB at most
-  return cudaGetLastError();
+  return launch_early(paged_release_kernel, dim3(1, 1, 1), kPlanNt, (size_t)a.requests * 4, st, a, shift);   // 32 KB at most
 }
 
 cudaError_t launch_append(const qwm_paged_append_args& a, int shift, cudaStream_t st) {
@@ -462,8 +464,7 @@ cudaError_t launch_append(const qwm_paged_append_args& a, int shift, cudaStream_
   const bool bf = a.dtype == QWM_BF16;
   auto kern = a.head_dim == 64 ? (bf ? paged_append_kernel<64, __nv_bfloat16> : paged_append_kernel<64, float>)
                                : (bf ? paged_append_kernel<128, __nv_bfloat16> : paged_append_kernel<128, float>);
-  kern<<<grid, kAppendNt, 0, st>>>(a, shift, mul, by);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kAppendNt, 0, st, a, shift, mul, by);
 }
 
 }  // namespace paged

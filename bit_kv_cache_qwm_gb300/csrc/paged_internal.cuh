@@ -388,7 +388,56 @@ __device__ __forceinline__ float* part_row(const AttendArgs& a, int worker, int 
   return a.part + (((int64_t)worker * 2 + slot) * R + r) * part_floats(d);
 }
 
+// A load of memory that the kernel ahead may have written: not one the compiler
+// may take for constant and move ahead of wait_for_kernel_ahead.
+template <class T>
+__device__ __forceinline__ T load_global(const T* p) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "a vector");
+  T x;
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(x)) : "l"(p));
+  } else if constexpr (sizeof(T) == 8) {
+    uint2& u = reinterpret_cast<uint2&>(x);
+    asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(p));
+  } else {
+    uint4& u = reinterpret_cast<uint4&>(x);
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  }
+  return x;
+}
+
+// Every kernel of the paged cache is launched so that its CTAs may be placed
+// while the kernel ahead of it on the stream runs out (of which it sees nothing
+// before it has ended), and lets the next one do the same: a step is a row of
+// short kernels, and this hides a launch's latency between two of them (single
+// token steps called one after another: append 6.1 -> 3.3 us, plan 6.1 -> 3.7,
+// norm and rotation 4.1 -> 2.2; captured, 0.3 to 0.7 us each).  Comes first in a
+// kernel, before any access to memory.
+__device__ __forceinline__ void wait_for_kernel_ahead() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+
 // ---- launchers
+inline cudaLaunchAttribute early_launch() {
+  cudaLaunchAttribute x = {};
+  x.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  x.val.programmaticStreamSerializationAllowed = 1;
+  return x;
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 struct Workers {
   int count;   // CTAs that share the work
   int rows;    // rows of one item

@@ -16,7 +16,7 @@
 // Bound by HBM (every element is read and written once) and, in bf16, by the
 // ~60 instructions of a step: with pairs in lanes apart (8 shuffles), per-head
 // addresses from the strides and scalar arithmetic a step took 215.  4,680 rows
-// of 48 heads, d = 128, bf16: 23.6 us (5.0 TB/s; 34 us with those 215), 32,760
+// of 48 heads, d = 128, bf16: 23.4 us (5.0 TB/s; 34 us with those 215), 32,760
 // rows of 16 heads, d = 64, float32: 48 us (5.7 TB/s).
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
@@ -65,6 +65,7 @@ template <int D, bool ADJ, class T>
 __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_kernel(const qwm_qk_norm_rope_args a, int splits,
                                                                                      int per_split) {
   constexpr int L = D / 8, PER = 32 / L;
+  wait_for_kernel_ahead();
   const int lane = threadIdx.x % L, sub = (threadIdx.x & 31) / L, heads = a.q_heads + a.k_heads;
   const int64_t unit = (int64_t)blockIdx.x * (kRopeNt / 32) + (threadIdx.x >> 5);
   const int64_t t = splits == 1 ? unit : unit / splits;
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
   int pos[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int x = 0; x < 4; ++x)
-    if (x < a.axes) pos[x] = __ldg(a.positions + t * a.axes + x);
+    if (x < a.axes) pos[x] = load_global(a.positions + t * a.axes + x);
   float2 co[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, si[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   bool first = true, dead = false;
   auto run = [&](const qwm_rows& in, const qwm_rows& out, const T* weight, int n0, int n1) {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
           if (x0 == axis(p0 + 3)) {
             // rot is a multiple of 16, so the vectors are aligned
             const float* r = row(x0) + p0;
-            const float4 c = __ldg(reinterpret_cast<const float4*>(r)), z = __ldg(reinterpret_cast<const float4*>(r + half));
+            const float4 c = load_global(reinterpret_cast<const float4*>(r)), z = load_global(reinterpret_cast<const float4*>(r + half));
             co[0] = make_float2(c.x, c.y), co[1] = make_float2(c.z, c.w);
             si[0] = make_float2(z.x, z.y), si[1] = make_float2(z.z, z.w);
           } else {
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float* r = row(axis(p0 + k)) + p0 + k;
-              c[k] = __ldg(r);
-              z[k] = __ldg(r + half);
+              c[k] = load_global(r);
+              z[k] = load_global(r + half);
             }
             co[0] = make_float2(c[0], c[1]), co[1] = make_float2(c[2], c[3]);
             si[0] = make_float2(z[0], z[1]), si[1] = make_float2(z[2], z[3]);
@@ -231,8 +232,7 @@ cudaError_t launch_qk_norm_rope(const qwm_qk_norm_rope_args& a, cudaStream_t st)
                                    : (bf ? qk_norm_rope_kernel<64, false, __nv_bfloat16> : qk_norm_rope_kernel<64, false, float>))
                   : (a.interleaved ? (bf ? qk_norm_rope_kernel<128, true, __nv_bfloat16> : qk_norm_rope_kernel<128, true, float>)
                                    : (bf ? qk_norm_rope_kernel<128, false, __nv_bfloat16> : qk_norm_rope_kernel<128, false, float>));
-  kern<<<grid, kRopeNt, 0, st>>>(a, splits, per);
-  return cudaGetLastError();
+  return launch_early(kern, grid, kRopeNt, 0, st, a, splits, per);
 }
 
 }  // namespace paged

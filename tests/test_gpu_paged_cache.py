@@ -406,3 +406,55 @@ def test_diagnostics_measure_the_paged_encoding(paged):
                       ("output_rel_error", rel(Oq, O))):
         assert got[key] == pytest.approx(want, rel=1e-3), key
     assert abs(got["top1_change"] - (L.argmax(-1) != Lq.argmax(-1)).mean()) <= 1 / 40
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_that_follow_without_a_pause(paged, dtype):
+    """The kernels of a step are placed on the GPU while the one ahead runs out:
+    prompts and decode steps through four layers give the same bits whether the
+    host waits after every call, never, or replays captured steps."""
+    B, hq, hk, d, page, layers = 8, 8, 2, 128, 16, 4
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xs = {n: torch.randn((layers, n, hq + 2 * hk, d), generator=g, device="cuda").to(td) for n in (B * 150, B)}
+    cs = dev(rope_table(300, d))
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def state():
+        return {"pool": [torch.full((120, hk, paged.qwm_paged_block_bytes(d, page)), 255, dtype=torch.uint8, device="cuda")
+                         for _ in range(layers)],
+                "t": torch.full((B, 16), -1, **i32), "fp": torch.arange(120, **i32), "fc": torch.tensor([120], **i32),
+                "kl": torch.zeros(B, **i32), "plan": {n: (torch.zeros(B + 1, **i32), torch.zeros(n, dtype=torch.int64, device="cuda"),
+                                                          torch.zeros(n, **i32)) for n in xs}}
+
+    def step(s, n, wait=lambda: None):
+        new = torch.full((B,), n // B, **i32)
+        p = paged.qwm_paged_plan(s["kl"], new, s["t"], s["fp"], s["fc"], page, n, out=paged.PagedPlan(s["kl"], s["fc"], *s["plan"][n]))
+        wait()
+        y = 0
+        for x, pool in zip(xs[n], s["pool"]):
+            x = x + y
+            q, k = paged.qwm_qk_norm_rope(x[:, :hq], x[:, hq:hq + hk], None, None, cs, p.positions)
+            wait()
+            paged.qwm_paged_append(k, x[:, hq + hk:], pool, p.slots)
+            wait()
+            o = paged.qwm_paged_attend(q, pool, s["t"], p.kv_len, p.cu_rows, max_new=n // B)
+            wait()
+            y = torch.cat([o, o[:, :2 * hk]], 1)
+        return o
+
+    a, b, c = state(), state(), state()
+    torch.cuda.synchronize()
+    want = [step(a, n, torch.cuda.synchronize).clone() for n in [B * 150] + [B] * 20]
+    got = [step(b, n).clone() for n in [B * 150] + [B] * 20]
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    step(c, B * 150)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        out = step(c, B)
+    for x in want[1:]:
+        graph.replay()
+        assert torch.equal(out, x)
+    for s in (b, c):
+        assert torch.equal(s["kl"], a["kl"]) and all(torch.equal(x, y) for x, y in zip(s["pool"], a["pool"]))
