@@ -458,3 +458,64 @@ def test_calls_that_follow_without_a_pause(paged, dtype):
         assert torch.equal(out, x)
     for s in (b, c):
         assert torch.equal(s["kl"], a["kl"]) and all(torch.equal(x, y) for x, y in zip(s["pool"], a["pool"]))
+
+
+def test_behind_copies_fills_and_other_streams(paged):
+    """What stands ahead of a call on its stream may be a copy, a fill, or work
+    of another stream that it waits for, captured or not."""
+    T, hq, hk, d, page = 300, 4, 2, 64, 32
+    r = torch.Generator(device="cuda").manual_seed(9)
+    src = [torch.randn((T, hq + 2 * hk, d), generator=r, device="cuda").bfloat16() for _ in range(4)]
+    pinned = [x.cpu().pin_memory() for x in src]
+    cs = dev(rope_table(T, d))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = -(-T // page)
+    x = torch.zeros_like(src[0])
+    v = torch.zeros((T, hk, d), dtype=torch.bfloat16, device="cuda")
+    pool = paged.paged_pool(width, hk, d, page)
+    table, out = torch.arange(width, **i32)[None].contiguous(), torch.zeros((T, hq, d), dtype=torch.bfloat16, device="cuda")
+    kl, cu, pos = torch.tensor([T], **i32), torch.tensor([0, T], **i32), torch.arange(T, **i32)
+    slots = torch.arange(T, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(copy):
+        side.wait_stream(main)
+        copy()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)
+            v.copy_(x[:, hq + hk:])
+        q, k = paged.qwm_qk_norm_rope(x[:, :hq], x[:, hq:hq + hk], None, None, cs, pos)
+        pool.zero_()
+        main.wait_stream(side)
+        paged.qwm_paged_append(k, v, pool, slots)
+        out.zero_()
+        paged.qwm_paged_attend(q, pool, table, kl, cu, max_new=T, out=out)
+
+    want = []
+    for y in src:
+        q, k = paged.qwm_qk_norm_rope(y[:, :hq], y[:, hq:hq + hk], None, None, cs, pos)
+        torch.cuda.synchronize()
+        p = torch.zeros_like(pool)
+        paged.qwm_paged_append(k, y[:, hq + hk:].contiguous(), p, slots)
+        torch.cuda.synchronize()
+        want.append(paged.qwm_paged_attend(q, p, table, kl, cu, max_new=T))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        for y, w in zip(pinned, want):
+            def copy():
+                x.copy_(y, non_blocking=True)
+                side.wait_stream(main)
+            step(copy)
+            assert torch.equal(out, w)
+    torch.cuda.synchronize()
+    feed = torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        def copy():
+            x.copy_(feed)
+            side.wait_stream(main)
+        step(copy)
+    for y, w in zip(src, want):
+        feed.copy_(y)
+        graph.replay()
+        assert torch.equal(out, w)
