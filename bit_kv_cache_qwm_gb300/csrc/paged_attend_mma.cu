@@ -515,11 +515,11 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
           const int rr = it.rt * R + r;
           const int64_t tok = it.rq.row0 + div_group(a, rr);
           const int head = it.h * a.group + rr - div_group(a, rr) * a.group;
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = inverse_sum(sum);
           const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
           *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + tok * a.o_row + head * a.o_head + ch) =
               make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
-          if (a.lse && ch == 0) a.lse[tok * a.heads + head] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          if (a.lse && ch == 0) a.lse[tok * a.heads + head] = log_sum(mx, sum);
         } else {
           float* dst = part_row(a, w, slot, R, r, D);
           *reinterpret_cast<float4*>(dst + ch) = v;

@@ -241,14 +241,14 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       if (whole) {
         const int64_t tok = it.rq.row0 + div_group(a, row0 + r);
         const int head = it.h * a.group + (row0 + r) - div_group(a, row0 + r) * a.group;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const float inv = inverse_sum(l[i]);
         T* dst = (T*)a.out + tok * a.o_row + head * a.o_head;
 #pragma unroll
         for (int j = 0; j < S::CT; j += 2) {
           const float2 y = __fmul2_rn(o[i][j / 2], make_float2(inv, inv));
           store_pair(dst + channel<S>(tx, j), y);
         }
-        if (a.lse && tx == 0) a.lse[tok * a.heads + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+        if (a.lse && tx == 0) a.lse[tok * a.heads + head] = log_sum(m[i], l[i]);
       } else {
         float* dst = part_row(a, w, slot, R, r, D);
 #pragma unroll
@@ -275,7 +275,7 @@ __device__ __forceinline__ void join_store(const AttendArgs& a, const Join& j, i
   const int y = j.row0 + r, tok = div_group(a, y);
   const int head = j.head * a.group + y - tok * a.group;
   const int64_t row = j.q_row0 + tok;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = inverse_sum(l);
   T* dst = (T*)a.out + row * a.o_row + head * a.o_head + ch;
   if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<float4*>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -283,7 +283,7 @@ __device__ __forceinline__ void join_store(const AttendArgs& a, const Join& j, i
     const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
   }
-  if (a.lse && ch == 0) a.lse[row * a.heads + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (a.lse && ch == 0) a.lse[row * a.heads + head] = log_sum(m, l);
 }
 
 template <int D, class T>

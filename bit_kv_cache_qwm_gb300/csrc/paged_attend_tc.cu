@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       // ---- O of the item by way of shared memory, 128 bytes a row at a time,
       // so that a row is stored by neighbouring lanes.  Column p of 8 holds
       // channel (p / 2) + 4 (p % 2).
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = inverse_sum(l_run);
       const int per = all ? 64 : 32;   // channels of a round: bf16 rows, or float32 parts
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += per) {
@@ -418,8 +418,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           part[D] = m_run, part[D + 1] = l_run;
         } else if (a.lse) {
           const int tok = div_group(a, y0 + i);
-          a.lse[(q_row0 + tok) * a.heads + head0 + y0 + i - tok * a.group] =
-              l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+          a.lse[(q_row0 + tok) * a.heads + head0 + y0 + i - tok * a.group] = log_sum(m_run, l_run);
         }
       }
       fence_before();   // the reads of O come before the next item's MMAs

@@ -69,6 +69,14 @@ __device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
 }
 
+// What a row's sum of weights, l = sum exp2(x_n - m), gives: the factor of O and
+// the log-sum-exp.  0 is the sum of a row that sees nothing; NaN (a row of NaN
+// in q) stays NaN in both.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 __device__ __forceinline__ int div_group(const AttendArgs& a, int x) {
   return (int)(((uint64_t)(uint32_t)x * a.group_mul) >> a.group_shift);
 }

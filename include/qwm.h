@@ -492,7 +492,7 @@ qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
  * when causal and n > P - window when window > 0 (window needs causal):
  *   O = softmax(scale q . k_hat_n) v_hat_n,   lse = log sum exp(scale q . k_hat_n)
  * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
- * no token gets O = 0 and lse = -inf.  Tokens that a row does not see have no
+ * no token gets O = 0 and lse = -inf; one with NaN in q gets NaN in both.  Tokens that a row does not see have no
  * effect on it.  Rows outside cu_rows[0 .. requests] are left as they were.
  * A page id outside [0, n_pages) hides its tokens, a kv_len outside
  * [0, max_blocks page_tokens] is clamped to it and cu_rows that decrease or
