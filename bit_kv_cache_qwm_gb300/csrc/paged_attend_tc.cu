@@ -32,9 +32,16 @@
 // Handoffs between threads are named barriers (K and V of a stage written, P
 // parts written), which do not queue behind the operand reads in the
 // shared-memory pipe; the tensor pipe's completions arrive on mbarriers.
-// Every mbarrier wait is bounded; after one runs out all roles go on through
-// their loops without waiting or issuing, so that the named barriers stay
-// matched, and the kernel returns with the status bit set.
+// Every mbarrier wait is bounded.  Named barriers cannot be, and the mbarriers
+// are what keeps their feeders (producers, softmax) from arriving twice before
+// the issuer has taken the first arrival.  So once a wait has run out every role
+// still goes through its loop with all arrivals, the issuer without issuing, and
+// a feeder whose wait has failed follows the issuer's count of finished tiles
+// from then on (its mbarriers stand still, and a parity two phases behind reads
+// as done).  A tile's arrivals need no more than the tile before to be finished,
+// so this always goes on; tests/test_paged_handoffs.py runs the hand-offs in
+// random orders.  The rows of an item that ends after a wait has run out are
+// NaN, the status bit is set, and the TMEM is freed after what is in flight.
 // Channel order of all operands within 8 channels: 0 4 1 5 2 6 3 7, the order
 // in which masks of a code word give float16 pairs.
 // TMEM columns: S_a [0,128), S_b [128,256), O_a [256,256+d), O_b [384,384+d).
@@ -91,6 +98,13 @@ __device__ __forceinline__ bool group_all(int g, bool v) {
                "selp.u32 %0, 1, 0, q;\n}"
                : "=r"(r) : "r"((uint32_t)v), "r"(kNbS + g) : "memory");
   return r != 0;
+}
+
+// until the issuer has finished `tiles` tiles
+__device__ __noinline__ void follow(const volatile int* finished, int tiles) {
+  const long long t0 = clock64();
+  while (*finished < tiles && clock64() - t0 < kWaitCycles) {
+  }
 }
 
 __device__ __forceinline__ bool loaders_all(bool v) {
@@ -216,9 +230,11 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   using W = Walker<kRows, kTk, kItem>;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t bars[10];
+  __shared__ __align__(8) uint64_t bars[11];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
+  __shared__ volatile int finished_sh;   // tiles that the issuer has taken all arrivals of
+  __shared__ volatile int late_sh;       // the last wait for the tensor pipe ran out
   // tokens of a tile on a page out of range, a word for each producer warp.
   // Four tiles deep: a slot is written again after S(u + 2) is complete, which
   // every softmax thread's P(u + 1) precedes
@@ -229,6 +245,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint64_t* v_free = &bars[6];    // [2]
   uint64_t* q_ready = &bars[8];   // Q_a and Q_b of the item written
   uint64_t* q_free = &bars[9];    // all S of the item complete
+  uint64_t* drained = &bars[10];  // nothing left in the tensor pipe
   // what the softmax needs of an item besides its logits, two items deep (a
   // slot is written again when all S of the item in between are complete)
   __shared__ uint8_t row_exp_sh[2][kRows];   // Q was scaled by 2^-this
@@ -237,10 +254,11 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   wait_for_kernel_ahead();
 
   if (tid == 0) {
-    abort_sh = 0;
+    abort_sh = finished_sh = late_sh = 0;
     for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
     bar_init(q_ready, kLoaders);
     bar_init(q_free, 1);
+    bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     a.join[w].last = -1;
   }
@@ -266,6 +284,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     uint32_t s_par = 0;
     int u = 0, slot_in = 0;
     uint32_t pv_par = 0;
+    bool ok = true;        // of the whole group
     while (true) {
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
       if (a.causal) {
@@ -286,7 +305,13 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         const int n0 = t * kTk, hi = top - n0;
         const bool full = n0 + kTk <= top_min;
         // one warp of the group polls the mbarrier, the vote hands the result on
-        group_all(g, (warp & 3) != 0 || bar_wait(&s_done[g], s_par, &abort_sh, a.timeout));
+        bool got = true;
+        if ((warp & 3) == 0) {
+          got = ok && bar_wait(&s_done[g], s_par, &abort_sh, a.timeout, a.wait_cycles);
+          if (!got) follow(&finished_sh, u);
+          __syncwarp();
+        }
+        ok = group_all(g, got);
         s_par ^= 1;
         fence_after();
         if (t == it.from) {
@@ -351,9 +376,16 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const int head0 = it.h * a.group;
       if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
       const bool more = it.next(a);
-      group_all(g, (warp & 3) != 0 || bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout));
+      // O is lost when any wait of the CTA has run out by now
+      bool got = true;
+      if ((warp & 3) == 0) {
+        got = ok && bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout, a.wait_cycles) && abort_sh == 0;
+        __syncwarp();
+      }
+      ok = group_all(g, got);
       pv_par ^= 1;
       fence_after();
+      if (!ok) l_run = __int_as_float(0x7fffffff);
       // ---- O of the item by way of shared memory, 128 bytes a row at a time,
       // so that a row is stored by neighbouring lanes.  Column p of 8 holds
       // channel (p / 2) + 4 (p % 2).
@@ -465,12 +497,18 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     load(vp, 1);
     more = advance();
     if (more) lookup();
-    bool ok = true;
+    bool ok = true;         // of the warp
+    // the stage of tile u was read by tile u - 2
+    auto wait_free = [&](uint64_t* bar, uint32_t par, int u) {
+      ok = warp_all(ok && bar_wait(bar, par, &abort_sh, a.timeout, a.wait_cycles));
+      if (!ok) follow(&finished_sh, u - 1);
+      __syncwarp();
+    };
     for (int u = 0;; ++u) {
       const int st = u & 1;
       const uint32_t par = (uint32_t)(((u >> 1) - 1) & 1);
       const bool have = more;
-      if (u >= 2) ok = bar_wait(&k_free[st], par, &abort_sh, a.timeout) && ok;
+      if (u >= 2) wait_free(&k_free[st], par, u);
       kp.store(sm + L::k + st * L::op, p);
       if ((p & 31) == 0) bad_sh[u & 3][p >> 5] = bad;
       fence_async_smem();
@@ -479,7 +517,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         resolve();
         load(kp, 0);
       }
-      if (u >= 2) ok = bar_wait(&v_free[st], par, &abort_sh, a.timeout) && ok;
+      if (u >= 2) wait_free(&v_free[st], par, u);
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);
@@ -519,7 +557,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     };
     do {
       nb_sync(kNbK + (u & 1));
-      ok = warp_all(bar_wait(q_ready, q_par, &abort_sh, a.timeout)) && ok;
+      ok = warp_all(ok && bar_wait(q_ready, q_par, &abort_sh, a.timeout, a.wait_cycles));
       q_par ^= 1;
       fence_after();
       if (ok) {
@@ -557,8 +595,13 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
             if (ok) issue_s(g, st ^ 1, t + 2 == it.to);
           }
         }
+        if ((tid & 31) == 0) finished_sh = u + 1;
       }
     } while (it.next(a));
+    // after a wait that ran out MMAs may still be on their way
+    if (elect_one()) commit(drained);
+    __syncwarp();
+    bar_wait(drained, 0, &late_sh, a.timeout);
   } else {
     // ------------------------------------------------------------ query loaders
     // The queries of an item to float16 in the order (0, 4), (1, 5), (2, 6),
@@ -571,7 +614,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     const int p = tid - kLoad * 32, cl = p % CH;
     int slot_out = 0;
     uint32_t free_par = 0;
-    bool more = true, first = true;
+    bool more = true, first = true, ok = true;
     while (more) {
       auto row_of = [&](int y) {
         const int x = it.rt * kRows + y, tok = div_group(a, x);
@@ -590,7 +633,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       for (int y = p >> 1; y < it.rows; y += kLoaders / 2)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(y) + (D / 2) * (p & 1)));
       if (!first) {
-        bar_wait(q_free, free_par, &abort_sh, a.timeout);
+        ok = ok && bar_wait(q_free, free_par, &abort_sh, a.timeout, a.wait_cycles);
         free_par ^= 1;
       }
       first = false;

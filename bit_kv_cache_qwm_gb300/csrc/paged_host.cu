@@ -5,6 +5,7 @@
 
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
+#include "tcgen05_util.cuh"
 
 using namespace qwm;
 using namespace qwm::paged;
@@ -199,6 +200,7 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   x.cu = a->cu_rows;
   x.status = a->status;
   x.timeout = a->status ? a->status : (uint32_t*)a->workspace;
+  x.wait_cycles = injected_wait_cycles(tcx::kWaitCycles);
   x.part = (float*)((uint8_t*)a->workspace + kHead);
   x.join = (Join*)((uint8_t*)a->workspace + kHead + ((part_bytes(w, d) + 255) & ~(size_t)255));
   x.rows = a->rows;

@@ -36,6 +36,7 @@ struct AttendArgs {
   const int32_t* cu;
   uint32_t* status;
   uint32_t* timeout;             // word for the bit of a bounded wait that ran out (never null)
+  int64_t wait_cycles;           // limit of a bounded wait
   float* part;                   // [workers][2][tile rows][part_floats(d)]
   struct Join* join;             // [workers]
   int64_t rows;

@@ -86,6 +86,13 @@ inline bool fault_injected(const char* what) {
   return v != nullptr && strcmp(v, what) == 0;
 }
 
+// QWM_FAULT_INJECT=wait=N limits the bounded waits of qwm_paged_attend's tcgen05
+// kernel to N SM cycles instead of `limit`, so that a test sees them run out.
+inline int64_t injected_wait_cycles(int64_t limit) {
+  const char* v = getenv("QWM_FAULT_INJECT");
+  return v != nullptr && strncmp(v, "wait=", 5) == 0 ? strtoll(v + 5, nullptr, 10) : limit;
+}
+
 // An NVTX range around one call of the ABI (recorded only when a profiler is
 // attached).
 struct NvtxRange {

@@ -492,8 +492,12 @@ qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
  * when causal and n > P - window when window > 0 (window needs causal):
  *   O = softmax(scale q . k_hat_n) v_hat_n,   lse = log sum exp(scale q . k_hat_n)
  * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
- * no token gets O = 0 and lse = -inf; one with NaN in q gets NaN in both.  Tokens that a row does not see have no
- * effect on it.  Rows outside cu_rows[0 .. requests] are left as they were.
+ * no token gets O = 0 and lse = -inf; one with NaN in q gets NaN in both.
+ * Tokens that a row does not see have no effect on it.  Rows outside
+ * cu_rows[0 .. requests] are left as they were.
+ * When a bounded device wait of kernel 3 runs out, which no input makes it do,
+ * the call still ends: the rows that were not done have NaN in O and lse, and
+ * QWM_DEV_TIMEOUT is set in `status`, where there is one.
  * A page id outside [0, n_pages) hides its tokens, a kv_len outside
  * [0, max_blocks page_tokens] is clamped to it and cu_rows that decrease or
  * leave [0, rows] are clamped; each sets QWM_DEV_BOUNDS.
