@@ -100,11 +100,33 @@ __device__ __forceinline__ bool group_all(int g, bool v) {
   return r != 0;
 }
 
-// until the issuer has finished `tiles` tiles
-__device__ __noinline__ void follow(const volatile int* finished, int tiles) {
+// what a wait that does not end at once needs
+struct Waits {
+  volatile int abort;      // a wait has run out
+  volatile int finished;   // tiles that the issuer has taken all arrivals of
+  uint32_t* status;
+  long long limit;
+};
+
+__device__ __noinline__ bool wait_long(bool ok, uint64_t* bar, uint32_t par, Waits* w, int tiles) {
+  if (ok && bar_wait(bar, par, &w->abort, w->status, w->limit)) return true;
   const long long t0 = clock64();
-  while (*finished < tiles && clock64() - t0 < kWaitCycles) {
+  while (w->finished < tiles && clock64() - t0 < kWaitCycles) {
   }
+  return false;
+}
+// The phase of parity `par` of an mbarrier; false when the wait for it, or one
+// before (not ok), ran out: then the issuer has finished `tiles` tiles.  What is
+// not the first look is out of line, so that it costs the loops no registers.
+__device__ __forceinline__ bool wait_for(bool ok, uint64_t* bar, uint32_t par, Waits* w, int tiles) {
+  if (ok) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 "selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(su32(bar)), "r"(par) : "memory");
+    if (done) return true;
+  }
+  return wait_long(ok, bar, par, w, tiles);
 }
 
 __device__ __forceinline__ bool loaders_all(bool v) {
@@ -232,8 +254,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
   __shared__ __align__(8) uint64_t bars[11];
   __shared__ uint32_t tmem_base_sh;
-  __shared__ volatile int abort_sh;
-  __shared__ volatile int finished_sh;   // tiles that the issuer has taken all arrivals of
+  __shared__ Waits waits;
   __shared__ volatile int late_sh;       // the last wait for the tensor pipe ran out
   // tokens of a tile on a page out of range, a word for each producer warp.
   // Four tiles deep: a slot is written again after S(u + 2) is complete, which
@@ -254,7 +275,9 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   wait_for_kernel_ahead();
 
   if (tid == 0) {
-    abort_sh = finished_sh = late_sh = 0;
+    waits.abort = waits.finished = late_sh = 0;
+    waits.status = a.timeout;
+    waits.limit = a.wait_cycles;
     for (int i = 0; i < 8; ++i) bar_init(&bars[i], 1);
     bar_init(q_ready, kLoaders);
     bar_init(q_free, 1);
@@ -281,9 +304,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
     uint8_t* stage = sm + L::stage + warp * 4096;
-    uint32_t s_par = 0;
     int u = 0, slot_in = 0;
-    uint32_t pv_par = 0;
     bool ok = true;        // of the whole group
     while (true) {
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
@@ -305,14 +326,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         const int n0 = t * kTk, hi = top - n0;
         const bool full = n0 + kTk <= top_min;
         // one warp of the group polls the mbarrier, the vote hands the result on
-        bool got = true;
-        if ((warp & 3) == 0) {
-          got = ok && bar_wait(&s_done[g], s_par, &abort_sh, a.timeout, a.wait_cycles);
-          if (!got) follow(&finished_sh, u);
-          __syncwarp();
-        }
-        ok = group_all(g, got);
-        s_par ^= 1;
+        ok = group_all(g, (warp & 3) != 0 || wait_for(ok, &s_done[g], u & 1, &waits, u));
         fence_after();
         if (t == it.from) {
           c2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + row_exp_sh[slot_in][128 * g + i]) << 23);
@@ -377,13 +391,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
       const bool more = it.next(a);
       // O is lost when any wait of the CTA has run out by now
-      bool got = true;
-      if ((warp & 3) == 0) {
-        got = ok && bar_wait(&pv_done[g], pv_par, &abort_sh, a.timeout, a.wait_cycles) && abort_sh == 0;
-        __syncwarp();
-      }
-      ok = group_all(g, got);
-      pv_par ^= 1;
+      ok = group_all(g, (warp & 3) != 0 || (wait_for(ok, &pv_done[g], slot_in ^ 1, &waits, 0) && waits.abort == 0));
       fence_after();
       if (!ok) l_run = __int_as_float(0x7fffffff);
       // ---- O of the item by way of shared memory, 128 bytes a row at a time,
@@ -500,9 +508,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     bool ok = true;         // of the warp
     // the stage of tile u was read by tile u - 2
     auto wait_free = [&](uint64_t* bar, uint32_t par, int u) {
-      ok = warp_all(ok && bar_wait(bar, par, &abort_sh, a.timeout, a.wait_cycles));
-      if (!ok) follow(&finished_sh, u - 1);
-      __syncwarp();
+      ok = wait_for(ok, bar, par, &waits, u - 1);
     };
     for (int u = 0;; ++u) {
       const int st = u & 1;
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     };
     do {
       nb_sync(kNbK + (u & 1));
-      ok = warp_all(ok && bar_wait(q_ready, q_par, &abort_sh, a.timeout, a.wait_cycles));
+      ok = warp_all(wait_for(ok, q_ready, q_par, &waits, 0));
       q_par ^= 1;
       fence_after();
       if (ok) {
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int st = u & 1;
         const bool last = t + 1 == it.to;
-        ok = ok && !__any_sync(0xffffffffu, abort_sh != 0);
+        ok = ok && !__any_sync(0xffffffffu, waits.abort != 0);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           nb_sync(kNbP1 + g);
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
             if (ok) issue_s(g, st ^ 1, t + 2 == it.to);
           }
         }
-        if ((tid & 31) == 0) finished_sh = u + 1;
+        if ((tid & 31) == 0) waits.finished = u + 1;
       }
     } while (it.next(a));
     // after a wait that ran out MMAs may still be on their way
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       for (int y = p >> 1; y < it.rows; y += kLoaders / 2)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(row_of(y) + (D / 2) * (p & 1)));
       if (!first) {
-        ok = ok && bar_wait(q_free, free_par, &abort_sh, a.timeout, a.wait_cycles);
+        ok = wait_for(ok, q_free, free_par, &waits, 0);
         free_par ^= 1;
       }
       first = false;
