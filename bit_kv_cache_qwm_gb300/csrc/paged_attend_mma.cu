@@ -27,8 +27,8 @@
 // (movmatrix).  A code c becomes float16 by one mask that puts it into the
 // mantissa of 1024 (1024 + c, or 1024 + 16 c for the upper nibble of a byte),
 // one exact subtraction (or fused multiply by 1/16), and c scale + zero by one
-// fused multiply-add: the only rounding of k_hat and v_hat.  Q is float16
-// scaled per row by a power of two (exact).  The rows' sums and O are float32;
+// fused multiply-add: the only rounding of k_hat and v_hat.  Q is float16 scaled
+// per row by a power of two, up or down (row_exponent).  The rows' sums and O are float32;
 // O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^15).
 // Tokens outside a request (or on a page out of range) have their logits
 // replaced and their value parameters zeroed, so garbage bytes do no harm.
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-      const int e = ex > 14 ? ex - 14 : 0;
-      const float qs = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the largest entry below 2^15
+      const int e = row_exponent(ex);
+      const float qs = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const float* y = x + 8 * i;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
         qf[nb][2 * i + 1][0] = h2u(__floats2half2_rn(y[2] * qs, y[6] * qs));
         qf[nb][2 * i + 1][1] = h2u(__floats2half2_rn(y[3] * qs, y[7] * qs));
       }
-      const float f = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float f = row_factor(a, 127 + e);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         c2[nb][k] = __shfl_sync(0xffffffffu, f, (2 * c + k) * 4);

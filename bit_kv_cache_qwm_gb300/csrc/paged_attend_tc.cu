@@ -72,6 +72,9 @@ constexpr float kNone = -3.0e38f;
 // when a logit passes x0 + 8: P <= 2^15 stays inside float16, and a token of a
 // long cache is lost only below 2^-25 / 2^7 of the largest weight
 constexpr float kBelow = 7.f, kGrow = 8.f;
+// an item's queries are scaled by 2^kUp together where their bf16 bits allow it
+constexpr int kUp = 6;
+constexpr uint32_t kFitLow = (127 - 2 - kUp) << 7, kFitHigh = (127 + 15 - kUp) << 7;
 // float16 x float16 -> float32, M = 128; N = 128 keys, or N = d channels with an MN-major B
 constexpr uint32_t kIdescS = (1u << 4) | (16u << 17) | (8u << 24);
 
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   uint64_t* drained = &bars[10];  // nothing left in the tensor pipe
   // what the softmax needs of an item besides its logits, two items deep (a
   // slot is written again when all S of the item in between are complete)
-  __shared__ uint8_t row_exp_sh[2][kRows];   // Q was scaled by 2^-this
+  __shared__ uint8_t row_exp_sh[2][kRows];   // Q was scaled by 2^(127 - this)
   __shared__ uint32_t bad_item_sh[2];        // some page of the item is out of range
   const int tid = threadIdx.x, warp = tid >> 5, w = blockIdx.x;
   wait_for_kernel_ahead();
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         ok = group_all(g, (warp & 3) != 0 || wait_for(ok, &s_done[g], u & 1, &waits, u));
         fence_after();
         if (t == it.from) {
-          c2 = a.scale_log2 * __uint_as_float((uint32_t)(127 + row_exp_sh[slot_in][128 * g + i]) << 23);
+          c2 = row_factor(a, row_exp_sh[slot_in][128 * g + i]);
           if (bad_item_sh[slot_in]) mend_until = 0x7fffffff;
           slot_in ^= 1;
         }
@@ -612,10 +615,13 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     // ------------------------------------------------------------ query loaders
     // The queries of an item to float16 in the order (0, 4), (1, 5), (2, 6),
     // (3, 7) into the Q tiles, CH lanes a row, rows behind the item's zero, as
-    // soon as all S of the item before are complete.  If an entry is 2^15 or
-    // more the rows are read again and each scaled by the power of two that
-    // brings it below; the softmax is told which.  Also: whether any page of
-    // the item is out of range.
+    // soon as all S of the item before are complete.  All rows are scaled by
+    // 2^6, which suits entries below 2^9; if one is larger, or the largest of 8
+    // neighbours (other than zeros) below 2^-8, the rows are read again and each
+    // scaled by the power of two that suits it (row_exponent).  So an entry loses
+    // bits only below 2^-23, and no more than 2^-31: 2^-23 of the largest of its
+    // neighbours.  The softmax is told the rows' scales.  Also: whether any
+    // page of the item is out of range.
     constexpr int CH = D / 8, STEP = kLoaders / CH;
     const int p = tid - kLoad * 32, cl = p % CH;
     int slot_out = 0;
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         free_par ^= 1;
       }
       first = false;
-      for (int y = p; y < kRows; y += kLoaders) row_exp_sh[slot_out][y] = 0;
+      for (int y = p; y < kRows; y += kLoaders) row_exp_sh[slot_out][y] = 127 - kUp;
 #pragma unroll 2
       for (int y = p / CH; y < kRows; y += STEP) {
         const bool live = y < it.rows;
@@ -652,25 +658,32 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       }
       cp_async_wait_all();
       // a thread converts the pieces it has copied
-      auto convert = [&](int y, float qs) {
-        uint4* at = reinterpret_cast<uint4*>(place(y));
-        const uint4 x = *at;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          o[2 * j] = h2u(__floats2half2_rn(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[2 + j] << 16) * qs));
-          o[2 * j + 1] = h2u(__floats2half2_rn(__uint_as_float(w[j] & 0xffff0000u) * qs,
-                                               __uint_as_float(w[2 + j] & 0xffff0000u) * qs));
-        }
-        *at = make_uint4(o[0], o[1], o[2], o[3]);
-        const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-        return max(m & 0xffffu, m >> 16);   // the largest magnitude's bits
+      auto store = [&](int y, float2 x0, float2 x1, float2 x2, float2 x3) {
+        *reinterpret_cast<uint4*>(place(y)) = make_uint4(h2u(__floats2half2_rn(x0.x, x2.x)), h2u(__floats2half2_rn(x0.y, x2.y)),
+                                                         h2u(__floats2half2_rn(x1.x, x3.x)), h2u(__floats2half2_rn(x1.y, x3.y)));
       };
-      uint32_t big = 0;
+      auto pair = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); };
+      auto largest = [](uint4 x) {   // the bits of the largest magnitude
+        uint32_t m;   // a NaN wins
+        asm("{\n.reg .b32 s, t;\nmax.NaN.xorsign.abs.bf16x2 s, %1, %2;\nmax.NaN.xorsign.abs.bf16x2 t, %3, %4;\n"
+            "max.NaN.xorsign.abs.bf16x2 s, s, t;\nand.b32 %0, s, 0x7fff7fff;\n}"
+            : "=r"(m) : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
+        return max(m & 0xffffu, m >> 16);
+      };
+      const __nv_bfloat162 up2 = __float2bfloat162_rn((float)(1 << kUp));
+      auto up = [&](uint32_t w) {
+        const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), up2);
+        return pair(*reinterpret_cast<const uint32_t*>(&x));
+      };
+      uint32_t high = 0, low = 0xffffffffu;
 #pragma unroll 4
-      for (int y = p / CH; y < kRows; y += STEP) big = max(big, convert(y, 1.f));
-      const bool all_fit = loaders_all(big < 0x4700u), all_good = loaders_all(good);   // 0x4700: 2^15
+      for (int y = p / CH; y < kRows; y += STEP) {
+        const uint4 x = *reinterpret_cast<const uint4*>(place(y));
+        store(y, up(x.x), up(x.y), up(x.z), up(x.w));
+        const uint32_t m = largest(x);
+        high = max(high, m), low = min(low, m - 1);   // zeros are no limit
+      }
+      const bool all_fit = loaders_all(high < kFitHigh && low >= kFitLow - 1), all_good = loaders_all(good);
       if (!all_fit) {
         // CH lanes share a row; the rows of a step need not divide 256
 #pragma unroll 1
@@ -679,15 +692,18 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
           const bool live = y < it.rows;
           uint4 v = make_uint4(0, 0, 0, 0);
           if (live) v = *reinterpret_cast<const uint4*>(row_of(y) + 8 * cl);
-          uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-          m = max(m & 0xffffu, m >> 16);
+          uint32_t m = largest(v);
 #pragma unroll
           for (int o = CH / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const int ex = (int)(m >> 7) - 127, e = ex > 14 ? ex - 14 : 0;
+          const int e = row_exponent((int)(m >> 7) - 127);
           if (live) {
-            *reinterpret_cast<uint4*>(place(y)) = v;
-            convert(y, __uint_as_float((uint32_t)(127 - e) << 23));
-            if (cl == 0) row_exp_sh[slot_out][y] = (uint8_t)e;
+            const float qs = __uint_as_float((uint32_t)(127 - e) << 23);
+            auto by = [&](uint32_t w) {
+              const float2 x = pair(w);
+              return make_float2(x.x * qs, x.y * qs);
+            };
+            store(y, by(v.x), by(v.y), by(v.z), by(v.w));
+            if (cl == 0) row_exp_sh[slot_out][y] = (uint8_t)(127 + e);
           }
         }
       }

@@ -78,6 +78,18 @@ __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+// Queries become float16 after an exact scaling of each row by 2^-e that brings
+// its largest entry (exponent ex; -127 for zeros and subnormals) to [2^14, 2^15),
+// up or down: entries down to 2^-31 of the largest keep all their bits.  e stays
+// where both factors are normal floats: at -126 a subnormal row lands above
+// 2^-8.  e is kept with 127 added, in a byte.
+__device__ __forceinline__ int row_exponent(int ex) { return max(ex - 14, -126); }
+// what the products of such a row are multiplied with; never 0, which would turn
+// a hidden token's -inf into NaN (2^-126 times a product is 0 in every logit)
+__device__ __forceinline__ float row_factor(const AttendArgs& a, int e127) {
+  return fmaxf(a.scale_log2 * __uint_as_float((uint32_t)e127 << 23), 1.1754944e-38f);
+}
+
 __device__ __forceinline__ int div_group(const AttendArgs& a, int x) {
   return (int)(((uint64_t)(uint32_t)x * a.group_mul) >> a.group_shift);
 }

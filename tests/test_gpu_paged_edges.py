@@ -1,10 +1,12 @@
 """The paged calls on inputs at the edge of what they promise."""
-
+import numpy as np
 import pytest
 import torch
 
-from paged_cases import Batch
+from oracle import paged_oracle as P
+from paged_cases import Batch, attend_tolerance, rounded
 from test_gpu_paged_attend import KERNELS, dev, kid
+from test_gpu_paged_cache import host
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,57 @@ def test_a_wait_that_runs_out_leaves_rows_of_nan(paged, monkeypatch, limit, cach
     status.zero_()
     out, lse = run()
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse) and int(status.item()) == 0
+
+
+# ------------------------------------------------------------------ size of the queries
+def check_size(paged, bt, kernel, scale):
+    """O and lse of a batch against the oracle.  O's bound is attend_tolerance.
+    A logit is off by delta = spread (131 2^-24 + 1.01 2^-11 for the tensor
+    kernels, whose k_hat is float16) as derived there, and so is the log-sum-exp
+    of logits; beside it the exponentials and the sum (n + 200 roundings), and
+    (m + log2 l) ln 2 with m and log2 l rounded: 4 2^-24 |lse|."""
+    q = dev(bt.q, "bf16")
+    lse = torch.full((bt.rows, bt.heads), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = paged.qwm_paged_attend(q, dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu), max_new=max(bt.new), scale=scale,
+                                 lse=lse, status=status, kernel=kernel)
+    O, want, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, True, 0, scale)
+    n, tensor = int(bt.kv_len.max()), kernel != paged.PAGED_SIMT
+    with np.errstate(over="ignore"):
+        tol = attend_tolerance(O, spread, vmax, n, "bf16", tensor)
+    got, l = host(out.float()).astype(np.float64), host(lse).astype(np.float64)
+    assert np.isfinite(got).all() and (np.abs(got - O) <= tol).all()
+    delta = spread * (131 * 2.0 ** -24 + (1.01 * 2.0 ** -11 if tensor else 0))
+    assert (np.abs(l - want) <= delta + np.abs(want) * 2.0 ** -22 + (n + 200) * 2.0 ** -22).all()
+    return int(status.item())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sigma,scale", [(1e-4, 1e3), (1e-6, 1e5), (1e-8, 1e7), (1e-20, 1e19), (1e-38, 1e37)])
+def test_small_queries(paged, kernel, d, sigma, scale):
+    """Queries far below float16's range (the last partly below float32's
+    normal one) with a scale that brings the logits back."""
+    bt = Batch(30, [100, 30, 200], [20, 1, 150], 4, 2, d, 16, q_sigma=sigma)
+    assert check_size(paged, bt, kid(paged, kernel), scale=scale) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("scale", [1e-2])
+def test_large_normal_small_and_zero_queries_in_one_batch(paged, kernel, scale):
+    """Each row's size is its own: rows of 1e5, 1, 1e-5, 1e-9 and 0 beside one
+    another, and one large channel among small ones."""
+    bt = Batch(31, [100, 30], [40, 300], 4, 2, 128, 16)
+    size = np.array([1e5, 1.0, 1e-5, 1e-9, 0.0])[np.random.default_rng(0).integers(0, 5, (bt.rows, 4, 1))]
+    bt.q = rounded(bt.q * size, "bf16")
+    bt.q[::7, :, 5] = 100.0
+    assert check_size(paged, bt, kid(paged, kernel), scale=scale) == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_zero_queries_and_a_small_scale(paged, kernel):
+    """A row of zeros weighs what it sees evenly, whatever the scale."""
+    bt = Batch(32, [70, 20], [5, 200], 4, 2, 64, 16)
+    bt.q[:] = 0
+    for scale in (1e-30, 1.0, 1e30):
+        assert check_size(paged, bt, kid(paged, kernel), scale=scale) == 0
