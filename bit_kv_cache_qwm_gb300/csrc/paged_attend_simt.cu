@@ -447,8 +447,7 @@ cudaError_t launch_attend_join(const AttendArgs& a, int d, bool bf16, Workers w,
   cfg.numAttrs = 1;
   auto kern = bf16 ? (d == 64 ? paged_attend_join_kernel<64, __nv_bfloat16> : paged_attend_join_kernel<128, __nv_bfloat16>)
                    : (d == 64 ? paged_attend_join_kernel<64, float> : paged_attend_join_kernel<128, float>);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, w.rows);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launched(cudaLaunchKernelEx(&cfg, kern, a, w.rows));
 }
 
 }  // namespace paged

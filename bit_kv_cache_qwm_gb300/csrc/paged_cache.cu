@@ -448,8 +448,9 @@ cudaError_t launch_plan(const qwm_paged_plan_args& a, int shift, cudaStream_t st
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = in_place && ctas > 1 ? 2 : 1;
-  return a.requests * 12 <= 48 * 1024 ? cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, shift, in_place)
-                                      : launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift, in_place);
+  // 48 KB without a raised limit hold the prefix sums and the kernel's own shared
+  // memory up to 4,052 requests only: the limit is raised whatever their number
+  return launch_smem(limit, kMaxRequests * 12, paged_plan_kernel, cfg, a, shift, in_place);
 }
 
 cudaError_t launch_release(const qwm_paged_release_args& a, int shift, cudaStream_t st) {

@@ -446,6 +446,12 @@ inline cudaLaunchAttribute early_launch() {
   x.val.programmaticStreamSerializationAllowed = 1;
   return x;
 }
+// A launch's result; an error is reported by this call alone, not left for the
+// caller's next look at the runtime's last error.
+inline cudaError_t launched(cudaError_t e) {
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
 template <class... P, class... A>
 cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -456,8 +462,7 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launched(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 struct Workers {
   int count;   // CTAs that share the work

@@ -1,4 +1,8 @@
 """The paged calls on inputs at the edge of what they promise."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,7 @@ from test_gpu_paged_attend import KERNELS, dev, kid
 from test_gpu_paged_cache import host
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -125,3 +130,34 @@ def test_zero_queries_and_a_small_scale(paged, kernel):
     bt.q[:] = 0
     for scale in (1e-30, 1.0, 1e30):
         assert check_size(paged, bt, kid(paged, kernel), scale=scale) == 0
+
+
+# ------------------------------------------------------------------ request counts
+def test_plan_at_every_size_of_its_shared_memory():
+    """A plan's prefix sums take 12 bytes a request beside the kernel's own
+    shared memory: counts around 48 KB, smaller ones first, in a process of its
+    own (a larger call before would have raised the limit)."""
+    code = """
+import numpy as np, torch
+from bit_kv_cache_qwm_gb300 import build, paged
+from oracle import paged_oracle as P
+build.build()
+i32 = dict(dtype=torch.int32, device="cuda")
+for n in (4052, 4053, 4095, 4096, 4097, 8192):
+    for in_place in (False, True):
+        r = np.random.default_rng(n)
+        new = r.integers(0, 3, n).astype(np.int32)
+        free = r.permutation(n).astype(np.int32)
+        rows = int(new.sum()) + 3
+        table = np.full((n, 1), -1, np.int32)
+        want = P.plan(np.zeros(n, np.int64), new, table, free, n, 16, rows)
+        t, kl, fc = torch.from_numpy(table).cuda(), torch.zeros(n, **i32), torch.tensor([n], **i32)
+        out = paged.PagedPlan(kl, fc, torch.empty(n + 1, **i32), torch.empty(rows, dtype=torch.int64, device="cuda"),
+                              torch.empty(rows, **i32)) if in_place else None
+        got = paged.qwm_paged_plan(kl, torch.from_numpy(new).cuda(), t, torch.from_numpy(free).cuda(), fc, 16, rows, out=out)
+        for a, b in zip((got.kv_len, got.free_count, got.cu_rows, got.slots, got.positions, t), want):
+            assert np.array_equal(a.cpu().numpy().ravel(), np.ravel(b)), n
+print("done")
+"""
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert res.returncode == 0 and res.stdout.strip() == "done", res.stderr[-2000:]
