@@ -437,11 +437,12 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
             uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
             uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
             if (!whole) {
-              // tokens outside the request, or on no page: their bytes may be anything
+              // tokens outside the request, on no page, or hidden from some row:
+              // their bytes may be anything
               const int y0 = n0 + 16 * e + r0, y1 = n0 + 16 * e + r1;
               const bool got = live >> e & 1;
-              if (!got || y0 < it.lo || y0 >= it.hi) p0 = 0;
-              if (!got || y1 < it.lo || y1 >= it.hi) p1 = 0;
+              p0 = !got || y0 < it.lo || y0 >= it.hi ? 0u : hidden_params(p0);
+              p1 = !got || y1 < it.lo || y1 >= it.hi ? 0u : hidden_params(p1);
             }
             vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
             vs[b] = u2h(__byte_perm(p0, p1, 0x7632));

@@ -116,6 +116,13 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
 #pragma unroll
       for (int j = 0; j < S::CT / 2; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
+    // every row of the item sees the tokens bottom_max <= n < top_min
+    int top_min = it.hi, bottom_max = it.lo;
+    if (a.causal) {
+      const int at = it.rq.n - it.rq.n_new;
+      top_min = at + div_group(a, row0) + 1;
+      if (a.window > 0) bottom_max = at + div_group(a, row0 + it.rows - 1) - a.window + 1;
+    }
     // the next tile's packed bytes, on their way during this one's arithmetic:
     // thread's code words i = tid, tid + 256, ... of [half][token][word]
     constexpr int IT = 2 * kTk * (D / 8) / kNt;
@@ -148,6 +155,7 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       for (int x = 0; x < IT; ++x) {
         const int i = tid + x * kNt, half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
         const int k = rem / (D / 8), wd = rem % (D / 8);
+        if (half && (n0 + kTk > top_min || n0 < bottom_max)) par[x] = hidden_params(par[x]);
         const __half2 p = *reinterpret_cast<const __half2*>(&par[x]);
         const float z = __low2float(p), sc = __high2float(p);
         float v[8];

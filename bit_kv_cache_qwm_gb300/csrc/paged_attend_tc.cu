@@ -179,6 +179,10 @@ struct Packed {
       for (int i = 0; i < D / 32; ++i) code[i] = make_uint4(0, 0, 0, 0), par[i] = 0;
     }
   }
+  __device__ __forceinline__ void hide() {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) par[i] = hidden_params(par[i]);
+  }
   __device__ __forceinline__ void store(uint8_t* tile, int row) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -527,6 +531,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         load(kp, 0);
       }
       if (u >= 2) wait_free(&v_free[st], par, u);
+      if (a.causal) vp.hide();   // in every tile: to find those with hidden tokens took longer
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);

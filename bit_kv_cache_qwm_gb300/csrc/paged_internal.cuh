@@ -90,6 +90,15 @@ __device__ __forceinline__ float row_factor(const AttendArgs& a, int e127) {
   return fmaxf(a.scale_log2 * __uint_as_float((uint32_t)e127 << 23), 1.1754944e-38f);
 }
 
+// A value's parameters (float16 zero, scale) where some row does not see the
+// token: its weight 0 there must not meet NaN or infinity, which bytes that no
+// append wrote may stand for.  Parameters with a value outside float16 count as 0.
+__device__ __forceinline__ uint32_t hidden_params(uint32_t par) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&par);
+  const __half most = __hfma(__habs(__high2half(x)), __float2half(15.f), __habs(__low2half(x)));
+  return __hle(most, __float2half(65504.f)) ? par : 0u;
+}
+
 __device__ __forceinline__ int div_group(const AttendArgs& a, int x) {
   return (int)(((uint64_t)(uint32_t)x * a.group_mul) >> a.group_shift);
 }

@@ -493,8 +493,10 @@ qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
  *   O = softmax(scale q . k_hat_n) v_hat_n,   lse = log sum exp(scale q . k_hat_n)
  * Query head h reads key/value head h / (heads / kv_heads).  A row that sees
  * no token gets O = 0 and lse = -inf; one with NaN in q gets NaN in both.
- * Tokens that a row does not see have no effect on it.  Rows outside
- * cu_rows[0 .. requests] are left as they were.
+ * Tokens that a row does not see have no effect on it, whatever bytes their
+ * slots hold; a row that sees a token whose slot no append has written may get
+ * any value, NaN included.  Rows outside cu_rows[0 .. requests] are left as they
+ * were.
  * When a bounded device wait of kernel 3 runs out, which no input makes it do,
  * the call still ends: the rows that were not done have NaN in O and lse, and
  * QWM_DEV_TIMEOUT is set in `status`, where there is one.

@@ -161,3 +161,64 @@ print("done")
 """
     res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert res.returncode == 0 and res.stdout.strip() == "done", res.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ tokens that a row does not see
+# (zero, scale) in float16 that no append writes: NaN, infinite, and finite ones
+# whose values leave float16
+BAD_PARAMS = [(np.nan, np.nan), (np.inf, 1.0), (-np.inf, 0.0), (0.0, np.inf), (1.0, np.nan), (60000.0, 60000.0)]
+
+
+def spoil(bt, b, token, pair):
+    """Every parameter of one token of a request becomes `pair`; its codes stay."""
+    off, w = P.block_offsets(bt.d, bt.page), bt.d // 32
+    pg, s = bt.table[b, token // bt.page], token % bt.page
+    raw = np.tile(np.array(pair, np.float16), w).view(np.uint8)
+    for o in (off["kqp"], off["vqp"]):
+        bt.pool[pg, :, o + s * 4 * w: o + (s + 1) * 4 * w] = raw
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pair", BAD_PARAMS)
+def test_hidden_tokens_have_no_effect(paged, kernel, d, pair):
+    """Bytes that no append writes, in tokens that one row sees and another does
+    not (behind a causal row, left of a window): the rows that do not see them
+    keep their bits."""
+    k = kid(paged, kernel)
+    for new, window, token, hidden in ((33, 0, 110, range(10)), (300, 0, 390, range(290)), (5, 0, 103, range(3)),
+                                       (33, 20, 95, range(15, 33)), (300, 130, 101, range(131, 300)),
+                                       (4, 90, 11, range(1, 4))):
+        bt = Batch(34, [100, 40], [new, 3], 4, 2, d, 16)
+        q, args = dev(bt.q, "bf16"), (dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+        f = lambda: paged.qwm_paged_attend(q, dev(bt.pool), *args, max_new=new, window=window, kernel=k)  # noqa: E731
+        ref = f()
+        spoil(bt, 0, token, pair)
+        got = f()
+        same = list(hidden) + list(range(new, bt.rows))
+        assert torch.equal(got[same], ref[same]), (new, window)
+
+
+@pytest.mark.parametrize("pair", BAD_PARAMS)
+def test_hidden_tokens_have_no_effect_in_float32(paged, pair):
+    for new, window, token, hidden in ((33, 0, 110, range(10)), (70, 20, 95, range(15, 70))):
+        bt = Batch(35, [100, 40], [new, 3], 4, 2, 64, 16, dtype="f32")
+        q, args = dev(bt.q, "f32"), (dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+        f = lambda: paged.qwm_paged_attend(q, dev(bt.pool), *args, max_new=new, window=window)  # noqa: E731
+        ref = f()
+        spoil(bt, 0, token, pair)
+        got = f()
+        same = list(hidden) + list(range(new, bt.rows))
+        assert torch.equal(got[same], ref[same])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_long_decode_step_with_a_spoilt_token_of_another_row(paged, kernel):
+    """Drafts over a long request: the last draft token's bytes reach no row
+    before it, in cut items too."""
+    bt = Batch(36, [9000], [4], 8, 2, 128, 64)
+    q, args = dev(bt.q, "bf16"), (dev(bt.table), dev(bt.kv_len), dev(bt.cu))
+    f = lambda: paged.qwm_paged_attend(q, dev(bt.pool), *args, max_new=4, kernel=kid(paged, kernel))  # noqa: E731
+    ref = f()
+    spoil(bt, 0, 9003, (np.nan, np.nan))
+    assert torch.equal(f()[:3], ref[:3])
