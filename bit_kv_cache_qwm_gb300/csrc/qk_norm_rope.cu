@@ -7,7 +7,7 @@
 // or 4 heads a step.  A rotating lane holds both channels of four pairs (two
 // pieces of four channels, rot/2 apart or, for adjacent pairs, side by side),
 // so no channel has to travel between lanes; the others hold eight channels
-// behind the rotated ones and turn by cos 1, sin 0.  A lane keeps four cos and
+// behind the rotated ones, which they only weigh (cos 1).  A lane keeps four cos and
 // sin for all heads of the row, multiplied by the weight once for the queries
 // and once for the keys:
 //   out_a = inv (a (w_a c) - b (w_b s)),  out_b = inv (b (w_b c) + a (w_a s))
@@ -194,8 +194,13 @@ __global__ void __launch_bounds__(kRopeNt, sizeof(T) == 2 ? 6 : 5) qk_norm_rope_
         for (int k = 0; k < 2; ++k) {
           x[k] = __fmul2_rn(x[k], i2);
           y[k] = __fmul2_rn(y[k], i2);
-          r[k] = __ffma2_rn(x[k], ca[k], __fmul2_rn(y[k], sb[k]));
-          z[k] = __ffma2_rn(y[k], cb[k], __fmul2_rn(x[k], sa[k]));
+          if (turned) {
+            r[k] = __ffma2_rn(x[k], ca[k], __fmul2_rn(y[k], sb[k]));
+            z[k] = __ffma2_rn(y[k], cb[k], __fmul2_rn(x[k], sa[k]));
+          } else {   // no product with a sine of 0: infinity times 0 is NaN
+            r[k] = __fmul2_rn(x[k], ca[k]);
+            z[k] = __fmul2_rn(y[k], cb[k]);
+          }
         }
         if (ADJ) {
           const float2 p[2] = {r[0], r[1]}, q[2] = {z[0], z[1]};

@@ -10,7 +10,7 @@ import torch
 from oracle import paged_oracle as P
 from paged_cases import Batch, attend_tolerance, rounded
 from test_gpu_paged_attend import KERNELS, dev, kid
-from test_gpu_paged_cache import host
+from test_gpu_paged_cache import host, rope_table, rope_tolerance
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -222,3 +222,33 @@ def test_a_long_decode_step_with_a_spoilt_token_of_another_row(paged, kernel):
     ref = f()
     spoil(bt, 0, 9003, (np.nan, np.nan))
     assert torch.equal(f()[:3], ref[:3])
+
+
+# ------------------------------------------------------------------ norm and rotation of what is not finite
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,interleaved", [(128, 64, False), (128, 32, True), (64, 16, False), (64, 48, True), (128, 128, False)])
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+def test_norm_and_rotation_of_what_is_not_finite(paged, dtype, d, rot, interleaved, what):
+    """An infinite channel makes itself NaN (inf times the norm's 0) and, where
+    it is rotated, its partner; an infinite or NaN weight reaches its own
+    channel and that partner: no other channel and no other head."""
+    r = np.random.default_rng(d + rot)
+    table, pos = rope_table(50, rot), np.array([3, 17, 40], np.int32)
+    axis = np.zeros(rot // 2, int)
+    for c in {0, 5, rot // 2, rot - 1, rot % d, (rot + 3) % d, d - 1}:
+        x = rounded(r.standard_normal((3, 5, d)), dtype)
+        w = rounded(1 + 0.2 * r.standard_normal(d), dtype)
+        bad = x.copy()
+        bad[1, 2, c] = what
+        wbad = w.copy()
+        wbad[c] = what
+        for xx, ww in ((bad, w), (x, wbad)):
+            got, _ = paged.qwm_qk_norm_rope(dev(xx, dtype), None, dev(ww, dtype), None, dev(table), dev(pos), interleaved=interleaved)
+            with np.errstate(all="ignore"):
+                want = P.norm_rope(xx, ww, table, pos[:, None], axis, 1e-6, interleaved)
+            g = host(got.float()).astype(np.float64)
+            assert np.array_equal(np.isnan(g), np.isnan(want)), c
+            finite = np.isfinite(want)
+            assert np.array_equal(g[~finite & ~np.isnan(want)], want[~finite & ~np.isnan(want)])
+            tol = rope_tolerance(np.where(finite, want, 0), dtype)
+            assert (np.abs(g[finite] - want[finite]) <= tol[finite]).all()
