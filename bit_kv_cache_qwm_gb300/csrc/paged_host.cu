@@ -23,6 +23,12 @@ int page_shift(int32_t page) {
 }
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// every one a multiple of 4 bytes (NULL is): a kernel that reads an int32 or a
+// float elsewhere faults
+template <class... P>
+bool words(const P*... p) {
+  return (aligned(p, 4) && ...);
+}
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
@@ -82,7 +88,7 @@ extern "C" qwm_status qwm_qk_norm_rope(const qwm_qk_norm_rope_args* a, void* str
   if (a->k_heads > 0 && (!rows_ok(a->k, a->rows, a->k_heads, a->head_dim, e, false) ||
                          !rows_ok(a->k_out, a->rows, a->k_heads, a->head_dim, e, true)))
     return QWM_ERR_INVALID_ARG;
-  if (!a->cos_sin || !aligned(a->cos_sin, 16) || !a->positions || !aligned(a->positions, 4) ||
+  if (!a->cos_sin || !aligned(a->cos_sin, 16) || !a->positions || !words(a->positions, a->status) ||
       !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))
     return QWM_ERR_INVALID_ARG;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
@@ -96,7 +102,9 @@ extern "C" qwm_status qwm_paged_plan(const qwm_paged_plan_args* a, void* stream)
     return QWM_ERR_INVALID_ARG;
   if (a->requests > kMaxRequests) return QWM_ERR_UNSUPPORTED;
   if (!a->kv_len || !a->new_len || !a->free_pages || !a->free_count || !a->block_table || !a->kv_len_out ||
-      !a->free_count_out || !a->cu_rows || (a->rows > 0 && (!a->slots || !a->positions)) || !aligned(a->slots, 8))
+      !a->free_count_out || !a->cu_rows || (a->rows > 0 && (!a->slots || !a->positions)) || !aligned(a->slots, 8) ||
+      !words(a->kv_len, a->new_len, a->free_pages, a->free_count, a->block_table, a->kv_len_out, a->free_count_out,
+             a->cu_rows, a->positions, a->status))
     return QWM_ERR_INVALID_ARG;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_plan");
@@ -108,7 +116,9 @@ extern "C" qwm_status qwm_paged_release(const qwm_paged_release_args* a, void* s
       page_shift(a->page_tokens) < 0)
     return QWM_ERR_INVALID_ARG;
   if (a->requests > kMaxRequests) return QWM_ERR_UNSUPPORTED;
-  if (!a->keep_len || !a->kv_len || !a->block_table || !a->free_pages || !a->free_count) return QWM_ERR_INVALID_ARG;
+  if (!a->keep_len || !a->kv_len || !a->block_table || !a->free_pages || !a->free_count ||
+      !words(a->keep_len, a->kv_len, a->block_table, a->free_pages, a->free_count, a->status))
+    return QWM_ERR_INVALID_ARG;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_release");
   return cuda_status(launch_release(*a, page_shift(a->page_tokens), S(stream)));
@@ -128,7 +138,8 @@ extern "C" qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* str
   if ((a->k_hat.ptr && !rows_ok(a->k_hat, a->rows, a->kv_heads, a->head_dim, e, true)) ||
       (a->v_hat.ptr && !rows_ok(a->v_hat, a->rows, a->kv_heads, a->head_dim, e, true)))
     return QWM_ERR_INVALID_ARG;
-  if (!a->pool || !aligned(a->pool, 16) || !a->slots || !aligned(a->slots, 8)) return QWM_ERR_INVALID_ARG;
+  if (!a->pool || !aligned(a->pool, 16) || !a->slots || !aligned(a->slots, 8) || !words(a->status))
+    return QWM_ERR_INVALID_ARG;
   if (a->rows * a->kv_heads > kInt) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged_append");
@@ -177,7 +188,8 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   if (!rows_ok(a->q, a->rows, a->heads, d, e, false) || !rows_ok(a->out, a->rows, a->heads, d, e, true))
     return QWM_ERR_INVALID_ARG;
   if (!a->pool || !aligned(a->pool, 16) || !a->block_table || !a->kv_len || !a->cu_rows || !a->workspace ||
-      !aligned(a->workspace, 256) || a->workspace_bytes < qwm_paged_attend_workspace_bytes(d))
+      !aligned(a->workspace, 256) || a->workspace_bytes < qwm_paged_attend_workspace_bytes(d) ||
+      !words(a->block_table, a->kv_len, a->cu_rows, a->lse, a->status))
     return QWM_ERR_INVALID_ARG;
   const int k = a->kernel ? a->kernel : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
   if (k != 1 && a->dtype == QWM_F32) return QWM_ERR_UNSUPPORTED;

@@ -340,7 +340,8 @@ int32_t qwm_version(const qwm_ctx* ctx);       /* current basis version, -1 befo
  * and qwm_paged_release when requests end or are cut back.
  *
  * These calls keep nothing between calls and need no context.  Every pointer
- * in the argument structs is a device address on the current device; all
+ * in the argument structs is a device address on the current device, aligned to
+ * its type at least (QWM_ERR_INVALID_ARG otherwise); all
  * lengths, tables and counts live on the device, so a step can be captured
  * into a CUDA graph and replayed with other lengths.  Calls are asynchronous
  * on `stream`, allocate nothing and write only what is documented, so calls
