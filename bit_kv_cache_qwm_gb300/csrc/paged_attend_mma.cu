@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][k] += __shfl_xor_sync(0xffffffffu, l[nb][k], d);
         const int r = nb * 8 + 2 * c + k;
-        if (g == 0) stat[warp * R + r] = make_float2(m[nb][k], l[nb][k]);
+        if (g == 0) stat[warp * R + r] = make_float2(m[nb][k], near_sum(m[nb][k], l[nb][k], kNone));
         // rows g and g + 8 of block j are the channels (2 MB) g + j and
         // (2 MB) g + MB + j, kept at 16 j + 2 g and 16 j + 2 g + 1
         float* row = merge + (warp * R + r) * Sm::LD;

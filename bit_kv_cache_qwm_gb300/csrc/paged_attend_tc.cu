@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       // O is lost when any wait of the CTA has run out by now
       ok = group_all(g, (warp & 3) != 0 || (wait_for(ok, &pv_done[g], slot_in ^ 1, &waits, 0) && waits.abort == 0));
       fence_after();
-      if (!ok) l_run = __int_as_float(0x7fffffff);
+      l_run = ok ? near_sum(m_run, l_run, kNone) : __int_as_float(0x7fffffff);
       // ---- O of the item by way of shared memory, 128 bytes a row at a time,
       // so that a row is stored by neighbouring lanes.  Column p of 8 holds
       // channel (p / 2) + 4 (p % 2).

@@ -99,6 +99,15 @@ __device__ __forceinline__ uint32_t hidden_params(uint32_t par) {
   return __hle(most, __float2half(65504.f)) ? par : 0u;
 }
 
+// Kernels 2 and 3 form exp2's argument as s c - m from a maximum m rounded to
+// float32.  Up to 2^23 that leaves it within 1/2 and P (at most 2^15 else) in
+// float16; beyond, a row's weights could overflow or all vanish, so its sum is
+// made NaN.  `none`: m of a row that has seen nothing.
+constexpr float kFarLogit = 8388608.f;
+__device__ __forceinline__ float near_sum(float m, float l, float none) {
+  return m != none && !(fabsf(m) <= kFarLogit) ? __int_as_float(0x7fffffff) : l;
+}
+
 __device__ __forceinline__ int div_group(const AttendArgs& a, int x) {
   return (int)(((uint64_t)(uint32_t)x * a.group_mul) >> a.group_shift);
 }

@@ -498,6 +498,8 @@ qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* stream);
  * slots hold; a row that sees a token whose slot no append has written may get
  * any value, NaN included.  Rows outside cu_rows[0 .. requests] are left as they
  * were.
+ * Kernels 2 and 3 take logits scale q . k_hat up to 2^22 in magnitude; a row
+ * that meets a larger one may have NaN in O and lse (kernel 1 takes any).
  * When a bounded device wait of kernel 3 runs out, which no input makes it do,
  * the call still ends: the rows that were not done have NaN in O and lse, and
  * QWM_DEV_TIMEOUT is set in `status`, where there is one.

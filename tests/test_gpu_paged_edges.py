@@ -252,3 +252,32 @@ def test_norm_and_rotation_of_what_is_not_finite(paged, dtype, d, rot, interleav
             assert np.array_equal(g[~finite & ~np.isnan(want)], want[~finite & ~np.isnan(want)])
             tol = rope_tolerance(np.where(finite, want, 0), dtype)
             assert (np.abs(g[finite] - want[finite]) <= tol[finite]).all()
+
+
+# ------------------------------------------------------------------ logits that float32 cannot tell apart
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e6, 1e7, 1e8, 1e10, 1e15])
+@pytest.mark.parametrize("cached,new", [([100, 30], [40, 300]), ([9000], [3])])
+def test_large_logits_are_right_or_nan(paged, kernel, size, cached, new):
+    """Rows of growing logits.  Kernel 1 takes them all.  A row of the others is
+    right, within the bound of its logits' rounding, or NaN in O and lse; it may
+    be NaN only where some logit is beyond 2^22."""
+    bt = Batch(38, cached, new, 4, 2, 128, 16)
+    bt.q = rounded(bt.q * size, "bf16")
+    k = kid(paged, kernel)
+    lse = torch.empty(bt.rows, bt.heads, device="cuda")
+    out = paged.qwm_paged_attend(dev(bt.q, "bf16"), dev(bt.pool), dev(bt.table), dev(bt.kv_len), dev(bt.cu), max_new=max(new),
+                                 lse=lse, kernel=k)
+    O, want, spread, vmax = P.attend(bt.q.astype(np.float64), bt.pool, bt.table, bt.kv_len, bt.cu, bt.page, True, 0, 128 ** -0.5)
+    n, tensor = int(bt.kv_len.max()), k != paged.PAGED_SIMT
+    with np.errstate(over="ignore"):
+        tol = attend_tolerance(O, spread, vmax, n, "bf16", tensor)
+    got, l = host(out.float()).astype(np.float64), host(lse).astype(np.float64)
+    lost = np.isnan(l)
+    assert tensor or not lost.any()
+    assert np.isnan(got[lost]).all() and not np.isnan(got[~lost]).any()
+    assert (np.abs(got - O)[~lost] <= tol[~lost]).all()
+    delta = spread * (131 * 2.0 ** -24 + (1.01 * 2.0 ** -11 if tensor else 0))
+    assert (np.abs(l - want) <= delta + np.abs(want) * 2.0 ** -22 + (n + 200) * 2.0 ** -22)[~lost].all()
+    # spread bounds every logit of the row from above
+    assert not (lost & (spread <= 2.0 ** 22)).any()
