@@ -167,7 +167,7 @@ extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int
   // 312 at 20, 277 and 313 at 32, where it reads twice; four requests of up to
   // 1,000 tokens 19 and 29 at 32; one of 98,280 tokens 85 and 96 at 30.  A third
   // pass from 33 rows on costs more than kernel 3.
-  return max_new * (heads / kv_heads) <= 32 ? 2 : 3;
+  return max_new <= 32 && max_new * (heads / kv_heads) <= 32 ? 2 : 3;   // the product stays small
 }
 
 extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {

@@ -34,3 +34,10 @@ def test_words_off_their_boundary(paged, by, status):  # noqa: F811
     assert L.qwm_paged_append(append_args(paged, status=FAKE + by), None) == status
     for name in ("lse", "table", "lens", "cu", "status"):
         assert L.qwm_paged_attend(attend_args(paged, **{name: FAKE + by}), None) == status, name
+
+
+@pytest.mark.parametrize("max_new", [33, 1 << 31, 1 << 61, (1 << 63) - 1])
+def test_kernel_choice_of_long_hints(paged, max_new):  # noqa: F811
+    """The hint times the head group does not leave 64 bits."""
+    for heads, kv_heads in ((1, 1), (8, 1), (8, 2), (48, 3)):
+        assert paged.lib().qwm_paged_attend_kernel_for(1, heads, kv_heads, max_new) == 3
