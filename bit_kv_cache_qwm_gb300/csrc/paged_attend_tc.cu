@@ -94,14 +94,13 @@ constexpr int kNbK = 1, kNbV = 3, kNbP1 = 5, kNbP2 = 7, kNbP3 = 9, kNbS = 11, kN
 constexpr int kLoaders = (kNt / 32 - kLoad) * 32;   // threads
 __device__ __forceinline__ void nb_arrive(int id) { asm volatile("bar.arrive %0, 160;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void nb_sync(int id) { asm volatile("bar.sync %0, 160;" ::"r"(id) : "memory"); }
-// the vote of a softmax group: one warp polls, all learn the result
-__device__ __forceinline__ bool group_all(int g, bool v) {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\n"
-               "selp.u32 %0, 1, 0, q;\n}"
-               : "=r"(r) : "r"((uint32_t)v), "r"(kNbS + g) : "memory");
-  return r != 0;
+// a softmax group meets (the barrier that also takes a vote made the better code
+// around the loop's wait: few rows 320 us, with the plain one 332)
+__device__ __forceinline__ void group_meet(int g, bool v) {
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %0, 0;\nbar.red.and.pred q, %1, 128, p;\n}"
+               ::"r"((uint32_t)v), "r"(kNbS + g) : "memory");
 }
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(kNbS + g) : "memory"); }
 
 // what a wait that does not end at once needs
 struct Waits {
@@ -111,11 +110,16 @@ struct Waits {
   long long limit;
 };
 
-__device__ __noinline__ bool wait_long(bool ok, uint64_t* bar, uint32_t par, Waits* w, int tiles) {
-  if (ok && bar_wait(bar, par, &w->abort, w->status, w->limit)) return true;
+// until the issuer has finished `tiles` tiles
+__device__ __noinline__ void follow(const Waits* w, int tiles) {
   const long long t0 = clock64();
   while (w->finished < tiles && clock64() - t0 < kWaitCycles) {
   }
+}
+
+__device__ __noinline__ bool wait_long(bool ok, uint64_t* bar, uint32_t par, Waits* w, int tiles) {
+  if (ok && bar_wait(bar, par, &w->abort, w->status, w->limit)) return true;
+  follow(w, tiles);
   return false;
 }
 // The phase of parity `par` of an mbarrier; false when the wait for it, or one
@@ -312,7 +316,6 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     const uint32_t sbase = tmem + lane_base + 128u * g, obase = tmem + lane_base + kColO + 128u * g;
     uint8_t* stage = sm + L::stage + warp * 4096;
     int u = 0, slot_in = 0;
-    bool ok = true;        // of the whole group
     while (true) {
       int top = it.hi, bottom = it.lo, top_min = it.hi, bottom_max = it.lo;
       if (a.causal) {
@@ -332,8 +335,16 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       for (int t = it.from; t < it.to; ++t, ++u) {
         const int n0 = t * kTk, hi = top - n0;
         const bool full = n0 + kTk <= top_min;
-        // one warp of the group polls the mbarrier, the vote hands the result on
-        ok = group_all(g, (warp & 3) != 0 || wait_for(ok, &s_done[g], u & 1, &waits, u));
+        // one warp of the group polls the mbarrier, the others wait for it.  When a
+        // wait had run out before, this one may have read a stale parity: it
+        // follows the issuer too.
+        auto arrived = [&]() {
+          const int gone = waits.abort;
+          wait_for(true, &s_done[g], u & 1, &waits, u);
+          if (gone) follow(&waits, u);
+          return true;
+        };
+        group_meet(g, (warp & 3) != 0 || arrived());
         fence_after();
         if (t == it.from) {
           c2 = row_factor(a, row_exp_sh[slot_in][128 * g + i]);
@@ -397,10 +408,11 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const int head0 = it.h * a.group;
       if (tid == 0 && it.begins() && !it.ends()) record_join(a, w, it, last_worker(sh, it.end_of(sh.first)), kRows);
       const bool more = it.next(a);
-      // O is lost when any wait of the CTA has run out by now
-      ok = group_all(g, (warp & 3) != 0 || (wait_for(ok, &pv_done[g], slot_in ^ 1, &waits, 0) && waits.abort == 0));
+      // O is lost when any wait of the CTA has run out by now (waits.abort below)
+      if ((warp & 3) == 0) wait_for(true, &pv_done[g], slot_in ^ 1, &waits, 0);
+      group_sync(g);
       fence_after();
-      l_run = ok ? near_sum(m_run, l_run, kNone) : __int_as_float(0x7fffffff);
+      l_run = waits.abort == 0 ? near_sum(m_run, l_run, kNone) : __int_as_float(0x7fffffff);
       // ---- O of the item by way of shared memory, 128 bytes a row at a time,
       // so that a row is stored by neighbouring lanes.  Column p of 8 holds
       // channel (p / 2) + 4 (p % 2).
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     };
     do {
       nb_sync(kNbK + (u & 1));
-      ok = warp_all(wait_for(ok, q_ready, q_par, &waits, 0));
+      ok = warp_all(bar_wait(q_ready, q_par, &waits.abort, a.timeout, a.wait_cycles)) && ok;
       q_par ^= 1;
       fence_after();
       if (ok) {

@@ -10,7 +10,7 @@ end, and no warp may arrive twice in one phase of a named barrier.
 
 With `lockstep` the feeders of the issuing warp do what the kernel does: where
 their mbarrier wait has run out, they wait for the issuer's count of finished
-tiles instead, from then on.  Without it they go on at once, and get two arrivals
+tiles, from then on (softmax: whenever any wait has run out before).  Without it they go on at once, and get two arrivals
 ahead of the issuer: that has to be seen.
 """
 import random
@@ -70,7 +70,6 @@ class Cta:
         self.v = [Named(PROD + 1) for _ in range(2)]
         self.pb = [[Named(SOFT + 1) for _ in range(3)] for _ in range(2)]
         self.group = [Named(SOFT) for _ in range(2)]
-        self.vote = [[True, True], [True, True]]   # two phases of each group's vote
         self.loaders = Named(LOAD)
         self.s_done, self.pv_done = [Mbar(), Mbar()], [Mbar(), Mbar()]
         self.k_free, self.v_free = [Mbar(), Mbar()], [Mbar(), Mbar()]
@@ -95,40 +94,25 @@ class Cta:
         while self.finished_tiles < tiles:
             yield "poll"
 
-    def all(self, g, who, value):
-        b = self.group[g]
-        i = b.phase & 1
-        self.vote[g][i] = self.vote[g][i] and value
-        yield from b.sync(who)
-        out = self.vote[g][i]
-        if who[1] == 0:
-            self.vote[g][i ^ 1] = True   # not yet in use: the next vote starts after this warp joins it
-        return out
-
     def softmax(self, g, n):
-        who, u, s_par, pv_par, ok = ("soft", n, g), 0, 0, 0, True
+        who, u = ("soft", n, g), 0
         for item, tiles in enumerate(self.items):
             for _ in range(tiles):
-                mine = True
                 if n == 0:
-                    if ok or not self.lockstep:
-                        mine = yield from self.wait(self.s_done[g], s_par)
-                    if self.lockstep and not (ok and mine):
-                        mine = False
+                    gone = self.abort
+                    got = yield from self.wait(self.s_done[g], u & 1)
+                    if self.lockstep and (gone or not got):
                         yield from self.follow(u)
-                ok = (yield from self.all(g, who, mine)) and ok
-                s_par ^= 1
+                yield from self.group[g].sync(who)
                 for part in range(3):
                     yield "step"
                     self.pb[g][part].arrive(who)
                 u += 1
-            mine = True
             if n == 0:
-                mine = ok and (yield from self.wait(self.pv_done[g], pv_par)) and not self.abort
-            pv_par ^= 1
-            ok = (yield from self.all(g, who, mine)) and ok
+                yield from self.wait(self.pv_done[g], item & 1)
+            yield from self.group[g].sync(who)
             if n == 0:
-                self.poisoned[g][item] = not ok
+                self.poisoned[g][item] = self.abort
                 self.stored[g] += 1
 
     def producer(self, n):
