@@ -28,15 +28,17 @@
 // mantissa of 1024 (1024 + c, or 1024 + 16 c for the upper nibble of a byte),
 // one exact subtraction (or fused multiply by 1/16), and c scale + zero by one
 // fused multiply-add: the only rounding of k_hat and v_hat.  Q is float16 scaled
-// per row by a power of two, up or down (row_exponent).  The rows' sums and O are float32;
-// O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^15).
+// per row by a power of two, up or down (row_exponent).  The rows' sums and O are
+// float32; O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^15).
 // Tokens outside a request (or on a page out of range) have their logits
 // replaced and their value parameters zeroed, so garbage bytes do no harm.
 //
-// Bound by HBM (1.25 d bytes a token) and the ~26 instructions a token and
-// warp, half of them the codes' way to float16: that batch (8 K tokens on
-// average, 32 query heads over 8, d = 128, pages of 16) runs at 4.6 TB/s with
-// 61% of the issue slots taken; without arithmetic the same copies take 84 us.
+// Bound by the latency of chains: the ~26 instructions a token and warp, half of
+// them the codes' way to float16, lie behind one another (copy, conversion, MMA,
+// softmax, MMA), and 12 warps an SM fill neither the issue slots (61%) nor HBM
+// (4.6 TB/s, 68% of a copy) with them: that batch (8 K tokens on average, 32
+// query heads over 8, d = 128, pages of 16) takes 103 us, the same copies without
+// arithmetic 84; 40% fewer float16 instructions in the conversions were no faster.
 // One request of 98,280 tokens (40 heads over 8) takes 35 us, 8 to 10 of them
 // the start, the first ids and copies, and the join.
 #include "paged_internal.cuh"

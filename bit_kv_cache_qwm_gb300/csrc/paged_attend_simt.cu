@@ -17,7 +17,8 @@
 // rate and the shared-memory reads beside it (96 wavefronts to 128 cycles of
 // FMA a step of 4 channels), with two warps a scheduler to overlap them.
 // Measured: three windowed requests (30 to 260 rows, 1,001 tokens visible, 8
-// heads over 4, d = 64) 32 us, of one-wide multiply-adds and scalar reads of V
+// heads over 4, d = 64) 33 us (32 before values that some row does not see were
+// checked), of one-wide multiply-adds and scalar reads of V
 // 35 us; 2,048 rows over 10,240 tokens 1.22 ms (32 TFLOP/s), at d = 128 2.08 ms
 // (37).  Two CTAs an SM (128 registers) bring the long d = 64 case to 1.09 ms,
 // but the short one to 37.5 us and d = 128, which spills, to 2.46 ms.

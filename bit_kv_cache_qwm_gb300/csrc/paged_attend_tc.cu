@@ -46,16 +46,19 @@
 // in which masks of a code word give float16 pairs.
 // TMEM columns: S_a [0,128), S_b [128,256), O_a [256,256+d), O_b [384,384+d).
 // Bound by the tensor pipe and the softmax between its MMAs.  Measured at d =
-// 128: 4,680 queries over 32,760 tokens, 24 heads, not causal, 1.34 ms (1.40
-// PFLOP/s); four ragged prompts of 900 to 4,096 tokens, 32 heads over 8,
-// causal, 0.41 ms (0.97 PFLOP/s of the visible products), where an item has
-// some 18 tiles and its first S, its end and its causal edge cost about 5 more.
-// The first without the producers' stores takes 1.22 ms, without exponentials
-// 1.30 and without either 1.18 (these three with the queries loaded by the
-// softmax warps, then 1.43 in all: the loads shared their registers); with the
-// producers loading the queries 1.55, the prompts 0.51.  What an item weighs in
-// tiles when work is dealt out (kItem): the prompts take 0.57 ms at 0, 0.45 at
-// 3, 0.42 at 4 to 6.
+// 128: 4,680 queries over 32,760 tokens, 24 heads, not causal, called back to
+// back 1.43 ms (1.32 PFLOP/s; the power cap holds the clock down), ten calls in a
+// graph after a pause 1.35 to 1.40 each; four ragged prompts of 900 to 4,096
+// tokens, 32 heads over 8, causal, 0.42 ms (0.95 PFLOP/s of the visible
+// products), where an item has some 18 tiles and its first S, its end and its
+// causal edge cost about 5 more.  Of these 0.42 ms the rows' scales up as well as
+// down take 5 us, the check of values that some row does not see 2.
+// In a graph, before those two, the first without the producers' stores took 1.22
+// ms, without exponentials 1.30 and without either 1.18 (these three with the
+// queries loaded by the softmax warps, then 1.43 in all: the loads shared their
+// registers); with the producers loading the queries 1.55, the prompts 0.51.
+// What an item weighs in tiles when work is dealt out (kItem): the prompts took
+// 0.57 ms at 0, 0.45 at 3, 0.42 at 4 to 6 (then 0.41 in all).
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         load(kp, 0);
       }
       if (u >= 2) wait_free(&v_free[st], par, u);
-      if (a.causal) vp.hide();   // in every tile: to find those with hidden tokens took longer
+      if (a.causal) vp.hide();   // in every tile: to tell those with hidden tokens apart is no faster
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);

@@ -163,10 +163,10 @@ extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int
   // Kernel 2 reads the pages once for 16 rows of a key/value head, kernel 3 once
   // for 256, of which few rows leave most of its tensor work and softmax empty.
   // Measured, kernel 2 against 3 in us, d = 128: 48 ragged requests (200 to 16,380
-  // tokens, 32 heads over 8) 105 and 305 at 4 rows, 149 and 309 at 16, 272 and
-  // 312 at 20, 277 and 313 at 32, where it reads twice; four requests of up to
-  // 1,000 tokens 19 and 29 at 32; one of 98,280 tokens 85 and 96 at 30.  A third
-  // pass from 33 rows on costs more than kernel 3.
+  // tokens, 32 heads over 8) 106 and 324 at 4 rows, 149 and 325 at 16, 279 and 325
+  // at 20, 281 and 327 at 32, where it reads twice, 411 and 327 at 36; four
+  // requests of up to 1,000 tokens 17 and 29 at 32; one of 98,280 tokens 80 and 95
+  // at 30.
   return max_new <= 32 && max_new * (heads / kv_heads) <= 32 ? 2 : 3;   // the product stays small
 }
 

@@ -7,8 +7,8 @@
 // or 4 heads a step.  A rotating lane holds both channels of four pairs (two
 // pieces of four channels, rot/2 apart or, for adjacent pairs, side by side),
 // so no channel has to travel between lanes; the others hold eight channels
-// behind the rotated ones, which they only weigh (cos 1).  A lane keeps four cos and
-// sin for all heads of the row, multiplied by the weight once for the queries
+// behind the rotated ones, which they only weigh (cos 1).  A lane keeps four cos
+// and sin for all heads of the row, multiplied by the weight once for the queries
 // and once for the keys:
 //   out_a = inv (a (w_a c) - b (w_b s)),  out_b = inv (b (w_b c) + a (w_a s))
 // in two-wide float32 arithmetic; the mean square is a shuffle sum.  The table

@@ -295,13 +295,15 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
                      status: Optional[torch.Tensor] = None, kernel: int = PAGED_AUTO) -> torch.Tensor:
     """Attention of the rows of a plan, q [rows, heads, d], over their
     requests' pages (kv_len and cu_rows as qwm_paged_plan returns them).
-    max_new: the most rows of one request as the host knows it (chooses the
-    kernel; all rows when absent).  Single tokens and prompts in one step are
+    max_new: the most rows of one request as the host knows it.  It chooses the
+    kernel; absent it is all rows, which runs single tokens of many requests on
+    the kernel for prompts, three times slower.  Single tokens and prompts in one step are
     better two calls, on slices block_table[a:b], kv_len[a:b] and
     cu_rows[a:b + 1] with the same q and out.  window > 0: only the last
     `window` tokens up to the row's own.  lse: float32 [rows, heads] to receive
     the log-sum-exp.  Rows behind the last request are left as they were in
-    `out`."""
+    `out`.  status: where a page out of range, or a device wait that ran out
+    (its rows are NaN), is reported."""
     qr = _rows(q, "q")
     T, hq, d = q.shape
     dev, dt = q.get_device(), q.dtype
