@@ -423,6 +423,7 @@ def _select(s):
     count = (end + page - 1) // page
     kind = (j < s["sink"]).int() + 2 * (j >= ((end - rows) // page)[:, None]).int()
     kind = torch.where(j < count[:, None], kind.clamp(max=2), -1)[:, None].expand(-1, hk, -1)
+    score = torch.where(kind == 1, math.inf, score)                                      # the first ones in their order
     order = torch.sort(score, dim=-1, descending=True, stable=True).indices              # then the kind goes first
     order = torch.gather(order, 2, torch.sort(torch.gather(kind, 2, order), dim=-1, descending=True, stable=True).indices)
     kept = torch.minimum(count, torch.full_like(count, width))
