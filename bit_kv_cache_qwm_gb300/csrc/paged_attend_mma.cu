@@ -555,13 +555,14 @@ cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
 
 }  // namespace
 
-Workers mma_workers(int64_t max_rows) {
+Workers mma_workers(int64_t max_rows, int bits) {
   const int sms = sm_count();
+  (void)bits;
   return max_rows <= 8 ? Workers{kCtas * sms, 8} : Workers{2 * sms, 16};
 }
 
 cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
-  const Workers w = mma_workers(max_rows);
+  const Workers w = mma_workers(max_rows, a.bits);
   const cudaError_t e = w.rows == 8 ? (d == 64 ? launch_mma<64, 1>(a, w.count, st) : launch_mma<128, 1>(a, w.count, st))
                                     : (d == 64 ? launch_mma<64, 2>(a, w.count, st) : launch_mma<128, 2>(a, w.count, st));
   return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);

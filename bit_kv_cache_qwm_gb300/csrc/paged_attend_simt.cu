@@ -68,10 +68,58 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 x) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x.x, x.y);
 }
 
-template <int D, int R, class T>
+// Eight channels of a token, codes and parameters as loaded, and what they stand
+// for.
+template <class F>
+struct Piece;
+template <>
+struct Piece<Int4> {
+  uint32_t code, par;
+  __device__ __forceinline__ void zero() { code = par = 0; }
+  template <int D>
+  __device__ __forceinline__ void load(const uint8_t* blk, int page, int half, int s, int wd) {
+    blk += half * page * (D / 2 + D / 8);
+    code = load_global(reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4));
+    par = load_global(reinterpret_cast<const uint32_t*>(blk + page * (D / 2) + (s * (D / 32) + wd / 4) * 4));
+  }
+  // in a tile of which some row does not see every token
+  __device__ __forceinline__ void hide() { par = hidden_params(par); }
+  __device__ __forceinline__ void get(int, float* v) const {
+    const __half2 p = *reinterpret_cast<const __half2*>(&par);
+    const float z = __low2float(p), sc = __high2float(p);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = fmaf((float)((code >> (4 * c)) & 15u), sc, z);
+  }
+};
+template <>
+struct Piece<E4m3> {
+  uint2 code;
+  uint32_t par;   // K's and V's scale
+  __device__ __forceinline__ void zero() { code = make_uint2(0, 0), par = 0; }
+  template <int D>
+  __device__ __forceinline__ void load(const uint8_t* blk, int page, int half, int s, int wd) {
+    code = load_global(reinterpret_cast<const uint2*>(blk + (half * page + s) * D + wd * 8));
+    par = load_global(reinterpret_cast<const uint32_t*>(blk + 2 * page * D + s / kScaleSlots * 4));
+  }
+  __device__ __forceinline__ void hide() {
+    code.x = known_codes(code.x), code.y = known_codes(code.y);
+    par = known_scales(par);
+  }
+  __device__ __forceinline__ void get(int half, float* v) const {
+    const __half2 p = *reinterpret_cast<const __half2*>(&par);
+    const float sc = half ? __high2float(p) : __low2float(p);
+    const uint32_t h[4] = {e4m3_lo(code.x), e4m3_hi(code.x), e4m3_lo(code.y), e4m3_hi(code.y)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[c]));
+      v[2 * c] = f.x * sc, v[2 * c + 1] = f.y * sc;
+    }
+  }
+};
+
+template <int D, int R, class T, class F>
 __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs a) {
   using S = Shape<D, R>;
-  constexpr int G = D / 32;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;                       // [R][LD], scaled by scale * log2(e)
   float* Ks = Qs + R * S::LD;           // [kTk][LD]
@@ -127,25 +175,24 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
     // the next tile's packed bytes, on their way during this one's arithmetic:
     // thread's code words i = tid, tid + 256, ... of [half][token][word]
     constexpr int IT = 2 * kTk * (D / 8) / kNt;
-    uint32_t code[IT], par[IT], live = 0;
+    Piece<F> got[IT];
+    uint32_t live = 0;
     auto fetch = [&](int n0) {
       live = 0;
 #pragma unroll
       for (int x = 0; x < IT; ++x) {
         const int i = tid + x * kNt, half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
         const int k = rem / (D / 8), wd = rem % (D / 8), n = n0 + k;
-        code[x] = par[x] = 0;
+        got[x].zero();
         if (n < it.lo || n >= it.hi) continue;
-        const int pg = load_global(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift));
+        const int pg = load_global(table_of<F>(a, it.b, it.h) + (n >> a.page_shift));
         if (pg < 0 || pg >= a.n_pages) {
           if (half == 0 && wd == 0) flag(a.status, QWM_DEV_BOUNDS);
           continue;
         }
         live |= 1u << x;
         const int s = n & (a.page - 1);
-        const uint8_t* blk = a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block + half * (a.block / 2);
-        code[x] = load_global(reinterpret_cast<const uint32_t*>(blk + s * (D / 2) + wd * 4));
-        par[x] = load_global(reinterpret_cast<const uint32_t*>(blk + a.page * (D / 2) + (s * G + wd / 4) * 4));
+        got[x].template load<D>(a.pool + ((int64_t)pg * a.kv_heads + it.h) * a.block, a.page, half, s, wd);
       }
     };
     fetch(it.from * kTk);
@@ -156,12 +203,9 @@ __global__ void __launch_bounds__(kNt) paged_attend_simt_kernel(const AttendArgs
       for (int x = 0; x < IT; ++x) {
         const int i = tid + x * kNt, half = i / (kTk * (D / 8)), rem = i % (kTk * (D / 8));
         const int k = rem / (D / 8), wd = rem % (D / 8);
-        if (half && (n0 + kTk > top_min || n0 < bottom_max)) par[x] = hidden_params(par[x]);
-        const __half2 p = *reinterpret_cast<const __half2*>(&par[x]);
-        const float z = __low2float(p), sc = __high2float(p);
+        if (half && (n0 + kTk > top_min || n0 < bottom_max)) got[x].hide();
         float v[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = fmaf((float)((code[x] >> (4 * c)) & 15u), sc, z);
+        got[x].get(half, v);
         float* dst = half ? Vs + k * D + wd * 8 : Ks + k * S::LD + wd * 8;
         *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -402,7 +446,7 @@ __global__ void __launch_bounds__(kJoinNt, 3) paged_attend_join_kernel(const Att
   }
 }
 
-template <int D, int R, class T>
+template <int D, int R, class T, class F>
 cudaError_t launch_simt(const AttendArgs& a, int workers, cudaStream_t st) {
   static SmemLimit limit;
   cudaLaunchConfig_t cfg = {};
@@ -413,13 +457,13 @@ cudaError_t launch_simt(const AttendArgs& a, int workers, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_simt_kernel<D, R, T>, cfg, a);
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_simt_kernel<D, R, T, F>, cfg, a);
 }
 
-template <class T>
+template <class T, class F>
 cudaError_t launch_simt_t(const AttendArgs& a, int d, Workers w, cudaStream_t st) {
-  if (w.rows == 64) return d == 64 ? launch_simt<64, 64, T>(a, w.count, st) : launch_simt<128, 64, T>(a, w.count, st);
-  return d == 64 ? launch_simt<64, 8, T>(a, w.count, st) : launch_simt<128, 8, T>(a, w.count, st);
+  if (w.rows == 64) return d == 64 ? launch_simt<64, 64, T, F>(a, w.count, st) : launch_simt<128, 64, T, F>(a, w.count, st);
+  return d == 64 ? launch_simt<64, 8, T, F>(a, w.count, st) : launch_simt<128, 8, T, F>(a, w.count, st);
 }
 
 }  // namespace
@@ -441,7 +485,8 @@ Workers simt_workers(int64_t max_rows) {
 
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st) {
   const Workers w = simt_workers(max_rows);
-  const cudaError_t e = bf16 ? launch_simt_t<__nv_bfloat16>(a, d, w, st) : launch_simt_t<float>(a, d, w, st);
+  const cudaError_t e = a.bits == 8 ? (bf16 ? launch_simt_t<__nv_bfloat16, E4m3>(a, d, w, st) : launch_simt_t<float, E4m3>(a, d, w, st))
+                                    : (bf16 ? launch_simt_t<__nv_bfloat16, Int4>(a, d, w, st) : launch_simt_t<float, Int4>(a, d, w, st));
   return e != cudaSuccess ? e : launch_attend_join(a, d, bf16, w, max_rows, st);
 }
 

@@ -1,4 +1,4 @@
-// Host side of the paged 4-bit cache: argument checks, kernel choice and
+// Host side of the paged caches: argument checks, kernel choice and
 // launches.  Nothing is kept between calls and nothing is allocated.
 #include <math.h>
 #include <string.h>
@@ -146,16 +146,21 @@ extern "C" qwm_status qwm_paged_append(const qwm_paged_append_args* a, void* str
   return cuda_status(launch_append(*a, shift, S(stream)));
 }
 
-extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) {
+namespace {
+size_t attend_workspace(int32_t head_dim, int bits) {
   if (!dim_ok(head_dim)) return 0;
   size_t n = 0, w = 0;
-  for (const Workers& x : {simt_workers(1), simt_workers(64), mma_workers(1), mma_workers(16), tc_workers()}) {
+  for (const Workers& x : {simt_workers(1), simt_workers(64), mma_workers(1, bits), mma_workers(16, bits), tc_workers()}) {
     const size_t b = part_bytes(x, head_dim);
     n = b > n ? b : n;
     w = (size_t)x.count > w ? (size_t)x.count : w;
   }
   return kHead + ((n + 255) & ~(size_t)255) + w * sizeof(Join);
 }
+}  // namespace
+
+extern "C" size_t qwm_paged_attend_workspace_bytes(int32_t head_dim) { return attend_workspace(head_dim, 4); }
+extern "C" size_t qwm_paged8_attend_workspace_bytes(int32_t head_dim) { return attend_workspace(head_dim, 8); }
 
 extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new) {
   if (!dtype_ok(dtype) || heads < 1 || kv_heads < 1 || heads % kv_heads || max_new < 0) return -1;
@@ -170,33 +175,35 @@ extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int
   return max_new <= 32 && max_new * (heads / kv_heads) <= 32 ? 2 : 3;   // the product stays small
 }
 
-extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {
-  if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 ||
+namespace {
+// Either cache's attention; table_heads: tables a request has.
+qwm_status attend(const qwm_paged_attend_args* a, int bits, int table_heads, const char* name, void* stream) {
+  if ( !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 ||
       a->kv_heads < 1 || a->kv_heads > a->heads || a->heads % a->kv_heads || a->requests < 0 || a->max_blocks < 1 ||
       a->n_pages < 1 || a->n_pages > kInt || a->window < 0 || (a->window > 0 && !a->causal) || a->max_new < 0 ||
       a->kernel < 0 || a->kernel > 3 || !(fabsf(a->scale) < INFINITY))
     return QWM_ERR_INVALID_ARG;
   const int shift = page_shift(a->page_tokens), d = a->head_dim;
   if (!dim_ok(d) || shift < 0) return QWM_ERR_UNSUPPORTED;
-  const int group = a->heads / a->kv_heads;
+  const int group = a->heads / a->kv_heads, block = bits == 4 ? block_bytes(d, a->page_tokens) : block8_bytes(d, a->page_tokens);
   // positions and the rows of one kv head's problem are kept in 32 bits
   if (a->rows * group > kHalf || (int64_t)a->max_blocks * a->page_tokens > kHalf ||
-      (int64_t)a->kv_heads * block_bytes(d, a->page_tokens) > kInt)
+      (int64_t)a->kv_heads * block > kInt)
     return QWM_ERR_UNSUPPORTED;
   if (a->rows == 0 || a->requests == 0) return QWM_OK;
   const int e = esize(a->dtype);
   if (!rows_ok(a->q, a->rows, a->heads, d, e, false) || !rows_ok(a->out, a->rows, a->heads, d, e, true))
     return QWM_ERR_INVALID_ARG;
   if (!a->pool || !aligned(a->pool, 16) || !a->block_table || !a->kv_len || !a->cu_rows || !a->workspace ||
-      !aligned(a->workspace, 256) || a->workspace_bytes < qwm_paged_attend_workspace_bytes(d) ||
+      !aligned(a->workspace, 256) || a->workspace_bytes < attend_workspace(d, bits) ||
       !words(a->block_table, a->kv_len, a->cu_rows, a->lse, a->status))
     return QWM_ERR_INVALID_ARG;
-  const int k = a->kernel ? a->kernel : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
-  if (k != 1 && a->dtype == QWM_F32) return QWM_ERR_UNSUPPORTED;
+  const int k = a->kernel ? a->kernel : bits == 8 ? 1 : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
+  if (k != 1 && (a->dtype == QWM_F32 || bits == 8)) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
-  NvtxRange range("qwm_paged_attend");
+  NvtxRange range(name);
   const int64_t max_rows = (a->max_new < 1 ? 1 : a->max_new > a->rows ? a->rows : a->max_new) * group;
-  const Workers w = k == 1 ? simt_workers(max_rows) : k == 2 ? mma_workers(max_rows) : tc_workers();
+  const Workers w = k == 1 ? simt_workers(max_rows) : k == 2 ? mma_workers(max_rows, bits) : tc_workers();
   AttendArgs x;
   memset(&x, 0, sizeof(x));
   x.q = a->q.ptr;
@@ -223,7 +230,10 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   fast_division(group, &x.group_mul, &x.group_shift);
   x.page = a->page_tokens;
   x.page_shift = shift;
-  x.block = block_bytes(d, a->page_tokens);
+  x.block = block;
+  x.bits = bits;
+  x.table_h = table_heads > 1 ? a->max_blocks : 0;
+  x.table_b = (int64_t)table_heads * a->max_blocks;
   x.requests = a->requests;
   x.max_blocks = a->max_blocks;
   x.causal = a->causal != 0;
@@ -235,4 +245,98 @@ extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* str
   return cuda_status(k == 1 ? launch_attend_simt(x, d, a->dtype == QWM_BF16, max_rows, S(stream))
                      : k == 2 ? launch_attend_mma(x, d, max_rows, S(stream))
                               : launch_attend_tc(x, d, max_rows, S(stream)));
+}
+}  // namespace
+
+extern "C" qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream) {
+  return a ? attend(a, 4, 1, "qwm_paged_attend", stream) : QWM_ERR_INVALID_ARG;
+}
+
+extern "C" qwm_status qwm_paged8_attend(const qwm_paged8_attend_args* a, void* stream) {
+  if (!a || (a->table_heads != 1 && a->table_heads != a->attend.kv_heads) || a->reserved != 0) return QWM_ERR_INVALID_ARG;
+  return attend(&a->attend, 8, a->table_heads, "qwm_paged8_attend", stream);
+}
+
+extern "C" size_t qwm_paged8_block_bytes(int32_t head_dim, int32_t page_tokens) {
+  return dim_ok(head_dim) && page_shift(page_tokens) >= 0 ? (size_t)block8_bytes(head_dim, page_tokens) : 0;
+}
+
+namespace {
+// what the 8-bit cache's calls ask of a step's requests: 0 or the status
+template <class A>
+qwm_status step_status(const A& a) {
+  if (a.requests < 0 || a.max_blocks < 1 || a.kv_heads < 1 || a.kv_heads > 65536 || a.n_pages < 1 || a.n_pages > kInt)
+    return QWM_ERR_INVALID_ARG;
+  if (!dim_ok(a.head_dim) || page_shift(a.page_tokens) < 0 || a.requests > kMaxRequests ||
+      (int64_t)a.max_blocks * a.page_tokens > kHalf)
+    return QWM_ERR_UNSUPPORTED;
+  return QWM_OK;
+}
+template <class A>
+bool step_pointers_ok(const A& a) {
+  return a.block_table && a.kv_len && a.cu_rows && words(a.block_table, a.kv_len, a.cu_rows, a.status);
+}
+}  // namespace
+
+extern "C" qwm_status qwm_paged8_append(const qwm_paged8_append_args* a, void* stream) {
+  if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt) return QWM_ERR_INVALID_ARG;
+  const qwm_status s = step_status(*a);
+  if (s != QWM_OK || a->rows == 0 || a->requests == 0) return s;
+  const int e = esize(a->dtype);
+  if (!rows_ok(a->k, a->rows, a->kv_heads, a->head_dim, e, false) ||
+      !rows_ok(a->v, a->rows, a->kv_heads, a->head_dim, e, false) ||
+      (a->k_hat.ptr && !rows_ok(a->k_hat, a->rows, a->kv_heads, a->head_dim, e, true)) ||
+      (a->v_hat.ptr && !rows_ok(a->v_hat, a->rows, a->kv_heads, a->head_dim, e, true)) || !a->pool || !aligned(a->pool, 16) ||
+      !step_pointers_ok(*a))
+    return QWM_ERR_INVALID_ARG;
+  if (fault_injected("launch")) return QWM_ERR_CUDA;
+  NvtxRange range("qwm_paged8_append");
+  return cuda_status(launch_append8(*a, page_shift(a->page_tokens), S(stream)));
+}
+
+extern "C" qwm_status qwm_paged8_read(const qwm_paged8_read_args* a, void* stream) {
+  if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt) return QWM_ERR_INVALID_ARG;
+  const qwm_status s = step_status(*a);
+  if (s != QWM_OK || a->rows == 0 || a->requests == 0) return s;
+  const int e = esize(a->dtype);
+  if (!rows_ok(a->k, a->rows, a->kv_heads, a->head_dim, e, true) ||
+      !rows_ok(a->v, a->rows, a->kv_heads, a->head_dim, e, true) || !a->pool || !aligned(a->pool, 16) || !step_pointers_ok(*a))
+    return QWM_ERR_INVALID_ARG;
+  if (fault_injected("launch")) return QWM_ERR_CUDA;
+  NvtxRange range("qwm_paged8_read");
+  return cuda_status(launch_read8(*a, page_shift(a->page_tokens), S(stream)));
+}
+
+extern "C" qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* stream) {
+  if (!a || a->max_new < 0) return QWM_ERR_INVALID_ARG;
+  const qwm_status s = step_status(*a);
+  if (s != QWM_OK || a->requests == 0) return s;
+  if (a->kv_heads > 65535) return QWM_ERR_UNSUPPORTED;
+  if (!a->pool || !aligned(a->pool, 16) || !a->bounds || !aligned(a->bounds, 16) || !step_pointers_ok(*a))
+    return QWM_ERR_INVALID_ARG;
+  if (fault_injected("launch")) return QWM_ERR_CUDA;
+  NvtxRange range("qwm_paged8_bounds");
+  return cuda_status(launch_bounds8(*a, page_shift(a->page_tokens), S(stream)));
+}
+
+extern "C" size_t qwm_paged8_select_workspace_bytes(int32_t requests, int32_t kv_heads, int32_t max_blocks) {
+  return requests < 1 || kv_heads < 1 || max_blocks < 1 ? 0 : (size_t)requests * kv_heads * max_blocks * 4;
+}
+
+extern "C" qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* stream) {
+  if (!a || !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 || a->width < 1 ||
+      a->sink < 0)
+    return QWM_ERR_INVALID_ARG;
+  const qwm_status s = step_status(*a);
+  if (s == QWM_ERR_INVALID_ARG || a->heads % a->kv_heads) return QWM_ERR_INVALID_ARG;
+  if (s != QWM_OK || a->requests == 0) return s;
+  if (a->kv_heads > 65535 || a->rows * (a->heads / a->kv_heads) > kHalf) return QWM_ERR_UNSUPPORTED;
+  if ((a->rows > 0 && !rows_ok(a->q, a->rows, a->heads, a->head_dim, esize(a->dtype), false)) || !a->bounds ||
+      !aligned(a->bounds, 16) || !a->pages || !a->len_out || a->len_out == a->kv_len || !words(a->pages, a->len_out) ||
+      !a->workspace || !aligned(a->workspace, 256) ||
+      a->workspace_bytes < qwm_paged8_select_workspace_bytes(a->requests, a->kv_heads, a->max_blocks) || !step_pointers_ok(*a))
+    return QWM_ERR_INVALID_ARG;
+  if (fault_injected("launch")) return QWM_ERR_CUDA;
+  NvtxRange range("qwm_paged8_select");
+  return cuda_status(launch_select8(*a, page_shift(a->page_tokens), S(stream)));
 }

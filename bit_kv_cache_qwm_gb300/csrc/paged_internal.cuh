@@ -1,4 +1,4 @@
-// Shared declarations of the paged 4-bit cache: the block layout, the work
+// Shared declarations of the paged caches: the block layouts, the work
 // partition of the attention kernels and their partial results.
 #pragma once
 
@@ -14,6 +14,28 @@ namespace paged {
 constexpr int kMaxRequests = 8192;
 
 inline __host__ __device__ int block_bytes(int d, int page) { return page * (d + d / 4); }
+
+// ---- the 8-bit cache: codes of K and of V, then the scales of each 16 slots
+constexpr int kScaleSlots = 16, kScaleLow = -15, kScaleHigh = 7;
+constexpr float kClamp8 = 57344.f;   // 448 2^kScaleHigh
+inline __host__ __device__ int block8_bytes(int d, int page) { return 2 * page * d + (page >= 64 ? page / 4 : 16); }
+
+// two e4m3 codes (the lower or the upper half of x) as float16, exact; 64 a clock
+// and SM, a third of the instructions of moving the bits into place
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t y;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t y;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, __half2 s) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), s);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
 
 // x / d = x mul >> shift for every x < 2^31: mul = ceil(2^(31 + l) / d) with 2^l >= d
 inline void fast_division(int d, uint32_t* mul, uint32_t* shift) {
@@ -48,7 +70,24 @@ struct AttendArgs {
   int32_t causal, window;
   float scale_log2;              // softmax scale * log2(e)
   uint32_t magic;                // 1024 twice in float16
+  int32_t bits;                  // of a channel's code: 4 or 8
+  int64_t table_b, table_h;      // 8 bits: strides of a request's and of a head's table
 };
+
+// The two encodings, as the kernels are told them.
+struct Int4 {
+  static constexpr int kBits = 4;
+};
+struct E4m3 {
+  static constexpr int kBits = 8;
+};
+
+// the table that a key/value head of a request reads by
+template <class F>
+__device__ __forceinline__ const int32_t* table_of(const AttendArgs& a, int b, int h) {
+  if constexpr (F::kBits == 8) return a.table + b * a.table_b + h * a.table_h;
+  else return a.table + (int64_t)b * a.max_blocks;
+}
 
 // A row of a partial result: O[d] unnormalised, running maximum (log2
 // domain), sum, pad to 16 bytes.
@@ -97,6 +136,17 @@ __device__ __forceinline__ uint32_t hidden_params(uint32_t par) {
   const __half2 x = *reinterpret_cast<const __half2*>(&par);
   const __half most = __hfma(__habs(__high2half(x)), __float2half(15.f), __habs(__low2half(x)));
   return __hle(most, __float2half(65504.f)) ? par : 0u;
+}
+
+// The same for 8 bits: codes that are NaN count as 0, scales beyond those that an
+// append leaves (or NaN) as 0.
+__device__ __forceinline__ uint32_t known_codes(uint32_t x) {
+  return x & ~__vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+__device__ __forceinline__ uint32_t known_scales(uint32_t par) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&par);
+  const uint32_t ok = __hle2_mask(__habs2(x), __float2half2_rn(128.f));   // false for NaN
+  return par & ok;
 }
 
 // Kernels 2 and 3 form exp2's argument as s c - m from a maximum m rounded to
@@ -512,7 +562,7 @@ cudaError_t launch_smem(SmemLimit& lim, size_t most, K kern, cudaLaunchConfig_t&
 }
 Workers simt_workers(int64_t max_rows);
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st);
-Workers mma_workers(int64_t max_rows);
+Workers mma_workers(int64_t max_rows, int bits);
 cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
 Workers tc_workers();
 cudaError_t launch_attend_tc(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);

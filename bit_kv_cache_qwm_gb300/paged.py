@@ -1,4 +1,4 @@
-"""Thin Python binding of libqwm's paged 4-bit cache (ctypes).
+"""Thin Python binding of libqwm's paged caches, 4 and 8 bits (ctypes).
 
 Argument checks and marshalling only; every step runs in the CUDA library, on
 the device of its tensors and that device's current stream.  Nothing is kept
@@ -13,6 +13,19 @@ A serving step:
     q, k = qwm_qk_norm_rope(q, k, w_q, w_k, cos_sin, plan.positions)
     qwm_paged_append(k, v, pool, plan.slots)
     o = qwm_paged_attend(q, pool, table, plan.kv_len, plan.cu_rows, max_new)
+
+With 8 bits the last two are
+
+    qwm_paged8_append(k, v, pool, table, plan.kv_len, plan.cu_rows)
+    o = qwm_paged8_attend(q, pool, table, plan.kv_len, plan.cu_rows, max_new)
+
+or, over the `width` pages of each request and key/value head that suit its
+queries best,
+
+    qwm_paged8_append(k, v, pool, table, plan.kv_len, plan.cu_rows)
+    qwm_paged8_bounds(pool, bounds, table, plan.kv_len, plan.cu_rows, max_new)
+    pages, lens = qwm_paged8_select(q, bounds, table, plan.kv_len, plan.cu_rows, page_tokens, width)
+    o = qwm_paged8_attend(q, pool, pages, lens, plan.cu_rows, max_new)
 """
 from __future__ import annotations
 
@@ -36,10 +49,16 @@ _PLAN = struct.Struct("=13q3i4x")
 _RELEASE = struct.Struct("=7q3i4x")
 _APPEND = struct.Struct("=17q4i")
 _ATTEND = struct.Struct("=17q9ifi4x")
+_APPEND8 = struct.Struct("=19q6i")
+_READ8 = struct.Struct("=13q6i")
+_ATTEND8 = struct.Struct("=17q9ifi4x2i")
+_BOUNDS8 = struct.Struct("=8q5i4x")
+_SELECT8 = struct.Struct("=14q9i4x")
 
 _Tensor, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
 _DTYPES = {torch.bfloat16: QWM_BF16, torch.float32: QWM_F32}
 _workspace_bytes: dict = {}
+_workspace8_bytes: dict = {}
 _INT_MAX = 2 ** 31 - 1   # a window beyond it is one as well
 
 
@@ -280,12 +299,12 @@ def qwm_paged_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, slots
                       T, n_pages, _DTYPES[dt], d, hk, page), "qwm_paged_append", dev)
 
 
-def _workspace_size(dev: int, d: int) -> int:
+def _workspace_size(known: dict, query, dev: int, d: int) -> int:
     with torch.cuda.device(dev):
-        n = int(lib().qwm_paged_attend_workspace_bytes(d))
+        n = int(query(d))
     if n == 0:
         raise ValueError(f"head_dim 64 or 128 is built, not {d}")
-    _workspace_bytes[dev, d] = n
+    known[dev, d] = n
     return n
 
 
@@ -320,7 +339,7 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
     lens = _array(kv_len, "kv_len", _I32, (B,), dev)
     cu = _array(cu_rows, "cu_rows", _I32, (B + 1,), dev)
     ls = 0 if lse is None else _array(lse, "lse", _F32, (T, hq), dev)
-    n_ws = _workspace_bytes.get((dev, d)) or _workspace_size(dev, d)
+    n_ws = _workspace_bytes.get((dev, d)) or _workspace_size(_workspace_bytes, lib().qwm_paged_attend_workspace_bytes, dev, d)
     ws = pool.new_empty(n_ws)
     _run(lib().qwm_paged_attend,
          _ATTEND.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
@@ -332,3 +351,193 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
 def paged_attend_kernel_for(dtype: torch.dtype, heads: int, kv_heads: int, max_new: int) -> int:
     """The attention kernel (PAGED_SIMT, PAGED_MMA or PAGED_TC) of the automatic choice."""
     return int(lib().qwm_paged_attend_kernel_for(_DTYPES[dtype], heads, kv_heads, max_new))
+
+
+# ---- the 8-bit cache
+
+def qwm_paged8_block_bytes(head_dim: int, page_tokens: int) -> int:
+    """Bytes of one block of the 8-bit cache: page_tokens slots of one key/value head."""
+    n = int(lib().qwm_paged8_block_bytes(head_dim, page_tokens))
+    if n == 0:
+        raise ValueError(f"head_dim 64 or 128 and page_tokens of {PAGE_TOKENS} are built, not {head_dim} and {page_tokens}")
+    return n
+
+
+def paged8_pool(n_pages: int, kv_heads: int, head_dim: int, page_tokens: int, device=None) -> torch.Tensor:
+    """An uninitialised 8-bit pool [n_pages, kv_heads, block bytes] (one per layer)."""
+    return torch.empty((n_pages, kv_heads, qwm_paged8_block_bytes(head_dim, page_tokens)), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def paged8_page_bounds(n_pages: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """Uninitialised bounds [n_pages, kv_heads, 2 head_dim + 16] of the pages of a pool."""
+    return torch.empty((n_pages, kv_heads, 2 * head_dim + 16), dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+# block bytes of the built sizes
+_PAGE8 = {(d, 2 * p * d + max(16, p // 4)): p for d in (64, 128) for p in PAGE_TOKENS}
+
+
+def _page8_tokens(pool, d: int) -> int:
+    """Tokens of a page of the 8-bit `pool` [pages, kv_heads, block] for heads of d channels."""
+    if not isinstance(pool, _Tensor) or not pool.is_cuda or pool.dtype is not torch.uint8 or pool.dim() != 3 \
+            or not pool.is_contiguous():
+        raise ValueError("pool: a contiguous CUDA uint8 tensor [pages, kv_heads, block bytes] is expected")
+    page = _PAGE8.get((d, pool.shape[2]))
+    if page is None:
+        raise ValueError(f"pool: {pool.shape[2]} bytes are no 8-bit block of a page of {PAGE_TOKENS} tokens at d = {d}")
+    return page
+
+
+def _step8(block_table, kv_len, cu_rows, index: int):
+    """Pointers of a step's block table, lengths and first rows; its requests and the table's width."""
+    table = _array(block_table, "block_table", _I32, (None, None), index)
+    B, width = block_table.shape
+    return (table, _array(kv_len, "kv_len", _I32, (B,), index), _array(cu_rows, "cu_rows", _I32, (B + 1,), index)), B, width
+
+
+def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                      cu_rows: torch.Tensor, k_hat: Optional[torch.Tensor] = None, v_hat: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None):
+    """Quantise the keys and values [rows, kv_heads, d] of a step (kv_len and
+    cu_rows as qwm_paged_plan returns them) to 8 bits into its requests' pages:
+    e4m3 codes, and a power of two as scale for every 16 slots and head, which
+    grows with larger tokens.  k_hat, v_hat receive the values that the stored
+    bytes stand for; rows behind the last request are left as they were in them."""
+    kr = _rows(k, "k")
+    shape, dt, dev = k.shape, k.dtype, k.get_device()
+    T, hk, d = shape
+    vr = _rows(v, "v", dt, dev, shape)
+    page = _page8_tokens(pool, d)
+    n_pages, hp, _ = pool.shape
+    if pool.get_device() != dev or hp != hk:
+        raise ValueError(f"pool: expected [pages, {hk}, block] on {k.device}, got {tuple(pool.shape)} on {pool.device}")
+    kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", dt, dev, shape)
+    vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", dt, dev, shape)
+    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+    _run(lib().qwm_paged8_append,
+         _APPEND8.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), *step, _status(status, dev), T, n_pages, _DTYPES[dt], d, hk, page,
+                       B, width), "qwm_paged8_append", dev)
+
+
+def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, cu_rows: torch.Tensor, rows: int,
+                    head_dim: int, dtype: torch.dtype = torch.bfloat16, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Keys and values [rows, kv_heads, head_dim] out of the pages: row
+    cu_rows[b] + i is the i-th of the last cu_rows[b + 1] - cu_rows[b] of the
+    first kv_len[b] tokens of request b.  Returns (k_out, v_out), new tensors of
+    `dtype` where none are given; rows behind the last request are left as they
+    were."""
+    page = _page8_tokens(pool, head_dim)
+    n_pages, hk, _ = pool.shape
+    dev = pool.get_device()
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype: bfloat16 or float32 is expected, got {dtype}")
+    shape = torch.Size((rows, hk, head_dim))
+    if k_out is None:
+        k_out = pool.new_empty(shape, dtype=dtype)
+    if v_out is None:
+        v_out = pool.new_empty(shape, dtype=dtype)
+    kr, vr = _rows(k_out, "k_out", dtype, dev, shape), _rows(v_out, "v_out", dtype, dev, shape)
+    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+    _run(lib().qwm_paged8_read,
+         _READ8.pack(*kr, *vr, pool.data_ptr(), *step, _status(status, dev), rows, n_pages, _DTYPES[dtype], head_dim, hk, page,
+                     B, width), "qwm_paged8_read", dev)
+    return k_out, v_out
+
+
+def qwm_paged8_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                      cu_rows: torch.Tensor, max_new: Optional[int] = None, causal: bool = True, window: int = 0,
+                      scale: float = 0.0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, kernel: int = PAGED_AUTO) -> torch.Tensor:
+    """qwm_paged_attend over the 8-bit pages, with the same arguments.
+    block_table and kv_len may be what qwm_paged8_select returns: a table
+    [requests, kv_heads, pages] lists the pages of each key/value head, and
+    kv_len, positions and the window count the tokens of that list."""
+    qr = _rows(q, "q")
+    T, hq, d = q.shape
+    dev, dt = q.get_device(), q.dtype
+    page = _page8_tokens(pool, d)
+    n_pages, hk, _ = pool.shape
+    if pool.get_device() != dev or hk < 1 or hq % hk:
+        raise ValueError(f"pool: kv heads that divide {hq} on {q.device} are expected, got {tuple(pool.shape)} on {pool.device}")
+    if out is None:
+        out, ot = _like(q)
+    else:
+        ot = _rows(out, "out", dt, dev, q.shape)
+    heads = 1
+    if isinstance(block_table, _Tensor) and block_table.dim() == 3:
+        heads = hk
+        table = _array(block_table, "block_table", _I32, (None, hk, None), dev)
+    else:
+        table = _array(block_table, "block_table", _I32, (None, None), dev)
+    B, width = block_table.shape[0], block_table.shape[-1]
+    lens = _array(kv_len, "kv_len", _I32, (B,), dev)
+    cu = _array(cu_rows, "cu_rows", _I32, (B + 1,), dev)
+    ls = 0 if lse is None else _array(lse, "lse", _F32, (T, hq), dev)
+    n_ws = _workspace8_bytes.get((dev, d)) or _workspace_size(_workspace8_bytes, lib().qwm_paged8_attend_workspace_bytes, dev, d)
+    ws = pool.new_empty(n_ws)
+    _run(lib().qwm_paged8_attend,
+         _ATTEND8.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
+                       T if max_new is None else max_new, _DTYPES[dt], d, hq, hk, page, B, width, 1 if causal else 0,
+                       min(window, _INT_MAX), scale, kernel, heads, 0), "qwm_paged8_attend", dev)
+    return out
+
+
+def _bounds8(bounds, n_pages, hk: int, d: int, dev: int) -> int:
+    p = _array(bounds, "bounds", torch.uint8, (n_pages, hk, 2 * d + 16), dev)
+    if p & 15:
+        raise ValueError("bounds: the pointer has to be a multiple of 16 bytes")
+    return p
+
+
+def qwm_paged8_bounds(pool: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                      cu_rows: torch.Tensor, max_new: int = 1, status: Optional[torch.Tensor] = None):
+    """Write the bounds (paged8_page_bounds) of the pages that hold a step's rows:
+    the largest and smallest value of each channel over all the keys in them, in
+    int8.  Call it after every append of a layer whose pages are selected.
+    max_new: the most rows of one request as the host knows it (any value is
+    right, a far too small one slow)."""
+    if not isinstance(bounds, _Tensor) or bounds.dim() != 3 or bounds.shape[2] not in (144, 272):
+        raise ValueError("bounds: [pages, kv_heads, 2 head_dim + 16] is expected")
+    d = (bounds.shape[2] - 16) // 2
+    page = _page8_tokens(pool, d)
+    n_pages, hk, _ = pool.shape
+    dev = pool.get_device()
+    at = _bounds8(bounds, n_pages, hk, d, dev)
+    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+    _run(lib().qwm_paged8_bounds,
+         _BOUNDS8.pack(pool.data_ptr(), at, *step, _status(status, dev), n_pages, max_new, d, hk, page, B, width),
+         "qwm_paged8_bounds", dev)
+
+
+def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                      cu_rows: torch.Tensor, page_tokens: int, width: int, sink: int = 0,
+                      pages: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None):
+    """The `width` pages (or all there are) that each request and key/value head
+    reads this step: those of the step's own tokens, the first `sink`, and the ones
+    with the highest scores, bounds of the products of the queries q [rows, heads,
+    d] with the keys in them.  Returns (pages int32 [requests, kv_heads, width],
+    lens int32 [requests]), the block_table and kv_len of a qwm_paged8_attend."""
+    qr = _rows(q, "q")
+    T, hq, d = q.shape
+    dev, dt = q.get_device(), q.dtype
+    hk = bounds.shape[1] if isinstance(bounds, _Tensor) and bounds.dim() == 3 else 0
+    at = _bounds8(bounds, None, hk, d, dev)
+    if hk < 1 or hq % hk:
+        raise ValueError(f"bounds: kv heads that divide {hq} are expected, got {tuple(bounds.shape)}")
+    step, B, blocks = _step8(block_table, kv_len, cu_rows, dev)
+    if width < 1:
+        raise ValueError("width: at least one page")
+    if pages is None:
+        pages = kv_len.new_empty((B, hk, width))
+    if lens is None:
+        lens = torch.empty_like(kv_len)
+    out = _array(pages, "pages", _I32, (B, hk, width), dev), _array(lens, "lens", _I32, (B,), dev)
+    n_ws = 4 * B * hk * blocks
+    ws = bounds.new_empty(max(n_ws, 1))
+    _run(lib().qwm_paged8_select,
+         _SELECT8.pack(*qr, at, *step, *out, _status(status, dev), ws.data_ptr(), n_ws, T, bounds.shape[0], _DTYPES[dt], d, hq,
+                       hk, page_tokens, B, blocks, width, sink), "qwm_paged8_select", dev)
+    return pages, lens

@@ -65,7 +65,11 @@ EXPORTS = ["qwm_status_string", "qwm_sizes", "qwm_create", "qwm_destroy", "qwm_s
            "qwm_dequantize", "qwm_selftest_wait_timeout", "qwm_num_tokens",
            "qwm_num_tiles", "qwm_num_segments", "qwm_version", "qwm_qk_norm_rope", "qwm_paged_plan",
            "qwm_paged_release", "qwm_paged_block_bytes", "qwm_paged_append", "qwm_paged_attend",
-           "qwm_paged_attend_workspace_bytes", "qwm_paged_attend_kernel_for"]
+           "qwm_paged_attend_workspace_bytes", "qwm_paged_attend_kernel_for",]
+# those of the paged 8-bit cache
+EXPORTS8 = ["qwm_paged8_block_bytes", "qwm_paged8_append", "qwm_paged8_read", "qwm_paged8_attend",
+            "qwm_paged8_attend_workspace_bytes", "qwm_paged8_bounds", "qwm_paged8_select",
+            "qwm_paged8_select_workspace_bytes"]
 
 _lib = None
 
@@ -106,6 +110,11 @@ def lib() -> ctypes.CDLL:
         "qwm_paged_release": [ctypes.c_char_p, VP],
         "qwm_paged_append": [ctypes.c_char_p, VP],
         "qwm_paged_attend": [ctypes.c_char_p, VP],
+        "qwm_paged8_append": [ctypes.c_char_p, VP],
+        "qwm_paged8_read": [ctypes.c_char_p, VP],
+        "qwm_paged8_attend": [ctypes.c_char_p, VP],
+        "qwm_paged8_bounds": [ctypes.c_char_p, VP],
+        "qwm_paged8_select": [ctypes.c_char_p, VP],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -117,6 +126,12 @@ def lib() -> ctypes.CDLL:
     L.qwm_paged_block_bytes.argtypes = [I32, I32]
     L.qwm_paged_attend_workspace_bytes.restype = ctypes.c_size_t
     L.qwm_paged_attend_workspace_bytes.argtypes = [I32]
+    L.qwm_paged8_block_bytes.restype = ctypes.c_size_t
+    L.qwm_paged8_block_bytes.argtypes = [I32, I32]
+    L.qwm_paged8_attend_workspace_bytes.restype = ctypes.c_size_t
+    L.qwm_paged8_attend_workspace_bytes.argtypes = [I32]
+    L.qwm_paged8_select_workspace_bytes.restype = ctypes.c_size_t
+    L.qwm_paged8_select_workspace_bytes.argtypes = [I32, I32, I32]
     L.qwm_paged_attend_kernel_for.restype = I32
     L.qwm_paged_attend_kernel_for.argtypes = [I32, I32, I32, I64]
     L.qwm_attend_kernel_for.restype = I32

@@ -545,6 +545,163 @@ size_t qwm_paged_attend_workspace_bytes(int32_t head_dim);
 /* The kernel (1 to 3) that the automatic choice runs. */
 int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new);
 
+/* ------------------------------------------------------------------------
+ * The paged 8-bit cache: the paged cache above with 8 bits a channel, for
+ * layers or models that 4 bits disturb, and attention over selected pages for
+ * streams too long to read at every step.  qwm_paged_plan, qwm_paged_release
+ * and qwm_qk_norm_rope serve both; in every layer a step is then
+ *   qwm_paged8_append   quantisation of the new keys and values into pages;
+ *   qwm_paged8_attend   attention of the new rows over their requests' pages;
+ * or, where a step is to read only some of the pages,
+ *   qwm_paged8_append, qwm_paged8_bounds, qwm_paged8_select, and
+ *   qwm_paged8_attend with the tables and lengths that select gives.
+ * qwm_paged8_read gives tokens back.  What is said above of pointers, streams,
+ * graphs and `status` holds here too.
+ *
+ * Pool: [n_pages][kv_heads][block], one pool per layer.  A block holds
+ * page_tokens slots (16, 32, 64, 128 or 256) of one key/value head:
+ *   K codes  [slot][d]          e4m3
+ *   V codes  [slot][d]
+ *   scales   [slot / 16][2]     fp16: of K and of V for 16 slots together
+ * and up to 12 unused bytes: qwm_paged8_block_bytes = 2 page_tokens d +
+ * max(16, page_tokens / 4).  A scale is a power of two from 2^-15 to 2^7, so
+ * every value code x scale is exact in fp16.  Token n of request b is in slot
+ * n mod page_tokens of page block_table[b][n / page_tokens].
+ *
+ * A step's rows: row cu_rows[b] + i is token
+ * kv_len[b] - (cu_rows[b + 1] - cu_rows[b]) + i of request b (kv_len with the
+ * new tokens, as a plan leaves it).  A kv_len outside
+ * [0, max_blocks page_tokens] and cu_rows that decrease or leave [0, rows] are
+ * clamped, a row before its request's first token and a page id outside
+ * [0, n_pages) are passed over; each sets QWM_DEV_BOUNDS. */
+
+/* Bytes of one block, or 0 for a head_dim or page_tokens that is not built. */
+size_t qwm_paged8_block_bytes(int32_t head_dim, int32_t page_tokens);
+
+/* Quantise the keys and values [rows][kv_heads][d] of a step.  For the tokens
+ * of 16 neighbouring slots (and a head, and k and v apart):
+ *   NaN -> 0 (QWM_DEV_NAN), then clamped to +-57344 (QWM_DEV_SATURATED)
+ *   scale = the least 2^e, -15 <= e <= 7, with 448 scale >= max |x| over the
+ *           block's new tokens; where the block holds earlier tokens of the
+ *           request, no less than its scale before
+ *   code  = e4m3(x / scale), nearest even;  x_hat = code scale
+ * Where a scale grows, the codes of the block's earlier tokens are rewritten for
+ * it: the same values, but for those that fall below e4m3's normal numbers
+ * (2^-6 of the scale), which are rounded to its multiples of 2^-9.
+ * k_hat and v_hat (optional; dtype, rows like the inputs) receive x_hat, exact
+ * in either dtype; they overlap neither the inputs nor each other, and rows
+ * outside cu_rows[0 .. requests] (or passed over) are left as they were.  Pages
+ * that the call writes must not be in two places of the tables. */
+typedef struct {
+  qwm_rows k, v;
+  qwm_rows k_hat, v_hat;         /* ptr NULL: not wanted                        */
+  void* pool;                    /* 16-byte aligned                             */
+  const int32_t* block_table;    /* [requests][max_blocks]                      */
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* cu_rows;        /* [requests + 1]                              */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t rows, n_pages;
+  int32_t dtype, head_dim, kv_heads, page_tokens;
+  int32_t requests, max_blocks;
+} qwm_paged8_append_args;
+qwm_status qwm_paged8_append(const qwm_paged8_append_args* a, void* stream);
+
+/* The values code x scale of the tokens of a step, or of any tokens: the last
+ * cu_rows[b + 1] - cu_rows[b] of the first kv_len[b] of request b.  Exact in
+ * either dtype.  Rows outside cu_rows[0 .. requests] are left as they were, rows
+ * passed over become 0. */
+typedef struct {
+  qwm_rows k, v;                 /* outputs [rows][kv_heads][d]                 */
+  const void* pool;              /* 16-byte aligned                             */
+  const int32_t* block_table;    /* [requests][max_blocks]                      */
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* cu_rows;        /* [requests + 1]                              */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t rows, n_pages;
+  int32_t dtype, head_dim, kv_heads, page_tokens;
+  int32_t requests, max_blocks;
+} qwm_paged8_read_args;
+qwm_status qwm_paged8_read(const qwm_paged8_read_args* a, void* stream);
+
+/* Attention of the rows of a step over their requests' pages, as
+ * qwm_paged_attend: the same arguments, results, kernels (1 float32 on the CUDA
+ * cores, 2 mma.sync for few rows, 3 tcgen05) and choice among them; what it says
+ * of hidden tokens, rows that see nothing, NaN in q, large logits and waits
+ * holds here too.
+ * table_heads: 1, or kv_heads for a table of its own for every key/value head,
+ * block_table [requests][kv_heads][max_blocks], as qwm_paged8_select writes
+ * them: each lists the pages that its head reads, and kv_len, positions and the
+ * window count the tokens of that list. */
+typedef struct {
+  qwm_paged_attend_args attend;
+  int32_t table_heads;
+  int32_t reserved;              /* 0                                           */
+} qwm_paged8_attend_args;
+qwm_status qwm_paged8_attend(const qwm_paged8_attend_args* a, void* stream);
+
+/* Bytes of workspace that any qwm_paged8_attend with this head_dim needs on the
+ * current device (0 for a head_dim that is not built). */
+size_t qwm_paged8_attend_workspace_bytes(int32_t head_dim);
+
+/* Bounds of the keys of the pages that hold a step's rows, over all the tokens
+ * in them (n < kv_len[b]).  bounds: [n_pages][kv_heads][2 d + 16] bytes,
+ *   int8 high[d], int8 low[d], float32 unit, 12 bytes of 0
+ *   unit = f32(max_c max(|max k_hat_c|, |min k_hat_c|) / 127)
+ *   high[c], low[c] = rint(f32(max k_hat_c / unit)), rint(f32(min k_hat_c / unit))
+ * (0 where unit is 0).  After every append of a layer whose pages are selected;
+ * pages that a step does not write keep theirs.  max_new is the most rows of one
+ * request as the host knows it: any value is right, a far too small one slow. */
+typedef struct {
+  const void* pool;              /* 16-byte aligned                             */
+  void* bounds;                  /* 16-byte aligned                             */
+  const int32_t* block_table;    /* [requests][max_blocks]                      */
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* cu_rows;        /* [requests + 1]                              */
+  uint32_t* status;              /* or NULL                                     */
+  int64_t n_pages, max_new;
+  int32_t head_dim, kv_heads, page_tokens;
+  int32_t requests, max_blocks;  /* at most 8192 requests                       */
+} qwm_paged8_bounds_args;
+qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* stream);
+
+/* The pages that each request and key/value head reads this step: `width` of
+ * them, or all there are.  Among them are always the pages from that of the
+ * step's first row on, then the first `sink` pages of the request, then those
+ * with the highest scores, the lower page first among equal ones.
+ * The score of a page is the largest, over the request's rows and the query
+ * heads of the key/value head, of
+ *   f32(f32(S unit_page) unit_row),  S = sum_c x_c (x_c >= 0 ? high_c : low_c)
+ *   unit_row = f32(max |q_c| / 127) (0 below 2^-100), x_c = rint(f32(q_c / unit_row))
+ * (NaN in q counts as 0, infinities as the largest float32; x = 0 where
+ * unit_row is 0): S is a whole number below 2^24, so the scores, and the choice,
+ * do not depend on the order of sums.  It bounds q . k over the page up to the
+ * roundings to int8.
+ *   pages[b][h][i]  the page ids, in the order of the request; -1 behind them
+ *   len_out[b]      tokens in them: kv_len[b] less those of the pages left out
+ * A request without rows gets no pages and length 0.  So does one whose own
+ * step's pages are more than `width`, which sets QWM_DEV_CAPACITY.  Page ids out of
+ * range, and bounds that are NaN, come last.  max_new as in qwm_paged8_bounds. */
+typedef struct {
+  qwm_rows q;                    /* [rows][heads][d] dtype                      */
+  const void* bounds;            /* 16-byte aligned                             */
+  const int32_t* block_table;    /* [requests][max_blocks]                      */
+  const int32_t* kv_len;         /* [requests]                                  */
+  const int32_t* cu_rows;        /* [requests + 1]                              */
+  int32_t* pages;                /* [requests][kv_heads][width]                 */
+  int32_t* len_out;              /* [requests]; not kv_len                      */
+  uint32_t* status;              /* or NULL                                     */
+  void* workspace;               /* 256-byte aligned                            */
+  size_t workspace_bytes;        /* >= qwm_paged8_select_workspace_bytes        */
+  int64_t rows, n_pages;
+  int32_t dtype, head_dim, heads, kv_heads, page_tokens;
+  int32_t requests, max_blocks;  /* at most 8192 requests                       */
+  int32_t width, sink;           /* >= 1, >= 0                                  */
+} qwm_paged8_select_args;
+qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* stream);
+
+/* Bytes of workspace of a selection over this many requests, heads and pages. */
+size_t qwm_paged8_select_workspace_bytes(int32_t requests, int32_t kv_heads, int32_t max_blocks);
+
 #ifdef __cplusplus
 }
 #endif
