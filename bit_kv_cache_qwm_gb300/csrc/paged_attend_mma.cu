@@ -50,7 +50,18 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kCw = 4, kCtas = 3, kStages = 2, kSub = 2, kTk = 16 * kSub * kCw, kNt = kCw * 32, kItem = 2;
+constexpr int kCw = 4, kNt = kCw * 32, kItem = 2;
+// CTAs an SM (of 8 rows), a warp's stages, and the blocks of 16 tokens in one
+template <class F>
+struct Plan;
+template <>
+struct Plan<Int4> {
+  static constexpr int kCtas = 3, kStages = 2, kSub = 2, kTk = 16 * kSub * kCw;
+};
+template <>
+struct Plan<E4m3> {
+  static constexpr int kCtas = 2, kStages = 2, kSub = 2, kTk = 16 * kSub * kCw;
+};
 constexpr float kNone = -3.0e38f;   // running maximum of a row that has seen nothing
 // Where a row's maximum is x0 when it is taken, m = x0 - 7, and it is taken again
 // when a logit passes x0 + 8: P <= 2^15 stays inside float16, and a token of a
@@ -93,8 +104,10 @@ __device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z, uint
 __device__ __forceinline__ int token_of(int n) { return (n & 1) ? 4 + ((n >> 1) ^ 1) : n >> 1; }
 
 // 16 tokens of one head as they lie in a ring stage
+template <int D, class F>
+struct Stage;
 template <int D>
-struct Stage {
+struct Stage<D, Int4> {
   static constexpr int G = D / 32;
   static constexpr int kcode = 0, kpar = 8 * D, vcode = kpar + 64 * G, vpar = vcode + 8 * D, bytes = vpar + 64 * G;
   static constexpr int copies = (bytes / 16 + 31) / 32;   // of 16 bytes, a lane
@@ -103,7 +116,8 @@ struct Stage {
   // the page's block, for 16-byte piece 32 k + lane of the stage.
   struct Source {
     int cst[copies], mul[copies];
-    __device__ __forceinline__ void init(int page, int half, int lane) {
+    __device__ __forceinline__ void init(int page, int block, int lane) {
+      const int half = block / 2;
 #pragma unroll
       for (int k = 0; k < copies; ++k) {
         const int o = 16 * (32 * k + lane);
@@ -124,17 +138,53 @@ struct Stage {
   }
 };
 
+// 8 bits: the rows' 16-byte pieces are swapped so that neither the loads of keys (8
+// lanes: two rows of opposite parity) nor those of values (four rows that follow
+// one another) meet in a bank.  A copy takes 512 bytes, whole rows, so a lane's
+// piece is the same in each.
+template <int D>
+struct Stage<D, E4m3> {
+  static constexpr int vcode = 16 * D, scale = 32 * D, bytes = 32 * D + 16;
+  // where piece x of a row lies
+  __device__ __forceinline__ static int k_at(int row, int x) { return row * D + ((D == 128 ? x ^ (row & 1) : x) << 4); }
+  __device__ __forceinline__ static int v_at(int row, int x) {
+    return vcode + row * D + ((D == 128 ? x ^ ((row & 3) << 1) : x ^ (row & 2)) << 4);
+  }
+  struct Source {
+    int k, v, scales;
+    __device__ __forceinline__ void init(int page, int block, int lane) {
+      const int row = lane / (D / 16), x = lane % (D / 16);
+      k = k_at(row, x);
+      v = v_at(row, x) - vcode + page * D;
+      scales = 2 * page * D;
+    }
+  };
+  __device__ __forceinline__ static void copy(uint32_t stage, const uint8_t* blk, int at, const Source& src, int lane) {
+    const uint8_t* kb = blk + (uint32_t)(src.k + at * D);
+    const uint8_t* vb = blk + (uint32_t)(src.v + at * D);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage + 512 * i), "l"(kb + 512 * i) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage + vcode + 512 * i), "l"(vb + 512 * i) : "memory");
+    }
+    if (lane == 0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stage + scale), "l"(blk + (uint32_t)(src.scales + at / 4)) : "memory");
+  }
+};
+
 // The blocks of one warp, in order, ahead of the arithmetic.  Its walker is in
 // shared memory: registers hold only what every block needs.
-template <int D, class W>
+template <int D, class F, class W>
 struct Ahead {
+  using St = Stage<D, F>;
+  static constexpr int kSub = Plan<F>::kSub, kTk = Plan<F>::kTk;
   W* walker;
   int t, to, base;       // next tile; end of the item's; first tile of the ids
   int lo, hi, ids[kSub];
   const int32_t* row;
   const uint8_t* head;   // pool + the head's offset in a page
   uint32_t page_bytes;   // of all heads
-  typename Stage<D>::Source src;
+  typename St::Source src;
   bool more;
 
   __device__ __forceinline__ void fetch_ids(const AttendArgs& a, int warp, int lane) {
@@ -152,7 +202,7 @@ struct Ahead {
   }
   __device__ __forceinline__ void open(const AttendArgs& a, const W& w, int warp, int lane) {
     t = w.from, to = w.to, lo = w.lo, hi = w.hi;
-    row = a.table + (int64_t)w.b * a.max_blocks;
+    row = table_of<F>(a, w.b, w.h);
     head = a.pool + (int64_t)w.h * a.block;
     fetch_ids(a, warp, lane);
   }
@@ -166,7 +216,7 @@ struct Ahead {
         const int pg = __shfl_sync(0xffffffffu, ids[x], t - base);
         if (pg >= 0) {
           have |= 1u << x;
-          Stage<D>::copy(stage + x * Stage<D>::bytes, head + (uint64_t)(uint32_t)pg * page_bytes,
+          St::copy(stage + x * St::bytes, head + (uint64_t)(uint32_t)pg * page_bytes,
                          (t * kTk + 16 * (kSub * warp + x)) & (a.page - 1), src, lane);
         }
       }
@@ -189,18 +239,20 @@ struct Ahead {
   }
 };
 
-template <int D, int NB>
+template <int D, int NB, class F>
 struct Smem {
   static constexpr int LD = D + 4;                          // rows 2 c of a store phase 8 banks apart
-  static constexpr int merge = kCw * kStages * kSub * Stage<D>::bytes;   // float [kCw][8 NB][LD]
+  static constexpr int merge = kCw * Plan<F>::kStages * Plan<F>::kSub * Stage<D, F>::bytes;   // float [kCw][8 NB][LD]
   static constexpr int stat = merge + kCw * 8 * NB * LD * 4;
   static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
 };
 
-template <int D, int NB>
-__global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
+template <int D, int NB, class F>
+__global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
   constexpr int R = 8 * NB, KW = D / 32, MB = D / 16;
-  using Sm = Smem<D, NB>;
+  constexpr int kStages = Plan<F>::kStages, kSub = Plan<F>::kSub, kTk = Plan<F>::kTk;
+  using Sm = Smem<D, NB, F>;
+  using St = Stage<D, F>;
   using W = Walker<R, kTk, kItem>;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ W ahead_sh[kCw];
@@ -213,14 +265,14 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   it.start(a, sh.b, sh.skip, sh.per, sh.n);
   if (lane == 0) ahead_sh[warp] = it;
   __syncwarp();
-  Ahead<D, W> ahead;
+  Ahead<D, F, W> ahead;
   ahead.walker = &ahead_sh[warp];
   ahead.more = true;
   ahead.page_bytes = (uint32_t)(a.kv_heads * a.block);
-  ahead.src.init(a.page, a.block / 2, lane);
+  ahead.src.init(a.page, a.block, lane);
   ahead.open(a, it, warp, lane);
   // the warp's stages; copies of a lane start 16 bytes a lane into one
-  const uint8_t* ring = sm + warp * kStages * kSub * Stage<D>::bytes;
+  const uint8_t* ring = sm + warp * kStages * kSub * St::bytes;
   const uint32_t ring_at = su32(ring) + 16 * lane;
   // the item's queries, sent for ahead of the copies, which they would queue
   // behind (2 to 3 us of a first item)
@@ -237,7 +289,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   };
   load_q();
   uint32_t have = 0;     // kSub bits for each stage: which 16 tokens there are
-  for (int i = 0; i < kStages; ++i) have |= ahead.copy(a, ring_at + i * kSub * Stage<D>::bytes, warp, lane) << (kSub * i);
+  for (int i = 0; i < kStages; ++i) have |= ahead.copy(a, ring_at + i * kSub * St::bytes, warp, lane) << (kSub * i);
   int st = 0;
   bool more = true;
 
@@ -275,10 +327,11 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const float* y = x + 8 * i;
-        qf[nb][2 * i][0] = h2u(__floats2half2_rn(y[0] * qs, y[4] * qs));
-        qf[nb][2 * i][1] = h2u(__floats2half2_rn(y[1] * qs, y[5] * qs));
-        qf[nb][2 * i + 1][0] = h2u(__floats2half2_rn(y[2] * qs, y[6] * qs));
-        qf[nb][2 * i + 1][1] = h2u(__floats2half2_rn(y[3] * qs, y[7] * qs));
+        constexpr bool nibbles = F::kBits == 4;   // else the channels follow one another
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          qf[nb][2 * i + (k >> 1)][k & 1] =
+              h2u(__floats2half2_rn(y[nibbles ? k : 2 * k] * qs, y[nibbles ? k + 4 : 2 * k + 1] * qs));
       }
       const float f = row_factor(a, 127 + e);
 #pragma unroll
@@ -309,7 +362,6 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
       for (int k = 0; k < 2; ++k) m[nb][k] = kNone, l[nb][k] = 0.f;
     }
     for (int t = it.from; t < it.to; ++t) {
-      using St = Stage<D>;
       const int n0 = t * kTk + 16 * kSub * warp;                   // the step's first token
       const uint32_t live = (have >> (kSub * st)) & ((1u << kSub) - 1);
       // every row sees all of them
@@ -324,41 +376,62 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
         for (int e = 0; e < kSub; ++e) {
           const uint8_t* x = x0 + e * St::bytes;
           float s2[NB][4];   // two sums: half the chain of dependent MMAs
-          uint32_t kw[2][KW];
-          __half2 ks[2], kz[2];
+          if constexpr (F::kBits == 8) {
+            uint32_t kw[2][2 * KW];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int row = 8 * b + tok0;
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4*>(x + St::kcode + row * 64 + 16 * c);
-              kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(x + St::kcode + row * 32 + 8 * c);
-              kw[b][0] = u.x, kw[b][1] = u.y;
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < KW / 2; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4*>(x + St::k_at(8 * b + tok0, c * (KW / 2) + i));
+                kw[b][4 * i] = u.x, kw[b][4 * i + 1] = u.y, kw[b][4 * i + 2] = u.z, kw[b][4 * i + 3] = u.w;
+              }
+#pragma unroll
+            for (int i = 0; i < 2 * KW; ++i) {
+              const uint32_t f[4] = {e4m3_lo(kw[0][i]), e4m3_lo(kw[1][i]), e4m3_hi(kw[0][i]), e4m3_hi(kw[1][i])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                float* to = (i & 1) ? s2[nb] : s[nb][e];
+                if (i < 2) mma0(to, f, qf[nb][i][0], qf[nb][i][1]);
+                else mma(to, f, qf[nb][i][0], qf[nb][i][1]);
+              }
             }
-            const __half2 par = *reinterpret_cast<const __half2*>(x + St::kpar + (row * St::G + c * St::G / 4) * 4);
-            kz[b] = __low2half2(par);
-            ks[b] = __high2half2(par);
-          }
-#pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            uint32_t f[4], f2[4];
+          } else {
+            uint32_t kw[2][KW];
+            __half2 ks[2], kz[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              f[b] = dq_lo(kw[b][i], ks[b], kz[b], magic);
-              f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b], magic);
-              const uint32_t up = kw[b][i] >> 8;
-              f2[b] = dq_lo(up, ks[b], kz[b], magic);
-              f2[2 + b] = dq_hi(up, ks[b], kz[b], magic);
+              const int row = 8 * b + tok0;
+              if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(x + St::kcode + row * 64 + 16 * c);
+                kw[b][0] = u.x, kw[b][1] = u.y, kw[b][2] = u.z, kw[b][3] = u.w;
+              } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(x + St::kcode + row * 32 + 8 * c);
+                kw[b][0] = u.x, kw[b][1] = u.y;
+              }
+              const __half2 par = *reinterpret_cast<const __half2*>(x + St::kpar + (row * St::G + c * St::G / 4) * 4);
+              kz[b] = __low2half2(par);
+              ks[b] = __high2half2(par);
             }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              if (i == 0) {
-                mma0(s[nb][e], f, qf[nb][0][0], qf[nb][0][1]);
-                mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
-              } else {
-                mma(s[nb][e], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-                mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+            for (int i = 0; i < KW; ++i) {
+              uint32_t f[4], f2[4];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                f[b] = dq_lo(kw[b][i], ks[b], kz[b], magic);
+                f[2 + b] = dq_hi(kw[b][i], ks[b], kz[b], magic);
+                const uint32_t up = kw[b][i] >> 8;
+                f2[b] = dq_lo(up, ks[b], kz[b], magic);
+                f2[2 + b] = dq_hi(up, ks[b], kz[b], magic);
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                if (i == 0) {
+                  mma0(s[nb][e], f, qf[nb][0][0], qf[nb][0][1]);
+                  mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
+                } else {
+                  mma(s[nb][e], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
+                  mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+                }
               }
             }
           }
@@ -366,6 +439,13 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[nb][e][i] += s2[nb][i];
+          if constexpr (F::kBits == 8) {   // the block's scale, behind the product
+            const float ks = __half2float(*reinterpret_cast<const __half*>(x + St::scale));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[nb][e][i] *= ks;
+          }
         }
         // ---- softmax: s[nb][e][2 b + k] is token 16 e + 8 b + tok0, row 2 c + k
         uint32_t pf[NB][kSub][2];
@@ -423,59 +503,110 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
 #pragma unroll
         for (int e = 0; e < kSub; ++e) {
           const uint8_t* x = x0 + e * St::bytes;
-          uint32_t v0[2][D / 64], v1[2][D / 64];
-          __half2 vz[2], vs[2];
+          if constexpr (F::kBits == 8) {
+            uint32_t v0[2][D / 32], v1[2][D / 32];
+            uint32_t par = *reinterpret_cast<const uint32_t*>(x + St::scale);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int r0 = 8 * b + ta, r1 = 8 * b + tb;
-            if constexpr (D == 128) {
-              const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::vcode + r0 * 64 + 8 * g);
-              const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::vcode + r1 * 64 + 8 * g);
-              v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
-            } else {
-              v0[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r0 * 32 + 4 * g);
-              v1[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r1 * 32 + 4 * g);
-            }
-            uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
-            uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
-            if (!whole) {
-              // tokens outside the request, on no page, or hidden from some row:
-              // their bytes may be anything
-              const int y0 = n0 + 16 * e + r0, y1 = n0 + 16 * e + r1;
-              const bool got = live >> e & 1;
-              p0 = !got || y0 < it.lo || y0 >= it.hi ? 0u : hidden_params(p0);
-              p1 = !got || y1 < it.lo || y1 >= it.hi ? 0u : hidden_params(p1);
-            }
-            vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
-            vs[b] = u2h(__byte_perm(p0, p1, 0x7632));
-          }
-          // two blocks j of 16 channels at a time: f[.][2 b] is channel row g,
-          // f[.][2 b + 1] row g + 8 (d = 128: of the two words; d = 64: of the
-          // two halves of the one)
-#pragma unroll
-          for (int y = 0; y < MB / 2; ++y) {
-            uint32_t f[2][4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                // byte y (or y + 2) of both tokens into bytes 0 and 2
-                const int word = D == 128 ? q : 0, byte = D == 128 ? y : y + 2 * q;
-                const uint32_t v = __byte_perm(v0[b][word], v1[b][word], byte * 0x0011 + (4 + byte) * 0x1100);
-                f[0][2 * b + q] = dq_lo(v, vs[b], vz[b], magic);
-                f[1][2 * b + q] = dq_hi(v, vs[b], vz[b], magic);
+            for (int b = 0; b < 2; ++b) {
+              const int r0 = 8 * b + ta, r1 = 8 * b + tb;
+              if constexpr (D == 128) {
+                const uint4 u0 = *reinterpret_cast<const uint4*>(x + St::v_at(r0, g));
+                const uint4 u1 = *reinterpret_cast<const uint4*>(x + St::v_at(r1, g));
+                v0[b][0] = u0.x, v0[b][1] = u0.y, v0[b][2] = u0.z, v0[b][3] = u0.w;
+                v1[b][0] = u1.x, v1[b][1] = u1.y, v1[b][2] = u1.z, v1[b][3] = u1.w;
+              } else {
+                const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::v_at(r0, g >> 1) + 8 * (g & 1));
+                const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::v_at(r1, g >> 1) + 8 * (g & 1));
+                v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
               }
+              if (!whole) {
+                // tokens outside the request, on no page, or hidden from some row:
+                // their bytes may be anything
+                const int y0 = n0 + 16 * e + r0, y1 = n0 + 16 * e + r1;
+                const bool got = live >> e & 1, in0 = got && y0 >= it.lo && y0 < it.hi, in1 = got && y1 >= it.lo && y1 < it.hi;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < D / 32; ++i) {
+                  v0[b][i] = in0 ? known_codes(v0[b][i]) : 0u;
+                  v1[b][i] = in1 ? known_codes(v1[b][i]) : 0u;
+                }
+              }
+            }
+            if (!whole) par = known_scales(par);
+            const __half2 vs = __high2half2(u2h(par));
+            // as below: byte j of the lane's channels is row g of block j, byte MB + j
+            // row g + 8
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+            for (int y = 0; y < MB / 2; ++y) {
+              uint32_t f[2][4];
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int word = (y >> 1) + MB / 4 * q;
+                  const uint32_t v = __byte_perm(v0[b][word], v1[b][word], (y & 1) ? 0x7362 : 0x5140);
+                  f[0][2 * b + q] = mul_f16x2(e4m3_lo(v), vs);
+                  f[1][2 * b + q] = mul_f16x2(e4m3_hi(v), vs);
+                }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+            }
+          } else {
+            uint32_t v0[2][D / 64], v1[2][D / 64];
+            __half2 vz[2], vs[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int r0 = 8 * b + ta, r1 = 8 * b + tb;
+              if constexpr (D == 128) {
+                const uint2 u0 = *reinterpret_cast<const uint2*>(x + St::vcode + r0 * 64 + 8 * g);
+                const uint2 u1 = *reinterpret_cast<const uint2*>(x + St::vcode + r1 * 64 + 8 * g);
+                v0[b][0] = u0.x, v0[b][1] = u0.y, v1[b][0] = u1.x, v1[b][1] = u1.y;
+              } else {
+                v0[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r0 * 32 + 4 * g);
+                v1[b][0] = *reinterpret_cast<const uint32_t*>(x + St::vcode + r1 * 32 + 4 * g);
+              }
+              uint32_t p0 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r0 * St::G + g * St::G / 8) * 4);
+              uint32_t p1 = *reinterpret_cast<const uint32_t*>(x + St::vpar + (r1 * St::G + g * St::G / 8) * 4);
+              if (!whole) {
+                // tokens outside the request, on no page, or hidden from some row:
+                // their bytes may be anything
+                const int y0 = n0 + 16 * e + r0, y1 = n0 + 16 * e + r1;
+                const bool got = live >> e & 1;
+                p0 = !got || y0 < it.lo || y0 >= it.hi ? 0u : hidden_params(p0);
+                p1 = !got || y1 < it.lo || y1 >= it.hi ? 0u : hidden_params(p1);
+              }
+              vz[b] = u2h(__byte_perm(p0, p1, 0x5410));
+              vs[b] = u2h(__byte_perm(p0, p1, 0x7632));
+            }
+            // two blocks j of 16 channels at a time: f[.][2 b] is channel row g,
+            // f[.][2 b + 1] row g + 8 (d = 128: of the two words; d = 64: of the
+            // two halves of the one)
+#pragma unroll
+            for (int y = 0; y < MB / 2; ++y) {
+              uint32_t f[2][4];
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  // byte y (or y + 2) of both tokens into bytes 0 and 2
+                  const int word = D == 128 ? q : 0, byte = D == 128 ? y : y + 2 * q;
+                  const uint32_t v = __byte_perm(v0[b][word], v1[b][word], byte * 0x0011 + (4 + byte) * 0x1100);
+                  f[0][2 * b + q] = dq_lo(v, vs[b], vz[b], magic);
+                  f[1][2 * b + q] = dq_hi(v, vs[b], vz[b], magic);
+                }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+            }
           }
         }
       }
       // the stage is read: the step kStages on takes it
       __syncwarp();
       have = (have & ~(((1u << kSub) - 1) << (kSub * st))) |
-             (ahead.copy(a, ring_at + st * kSub * Stage<D>::bytes, warp, lane) << (kSub * st));
+             (ahead.copy(a, ring_at + st * kSub * St::bytes, warp, lane) << (kSub * st));
       if (++st == kStages) st = 0;
     }
     // ---- the warps' parts of the item meet
@@ -539,33 +670,40 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? kCtas : 2) paged_attend_mma_ker
   } while (more);
 }
 
-template <int D, int NB>
+template <int D, int NB, class F>
 cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
   static SmemLimit limit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)workers, 1, 1);
   cfg.blockDim = dim3(kNt, 1, 1);
-  cfg.dynamicSmemBytes = Smem<D, NB>::bytes;
+  cfg.dynamicSmemBytes = Smem<D, NB, F>::bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB>, cfg, a);
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB, F>, cfg, a);
+}
+
+template <class F>
+Workers workers_of(int64_t max_rows) {
+  const int sms = sm_count();
+  return max_rows <= 8 ? Workers{Plan<F>::kCtas * sms, 8} : Workers{2 * sms, 16};
+}
+
+template <class F>
+cudaError_t launch_mma_of(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
+  const Workers w = workers_of<F>(max_rows);
+  const cudaError_t e = w.rows == 8 ? (d == 64 ? launch_mma<64, 1, F>(a, w.count, st) : launch_mma<128, 1, F>(a, w.count, st))
+                                    : (d == 64 ? launch_mma<64, 2, F>(a, w.count, st) : launch_mma<128, 2, F>(a, w.count, st));
+  return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);
 }
 
 }  // namespace
 
-Workers mma_workers(int64_t max_rows, int bits) {
-  const int sms = sm_count();
-  (void)bits;
-  return max_rows <= 8 ? Workers{kCtas * sms, 8} : Workers{2 * sms, 16};
-}
+Workers mma_workers(int64_t max_rows, int bits) { return bits == 8 ? workers_of<E4m3>(max_rows) : workers_of<Int4>(max_rows); }
 
 cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
-  const Workers w = mma_workers(max_rows, a.bits);
-  const cudaError_t e = w.rows == 8 ? (d == 64 ? launch_mma<64, 1>(a, w.count, st) : launch_mma<128, 1>(a, w.count, st))
-                                    : (d == 64 ? launch_mma<64, 2>(a, w.count, st) : launch_mma<128, 2>(a, w.count, st));
-  return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);
+  return a.bits == 8 ? launch_mma_of<E4m3>(a, d, max_rows, st) : launch_mma_of<Int4>(a, d, max_rows, st);
 }
 
 }  // namespace paged

@@ -165,14 +165,19 @@ __device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z) {
   return h2u(__hfma2(c, s, z));
 }
 
-// one token's packed codes and parameters of K or V
+// one token's packed codes and parameters of K or V (half 0 or 1)
+template <int D, class F>
+struct Packed;
 template <int D>
-struct Packed {
+struct Packed<D, Int4> {
   uint4 code[D / 32];
   uint32_t par[D / 32];
 
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* params) {
-    if (codes) {
+  __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* blk, int half, int s) {
+    if (blk) {
+      const uint8_t* b = blk + half * (a.block / 2);
+      const uint8_t* codes = b + s * (D / 2);
+      const uint8_t* params = b + a.page * (D / 2) + s * (D / 32 * 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) code[i] = load_global(reinterpret_cast<const uint4*>(codes) + i);
       if constexpr (D == 128) {
@@ -200,6 +205,44 @@ struct Packed {
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<uint4*>(tile + op_off(row, 4 * i + j)) =
             make_uint4(dq_lo(w[j], s, z), dq_hi(w[j], s, z), dq_lo(w[j] >> 8, s, z), dq_hi(w[j] >> 8, s, z));
+    }
+  }
+};
+template <int D>
+struct Packed<D, E4m3> {
+  uint4 code[D / 16];
+  uint32_t par;            // K's and V's scale
+
+  __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* blk, int half, int s) {
+    if (blk) {
+      const uint4* codes = reinterpret_cast<const uint4*>(blk + (half * a.page + s) * D);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) code[i] = load_global(codes + i);
+      par = load_global(reinterpret_cast<const uint32_t*>(blk + 2 * a.page * D + s / kScaleSlots * 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) code[i] = make_uint4(0, 0, 0, 0);
+      par = 0;
+    }
+    par = __byte_perm(par, 0, half ? 0x3232 : 0x1010);   // twice its own
+  }
+  __device__ __forceinline__ void hide() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      code[i] = make_uint4(known_codes(code[i].x), known_codes(code[i].y), known_codes(code[i].z), known_codes(code[i].w));
+    par = known_scales(par);
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int row) const {
+    const __half2 s = u2h(par);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t x = __byte_perm(w[2 * j], w[2 * j + 1], 0x5140), y = __byte_perm(w[2 * j], w[2 * j + 1], 0x7362);
+        *reinterpret_cast<uint4*>(tile + op_off(row, 2 * i + j)) =
+            make_uint4(mul_f16x2(e4m3_lo(x), s), mul_f16x2(e4m3_hi(x), s), mul_f16x2(e4m3_lo(y), s), mul_f16x2(e4m3_hi(y), s));
+      }
     }
   }
 };
@@ -261,7 +304,7 @@ __device__ __noinline__ void mend_logits(uint32_t sbase, const uint32_t* bad, in
   tmem_wait_st();
 }
 
-template <int D>
+template <int D, class F>
 __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArgs a) {
   using L = Lay<D>;
   using W = Walker<kRows, kTk, kItem>;
@@ -490,17 +533,23 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   } else if (warp < kMma) {
     // ------------------------------------------------------------ producers
     const int p = tid - kProd * 32;
-    constexpr int G = D / 32;
-    Packed<D> kp, vp;
+    Packed<D, F> kp, vp;
     int t = it.from;        // the tile whose page id is in flight
     int pg = -1, n = 0, h = 0;
     bool in = false, more = true;
+    bool part = true, part_k = true, part_v = true;   // of the tile in flight, loaded, and being stored
     // the page id of this thread's token of tile t of the current item
     auto lookup = [&]() {
       n = t * kTk + p;
       h = it.h;
       in = n >= it.lo && n < it.hi;
-      pg = in ? load_global(a.table + (int64_t)it.b * a.max_blocks + (n >> a.page_shift)) : -1;
+      pg = in ? load_global(table_of<F>(a, it.b, it.h) + (n >> a.page_shift)) : -1;
+      if constexpr (F::kBits == 8) {
+        // some row of the item does not see all of the tile
+        const int at = it.rq.n - it.rq.n_new;
+        part = a.causal && ((t + 1) * kTk > at + div_group(a, it.rt * kRows) + 1 ||
+                            (a.window > 0 && t * kTk <= at + div_group(a, it.rt * kRows + it.rows - 1) - a.window));
+      }
     };
     auto advance = [&]() {
       if (++t < it.to) return true;
@@ -517,10 +566,11 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       bad = __ballot_sync(0xffffffffu, in && !good);
       s = n & (a.page - 1);
       blk = good ? a.pool + ((int64_t)pg * a.kv_heads + h) * a.block : nullptr;
+      part_k = part;
     };
-    auto load = [&](Packed<D>& x, int half) {
-      const uint8_t* b = blk ? blk + half * (a.block / 2) : nullptr;
-      x.load(b ? b + s * (D / 2) : nullptr, b ? b + a.page * (D / 2) + s * (G * 4) : nullptr);
+    auto load = [&](Packed<D, F>& x, int half) {
+      x.load(a, blk, half, s);
+      if (half) part_v = part_k;
     };
     lookup();
     resolve();
@@ -547,7 +597,8 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
         load(kp, 0);
       }
       if (u >= 2) wait_free(&v_free[st], par, u);
-      if (a.causal) vp.hide();   // in every tile: to tell those with hidden tokens apart is no faster
+      // 4 bits: in every tile, to tell those with hidden tokens apart is no faster
+      if (F::kBits == 8 ? part_v : a.causal != 0) vp.hide();
       vp.store(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);
@@ -658,7 +709,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const int last = (min(it.hi, it.to * kTk) - 1) >> a.page_shift;
 #pragma unroll 1
       for (int x = (max(it.lo, it.from * kTk) >> a.page_shift) + p; x <= last; x += kLoaders) {
-        const int id = load_global(a.table + (int64_t)it.b * a.max_blocks + x);
+        const int id = load_global(table_of<F>(a, it.b, it.h) + x);
         good = good && id >= 0 && id < a.n_pages;
       }
       // on their way to L2 before the tiles are free
@@ -741,7 +792,7 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
   if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D>
+template <int D, class F>
 cudaError_t launch_tc(const AttendArgs& a, int workers, cudaStream_t st) {
   static SmemLimit limit;
   cudaLaunchConfig_t cfg = {};
@@ -752,7 +803,7 @@ cudaError_t launch_tc(const AttendArgs& a, int workers, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_tc_kernel<D>, cfg, a);
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_tc_kernel<D, F>, cfg, a);
 }
 
 }  // namespace
@@ -761,7 +812,8 @@ Workers tc_workers() { return Workers{sm_count(), kRows}; }
 
 cudaError_t launch_attend_tc(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
   const Workers w = tc_workers();
-  const cudaError_t e = d == 64 ? launch_tc<64>(a, w.count, st) : launch_tc<128>(a, w.count, st);
+  const cudaError_t e = a.bits == 8 ? (d == 64 ? launch_tc<64, E4m3>(a, w.count, st) : launch_tc<128, E4m3>(a, w.count, st))
+                                    : (d == 64 ? launch_tc<64, Int4>(a, w.count, st) : launch_tc<128, Int4>(a, w.count, st));
   return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);
 }
 

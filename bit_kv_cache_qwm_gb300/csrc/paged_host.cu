@@ -198,8 +198,8 @@ qwm_status attend(const qwm_paged_attend_args* a, int bits, int table_heads, con
       !aligned(a->workspace, 256) || a->workspace_bytes < attend_workspace(d, bits) ||
       !words(a->block_table, a->kv_len, a->cu_rows, a->lse, a->status))
     return QWM_ERR_INVALID_ARG;
-  const int k = a->kernel ? a->kernel : bits == 8 ? 1 : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
-  if (k != 1 && (a->dtype == QWM_F32 || bits == 8)) return QWM_ERR_UNSUPPORTED;
+  const int k = a->kernel ? a->kernel : qwm_paged_attend_kernel_for(a->dtype, a->heads, a->kv_heads, a->max_new);
+  if (k != 1 && a->dtype == QWM_F32) return QWM_ERR_UNSUPPORTED;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range(name);
   const int64_t max_rows = (a->max_new < 1 ? 1 : a->max_new > a->rows ? a->rows : a->max_new) * group;

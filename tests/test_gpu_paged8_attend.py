@@ -11,7 +11,7 @@ from test_gpu_paged8_cache import BOUNDS, all_bounds, dev, host, paged  # noqa: 
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = [1]
+KERNELS = [1, 2, 3]
 
 
 def run(paged, B, kernel, causal=True, window=0, pool=None, table=None, lens=None, scale=0.0, q=None, max_new=None, status=None):
