@@ -165,19 +165,48 @@ __device__ __forceinline__ uint32_t dq_hi(uint32_t x, __half2 s, __half2 z) {
   return h2u(__hfma2(c, s, z));
 }
 
-// one token's packed codes and parameters of K or V (half 0 or 1)
+// What a producer thread loads of a tile, in two steps: page ids (`start`), then
+// addresses (`resolve`, which returns the tokens of the warp on pages out of range),
+// and what of K or V (half 0 or 1) it has loaded and stores as operands.
+template <class F>
+struct Lookup;
 template <int D, class F>
 struct Packed;
+
+// 4 bits: thread = token
+template <>
+struct Lookup<Int4> {
+  int pg = -1, n = 0, h = 0, s = 0;
+  bool in = false;
+  const uint8_t* blk = nullptr;
+
+  template <class W>
+  __device__ __forceinline__ void start(const AttendArgs& a, const W& it, int t, int p) {
+    n = t * kTk + p;
+    h = it.h;
+    in = n >= it.lo && n < it.hi;
+    pg = in ? load_global(table_of<Int4>(a, it.b, it.h) + (n >> a.page_shift)) : -1;
+  }
+  __device__ __forceinline__ uint32_t resolve(const AttendArgs& a, int) {
+    const bool good = in && pg >= 0 && pg < a.n_pages;
+    if (in && !good) flag(a.status, QWM_DEV_BOUNDS);
+    s = n & (a.page - 1);
+    blk = good ? a.pool + ((int64_t)pg * a.kv_heads + h) * a.block : nullptr;
+    return __ballot_sync(0xffffffffu, in && !good);
+  }
+  // some row does not see all of the tile (to tell those tiles apart is no faster)
+  __device__ __forceinline__ bool partial(const AttendArgs& a) const { return a.causal; }
+};
 template <int D>
 struct Packed<D, Int4> {
   uint4 code[D / 32];
   uint32_t par[D / 32];
 
-  __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* blk, int half, int s) {
-    if (blk) {
-      const uint8_t* b = blk + half * (a.block / 2);
-      const uint8_t* codes = b + s * (D / 2);
-      const uint8_t* params = b + a.page * (D / 2) + s * (D / 32 * 4);
+  __device__ __forceinline__ void load(const AttendArgs& a, const Lookup<Int4>& x, int half, int) {
+    if (x.blk) {
+      const uint8_t* b = x.blk + half * (a.block / 2);
+      const uint8_t* codes = b + x.s * (D / 2);
+      const uint8_t* params = b + a.page * (D / 2) + x.s * (D / 32 * 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) code[i] = load_global(reinterpret_cast<const uint4*>(codes) + i);
       if constexpr (D == 128) {
@@ -196,6 +225,7 @@ struct Packed<D, Int4> {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) par[i] = hidden_params(par[i]);
   }
+  template <int HALF>
   __device__ __forceinline__ void store(uint8_t* tile, int row) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -208,40 +238,108 @@ struct Packed<D, Int4> {
     }
   }
 };
+
+// 8 bits: a warp's 32 tokens are two blocks of 16 slots, each on one page with one
+// scale.  Lane = 16-byte pieces lane % 4 (and + 4) of rows lane / 4 + 8 k: a load
+// takes half of eight rows, eight lines instead of 32 with a token a thread (the
+// chunk below 2.0 ms), and the eight lanes of a store phase have two rows, whose
+// swizzles differ in their lowest bit.
+template <>
+struct Lookup<E4m3> {
+  int pg[2] = {-1, -1}, n0 = 0, h = 0, lo = 0, hi = 0;
+  bool part = true;
+  // resolved
+  const uint8_t* blk[2] = {nullptr, nullptr};
+  uint32_t live = 0;       // a bit for each k: the row is there; 4 and 5: the block is
+  int at = 0;
+  bool part_now = true;
+
+  template <class W>
+  __device__ __forceinline__ void start(const AttendArgs& a, const W& it, int t, int p) {
+    n0 = t * kTk + (p & ~31);
+    h = it.h, lo = it.lo, hi = it.hi;
+    const int32_t* table = table_of<E4m3>(a, it.b, it.h);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int n = n0 + kScaleSlots * x;
+      pg[x] = n < hi && n + kScaleSlots > lo ? load_global(table + (n >> a.page_shift)) : 0;
+    }
+    const int first = it.rq.n - it.rq.n_new;
+    part = a.causal && ((t + 1) * kTk > first + div_group(a, it.rt * kRows) + 1 ||
+                        (a.window > 0 && t * kTk <= first + div_group(a, it.rt * kRows + it.rows - 1) - a.window));
+  }
+  __device__ __forceinline__ uint32_t resolve(const AttendArgs& a, int p) {
+    uint32_t bad = 0;
+    live = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int n = n0 + kScaleSlots * x;
+      const bool in = n < hi && n + kScaleSlots > lo, good = in && pg[x] >= 0 && pg[x] < a.n_pages;
+      if (in && !good) {
+        flag(a.status, QWM_DEV_BOUNDS);
+        bad |= 0xffffu << (16 * x);
+      }
+      if (good) live |= 16u << x;
+      blk[x] = a.pool + ((int64_t)(good ? pg[x] : 0) * a.kv_heads + h) * a.block;
+#pragma unroll
+      for (int k = 2 * x; k < 2 * x + 2; ++k) {
+        const int row = n0 + ((p & 31) >> 2) + 8 * k;
+        if (good && row >= lo && row < hi) live |= 1u << k;
+      }
+    }
+    at = n0 & (a.page - 1);
+    part_now = part;
+    return bad;
+  }
+  __device__ __forceinline__ bool partial(const AttendArgs&) const { return part_now || live != 0x3f; }
+};
 template <int D>
 struct Packed<D, E4m3> {
-  uint4 code[D / 16];
-  uint32_t par;            // K's and V's scale
+  static constexpr int P = D / 64;
+  uint4 code[4][P];
+  uint32_t par[2];         // K's and V's scale of a block
+  uint32_t live;           // as in Lookup
 
-  __device__ __forceinline__ void load(const AttendArgs& a, const uint8_t* blk, int half, int s) {
-    if (blk) {
-      const uint4* codes = reinterpret_cast<const uint4*>(blk + (half * a.page + s) * D);
+  __device__ __forceinline__ void load(const AttendArgs& a, const Lookup<E4m3>& x, int half, int p) {
+    const int row = (p & 31) >> 2, piece = p & 3;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) code[i] = load_global(codes + i);
-      par = load_global(reinterpret_cast<const uint32_t*>(blk + 2 * a.page * D + s / kScaleSlots * 4));
-    } else {
+    for (int k = 0; k < 4; ++k) {
+      // the second block may be the first of another page
+      const int s = (x.at + 8 * k) & (a.page - 1);
+      const uint8_t* src = x.blk[k >> 1] + (half * a.page + s + row) * D + 16 * piece;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) code[i] = make_uint4(0, 0, 0, 0);
-      par = 0;
+      for (int i = 0; i < P; ++i) code[k][i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
+      if ((k & 1) == 0) par[k >> 1] = load_global(reinterpret_cast<const uint32_t*>(x.blk[k >> 1] + 2 * a.page * D + s / kScaleSlots * 4));
     }
-    par = __byte_perm(par, 0, half ? 0x3232 : 0x1010);   // twice its own
+    live = x.live;
   }
+  // Values alone: a key that is not there may be anything, its logits are replaced.
   __device__ __forceinline__ void hide() {
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-      code[i] = make_uint4(known_codes(code[i].x), known_codes(code[i].y), known_codes(code[i].z), known_codes(code[i].w));
-    par = known_scales(par);
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t keep = (live >> k & 1) ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        code[k][i] = make_uint4(known_codes(code[k][i].x) & keep, known_codes(code[k][i].y) & keep,
+                                known_codes(code[k][i].z) & keep, known_codes(code[k][i].w) & keep);
+    }
+    par[0] = known_scales(par[0]), par[1] = known_scales(par[1]);
   }
-  __device__ __forceinline__ void store(uint8_t* tile, int row) const {
-    const __half2 s = u2h(par);
+  template <int HALF>
+  __device__ __forceinline__ void store(uint8_t* tile, int p) const {
+    const int row = (p & ~31) + ((p & 31) >> 2), piece = p & 3;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+    for (int k = 0; k < 4; ++k) {
+      const __half2 s = HALF ? __high2half2(u2h(par[k >> 1])) : __low2half2(u2h(par[k >> 1]));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t x = __byte_perm(w[2 * j], w[2 * j + 1], 0x5140), y = __byte_perm(w[2 * j], w[2 * j + 1], 0x7362);
-        *reinterpret_cast<uint4*>(tile + op_off(row, 2 * i + j)) =
-            make_uint4(mul_f16x2(e4m3_lo(x), s), mul_f16x2(e4m3_hi(x), s), mul_f16x2(e4m3_lo(y), s), mul_f16x2(e4m3_hi(y), s));
+      for (int i = 0; i < P; ++i) {
+        const uint32_t w[4] = {code[k][i].x, code[k][i].y, code[k][i].z, code[k][i].w};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x = __byte_perm(w[2 * j], w[2 * j + 1], 0x5140), y = __byte_perm(w[2 * j], w[2 * j + 1], 0x7362);
+          *reinterpret_cast<uint4*>(tile + op_off(row + 8 * k, 2 * (piece + 4 * i) + j)) =
+              make_uint4(mul_f16x2(e4m3_lo(x), s), mul_f16x2(e4m3_hi(x), s), mul_f16x2(e4m3_lo(y), s), mul_f16x2(e4m3_hi(y), s));
+        }
       }
     }
   }
@@ -534,50 +632,26 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
     // ------------------------------------------------------------ producers
     const int p = tid - kProd * 32;
     Packed<D, F> kp, vp;
-    int t = it.from;        // the tile whose page id is in flight
-    int pg = -1, n = 0, h = 0;
-    bool in = false, more = true;
-    bool part = true, part_k = true, part_v = true;   // of the tile in flight, loaded, and being stored
-    // the page id of this thread's token of tile t of the current item
-    auto lookup = [&]() {
-      n = t * kTk + p;
-      h = it.h;
-      in = n >= it.lo && n < it.hi;
-      pg = in ? load_global(table_of<F>(a, it.b, it.h) + (n >> a.page_shift)) : -1;
-      if constexpr (F::kBits == 8) {
-        // some row of the item does not see all of the tile
-        const int at = it.rq.n - it.rq.n_new;
-        part = a.causal && ((t + 1) * kTk > at + div_group(a, it.rt * kRows) + 1 ||
-                            (a.window > 0 && t * kTk <= at + div_group(a, it.rt * kRows + it.rows - 1) - a.window));
-      }
-    };
+    Lookup<F> look;
+    int t = it.from;        // the tile whose page ids are in flight
+    bool more = true, hide_v = true;
     auto advance = [&]() {
       if (++t < it.to) return true;
       if (!it.next(a)) return false;
       t = it.from;
       return true;
     };
-    const uint8_t* blk = nullptr;
-    int s = 0;
     uint32_t bad = 0;
-    auto resolve = [&]() {
-      const bool good = in && pg >= 0 && pg < a.n_pages;
-      if (in && !good) flag(a.status, QWM_DEV_BOUNDS);
-      bad = __ballot_sync(0xffffffffu, in && !good);
-      s = n & (a.page - 1);
-      blk = good ? a.pool + ((int64_t)pg * a.kv_heads + h) * a.block : nullptr;
-      part_k = part;
+    auto load_v = [&]() {
+      vp.load(a, look, 1, p);
+      hide_v = look.partial(a);
     };
-    auto load = [&](Packed<D, F>& x, int half) {
-      x.load(a, blk, half, s);
-      if (half) part_v = part_k;
-    };
-    lookup();
-    resolve();
-    load(kp, 0);
-    load(vp, 1);
+    look.start(a, it, t, p);
+    bad = look.resolve(a, p);
+    kp.load(a, look, 0, p);
+    load_v();
     more = advance();
-    if (more) lookup();
+    if (more) look.start(a, it, t, p);
     bool ok = true;         // no wait of this thread has run out
     // the stage of tile u was read by tile u - 2
     auto wait_free = [&](uint64_t* bar, uint32_t par, int u) {
@@ -588,24 +662,23 @@ __global__ void __launch_bounds__(kNt, 1) paged_attend_tc_kernel(const AttendArg
       const uint32_t par = (uint32_t)(((u >> 1) - 1) & 1);
       const bool have = more;
       if (u >= 2) wait_free(&k_free[st], par, u);
-      kp.store(sm + L::k + st * L::op, p);
+      kp.template store<0>(sm + L::k + st * L::op, p);
       if ((p & 31) == 0) bad_sh[u & 3][p >> 5] = bad;
       fence_async_smem();
       nb_arrive(kNbK + st);
       if (have) {
-        resolve();
-        load(kp, 0);
+        bad = look.resolve(a, p);
+        kp.load(a, look, 0, p);
       }
       if (u >= 2) wait_free(&v_free[st], par, u);
-      // 4 bits: in every tile, to tell those with hidden tokens apart is no faster
-      if (F::kBits == 8 ? part_v : a.causal != 0) vp.hide();
-      vp.store(sm + L::v + st * L::op, p);
+      if (hide_v) vp.hide();
+      vp.template store<1>(sm + L::v + st * L::op, p);
       fence_async_smem();
       nb_arrive(kNbV + st);
       if (!have) break;
-      load(vp, 1);
+      load_v();
       more = advance();
-      if (more) lookup();
+      if (more) look.start(a, it, t, p);
     }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issuer
