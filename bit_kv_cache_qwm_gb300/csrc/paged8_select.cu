@@ -12,8 +12,6 @@ namespace qwm {
 namespace paged {
 namespace {
 
-constexpr int kNt = 256, kWarps = kNt / 32, kPages = 16 * kWarps;
-
 // A request of the call: its rows, its pages (count in all, those from `tail` on
 // are the step's own) and how many of them are kept.
 struct Pages {
@@ -72,146 +70,287 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[N]) 
   }
 }
 
-// A CTA scores 128 pages of one request and head, a warp 16 of them, whose bounds
-// stay in its registers.  Its warps turn 8 rows each (a row a query head of a
-// token) into whole numbers, share them as MMA operands, and go through all 64;
-// lane (g, c) of a warp has channels c d/4 ... of row g, and of pages g and g + 8.
-template <int D, class T>
-__global__ void __launch_bounds__(kNt) paged8_score_kernel(const qwm_paged8_select_args a, int shift) {
-  constexpr int C = D / 4, KS = D / 16;
-  __shared__ __align__(16) uint4 rows_sh[kWarps][KS][32];   // b0, b1 of x^+, then of x^-
-  __shared__ float unit_sh[kWarps * 8];
-  wait_for_kernel_ahead();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, group = a.heads / a.kv_heads;
-  const Pages p = load_pages(a, shift, b);
-  // the step's own pages, and all where all are kept, need no score
-  if (p.first >= p.n || p.count <= a.width || (int)blockIdx.x * kPages >= p.tail) return;
-  const int j0 = blockIdx.x * kPages + 16 * warp;
-  uint32_t high[KS][4], low[KS][4];
-  float unit[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int j = j0 + g + 8 * x;
-    int id = j < p.tail ? load_global(a.block_table + (int64_t)b * a.max_blocks + j) : -1;
-    if (id < 0 || id >= a.n_pages) {
-      if (j < p.tail && c == 0) flag(a.status, QWM_DEV_BOUNDS);
-      id = -1;
-    }
-    unit[x] = __int_as_float(0x7fffffff);   // such a page's scores are NaN
-    const uint8_t* src = (const uint8_t*)a.bounds + ((int64_t)(id < 0 ? 0 : id) * a.kv_heads + h) * (2 * D + 16);
-    if (id >= 0) unit[x] = load_global(reinterpret_cast<const float*>(src + 2 * D));
-#pragma unroll
-    for (int q = 0; q < C / 16; ++q) {
-      const uint4 u = load_global(reinterpret_cast<const uint4*>(src + c * C) + q), v = load_global(reinterpret_cast<const uint4*>(src + D + c * C) + q);
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        whole(uw[i], &high[4 * q + i][x], &high[4 * q + i][2 + x]);
-        whole(vw[i], &low[4 * q + i][x], &low[4 * q + i][2 + x]);
-      }
-    }
-  }
-  float best[2] = {-INFINITY, -INFINITY};
-  const int64_t rows = (int64_t)(p.n - p.first) * group;
-  for (int64_t r0 = 0; r0 < rows; r0 += 8 * kWarps) {
-    const int64_t r = r0 + 8 * warp + g;
-    if (r0 + 8 * warp < rows) {
-      float x[C];
-      const int64_t tok = r / group;
-      if (r < rows) {
-        load_row(static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride + c * C, x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = 0.f;
-      }
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -3.402823466e38f), 3.402823466e38f) : 0.f;
-        top = fmaxf(top, fabsf(x[i]));
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float u = top >= 7.888609052e-31f ? __fdiv_rn(top, 127.f) : 0.f;   // 2^-100
-      const __half2 zero = __float2half2_rn(0.f);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        __half2 w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float y[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) y[e] = u > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[4 * i + 2 * k + e], u)), -127.f), 127.f) : 0.f;
-          w[k] = __floats2half2_rn(y[0], y[1]);
-        }
-        rows_sh[warp][i][lane] = make_uint4(h2u(__hmax2(w[0], zero)), h2u(__hmax2(w[1], zero)), h2u(__hmin2(w[0], zero)),
-                                            h2u(__hmin2(w[1], zero)));
-      }
-      // a row that is not there is NaN, which no maximum takes
-      if (c == 0) unit_sh[8 * warp + g] = r < rows ? u : __int_as_float(0x7fffffff);
-    }
-    __syncthreads();
-    const int blocks = (int)min((rows - r0 + 7) / 8, (int64_t)kWarps);
-    if (j0 < p.tail) {
-      for (int y = 0; y < blocks; ++y) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const uint4 w = rows_sh[y][i][lane];
-          mma(s, high[i], w.x, w.y);
-          mma(t, low[i], w.z, w.w);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float u = unit_sh[8 * y + 2 * c + k];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) best[x] = fmaxf(best[x], __fmul_rn(__fmul_rn(s[2 * x + k] + t[2 * x + k], unit[x]), u));
-        }
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
-    best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
-    const int j = j0 + g + 8 * x;
-    if (c == 0 && j < p.tail) static_cast<float*>(a.workspace)[((int64_t)b * a.kv_heads + h) * a.max_blocks + j] = best[x];
-  }
-}
-
-// One CTA a request and head.  The scores become keys that order like them; the
-// least key kept is found digit by digit (8 bits, counted from the highest bit in
-// which the keys differ, so that a digit's counts spread), then every thread
-// writes those of its range of pages.  Keys stay in shared memory where they fit.
-// Bound by the latency of its barriers.
-constexpr int kSelNt = 512, kSelWarps = kSelNt / 32, kKeys = 16384;
-
-__device__ __forceinline__ uint32_t key_of(float s) {   // NaN below all, -0 as 0
+// A score's key: keys order as scores do, NaN below all, -0 as 0.
+__device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t u = __float_as_uint(s + 0.f);
   return s != s ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// exclusive sums of (x, y) over the CTA
-__device__ __forceinline__ void scan2(int& x, int& y, int2* sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x0 = x, y0 = y;
+// Row r of a request and head (a query head of a token; lanes 4 g .. 4 g + 3 share
+// one, d/4 channels each) as whole numbers: the MMA operands of x^+ and of x^-, and
+// the row's unit (NaN where there is no such row: no maximum takes it).
+// The definition divides once a channel.  Here a product with 1/unit, off by less
+// than 2^-15 (127 times 2^-22), gives the same whole number unless it comes within
+// 10^-4 of a tie, where the warp divides after all.
+template <int D, class T>
+__device__ __forceinline__ float quantise_row(const qwm_paged8_select_args& a, const Pages& p, int h, int group, int64_t r, int64_t rows,
+                                              uint4 (&w)[D / 16]) {
+  constexpr int C = D / 4, KS = D / 16;
+  const int c = threadIdx.x & 3;
+  float x[C];
+  const int64_t tok = r / group;
+  if (r < rows) {
+    load_row(static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride + c * C, x);
+  } else {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) x += p, y += q;
+    for (int i = 0; i < C; ++i) x[i] = 0.f;
   }
-  if (lane == 31) sums[warp] = make_int2(x, y);
-  __syncthreads();
-  x -= x0, y -= y0;
-  for (int w = 0; w < warp; ++w) x += sums[w].x, y += sums[w].y;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) bits = max(bits, __float_as_uint(x[i]) & 0x7fffffffu);
+  if (__any_sync(0xffffffffu, bits >= 0x7f800000u)) {   // NaN or infinite
+    bits = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -3.402823466e38f), 3.402823466e38f) : 0.f;
+      bits = max(bits, __float_as_uint(x[i]) & 0x7fffffffu);
+    }
+  }
+  float top = __uint_as_float(bits);
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool some = top >= 7.888609052e-31f;   // 2^-100
+  const float u = some ? __fdiv_rn(top, 127.f) : 0.f, inv = some ? __frcp_rn(u) : 0.f;
+  const float round = 12582912.f;   // 1.5 2^23: adding it rounds to the nearest even
+  float far = 0.f, y[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const float q = x[i] * inv;
+    y[i] = __fsub_rn(__fadd_rn(q, round), round);
+    far = fmaxf(far, fabsf(q - y[i]));
+  }
+  if (__any_sync(0xffffffffu, far > 0.4999f)) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) y[i] = some ? rintf(__fdiv_rn(x[i], u)) : 0.f;
+  }
+  const __half2 zero = __float2half2_rn(0.f);
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    __half2 v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      v[k] = __floats2half2_rn(fminf(fmaxf(y[4 * i + 2 * k], -127.f), 127.f), fminf(fmaxf(y[4 * i + 2 * k + 1], -127.f), 127.f));
+    w[i] = make_uint4(h2u(__hmax2(v[0], zero)), h2u(__hmax2(v[1], zero)), h2u(__hmin2(v[0], zero)), h2u(__hmin2(v[1], zero)));
+  }
+  return r < rows ? u : __int_as_float(0x7fffffff);
 }
 
-__global__ void __launch_bounds__(kSelNt) paged8_select_kernel(const qwm_paged8_select_args a, int shift) {
-  extern __shared__ uint32_t keys_sh[];
-  __shared__ uint32_t count_sh[256], least_sh, most_sh;
-  __shared__ int digit_sh, left_sh;
-  __shared__ int2 sums_sh[kSelWarps];
+// The bounds of 16 pages as a warp loads them: lane (g, c) has channels c d/4 ... of
+// pages g and g + 8.
+template <int D>
+struct Tile {
+  static constexpr int Q = D / 64;
+  uint4 high[2][Q], low[2][Q];
+  float unit[2];
+
+  // ids of pages g and g + 8; < 0: no page, whose scores are NaN
+  __device__ __forceinline__ void load(const qwm_paged8_select_args& a, int h, const int* id) {
+    const int c = threadIdx.x & 3;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* src = (const uint8_t*)a.bounds + ((int64_t)max(id[x], 0) * a.kv_heads + h) * (2 * D + 16);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        high[x][q] = load_global(reinterpret_cast<const uint4*>(src + c * (D / 4)) + q);
+        low[x][q] = load_global(reinterpret_cast<const uint4*>(src + D + c * (D / 4)) + q);
+      }
+      unit[x] = load_global(reinterpret_cast<const float*>(src + 2 * D));
+      if (id[x] < 0) unit[x] = __int_as_float(0x7fffffff);
+    }
+  }
+  // operands of step i: 4 channels of each lane
+  __device__ __forceinline__ static void operand(const uint4 (&b)[2][Q], int i, uint32_t* f) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint4& u = b[x][i >> 2];
+      whole((i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w, &f[x], &f[2 + x]);
+    }
+  }
+};
+
+__device__ __forceinline__ int page_id(const qwm_paged8_select_args& a, int b, int j, int tail) {
+  int id = j < tail ? load_global(a.block_table + (int64_t)b * a.max_blocks + j) : -1;
+  if (id >= a.n_pages || id < 0) {
+    if (j < tail) flag(a.status, QWM_DEV_BOUNDS);
+    id = -1;
+  }
+  return id;
+}
+
+// the larger of two scores; a page's scores over rows 2 c, 2 c + 1 of the lanes
+__device__ __forceinline__ void take(float* best, const float* s, const float* t, const float* unit, float u0, float u1) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      best[x] = fmaxf(best[x], __fmul_rn(__fmul_rn(s[2 * x + k] + t[2 * x + k], unit[x]), k ? u1 : u0));
+}
+
+// ---- few rows: a step of single tokens
+//
+// A warp has 8 rows in its registers and goes through tiles of 16 pages, the next
+// tile's bounds on their way; their ids come first, together.  More rows take
+// another walk each 8.  Bound by latency (rows, ids, bounds) where a warp has one
+// or two tiles, else by the bounds' way from HBM.
+constexpr int kFewNt = 128, kFewWarps = kFewNt / 32, kMostTiles = 8;
+
+template <int D, class T>
+__global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_paged8_select_args a, int shift, int tiles) {
+  constexpr int KS = D / 16;
+  wait_for_kernel_ahead();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int h = blockIdx.y, b = blockIdx.z, group = a.heads / a.kv_heads;
+  const Pages p = load_pages(a, shift, b);
+  const int j0 = 16 * (blockIdx.x * kFewWarps + warp) * tiles;
+  // the step's own pages, and all where all are kept, need no score
+  if (p.first >= p.n || p.count <= a.width || j0 >= p.tail) return;
+  const int mine = min(tiles, (p.tail - j0 + 15) / 16);
+  int ids[kMostTiles / 2];
+#pragma unroll
+  for (int i = 0; i < kMostTiles / 2; ++i) ids[i] = 2 * i < mine ? page_id(a, b, j0 + 32 * i + lane, p.tail) : -1;
+  uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
+  const int64_t rows = (int64_t)(p.n - p.first) * group;
+  auto fetch = [&](Tile<D>& t, int i) {
+    int two = ids[0];
+#pragma unroll
+    for (int k = 1; k < kMostTiles / 2; ++k) two = (i >> 1) == k ? ids[k] : two;
+    const int id[2] = {__shfl_sync(0xffffffffu, two, 16 * (i & 1) + g), __shfl_sync(0xffffffffu, two, 16 * (i & 1) + g + 8)};
+    t.load(a, h, id);
+  };
+  for (int64_t r0 = 0; r0 < rows; r0 += 8) {
+    Tile<D> next;
+    fetch(next, 0);
+    uint4 w[KS];
+    const float u = quantise_row<D, T>(a, p, h, group, r0 + g, rows, w);
+    const float u0 = __shfl_sync(0xffffffffu, u, 8 * c), u1 = __shfl_sync(0xffffffffu, u, 8 * c + 4);
+    for (int i = 0; i < mine; ++i) {
+      const Tile<D> t = next;
+      if (i + 1 < mine) fetch(next, i + 1);
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t f[4];
+        Tile<D>::operand(t.high, k, f);
+        mma(s, f, w[k].x, w[k].y);
+        Tile<D>::operand(t.low, k, f);
+        mma(v, f, w[k].z, w[k].w);
+      }
+      float best[2] = {-INFINITY, -INFINITY};
+      take(best, s, v, t.unit, u0, u1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
+        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
+        const int j = j0 + 16 * i + g + 8 * x;
+        if (c == 0 && j < p.tail) {
+          uint32_t k = key_of(best[x]);
+          if (r0) k = max(k, keys[j]);
+          keys[j] = k;
+        }
+      }
+    }
+  }
+}
+
+// ---- many rows: drafts, prompts and chunks
+//
+// A CTA takes the pages of a request and head and every `splits`-th 64 of its rows:
+// each warp turns 8 of them into operands in shared memory, then goes through its
+// tiles of 16 pages with all 64.  Maxima meet in the keys by atomicMax, whose order
+// does not matter.  Bound by the MMAs.
+constexpr int kNt = 256, kWarps = kNt / 32;
+
+template <int D, class T>
+__global__ void __launch_bounds__(kNt, 2) paged8_score_many_kernel(const qwm_paged8_select_args a, int shift) {
+  constexpr int KS = D / 16;
+  __shared__ __align__(16) uint4 rows_sh[kWarps][KS][32];   // b0, b1 of x^+, then of x^-
+  __shared__ float unit_sh[kWarps * 8];
+  wait_for_kernel_ahead();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int h = blockIdx.y, b = blockIdx.z, group = a.heads / a.kv_heads;
+  const Pages p = load_pages(a, shift, b);
+  if (p.first >= p.n || p.count <= a.width) return;
+  uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
+  const int64_t rows = (int64_t)(p.n - p.first) * group;
+  for (int64_t r0 = (int64_t)blockIdx.x * 8 * kWarps; r0 < rows; r0 += (int64_t)gridDim.x * 8 * kWarps) {
+    if (r0 + 8 * warp < rows) {
+      uint4 w[KS];
+      const float u = quantise_row<D, T>(a, p, h, group, r0 + 8 * warp + g, rows, w);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) rows_sh[warp][i][lane] = w[i];
+      if (c == 0) unit_sh[8 * warp + g] = u;
+    }
+    __syncthreads();
+    const int blocks = (int)min((rows - r0 + 7) / 8, (int64_t)kWarps);
+    for (int j0 = 16 * warp; j0 < p.tail; j0 += 16 * kWarps) {
+      uint32_t high[KS][4], low[KS][4];
+      float unit[2];
+      {
+        Tile<D> t;
+        const int id[2] = {page_id(a, b, j0 + g, p.tail), page_id(a, b, j0 + g + 8, p.tail)};
+        t.load(a, h, id);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          Tile<D>::operand(t.high, k, high[k]);
+          Tile<D>::operand(t.low, k, low[k]);
+        }
+        unit[0] = t.unit[0], unit[1] = t.unit[1];
+      }
+      float best[2] = {-INFINITY, -INFINITY};
+      for (int y = 0; y < blocks; ++y) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint4 w = rows_sh[y][k][lane];
+          mma(s, high[k], w.x, w.y);
+          mma(v, low[k], w.z, w.w);
+        }
+        take(best, s, v, unit, unit_sh[8 * y + 2 * c], unit_sh[8 * y + 2 * c + 1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
+        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
+        const int j = j0 + g + 8 * x;
+        if (c == 0 && j < p.tail) atomicMax(keys + j, key_of(best[x]));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- the choice
+//
+// One CTA a request and head.  The least key kept is found digit by digit (8 bits,
+// counted from the highest bit in which the keys differ, so that a digit's counts
+// spread); once no more than a thread each are left in question, each counts those
+// ahead of its own instead.  Then every thread writes those of its range of pages.
+// Keys stay in registers where E a thread are enough, else they are read again for
+// every step.  Bound by the latency of its barriers.
+constexpr int kE = 8;
+
+// exclusive sum of x over the CTA
+template <int NT>
+__device__ __forceinline__ int scan(int x, int* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x0 = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int p = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += p;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int before = lane < warp ? sums[lane] : 0;
+  before = (int)__reduce_add_sync(0xffffffffu, (unsigned)before);
+  return x - x0 + before;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) paged8_select_kernel(const qwm_paged8_select_args a, int shift) {
+  __shared__ uint32_t count_sh[256], least_sh, most_sh, found_sh;
+  __shared__ int digit_sh, left_sh, in_sh, index_sh;
+  __shared__ int sums_sh[NT / 32];
+  __shared__ uint2 some_sh[NT];   // (key, index) of those in question
   wait_for_kernel_ahead();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.x, b = blockIdx.y;
   const Pages p = load_pages(a, shift, b);
@@ -224,49 +363,60 @@ __global__ void __launch_bounds__(kSelNt) paged8_select_kernel(const qwm_paged8_
   const int kept = any && fits ? p.kept : 0;
   int32_t* out = a.pages + ((int64_t)b * a.kv_heads + h) * a.width;
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
-  for (int i = kept + tid; i < a.width; i += kSelNt) out[i] = -1;
+  for (int i = kept + tid; i < a.width; i += NT) out[i] = -1;
   if (kept == 0) return;
   if (kept == p.count) {
-    for (int i = tid; i < kept; i += kSelNt) out[i] = load_global(table + i);
+    for (int i = tid; i < kept; i += NT) out[i] = load_global(table + i);
     return;
   }
   const int own = p.count - p.tail, sink = min(min(a.sink, p.tail), kept - own);
-  for (int i = tid; i < own; i += kSelNt) out[kept - own + i] = load_global(table + p.tail + i);
-  for (int i = tid; i < sink; i += kSelNt) out[i] = load_global(table + i);
+  for (int i = tid; i < own; i += NT) out[kept - own + i] = load_global(table + p.tail + i);
+  for (int i = tid; i < sink; i += NT) out[i] = load_global(table + i);
   // of pages sink ... tail - 1, the `left` with the highest keys
   const int n = p.tail - sink, want = kept - own - sink;
   if (want == 0) return;
-  const float* score = static_cast<const float*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks + sink;
-  const bool staged = n <= kKeys;
+  const uint32_t* keys = static_cast<const uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks + sink;
+  // a thread's range of pages
+  const int per = (n + NT - 1) / NT, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  const bool held = per <= kE;
+  uint32_t mine[kE];
+  if (held) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) mine[e] = i0 + e < i1 ? load_global(keys + i0 + e) : 0u;
+  }
+  auto each = [&](auto f) {   // f(key, index) over the thread's range
+    if (held) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (i0 + e < i1) f(mine[e], i0 + e);
+    } else {
+      for (int i = i0; i < i1; ++i) f(load_global(keys + i), i);
+    }
+  };
   if (tid == 0) least_sh = 0xffffffffu, most_sh = 0;
   __syncthreads();
   uint32_t least = 0xffffffffu, most = 0;
-  for (int i = tid; i < n; i += kSelNt) {
-    const uint32_t k = key_of(load_global(score + i));
-    if (staged) keys_sh[i] = k;
-    least = min(least, k), most = max(most, k);
-  }
+  each([&](uint32_t k, int) { least = min(least, k), most = max(most, k); });
   least = __reduce_min_sync(0xffffffffu, least), most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) atomicMin(&least_sh, least), atomicMax(&most_sh, most);
   __syncthreads();
   least = least_sh, most = most_sh;
-  auto key = [&](int i) { return (staged ? keys_sh[i] : key_of(load_global(score + i))) - least; };
-  int bits = 32 - __clz(most - least), left = want;
+  int bits = 32 - __clz(most - least), left = want, in = n;
   uint32_t found = 0;   // the digits so far, of the least key kept
-  while (bits > 0) {
+  while (bits > 0 && in > NT) {
     const int down = max(bits - 8, 0), width = bits - down;
-    if (tid < 256) count_sh[tid] = 0;
+    for (int i = tid; i < 256; i += NT) count_sh[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kSelNt) {
-      const uint32_t k = key(i);
+    each([&](uint32_t k, int) {
+      k -= least;
       if ((uint64_t)k >> bits == found) atomicAdd(&count_sh[(k >> down) & ((1u << width) - 1)], 1u);
-    }
+    });
     __syncthreads();
     if (warp == 0) {
       // lane 0 has the highest 8 digits
-      uint32_t mine[8], sum = 0;
+      uint32_t has[8], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine[i] = count_sh[255 - 8 * lane - i], sum += mine[i];
+      for (int i = 0; i < 8; ++i) has[i] = count_sh[255 - 8 * lane - i], sum += has[i];
       uint32_t upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -277,56 +427,104 @@ __global__ void __launch_bounds__(kSelNt) paged8_select_kernel(const qwm_paged8_
       if (before < (uint32_t)left && (uint32_t)left <= upto) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (before < (uint32_t)left && (uint32_t)left <= before + mine[i]) {
+          if (before < (uint32_t)left && (uint32_t)left <= before + has[i]) {
             digit_sh = 255 - 8 * lane - i;
             left_sh = left - (int)before;
+            in_sh = (int)has[i];
           }
-          before += mine[i];
+          before += has[i];
         }
       }
     }
     __syncthreads();
     found = (found << width) | (uint32_t)digit_sh;
-    left = left_sh;
+    left = left_sh, in = in_sh;
     bits = down;
   }
-  // keys above `found` are kept, and the first `left` of those equal to it
-  const int per = (n + kSelNt - 1) / kSelNt, i0 = min(tid * per, n), i1 = min(i0 + per, n);
-  int above = 0, equal = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    above += k > found, equal += k == found;
+  // Of the `in` keys that start with `found`, `left` are kept.  Those above are kept
+  // all.  `last`: the last page kept among those of the least key kept.
+  int last = 0x7fffffff;
+  if (in > left) {
+    if (in <= NT) {
+      int m = 0;
+      each([&](uint32_t k, int) { m += (uint64_t)(k - least) >> bits == found; });
+      int at = scan<NT>(m, sums_sh);
+      each([&](uint32_t k, int i) {
+        if ((uint64_t)(k - least) >> bits == found) some_sh[at++] = make_uint2(k - least, (uint32_t)i);
+      });
+      __syncthreads();
+      if (tid < in) {
+        const uint2 x = some_sh[tid];
+        int ahead = 0;   // the list is in the order of the pages
+        for (int i = 0; i < in; ++i) {
+          const uint32_t k = some_sh[i].x;
+          ahead += k > x.x || (k == x.x && i < tid);
+        }
+        if (ahead == left - 1) found_sh = x.x, index_sh = (int)x.y;
+      }
+      __syncthreads();
+      found = found_sh, last = index_sh;
+    } else {   // all of one key: the first `left` of them
+      int m = 0;
+      each([&](uint32_t k, int) { m += k - least == found; });
+      int at = scan<NT>(m, sums_sh);
+      each([&](uint32_t k, int i) {
+        if (k - least == found && at++ == left - 1) index_sh = i;
+      });
+      __syncthreads();
+      last = index_sh;
+    }
+    bits = 0;
   }
-  scan2(above, equal, sums_sh);
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    if (k > found || (k == found && equal < left)) out[sink + above + min(equal, left)] = load_global(table + sink + i);
-    above += k > found, equal += k == found;
-  }
+  auto keep = [&](uint32_t k, int i) {
+    const uint64_t y = (uint64_t)(k - least) >> bits;
+    return y > found || (y == found && i <= last);
+  };
+  int m = 0;
+  each([&](uint32_t k, int i) { m += keep(k, i); });
+  __syncthreads();
+  int at = sink + scan<NT>(m, sums_sh);
+  each([&](uint32_t k, int i) {
+    if (keep(k, i)) out[at++] = load_global(table + sink + i);
+  });
+}
+
+template <int NT>
+cudaError_t launch_choice(const qwm_paged8_select_args& a, int shift, cudaStream_t st) {
+  return launch_early(paged8_select_kernel<NT>, dim3((unsigned)a.kv_heads, (unsigned)a.requests, 1), NT, 0, st, a, shift);
 }
 
 }  // namespace
 
 cudaError_t launch_select8(const qwm_paged8_select_args& a, int shift, cudaStream_t st) {
-  const bool bf = a.dtype == QWM_BF16;
+  const bool bf = a.dtype == QWM_BF16, wide = a.head_dim == 128;
   if (a.max_blocks > a.width) {   // else all pages are kept
-    const dim3 grid((unsigned)(((int64_t)a.max_blocks + kPages - 1) / kPages), (unsigned)a.kv_heads, (unsigned)a.requests);
-    auto kern = a.head_dim == 64 ? (bf ? paged8_score_kernel<64, __nv_bfloat16> : paged8_score_kernel<64, float>)
-                                 : (bf ? paged8_score_kernel<128, __nv_bfloat16> : paged8_score_kernel<128, float>);
-    const cudaError_t e = launch_early(kern, grid, kNt, 0, st, a, shift);
+    const int64_t pairs = (int64_t)a.requests * a.kv_heads, sms = sm_count();
+    const dim3 grid(1, (unsigned)a.kv_heads, (unsigned)a.requests);
+    cudaError_t e;
+    if (a.rows * (a.heads / a.kv_heads) <= 8 * (int64_t)a.requests) {
+      // tiles of 16 pages for a warp: one, or as many as keep 16 warps an SM busy
+      const int64_t all = ((int64_t)a.max_blocks + 15) / 16, fair = all * pairs / (16 * sms);
+      const int tiles = (int)(fair < 1 ? 1 : fair < kMostTiles ? fair : kMostTiles);
+      dim3 g = grid;
+      g.x = (unsigned)((all + kFewWarps * tiles - 1) / (kFewWarps * tiles));
+      auto kern = wide ? (bf ? paged8_score_few_kernel<128, __nv_bfloat16> : paged8_score_few_kernel<128, float>)
+                       : (bf ? paged8_score_few_kernel<64, __nv_bfloat16> : paged8_score_few_kernel<64, float>);
+      e = launch_early(kern, g, kFewNt, 0, st, a, shift, tiles);
+    } else {
+      e = cudaMemsetAsync(a.workspace, 0, (size_t)pairs * a.max_blocks * 4, st);
+      if (e != cudaSuccess) return launched(e);
+      // two CTAs an SM, if there are so many 64s of rows
+      const int64_t splits = (2 * sms + pairs - 1) / pairs, most = (a.rows * (a.heads / a.kv_heads) + 63) / 64;
+      dim3 g = grid;
+      g.x = (unsigned)(splits < most ? splits : most);
+      auto kern = wide ? (bf ? paged8_score_many_kernel<128, __nv_bfloat16> : paged8_score_many_kernel<128, float>)
+                       : (bf ? paged8_score_many_kernel<64, __nv_bfloat16> : paged8_score_many_kernel<64, float>);
+      e = launch_early(kern, g, kNt, 0, st, a, shift);
+    }
     if (e != cudaSuccess) return e;
   }
-  static SmemLimit limit;
-  const int keys = a.max_blocks < kKeys ? a.max_blocks : kKeys;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.kv_heads, (unsigned)a.requests, 1);
-  cfg.blockDim = dim3(kSelNt, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)keys * 4;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1] = {early_launch()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return launched(launch_smem(limit, kKeys * 4, paged8_select_kernel, cfg, a, shift));
+  return a.max_blocks <= 256 * kE ? launch_choice<256>(a, shift, st) : launch_choice<1024>(a, shift, st);
 }
 
 }  // namespace paged
