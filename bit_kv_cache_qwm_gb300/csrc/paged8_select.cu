@@ -7,6 +7,7 @@
 // float32 sums exactly in any order: mma.m16n8k16, 16 pages by 8 rows.
 #include "paged_internal.cuh"
 #include "paged_launch.cuh"
+#include "tcgen05_util.cuh"
 
 namespace qwm {
 namespace paged {
@@ -254,69 +255,196 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
 
 // ---- many rows: drafts, prompts and chunks
 //
-// A CTA takes the pages of a request and head and every `splits`-th 64 of its rows:
-// each warp turns 8 of them into operands in shared memory, then goes through its
-// tiles of 16 pages with all 64.  Maxima meet in the keys by atomicMax, whose order
-// does not matter.  Bound by the MMAs.
-constexpr int kNt = 256, kWarps = kNt / 32;
+// The same products on the 5th-generation tensor cores: M = 128 pages (thread =
+// page = TMEM lane, so that a page's maximum over the rows stays in its thread),
+// N = up to 128 rows, K = 2 d.  A CTA keeps 128 rows of one request and head as an
+// operand and goes through the pages: while tile t is multiplied, warps 4-7 turn the
+// bounds of tile t + 1 into the other operand and warps 0-3 take the maxima of tile
+// t - 1 into the keys, by atomicMax, whose order does not matter.
+// Bound by the tensor pipe (1.3K cycles a tile at d = 128) behind the 128 rows'
+// conversion.  On mma.sync, with the rows' operands shared by the eight warps of a
+// CTA, the chunk of 4,680 rows and 24 heads over 767 pages took 250 us.
+constexpr int kManyNt = 256, kRowsTile = 128, kPagesTile = 128;
+
+template <int D>
+struct Lay {
+  static constexpr int op = 128 * 2 * D * 2;   // 128 rows or pages of 2 d float16
+  static constexpr int bytes = 3 * op + 1024;  // the rows, two of pages, and room to align
+};
+
+// byte offset of 8 channels (chunk) of a row in an operand of SW128 atoms of 64 elements
+__device__ __forceinline__ int op_off(int row, int chunk) {
+  return (chunk >> 3) * 16384 + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
 
 template <int D, class T>
-__global__ void __launch_bounds__(kNt, 2) paged8_score_many_kernel(const qwm_paged8_select_args a, int shift) {
+__global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm_paged8_select_args a, int shift, int64_t wait_cycles) {
+  using namespace tcx;
   constexpr int KS = D / 16;
-  __shared__ __align__(16) uint4 rows_sh[kWarps][KS][32];   // b0, b1 of x^+, then of x^-
-  __shared__ float unit_sh[kWarps * 8];
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
+  __shared__ __align__(8) uint64_t done[2], drained;     // a tile complete, by its parity; nothing left in the pipe
+  __shared__ __align__(16) float unit_row[kRowsTile];   // NaN: no such row
+  __shared__ float unit_page[2][kPagesTile];
+  __shared__ uint32_t tmem_sh;
+  __shared__ volatile int abort_sh, late_sh;
+  __shared__ uint32_t nowhere;
   wait_for_kernel_ahead();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z, group = a.heads / a.kv_heads;
   const Pages p = load_pages(a, shift, b);
-  if (p.first >= p.n || p.count <= a.width) return;
-  uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
   const int64_t rows = (int64_t)(p.n - p.first) * group;
-  for (int64_t r0 = (int64_t)blockIdx.x * 8 * kWarps; r0 < rows; r0 += (int64_t)gridDim.x * 8 * kWarps) {
-    if (r0 + 8 * warp < rows) {
-      uint4 w[KS];
-      const float u = quantise_row<D, T>(a, p, h, group, r0 + 8 * warp + g, rows, w);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) rows_sh[warp][i][lane] = w[i];
-      if (c == 0) unit_sh[8 * warp + g] = u;
-    }
-    __syncthreads();
-    const int blocks = (int)min((rows - r0 + 7) / 8, (int64_t)kWarps);
-    for (int j0 = 16 * warp; j0 < p.tail; j0 += 16 * kWarps) {
-      uint32_t high[KS][4], low[KS][4];
-      float unit[2];
-      {
-        Tile<D> t;
-        const int id[2] = {page_id(a, b, j0 + g, p.tail), page_id(a, b, j0 + g + 8, p.tail)};
-        t.load(a, h, id);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          Tile<D>::operand(t.high, k, high[k]);
-          Tile<D>::operand(t.low, k, low[k]);
-        }
-        unit[0] = t.unit[0], unit[1] = t.unit[1];
-      }
-      float best[2] = {-INFINITY, -INFINITY};
-      for (int y = 0; y < blocks; ++y) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint4 w = rows_sh[y][k][lane];
-          mma(s, high[k], w.x, w.y);
-          mma(v, low[k], w.z, w.w);
-        }
-        take(best, s, v, unit, unit_sh[8 * y + 2 * c], unit_sh[8 * y + 2 * c + 1]);
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
-        best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
-        const int j = j0 + g + 8 * x;
-        if (c == 0 && j < p.tail) atomicMax(keys + j, key_of(best[x]));
-      }
-    }
-    __syncthreads();
+  if (p.first >= p.n || p.count <= a.width || p.tail == 0 || (int64_t)blockIdx.x * kRowsTile >= rows) return;
+  if (tid == 0) {
+    abort_sh = late_sh = 0, nowhere = 0;
+    bar_init(&done[0], 1);
+    bar_init(&done[1], 1);
+    bar_init(&drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(su32(&tmem_sh)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_sh;
+  uint32_t* status = a.status ? a.status : &nowhere;
+  uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
+  const int tiles = (p.tail + kPagesTile - 1) / kPagesTile;
+  uint8_t* pages_at = sm + Lay<D>::op;
+
+  // Tiles are counted on (v) over the rows' tiles: operands, accumulators and barriers
+  // go by the parity of that, barriers' phases by half of it.
+  // The bounds of tile t, 32 pages a warp: a load takes 64 bytes of eight pages, and
+  // the eight lanes of a store phase have two pages, whose swizzles differ
+  auto convert = [&](int t, int v) {
+    const int w = warp - 4, j = t * kPagesTile + 32 * w + lane;
+    int id = page_id(a, b, j, p.tail);
+    unit_page[v & 1][32 * w + lane] = id < 0 ? __int_as_float(0x7fffffff)
+        : load_global(reinterpret_cast<const float*>((const uint8_t*)a.bounds + ((int64_t)id * a.kv_heads + h) * (2 * D + 16) + 2 * D));
+    id = max(id, 0);
+    uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint8_t* src = (const uint8_t*)a.bounds +
+                           ((int64_t)__shfl_sync(0xffffffffu, id, 8 * k + g) * a.kv_heads + h) * (2 * D + 16) + 16 * c;
+      uint4 u[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) u[i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t f[8];
+        whole(u[i].x, &f[0], &f[1]);
+        whole(u[i].y, &f[2], &f[3]);
+        whole(u[i].z, &f[4], &f[5]);
+        whole(u[i].w, &f[6], &f[7]);
+        const int row = 32 * w + 8 * k + g, chunk = 2 * (c + 4 * i);
+        *reinterpret_cast<uint4*>(to + op_off(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(to + op_off(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+      }
+    }
+    fence_async_smem();
+  };
+  // the largest score of each page of tile t over the rows
+  auto reduce = [&](int t, int v, int n, bool ok) {
+    const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + 128u * (v & 1);
+    const float up = unit_page[v & 1][tid];
+    float best = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 32) {
+      uint32_t s[32];
+      tmem_ld32(at + i, s);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; k += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(&unit_row[i + k]);
+        const float x0 = __fmul_rn(__fmul_rn(__uint_as_float(s[k]), up), u.x), x1 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 1]), up), u.y);
+        const float x2 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 2]), up), u.z), x3 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 3]), up), u.w);
+        best = max3f(max3f(best, x0, x1), x2, x3);
+      }
+    }
+    const int j = t * kPagesTile + tid;
+    if (ok && j < p.tail) atomicMax(keys + j, key_of(best));
+    fence_before();
+  };
+
+  int v0 = 0;   // tiles of the rows before
+  for (int64_t r0 = (int64_t)blockIdx.x * kRowsTile; r0 < rows; r0 += (int64_t)gridDim.x * kRowsTile, v0 += tiles) {
+    const int n = (int)min((rows - r0 + 31) & ~(int64_t)31, (int64_t)kRowsTile);
+#pragma unroll 1
+    for (int y = 8 * warp; y < n; y += 64) {
+      uint4 w[KS];
+      const float x = quantise_row<D, T>(a, p, h, group, r0 + y + g, rows, w);
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const int chunk = c * (KS / 2) + i;
+        *reinterpret_cast<uint4*>(sm + op_off(y + g, chunk)) = make_uint4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
+        *reinterpret_cast<uint4*>(sm + op_off(y + g, D / 8 + chunk)) = make_uint4(w[2 * i].z, w[2 * i].w, w[2 * i + 1].z, w[2 * i + 1].w);
+      }
+      if (c == 0) unit_row[y + g] = x;
+    }
+    fence_async_smem();
+    if (warp >= 4) convert(0, v0);
+    __syncthreads();
+    fence_after();
+    for (int t = 0; t <= tiles; ++t) {
+      const int v = v0 + t;
+      if (t < tiles && warp == 0) {
+        const bool go = !__any_sync(0xffffffffu, abort_sh != 0);
+        if (go && elect_one()) {
+          const uint32_t idesc = (1u << 4) | ((uint32_t)(n / 8) << 17) | (8u << 24);
+          const uint32_t pa = su32(pages_at + (v & 1) * Lay<D>::op), ra = su32(sm);
+#pragma unroll
+          for (int k = 0; k < 2 * D / 16; ++k) {
+            const uint32_t ko = (k >> 2) * 16384 + (k & 3) * 32;
+            mma_ss(tmem + 128u * (v & 1), desc_sw128(pa + ko), desc_sw128(ra + ko), idesc, k > 0);
+          }
+          commit(&done[v & 1]);
+        }
+        __syncwarp();
+      }
+      // tile t - 1 complete: its products are there, its operand is free
+      bool ok = true;
+      if (t > 0) {
+        ok = warp_all(bar_wait(&done[(v - 1) & 1], ((v - 1) >> 1) & 1, &abort_sh, status, wait_cycles));
+        fence_after();
+      }
+      if (warp >= 4) {
+        if (t + 1 < tiles) convert(t + 1, v + 1);
+      } else if (t > 0) {
+        reduce(t - 1, v - 1, n, ok);
+      }
+      __syncthreads();
+      fence_after();
+    }
+  }
+  // after a wait that ran out MMAs may still be on their way
+  if (warp == 0) {
+    if (elect_one()) commit(&drained);
+    __syncwarp();
+    bar_wait(&drained, 0, &late_sh, status);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+}
+
+template <int D, class T>
+cudaError_t launch_many(const qwm_paged8_select_args& a, int shift, dim3 grid, cudaStream_t st) {
+  static SmemLimit limit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kManyNt, 1, 1);
+  cfg.dynamicSmemBytes = Lay<D>::bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {early_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launched(launch_smem(limit, cfg.dynamicSmemBytes, paged8_score_many_kernel<D, T>, cfg, a, shift,
+                              injected_wait_cycles(tcx::kWaitCycles)));
 }
 
 // ---- the choice
@@ -514,13 +642,12 @@ cudaError_t launch_select8(const qwm_paged8_select_args& a, int shift, cudaStrea
     } else {
       e = cudaMemsetAsync(a.workspace, 0, (size_t)pairs * a.max_blocks * 4, st);
       if (e != cudaSuccess) return launched(e);
-      // two CTAs an SM, if there are so many 64s of rows
-      const int64_t splits = (2 * sms + pairs - 1) / pairs, most = (a.rows * (a.heads / a.kv_heads) + 63) / 64;
+      // a CTA for every 128 rows of a request of average length, up to eight an SM
+      const int64_t each = (a.rows * (a.heads / a.kv_heads) / a.requests + kRowsTile - 1) / kRowsTile, most = (8 * sms + pairs - 1) / pairs;
       dim3 g = grid;
-      g.x = (unsigned)(splits < most ? splits : most);
-      auto kern = wide ? (bf ? paged8_score_many_kernel<128, __nv_bfloat16> : paged8_score_many_kernel<128, float>)
-                       : (bf ? paged8_score_many_kernel<64, __nv_bfloat16> : paged8_score_many_kernel<64, float>);
-      e = launch_early(kern, g, kNt, 0, st, a, shift);
+      g.x = (unsigned)(each < 1 ? 1 : each < most ? each : most);
+      e = wide ? (bf ? launch_many<128, __nv_bfloat16>(a, shift, g, st) : launch_many<128, float>(a, shift, g, st))
+               : (bf ? launch_many<64, __nv_bfloat16>(a, shift, g, st) : launch_many<64, float>(a, shift, g, st));
     }
     if (e != cudaSuccess) return e;
   }
