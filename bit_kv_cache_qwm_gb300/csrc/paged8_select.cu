@@ -317,36 +317,54 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
 
   // Tiles are counted on (v) over the rows' tiles: operands, accumulators and barriers
   // go by the parity of that, barriers' phases by half of it.
-  // The bounds of tile t, 32 pages a warp: a load takes 64 bytes of eight pages, and
-  // the eight lanes of a store phase have two pages, whose swizzles differ
-  auto convert = [&](int t, int v) {
-    const int w = warp - 4, j = t * kPagesTile + 32 * w + lane;
-    int id = page_id(a, b, j, p.tail);
-    unit_page[v & 1][32 * w + lane] = id < 0 ? __int_as_float(0x7fffffff)
-        : load_global(reinterpret_cast<const float*>((const uint8_t*)a.bounds + ((int64_t)id * a.kv_heads + h) * (2 * D + 16) + 2 * D));
-    id = max(id, 0);
-    uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
+  // A tile's bounds, 32 pages a warp: a load takes 64 bytes of eight pages, and the
+  // eight lanes of a store phase have two pages, whose swizzles differ.  The pages'
+  // ids are loaded two tiles ahead, the bounds one.
+  uint4 raw[4][D / 32];
+  float unit = 0.f;
+  int id = 0, ahead = 0;   // the tile whose ids are on their way
+  auto look = [&]() {
+    id = page_id(a, b, ahead * kPagesTile + 32 * (warp & 3) + lane, p.tail);
+    if (++ahead == tiles) ahead = 0;   // the next rows' first tile
+  };
+  auto fetch = [&]() {
+    const int at = max(id, 0);
+    unit = load_global(reinterpret_cast<const float*>((const uint8_t*)a.bounds + ((int64_t)at * a.kv_heads + h) * (2 * D + 16) + 2 * D));
+    if (id < 0) unit = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint8_t* src = (const uint8_t*)a.bounds +
-                           ((int64_t)__shfl_sync(0xffffffffu, id, 8 * k + g) * a.kv_heads + h) * (2 * D + 16) + 16 * c;
-      uint4 u[D / 32];
+                           ((int64_t)__shfl_sync(0xffffffffu, at, 8 * k + g) * a.kv_heads + h) * (2 * D + 16) + 16 * c;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) u[i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
+      for (int i = 0; i < D / 32; ++i) raw[k][i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
+    }
+    look();
+  };
+  auto convert = [&](int v) {
+    const int w = warp & 3;
+    unit_page[v & 1][32 * w + lane] = unit;
+    uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
+        const uint4 u = raw[k][i];
         uint32_t f[8];
-        whole(u[i].x, &f[0], &f[1]);
-        whole(u[i].y, &f[2], &f[3]);
-        whole(u[i].z, &f[4], &f[5]);
-        whole(u[i].w, &f[6], &f[7]);
+        whole(u.x, &f[0], &f[1]);
+        whole(u.y, &f[2], &f[3]);
+        whole(u.z, &f[4], &f[5]);
+        whole(u.w, &f[6], &f[7]);
         const int row = 32 * w + 8 * k + g, chunk = 2 * (c + 4 * i);
         *reinterpret_cast<uint4*>(to + op_off(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(to + op_off(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
-    }
     fence_async_smem();
+    fetch();
   };
+  if (warp >= 4) {
+    look();
+    fetch();
+  }
   // the largest score of each page of tile t over the rows
   auto reduce = [&](int t, int v, int n, bool ok) {
     const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + 128u * (v & 1);
@@ -386,7 +404,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
       if (c == 0) unit_row[y + g] = x;
     }
     fence_async_smem();
-    if (warp >= 4) convert(0, v0);
+    if (warp >= 4) convert(v0);
     __syncthreads();
     fence_after();
     for (int t = 0; t <= tiles; ++t) {
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
         fence_after();
       }
       if (warp >= 4) {
-        if (t + 1 < tiles) convert(t + 1, v + 1);
+        if (t + 1 < tiles) convert(v + 1);
       } else if (t > 0) {
         reduce(t - 1, v - 1, n, ok);
       }
