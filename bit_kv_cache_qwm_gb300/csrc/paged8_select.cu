@@ -258,13 +258,14 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
 // The same products on the 5th-generation tensor cores: M = 128 pages (thread =
 // page = TMEM lane, so that a page's maximum over the rows stays in its thread),
 // N = up to 128 rows, K = 2 d.  A CTA keeps 128 rows of one request and head as an
-// operand and goes through the pages: while tile t is multiplied, warps 4-7 turn the
-// bounds of tile t + 1 into the other operand and warps 0-3 take the maxima of tile
-// t - 1 into the keys, by atomicMax, whose order does not matter.
+// operand and goes through the pages: while tile t is multiplied, warps 8-15 turn the
+// bounds of tile t + 1 into the other operand and warps 0-7 take the maxima of tile
+// t - 1 (four the first 64 rows, four the others) into the keys, by atomicMax, whose
+// order does not matter.
 // Bound by the tensor pipe (1.3K cycles a tile at d = 128) behind the 128 rows'
 // conversion.  On mma.sync, with the rows' operands shared by the eight warps of a
 // CTA, the chunk of 4,680 rows and 24 heads over 767 pages took 250 us.
-constexpr int kManyNt = 256, kRowsTile = 128, kPagesTile = 128;
+constexpr int kManyNt = 512, kRowsTile = 128, kPagesTile = 128;
 
 template <int D>
 struct Lay {
@@ -317,14 +318,14 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
 
   // Tiles are counted on (v) over the rows' tiles: operands, accumulators and barriers
   // go by the parity of that, barriers' phases by half of it.
-  // A tile's bounds, 32 pages a warp: a load takes 64 bytes of eight pages, and the
+  // A tile's bounds, 16 pages a warp: a load takes 64 bytes of eight pages, and the
   // eight lanes of a store phase have two pages, whose swizzles differ.  The pages'
   // ids are loaded two tiles ahead, the bounds one.
-  uint4 raw[4][D / 32];
+  uint4 raw[2][D / 32];
   float unit = 0.f;
   int id = 0, ahead = 0;   // the tile whose ids are on their way
   auto look = [&]() {
-    id = page_id(a, b, ahead * kPagesTile + 32 * (warp & 3) + lane, p.tail);
+    id = page_id(a, b, ahead * kPagesTile + 16 * (warp & 7) + (lane & 15), p.tail);
     if (++ahead == tiles) ahead = 0;   // the next rows' first tile
   };
   auto fetch = [&]() {
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
     unit = load_global(reinterpret_cast<const float*>((const uint8_t*)a.bounds + ((int64_t)at * a.kv_heads + h) * (2 * D + 16) + 2 * D));
     if (id < 0) unit = __int_as_float(0x7fffffff);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const uint8_t* src = (const uint8_t*)a.bounds +
                            ((int64_t)__shfl_sync(0xffffffffu, at, 8 * k + g) * a.kv_heads + h) * (2 * D + 16) + 16 * c;
 #pragma unroll
@@ -341,11 +342,11 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
     look();
   };
   auto convert = [&](int v) {
-    const int w = warp & 3;
-    unit_page[v & 1][32 * w + lane] = unit;
+    const int w = warp & 7;
+    if (lane < 16) unit_page[v & 1][16 * w + lane] = unit;
     uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 u = raw[k][i];
@@ -354,37 +355,38 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
         whole(u.y, &f[2], &f[3]);
         whole(u.z, &f[4], &f[5]);
         whole(u.w, &f[6], &f[7]);
-        const int row = 32 * w + 8 * k + g, chunk = 2 * (c + 4 * i);
+        const int row = 16 * w + 8 * k + g, chunk = 2 * (c + 4 * i);
         *reinterpret_cast<uint4*>(to + op_off(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(to + op_off(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
     fence_async_smem();
     fetch();
   };
-  if (warp >= 4) {
+  if (warp >= 8) {
     look();
     fetch();
   }
-  // the largest score of each page of tile t over the rows
+  // the largest score of each page of tile t over half of the rows
   auto reduce = [&](int t, int v, int n, bool ok) {
-    const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + 128u * (v & 1);
-    const float up = unit_page[v & 1][tid];
+    const int page = tid & 127, i0 = 64 * (warp >> 2);
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (v & 1);
+    const float2 up = make_float2(unit_page[v & 1][page], unit_page[v & 1][page]);
     float best = -INFINITY;
 #pragma unroll 1
-    for (int i = 0; i < n; i += 32) {
+    for (int i = i0; i < min(n, i0 + 64); i += 32) {
       uint32_t s[32];
       tmem_ld32(at + i, s);
       tmem_wait_ld();
 #pragma unroll
       for (int k = 0; k < 32; k += 4) {
         const float4 u = *reinterpret_cast<const float4*>(&unit_row[i + k]);
-        const float x0 = __fmul_rn(__fmul_rn(__uint_as_float(s[k]), up), u.x), x1 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 1]), up), u.y);
-        const float x2 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 2]), up), u.z), x3 = __fmul_rn(__fmul_rn(__uint_as_float(s[k + 3]), up), u.w);
-        best = max3f(max3f(best, x0, x1), x2, x3);
+        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), up), make_float2(u.x, u.y));
+        const float2 y = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), up), make_float2(u.z, u.w));
+        best = max3f(max3f(best, x.x, x.y), y.x, y.y);
       }
     }
-    const int j = t * kPagesTile + tid;
-    if (ok && j < p.tail) atomicMax(keys + j, key_of(best));
+    const int j = t * kPagesTile + page;
+    if (ok && j < p.tail && i0 < n) atomicMax(keys + j, key_of(best));
     fence_before();
   };
 
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   for (int64_t r0 = (int64_t)blockIdx.x * kRowsTile; r0 < rows; r0 += (int64_t)gridDim.x * kRowsTile, v0 += tiles) {
     const int n = (int)min((rows - r0 + 31) & ~(int64_t)31, (int64_t)kRowsTile);
 #pragma unroll 1
-    for (int y = 8 * warp; y < n; y += 64) {
+    for (int y = 8 * warp; y < n; y += 8 * (kManyNt / 32)) {
       uint4 w[KS];
       const float x = quantise_row<D, T>(a, p, h, group, r0 + y + g, rows, w);
 #pragma unroll
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
       if (c == 0) unit_row[y + g] = x;
     }
     fence_async_smem();
-    if (warp >= 4) convert(v0);
+    if (warp >= 8) convert(v0);
     __syncthreads();
     fence_after();
     for (int t = 0; t <= tiles; ++t) {
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
         ok = warp_all(bar_wait(&done[(v - 1) & 1], ((v - 1) >> 1) & 1, &abort_sh, status, wait_cycles));
         fence_after();
       }
-      if (warp >= 4) {
+      if (warp >= 8) {
         if (t + 1 < tiles) convert(v + 1);
       } else if (t > 0) {
         reduce(t - 1, v - 1, n, ok);
