@@ -471,11 +471,11 @@ cudaError_t launch_many(const qwm_paged8_select_args& a, int shift, dim3 grid, c
 //
 // One CTA a request and head.  The least key kept is found digit by digit (8 bits,
 // counted from the highest bit in which the keys differ, so that a digit's counts
-// spread); once no more than a thread each are left in question, each counts those
+// spread); once no more than kFew are left in question, a thread each counts those
 // ahead of its own instead.  Then every thread writes those of its range of pages.
 // Keys stay in registers where E a thread are enough, else they are read again for
 // every step.  Bound by the latency of its barriers.
-constexpr int kE = 8;
+constexpr int kE = 8, kFew = 128;
 
 // exclusive sum of x over the CTA
 template <int NT>
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(NT) paged8_select_kernel(const qwm_paged8_sele
   __shared__ uint32_t count_sh[256], least_sh, most_sh, found_sh;
   __shared__ int digit_sh, left_sh, in_sh, index_sh;
   __shared__ int sums_sh[NT / 32];
-  __shared__ uint2 some_sh[NT];   // (key, index) of those in question
+  __shared__ uint2 some_sh[kFew];   // (key, index) of those in question
   wait_for_kernel_ahead();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.x, b = blockIdx.y;
   const Pages p = load_pages(a, shift, b);
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(NT) paged8_select_kernel(const qwm_paged8_sele
   least = least_sh, most = most_sh;
   int bits = 32 - __clz(most - least), left = want, in = n;
   uint32_t found = 0;   // the digits so far, of the least key kept
-  while (bits > 0 && in > NT) {
+  while (bits > 0 && in > kFew) {
     const int down = max(bits - 8, 0), width = bits - down;
     for (int i = tid; i < 256; i += NT) count_sh[i] = 0;
     __syncthreads();
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(NT) paged8_select_kernel(const qwm_paged8_sele
   // all.  `last`: the last page kept among those of the least key kept.
   int last = 0x7fffffff;
   if (in > left) {
-    if (in <= NT) {
+    if (in <= kFew) {
       int m = 0;
       each([&](uint32_t k, int) { m += (uint64_t)(k - least) >> bits == found; });
       int at = scan<NT>(m, sums_sh);
@@ -651,8 +651,9 @@ cudaError_t launch_select8(const qwm_paged8_select_args& a, int shift, cudaStrea
     const dim3 grid(1, (unsigned)a.kv_heads, (unsigned)a.requests);
     cudaError_t e;
     if (a.rows * (a.heads / a.kv_heads) <= 8 * (int64_t)a.requests) {
-      // tiles of 16 pages for a warp: one, or as many as keep 16 warps an SM busy
-      const int64_t all = ((int64_t)a.max_blocks + 15) / 16, fair = all * pairs / (16 * sms);
+      // tiles of 16 pages for a warp: as many as leave no more than the 16 warps an SM
+      // that fit at once
+      const int64_t all = ((int64_t)a.max_blocks + 15) / 16, fair = (all * pairs + 16 * sms - 1) / (16 * sms);
       const int tiles = (int)(fair < 1 ? 1 : fair < kMostTiles ? fair : kMostTiles);
       dim3 g = grid;
       g.x = (unsigned)((all + kFewWarps * tiles - 1) / (kFewWarps * tiles));
