@@ -88,6 +88,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
+// Two values as float16 pairs, each: one, or in float32 two that add up to them but
+// for 2^-22 of either (22 of 24 bits).
+template <int TERMS, class Put>
+__device__ __forceinline__ void split(float x, float y, Put put) {
+  const __half2 h = __floats2half2_rn(x, y);
+  put(0, h2u(h));
+  if constexpr (TERMS == 2) {
+    const float2 f = __half22float2(h);
+    put(1, h2u(__floats2half2_rn(x - f.x, y - f.y)));
+  }
+}
+
 // c scale + zero for the lower (upper) nibbles of bytes 0 and 2 of x.  `magic`
 // (1024 twice in float16) comes from the call's arguments: with a mask and a
 // register one instruction puts the codes into place, with two constants known
@@ -254,8 +266,10 @@ struct Smem {
   static constexpr int bytes = stat + kCw * 8 * NB * 8;     // float2 (m, l) [kCw][8 NB]
 };
 
-template <int D, int NB, class F>
-__global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
+template <int D, int NB, class F, class T>
+__global__ void __launch_bounds__(kNt, NB == 1 && sizeof(T) == 2 ? Plan<F>::kCtas : 2) paged_attend_mma_kernel(const AttendArgs a) {
+  constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
+  static_assert(TERMS == 1 || F::kBits == 8, "float32 needs keys and values that float16 holds");
   constexpr int R = 8 * NB, KW = D / 32, MB = D / 16;
   constexpr int kStages = Plan<F>::kStages, kSub = Plan<F>::kSub, kTk = Plan<F>::kTk, kNote = Plan<F>::kNote;
   constexpr uint32_t kNotes = (1u << kNote * kSub) - 1, kLive = kNotes / ((1u << kNote) - 1);   // of a stage; their first bits
@@ -285,15 +299,15 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
   const uint32_t ring_at = su32(ring) + (F::kBits == 4 ? 16 * lane : 0);
   // the item's queries, sent for ahead of the copies, which they would queue
   // behind (2 to 3 us of a first item)
-  uint4 qraw[NB][KW];
+  uint4 qraw[NB][KW * TERMS];
   auto load_q = [&]() {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = nb * 8 + (lane >> 2), rr = it.rt * R + r, tok = div_group(a, rr);
-      const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
+      const uint4* src = reinterpret_cast<const uint4*>((const T*)a.q + (int64_t)(it.rq.row0 + tok) * a.q_row +
                                                        (int64_t)(it.h * a.group + rr - tok * a.group) * a.q_head + (lane & 3) * (D / 4));
 #pragma unroll
-      for (int i = 0; i < KW; ++i) qraw[nb][i] = r < it.rows ? src[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < KW * TERMS; ++i) qraw[nb][i] = r < it.rows ? src[i] : make_uint4(0, 0, 0, 0);
     }
   };
   load_q();
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
   float2* stat = reinterpret_cast<float2*>(sm + Sm::stat);
   do {
     // Q^T fragments: row g of each block of 8, in the order of the codes
-    uint32_t qf[NB][MB][2];
+    uint32_t qf[TERMS][NB][MB][2];
     float c2[NB][2];       // logit factor of rows 2 c and 2 c + 1
     int top[NB][2], bottom[NB][2];
     int top_min = it.hi, bottom_max = it.lo;
@@ -318,16 +332,21 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
       float x[D / 4];
       float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < KW * TERMS; ++i) {
         const uint4 u = qraw[nb][i];
         const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          x[8 * i + 2 * k] = __uint_as_float(v[k] << 16);
-          x[8 * i + 2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
-          mx = max3f(mx, fabsf(x[8 * i + 2 * k]), fabsf(x[8 * i + 2 * k + 1]));
+          if constexpr (TERMS == 2) {
+            x[4 * i + k] = __uint_as_float(v[k]);
+          } else {
+            x[8 * i + 2 * k] = __uint_as_float(v[k] << 16);
+            x[8 * i + 2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < D / 4; i += 2) mx = max3f(mx, fabsf(x[i]), fabsf(x[i + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int ex = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
@@ -338,9 +357,10 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
         const float* y = x + 8 * i;
         constexpr bool nibbles = F::kBits == 4;   // else the channels follow one another
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          qf[nb][2 * i + (k >> 1)][k & 1] =
-              h2u(__floats2half2_rn(y[nibbles ? k : 2 * k] * qs, y[nibbles ? k + 4 : 2 * k + 1] * qs));
+        for (int k = 0; k < 4; ++k) {
+          const float y0 = y[nibbles ? k : 2 * k] * qs, y1 = y[nibbles ? k + 4 : 2 * k + 1] * qs;
+          split<TERMS>(y0, y1, [&](int term, uint32_t h) { qf[term][nb][2 * i + (k >> 1)][k & 1] = h; });
+        }
       }
       const float f = row_factor(a, 127 + e);
 #pragma unroll
@@ -402,8 +422,9 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 float* to = (i & 1) ? s2[nb] : s[nb][e];
-                if (i < 2) mma0(to, f, qf[nb][i][0], qf[nb][i][1]);
-                else mma(to, f, qf[nb][i][0], qf[nb][i][1]);
+                if (i < 2) mma0(to, f, qf[0][nb][i][0], qf[0][nb][i][1]);
+                else mma(to, f, qf[0][nb][i][0], qf[0][nb][i][1]);
+                if constexpr (TERMS == 2) mma(to, f, qf[1][nb][i][0], qf[1][nb][i][1]);
               }
             }
           } else {
@@ -437,11 +458,11 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 if (i == 0) {
-                  mma0(s[nb][e], f, qf[nb][0][0], qf[nb][0][1]);
-                  mma0(s2[nb], f2, qf[nb][1][0], qf[nb][1][1]);
+                  mma0(s[nb][e], f, qf[0][nb][0][0], qf[0][nb][0][1]);
+                  mma0(s2[nb], f2, qf[0][nb][1][0], qf[0][nb][1][1]);
                 } else {
-                  mma(s[nb][e], f, qf[nb][2 * i][0], qf[nb][2 * i][1]);
-                  mma(s2[nb], f2, qf[nb][2 * i + 1][0], qf[nb][2 * i + 1][1]);
+                  mma(s[nb][e], f, qf[0][nb][2 * i][0], qf[0][nb][2 * i][1]);
+                  mma(s2[nb], f2, qf[0][nb][2 * i + 1][0], qf[0][nb][2 * i + 1][1]);
                 }
               }
             }
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
           }
         }
         // ---- softmax: s[nb][e][2 b + k] is token 16 e + 8 b + tok0, row 2 c + k
-        uint32_t pf[NB][kSub][2];
+        uint32_t pf[TERMS][NB][kSub][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (!whole) {
@@ -506,8 +527,8 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
             for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(s[nb][e][i], c2[nb][i & 1], -m[nb][i & 1]));
             l[nb][0] += p[0] + p[2];
             l[nb][1] += p[1] + p[3];
-            pf[nb][e][0] = transpose8(h2u(__floats2half2_rn(p[0], p[1])));
-            pf[nb][e][1] = transpose8(h2u(__floats2half2_rn(p[2], p[3])));
+            split<TERMS>(p[0], p[1], [&](int term, uint32_t h) { pf[term][nb][e][0] = transpose8(h); });
+            split<TERMS>(p[2], p[3], [&](int term, uint32_t h) { pf[term][nb][e][1] = transpose8(h); });
           }
         }
         // ---- O^T: tokens ta, tb (columns 2 c, 2 c + 1) of both blocks of 8
@@ -565,7 +586,18 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+                for (int nb = 0; nb < NB; ++nb) {
+                  if constexpr (TERMS == 2) {
+                    // summed up apart: the tensor cores' sums are cut off, these rounded
+                    float part[4];
+                    mma0(part, f[j], pf[0][nb][e][0], pf[0][nb][e][1]);
+                    mma(part, f[j], pf[1][nb][e][0], pf[1][nb][e][1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[nb][2 * y + j][k] += part[k];
+                  } else {
+                    mma(o[nb][2 * y + j], f[j], pf[0][nb][e][0], pf[0][nb][e][1]);
+                  }
+                }
             }
           } else {
             uint32_t v0[2][D / 64], v1[2][D / 64];
@@ -613,7 +645,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[nb][e][0], pf[nb][e][1]);
+                for (int nb = 0; nb < NB; ++nb) mma(o[nb][2 * y + j], f[j], pf[0][nb][e][0], pf[0][nb][e][1]);
             }
           }
         }
@@ -665,9 +697,13 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
           const int64_t tok = it.rq.row0 + div_group(a, rr);
           const int head = it.h * a.group + rr - div_group(a, rr) * a.group;
           const float inv = inverse_sum(sum);
-          const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-          *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + tok * a.o_row + head * a.o_head + ch) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+          T* dst = (T*)a.out + tok * a.o_row + head * a.o_head + ch;
+          if constexpr (TERMS == 2) {
+            *reinterpret_cast<float4*>(dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          } else {
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), b1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+          }
           if (a.lse && ch == 0) a.lse[tok * a.heads + head] = log_sum(mx, sum);
         } else {
           float* dst = part_row(a, w, slot, R, r, D);
@@ -685,7 +721,7 @@ __global__ void __launch_bounds__(kNt, NB == 1 ? Plan<F>::kCtas : 2) paged_atten
   } while (more);
 }
 
-template <int D, int NB, class F>
+template <int D, int NB, class F, class T>
 cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
   static SmemLimit limit;
   cudaLaunchConfig_t cfg = {};
@@ -696,29 +732,36 @@ cudaError_t launch_mma(const AttendArgs& a, int workers, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB, F>, cfg, a);
+  return launch_smem(limit, cfg.dynamicSmemBytes, paged_attend_mma_kernel<D, NB, F, T>, cfg, a);
 }
 
-template <class F>
-Workers workers_of(int64_t max_rows) {
+// float32 at d = 128 has no registers for 16 rows
+Workers workers_of(int64_t max_rows, int bits, bool f32, int d) {
   const int sms = sm_count();
-  return max_rows <= 8 ? Workers{Plan<F>::kCtas * sms, 8} : Workers{2 * sms, 16};
+  if (max_rows <= 8) return Workers{(f32 ? 2 : bits == 8 ? Plan<E4m3>::kCtas : Plan<Int4>::kCtas) * sms, 8};
+  return Workers{2 * sms, f32 && d == 128 ? 8 : 16};
 }
 
-template <class F>
-cudaError_t launch_mma_of(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
-  const Workers w = workers_of<F>(max_rows);
-  const cudaError_t e = w.rows == 8 ? (d == 64 ? launch_mma<64, 1, F>(a, w.count, st) : launch_mma<128, 1, F>(a, w.count, st))
-                                    : (d == 64 ? launch_mma<64, 2, F>(a, w.count, st) : launch_mma<128, 2, F>(a, w.count, st));
-  return e != cudaSuccess ? e : launch_attend_join(a, d, true, w, max_rows, st);
+template <int D, class F, class T>
+cudaError_t launch_rows(const AttendArgs& a, Workers w, cudaStream_t st) {
+  if constexpr (sizeof(T) == 4 && D == 128) return launch_mma<D, 1, F, T>(a, w.count, st);
+  else return w.rows == 8 ? launch_mma<D, 1, F, T>(a, w.count, st) : launch_mma<D, 2, F, T>(a, w.count, st);
+}
+
+template <class F, class T>
+cudaError_t launch_dim(const AttendArgs& a, int d, Workers w, cudaStream_t st) {
+  return d == 64 ? launch_rows<64, F, T>(a, w, st) : launch_rows<128, F, T>(a, w, st);
 }
 
 }  // namespace
 
-Workers mma_workers(int64_t max_rows, int bits) { return bits == 8 ? workers_of<E4m3>(max_rows) : workers_of<Int4>(max_rows); }
+Workers mma_workers(int64_t max_rows, int bits, bool f32, int d) { return workers_of(max_rows, bits, f32, d); }
 
-cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st) {
-  return a.bits == 8 ? launch_mma_of<E4m3>(a, d, max_rows, st) : launch_mma_of<Int4>(a, d, max_rows, st);
+cudaError_t launch_attend_mma(const AttendArgs& a, int d, bool f32, int64_t max_rows, cudaStream_t st) {
+  const Workers w = workers_of(max_rows, a.bits, f32, d);
+  const cudaError_t e = f32 ? launch_dim<E4m3, float>(a, d, w, st)
+                        : a.bits == 8 ? launch_dim<E4m3, __nv_bfloat16>(a, d, w, st) : launch_dim<Int4, __nv_bfloat16>(a, d, w, st);
+  return e != cudaSuccess ? e : launch_attend_join(a, d, !f32, w, max_rows, st);
 }
 
 }  // namespace paged

@@ -562,8 +562,8 @@ cudaError_t launch_smem(SmemLimit& lim, size_t most, K kern, cudaLaunchConfig_t&
 }
 Workers simt_workers(int64_t max_rows);
 cudaError_t launch_attend_simt(const AttendArgs& a, int d, bool bf16, int64_t max_rows, cudaStream_t st);
-Workers mma_workers(int64_t max_rows, int bits);
-cudaError_t launch_attend_mma(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
+Workers mma_workers(int64_t max_rows, int bits, bool f32, int d);
+cudaError_t launch_attend_mma(const AttendArgs& a, int d, bool f32, int64_t max_rows, cudaStream_t st);
 Workers tc_workers();
 cudaError_t launch_attend_tc(const AttendArgs& a, int d, int64_t max_rows, cudaStream_t st);
 // joins the parts of the items that were cut; max_rows: the rows of a

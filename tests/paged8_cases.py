@@ -54,9 +54,15 @@ def attend8_tolerance(O, spread, vmax, n: int, dtype: str, tensor: bool):
     of p v add at most (n / 16 + 100) roundings each in the float32 kernel and
     n + 200 in the tensor kernels, which round P to float16 besides (2^-11, and
     below float16's normal range 2^-25 absolute) and whose exp2 and rescaling are
-    off by 2^-21.  Then one rounding to the output's dtype."""
+    off by 2^-21.  Kernel 2 in float32 takes q and P as two float16 terms, off by 2^-22
+    of each (4 2^-24 more in delta, 2^-22 in P), sums a step's 16 tokens in two MMAs
+    that cut off below 2^-23 each, and adds the steps up like the float32 kernel.
+    Then one rounding to the output's dtype."""
     d32 = 131 * EPS2["f32"]
-    if tensor:
+    if tensor and dtype == "f32":
+        delta = spread * (d32 + 4 * EPS2["f32"]) + 2.0 ** -21
+        rel = np.expm1(2 * delta) + 2 * 2.0 ** -22 + 2 * (n / 16 + 100) * EPS2["f32"]
+    elif tensor:
         delta = spread * d32 + 2.0 ** -21
         rel = np.expm1(2 * delta) + 1.01 * EPS2["f16"] + n * 2.0 ** -25 + (n + 200) * EPS2["f32"]
     else:

@@ -136,7 +136,7 @@ def attend_args(paged, **kw):
     (dict(window=-1), 1), (dict(window=5, causal=0), 1), (dict(scale=float("nan")), 1), (dict(kernel=4), 1), (dict(max_new=-1), 1),
     (dict(max_blocks=1 << 27), 2), (dict(pool=FAKE + 8), 1), (dict(table=FAKE + 1), 1), (dict(lens=FAKE + 2), 1),
     (dict(cu=FAKE + 3), 1), (dict(lse=FAKE + 1), 1), (dict(status=FAKE + 1), 1), (dict(ws=FAKE + 64), 1), (dict(ws_bytes=100), 1),
-    (dict(q=(FAKE + 4, 768, 128)), 1), (dict(out=(FAKE, 512, 128)), 1), (dict(rows=1 << 29), 2), (dict(dtype=0, kernel=2), 2),
+    (dict(q=(FAKE + 4, 768, 128)), 1), (dict(out=(FAKE, 512, 128)), 1), (dict(rows=1 << 29), 2), (dict(dtype=0, kernel=2), 6),
     (dict(dtype=0, kernel=3), 2), (dict(dtype=0), 6), (dict(hk=1 << 16, hq=1 << 16, page=256, q=(FAKE, 1 << 23, 128), out=(FAKE, 1 << 23, 128)), 2)])
 def test_attend_refusals(paged, kw, status):
     assert paged.lib().qwm_paged8_attend(attend_args(paged, **kw), None) == status
