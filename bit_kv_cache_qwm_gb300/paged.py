@@ -56,6 +56,7 @@ _BOUNDS8 = struct.Struct("=8q5i4x")
 _SELECT8 = struct.Struct("=14q9i4x")
 
 _Tensor, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
+_U8 = torch.uint8
 _DTYPES = {torch.bfloat16: QWM_BF16, torch.float32: QWM_F32}
 _workspace_bytes: dict = {}
 _workspace8_bytes: dict = {}
@@ -378,22 +379,36 @@ def paged8_page_bounds(n_pages: int, kv_heads: int, head_dim: int, device=None) 
 _PAGE8 = {(d, 2 * p * d + max(16, p // 4)): p for d in (64, 128) for p in PAGE_TOKENS}
 
 
-def _page8_tokens(pool, d: int) -> int:
-    """Tokens of a page of the 8-bit `pool` [pages, kv_heads, block] for heads of d channels."""
-    if not isinstance(pool, _Tensor) or not pool.is_cuda or pool.dtype is not torch.uint8 or pool.dim() != 3 \
+def _pool8(pool, d: int, index: int, kv_heads=None):
+    """Pointer, pages, kv heads and tokens of a page of an 8-bit `pool` [pages, kv_heads, block] on device `index` for
+    heads of d channels."""
+    if not isinstance(pool, _Tensor) or pool.dtype is not _U8 or pool.get_device() != index or index < 0 \
             or not pool.is_contiguous():
-        raise ValueError("pool: a contiguous CUDA uint8 tensor [pages, kv_heads, block bytes] is expected")
-    page = _PAGE8.get((d, pool.shape[2]))
+        raise ValueError("pool: a contiguous CUDA uint8 tensor [pages, kv_heads, block bytes] on the other tensors' device is "
+                         "expected")
+    have = pool.shape
+    if len(have) != 3 or (kv_heads is not None and have[1] != kv_heads):
+        raise ValueError(f"pool: expected [pages, {'kv_heads' if kv_heads is None else kv_heads}, block], got {tuple(have)}")
+    n_pages, hk, block = have
+    page = _PAGE8.get((d, block))
     if page is None:
-        raise ValueError(f"pool: {pool.shape[2]} bytes are no 8-bit block of a page of {PAGE_TOKENS} tokens at d = {d}")
-    return page
+        raise ValueError(f"pool: {block} bytes are no 8-bit block of a page of {PAGE_TOKENS} tokens at d = {d}")
+    return pool.data_ptr(), n_pages, hk, page
 
 
-def _step8(block_table, kv_len, cu_rows, index: int):
-    """Pointers of a step's block table, lengths and first rows; its requests and the table's width."""
-    table = _array(block_table, "block_table", _I32, (None, None), index)
-    B, width = block_table.shape
-    return (table, _array(kv_len, "kv_len", _I32, (B,), index), _array(cu_rows, "cu_rows", _I32, (B + 1,), index)), B, width
+def _step8(block_table, kv_len, cu_rows, index: int, kv_heads=None):
+    """Pointers of a step's block table [requests, pages] (or [requests, kv_heads, pages]), lengths and first rows;
+    requests, pages and the tables' heads."""
+    heads = 1
+    if kv_heads is not None and isinstance(block_table, _Tensor) and block_table.dim() == 3:
+        heads = kv_heads
+        table = _array(block_table, "block_table", _I32, (None, kv_heads, None), index)
+        B, _, width = block_table.shape
+    else:
+        table = _array(block_table, "block_table", _I32, (None, None), index)
+        B, width = block_table.shape
+    lens, cu = _array(kv_len, "kv_len", _I32, (B,), index), _array(cu_rows, "cu_rows", _I32, (B + 1,), index)
+    return (table, lens, cu), B, width, heads
 
 
 def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -408,16 +423,13 @@ def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, bloc
     shape, dt, dev = k.shape, k.dtype, k.get_device()
     T, hk, d = shape
     vr = _rows(v, "v", dt, dev, shape)
-    page = _page8_tokens(pool, d)
-    n_pages, hp, _ = pool.shape
-    if pool.get_device() != dev or hp != hk:
-        raise ValueError(f"pool: expected [pages, {hk}, block] on {k.device}, got {tuple(pool.shape)} on {pool.device}")
+    at, n_pages, _, page = _pool8(pool, d, dev, hk)
     kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", dt, dev, shape)
     vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", dt, dev, shape)
-    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+    step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_append,
-         _APPEND8.pack(*kr, *vr, *kh, *vh, pool.data_ptr(), *step, _status(status, dev), T, n_pages, _DTYPES[dt], d, hk, page,
-                       B, width), "qwm_paged8_append", dev)
+         _APPEND8.pack(*kr, *vr, *kh, *vh, at, *step, _status(status, dev), T, n_pages, _DTYPES[dt], d, hk, page, B, width),
+         "qwm_paged8_append", dev)
 
 
 def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor, cu_rows: torch.Tensor, rows: int,
@@ -428,21 +440,21 @@ def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch
     first kv_len[b] tokens of request b.  Returns (k_out, v_out), new tensors of
     `dtype` where none are given; rows behind the last request are left as they
     were."""
-    page = _page8_tokens(pool, head_dim)
-    n_pages, hk, _ = pool.shape
-    dev = pool.get_device()
+    dev = pool.get_device() if isinstance(pool, _Tensor) else -1
+    at, n_pages, hk, page = _pool8(pool, head_dim, dev)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype: bfloat16 or float32 is expected, got {dtype}")
-    shape = torch.Size((rows, hk, head_dim))
+    shape = (rows, hk, head_dim)
     if k_out is None:
-        k_out = pool.new_empty(shape, dtype=dtype)
+        k_out = torch.empty(shape, dtype=dtype, device=pool.device)
+    kr = _rows(k_out, "k_out", dtype, dev, shape)
     if v_out is None:
-        v_out = pool.new_empty(shape, dtype=dtype)
-    kr, vr = _rows(k_out, "k_out", dtype, dev, shape), _rows(v_out, "v_out", dtype, dev, shape)
-    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+        v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
+    vr = _rows(v_out, "v_out", dtype, dev, shape)
+    step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_read,
-         _READ8.pack(*kr, *vr, pool.data_ptr(), *step, _status(status, dev), rows, n_pages, _DTYPES[dtype], head_dim, hk, page,
-                     B, width), "qwm_paged8_read", dev)
+         _READ8.pack(*kr, *vr, at, *step, _status(status, dev), rows, n_pages, _DTYPES[dtype], head_dim, hk, page, B, width),
+         "qwm_paged8_read", dev)
     return k_out, v_out
 
 
@@ -453,42 +465,28 @@ def qwm_paged8_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Te
     """qwm_paged_attend over the 8-bit pages, with the same arguments.
     block_table and kv_len may be what qwm_paged8_select returns: a table
     [requests, kv_heads, pages] lists the pages of each key/value head, and
-    kv_len, positions and the window count the tokens of that list."""
+    kv_len, positions and the window count the tokens of that list.  float32
+    runs on the tensor cores too (PAGED_MMA)."""
     qr = _rows(q, "q")
-    T, hq, d = q.shape
-    dev, dt = q.get_device(), q.dtype
-    page = _page8_tokens(pool, d)
-    n_pages, hk, _ = pool.shape
-    if pool.get_device() != dev or hk < 1 or hq % hk:
-        raise ValueError(f"pool: kv heads that divide {hq} on {q.device} are expected, got {tuple(pool.shape)} on {pool.device}")
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    T, hq, d = shape
+    at, n_pages, hk, page = _pool8(pool, d, dev)
+    if hk < 1 or hq % hk:
+        raise ValueError(f"pool: kv heads that divide {hq} are expected, got {hk}")
     if out is None:
-        out, ot = _like(q)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ot = (out.data_ptr(), hq * d, d)
     else:
-        ot = _rows(out, "out", dt, dev, q.shape)
-    heads = 1
-    if isinstance(block_table, _Tensor) and block_table.dim() == 3:
-        heads = hk
-        table = _array(block_table, "block_table", _I32, (None, hk, None), dev)
-    else:
-        table = _array(block_table, "block_table", _I32, (None, None), dev)
-    B, width = block_table.shape[0], block_table.shape[-1]
-    lens = _array(kv_len, "kv_len", _I32, (B,), dev)
-    cu = _array(cu_rows, "cu_rows", _I32, (B + 1,), dev)
+        ot = _rows(out, "out", dt, dev, shape)
+    step, B, width, heads = _step8(block_table, kv_len, cu_rows, dev, hk)
     ls = 0 if lse is None else _array(lse, "lse", _F32, (T, hq), dev)
     n_ws = _workspace8_bytes.get((dev, d)) or _workspace_size(_workspace8_bytes, lib().qwm_paged8_attend_workspace_bytes, dev, d)
-    ws = pool.new_empty(n_ws)
+    ws = torch.empty(n_ws, dtype=_U8, device=q.device)
     _run(lib().qwm_paged8_attend,
-         _ATTEND8.pack(*qr, *ot, ls, pool.data_ptr(), table, lens, cu, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
+         _ATTEND8.pack(*qr, *ot, ls, at, *step, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages,
                        T if max_new is None else max_new, _DTYPES[dt], d, hq, hk, page, B, width, 1 if causal else 0,
                        min(window, _INT_MAX), scale, kernel, heads, 0), "qwm_paged8_attend", dev)
     return out
-
-
-def _bounds8(bounds, n_pages, hk: int, d: int, dev: int) -> int:
-    p = _array(bounds, "bounds", torch.uint8, (n_pages, hk, 2 * d + 16), dev)
-    if p & 15:
-        raise ValueError("bounds: the pointer has to be a multiple of 16 bytes")
-    return p
 
 
 def qwm_paged8_bounds(pool: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -501,14 +499,14 @@ def qwm_paged8_bounds(pool: torch.Tensor, bounds: torch.Tensor, block_table: tor
     if not isinstance(bounds, _Tensor) or bounds.dim() != 3 or bounds.shape[2] not in (144, 272):
         raise ValueError("bounds: [pages, kv_heads, 2 head_dim + 16] is expected")
     d = (bounds.shape[2] - 16) // 2
-    page = _page8_tokens(pool, d)
-    n_pages, hk, _ = pool.shape
-    dev = pool.get_device()
-    at = _bounds8(bounds, n_pages, hk, d, dev)
-    step, B, width = _step8(block_table, kv_len, cu_rows, dev)
+    dev = pool.get_device() if isinstance(pool, _Tensor) else -1
+    at, n_pages, hk, page = _pool8(pool, d, dev)
+    to = _array(bounds, "bounds", _U8, (n_pages, hk, 2 * d + 16), dev)
+    if to & 15:
+        raise ValueError("bounds: the pointer has to be a multiple of 16 bytes")
+    step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_bounds,
-         _BOUNDS8.pack(pool.data_ptr(), at, *step, _status(status, dev), n_pages, max_new, d, hk, page, B, width),
-         "qwm_paged8_bounds", dev)
+         _BOUNDS8.pack(at, to, *step, _status(status, dev), n_pages, max_new, d, hk, page, B, width), "qwm_paged8_bounds", dev)
 
 
 def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -521,23 +519,24 @@ def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.
     d] with the keys in them.  Returns (pages int32 [requests, kv_heads, width],
     lens int32 [requests]), the block_table and kv_len of a qwm_paged8_attend."""
     qr = _rows(q, "q")
+    dt, dev = q.dtype, q.get_device()
     T, hq, d = q.shape
-    dev, dt = q.get_device(), q.dtype
-    hk = bounds.shape[1] if isinstance(bounds, _Tensor) and bounds.dim() == 3 else 0
-    at = _bounds8(bounds, None, hk, d, dev)
-    if hk < 1 or hq % hk:
-        raise ValueError(f"bounds: kv heads that divide {hq} are expected, got {tuple(bounds.shape)}")
-    step, B, blocks = _step8(block_table, kv_len, cu_rows, dev)
+    at = _array(bounds, "bounds", _U8, (None, None, 2 * d + 16), dev)
+    n_pages, hk, _ = bounds.shape
+    if at & 15 or hk < 1 or hq % hk:
+        raise ValueError(f"bounds: kv heads that divide {hq} at a multiple of 16 bytes are expected, got {hk}")
+    step, B, blocks, _ = _step8(block_table, kv_len, cu_rows, dev)
     if width < 1:
         raise ValueError("width: at least one page")
+    device = q.device
     if pages is None:
-        pages = kv_len.new_empty((B, hk, width))
+        pages = torch.empty((B, hk, width), dtype=_I32, device=device)
     if lens is None:
         lens = torch.empty_like(kv_len)
     out = _array(pages, "pages", _I32, (B, hk, width), dev), _array(lens, "lens", _I32, (B,), dev)
     n_ws = 4 * B * hk * blocks
-    ws = bounds.new_empty(max(n_ws, 1))
+    ws = torch.empty(n_ws or 1, dtype=_U8, device=device)
     _run(lib().qwm_paged8_select,
-         _SELECT8.pack(*qr, at, *step, *out, _status(status, dev), ws.data_ptr(), n_ws, T, bounds.shape[0], _DTYPES[dt], d, hq,
-                       hk, page_tokens, B, blocks, width, sink), "qwm_paged8_select", dev)
+         _SELECT8.pack(*qr, at, *step, *out, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages, _DTYPES[dt], d, hq, hk,
+                       page_tokens, B, blocks, min(width, _INT_MAX), min(sink, _INT_MAX)), "qwm_paged8_select", dev)
     return pages, lens
