@@ -52,11 +52,12 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A lane's channels of a row: 16 of every 64, so that four lanes load 64 neighbours
 template <int N>
 __device__ __forceinline__ void load_row(const float* p, float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const float4 u = load_global(reinterpret_cast<const float4*>(p) + i);
+    const float4 u = load_global(reinterpret_cast<const float4*>(p) + (i >> 2) * 16 + (i & 3));
     x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
   }
 }
@@ -64,7 +65,7 @@ template <int N>
 __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N / 8; ++i) {
-    const uint4 u = load_global(reinterpret_cast<const uint4*>(p) + i);
+    const uint4 u = load_global(reinterpret_cast<const uint4*>(p) + (i >> 1) * 8 + (i & 1));
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[8 * i + 2 * k] = __uint_as_float(w[k] << 16), x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
@@ -91,7 +92,7 @@ __device__ __forceinline__ float quantise_row(const qwm_paged8_select_args& a, c
   float x[C];
   const int64_t tok = r / group;
   if (r < rows) {
-    load_row(static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride + c * C, x);
+    load_row(static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride + 16 * c, x);
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i) x[i] = 0.f;
@@ -136,8 +137,8 @@ __device__ __forceinline__ float quantise_row(const qwm_paged8_select_args& a, c
   return r < rows ? u : __int_as_float(0x7fffffff);
 }
 
-// The bounds of 16 pages as a warp loads them: lane (g, c) has channels c d/4 ... of
-// pages g and g + 8.
+// The bounds of 16 pages as a warp loads them: lane (g, c) has channels 16 c ... and
+// 64 + 16 c ... of pages g and g + 8.
 template <int D>
 struct Tile {
   static constexpr int Q = D / 64;
@@ -152,8 +153,8 @@ struct Tile {
       const uint8_t* src = (const uint8_t*)a.bounds + ((int64_t)max(id[x], 0) * a.kv_heads + h) * (2 * D + 16);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        high[x][q] = load_global(reinterpret_cast<const uint4*>(src + c * (D / 4)) + q);
-        low[x][q] = load_global(reinterpret_cast<const uint4*>(src + D + c * (D / 4)) + q);
+        high[x][q] = load_global(reinterpret_cast<const uint4*>(src + 16 * c) + 4 * q);
+        low[x][q] = load_global(reinterpret_cast<const uint4*>(src + D + 16 * c) + 4 * q);
       }
       unit[x] = load_global(reinterpret_cast<const float*>(src + 2 * D));
       if (id[x] < 0) unit[x] = __int_as_float(0x7fffffff);
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
       const float x = quantise_row<D, T>(a, p, h, group, r0 + y + g, rows, w);
 #pragma unroll
       for (int i = 0; i < KS / 2; ++i) {
-        const int chunk = c * (KS / 2) + i;
+        const int chunk = (i >> 1) * 8 + 2 * c + (i & 1);
         *reinterpret_cast<uint4*>(sm + op_off(y + g, chunk)) = make_uint4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
         *reinterpret_cast<uint4*>(sm + op_off(y + g, D / 8 + chunk)) = make_uint4(w[2 * i].z, w[2 * i].w, w[2 * i + 1].z, w[2 * i + 1].w);
       }
