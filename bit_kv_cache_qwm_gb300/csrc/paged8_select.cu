@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
   __shared__ __align__(8) uint64_t done[2], drained;     // a tile complete, by its parity; nothing left in the pipe
   __shared__ __align__(16) float unit_row[kRowsTile];   // NaN: no such row
-  __shared__ float unit_page[2][kPagesTile];
+  __shared__ float unit_page[4][kPagesTile];            // by v mod 4: v + 1 is written while v - 1 is read
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int abort_sh, late_sh;
   __shared__ uint32_t nowhere;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   };
   auto convert = [&](int v) {
     const int w = warp & 7;
-    if (lane < 16) unit_page[v & 1][16 * w + lane] = unit;
+    if (lane < 16) unit_page[v & 3][16 * w + lane] = unit;
     uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   auto reduce = [&](int t, int v, int n, bool ok) {
     const int page = tid & 127, i0 = 64 * (warp >> 2);
     const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (v & 1);
-    const float2 up = make_float2(unit_page[v & 1][page], unit_page[v & 1][page]);
+    const float2 up = make_float2(unit_page[v & 3][page], unit_page[v & 3][page]);
     float best = -INFINITY;
 #pragma unroll 1
     for (int i = i0; i < min(n, i0 + 64); i += 32) {

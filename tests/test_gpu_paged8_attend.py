@@ -42,7 +42,7 @@ def check(paged, B, kernel, causal=True, window=0, table=None, lens=None, scale=
 
 
 SHAPES = [([0], [1]), ([63], [1]), ([500, 0, 33, 128], [1, 1, 1, 0]), ([1000], [2]), ([0, 70, 1], [4, 3, 1]), ([5, 900], [30, 7]),
-          ([0, 200], [129, 40]), ([300], [257])]
+          ([0, 200], [129, 40]), ([300], [257]), ([0, 0, 9], [0, 1, 0])]
 
 
 @pytest.mark.parametrize("kernel", KERNELS)

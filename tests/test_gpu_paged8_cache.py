@@ -38,7 +38,7 @@ def before(B):
 
 
 STEPS = [([0], [1]), ([5], [1]), ([15, 16, 17, 0], [1, 1, 1, 1]), ([0, 3, 100], [0, 45, 7]), ([31], [66]), ([0] * 5, [1, 2, 16, 17, 33]),
-         ([7, 40, 9], [9, 0, 24]), (list(range(40)), [1] * 40), ([1] * 70, [3, 0] * 35)]
+         ([7, 40, 9], [9, 0, 24]), ([0, 0, 5, 0], [0, 3, 0, 0]), (list(range(40)), [1] * 40), ([1] * 70, [3, 0] * 35)]
 
 
 @pytest.mark.parametrize("d,page,dtype", [(128, 16, "bf16"), (64, 32, "f32"), (128, 64, "f32"), (64, 256, "bf16"), (128, 128, "bf16")])
