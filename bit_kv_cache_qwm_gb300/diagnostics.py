@@ -12,9 +12,10 @@ encodings of the same keys and values: nearest-centroid assignment without
 compensation (the QVG-style baseline the pages compare with), QSAC without
 compensation, and QSAC with PSAC (rank r); `qwm_dequantize` gives their
 keys, values and coefficients in float32, and the comparisons against the
-unquantised keys and values run here in torch (float32).  The paged cache's
-INT4 quantiser (`qwm_paged_append`, no calibration) is measured next to them
-on the same keys, values and queries.  Measured per encoding:
+unquantised keys and values run here in torch (float32).  The paged caches'
+quantisers (INT4 `qwm_paged_append` and e4m3 `qwm_paged8_append`, no calibration)
+are measured next to them on the same keys, values and queries, and for the
+attention over selected pages the share of the softmax weight that they hold.  Measured per encoding:
   top1_change        fraction of (head, query) pairs whose argmax token differs
   logit_rel_error    RMS(q.k - l_quant) / RMS(q.k) over all (query, token) pairs
   key_rel_error      ||K - K_hat|| / ||K||  (Frobenius, all heads)
@@ -67,6 +68,36 @@ def measure_paged(K, V, q, sigma: float, page_tokens: int = 64) -> dict:
     paged.qwm_paged_append(K.float().transpose(0, 1), V.float().transpose(0, 1), pool, torch.arange(N, device=K.device),
                            k_hat=kh.transpose(0, 1), v_hat=vh.transpose(0, 1))
     return compare(K.float(), V.float(), q, sigma, kh, vh, q @ kh.transpose(1, 2))
+
+
+def measure_paged8(K, V, q, sigma: float, page_tokens: int = 64, widths=(16, 64)) -> dict:
+    """The same diagnostics of the paged 8-bit cache, read back from its pages, and
+    `weight_in_N_pages`: the mean share of a row's softmax weight in the N pages
+    that the selection names for that row alone, the last page and the first among
+    them."""
+    from . import paged
+    H, N, d = K.shape
+    M = q.shape[1]
+    n_pages = (N + page_tokens - 1) // page_tokens
+    pool = paged.paged8_pool(n_pages, H, d, page_tokens, device=K.device)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=K.device)  # noqa: E731
+    table = torch.arange(n_pages, dtype=torch.int32, device=K.device)[None]
+    step = table, i32([N]), i32([0, N])
+    paged.qwm_paged8_append(K.float().transpose(0, 1), V.float().transpose(0, 1), pool, *step)
+    kh, vh = (x.transpose(0, 1) for x in paged.qwm_paged8_read(pool, *step, N, d, dtype=torch.float32))
+    res = compare(K.float(), V.float(), q, sigma, kh, vh, q @ kh.transpose(1, 2))
+    bounds = paged.paged8_page_bounds(n_pages, H, d, device=K.device)
+    paged.qwm_paged8_bounds(pool, bounds, *step, max_new=N)
+    # every query as a request's last token
+    rows = q.float().transpose(0, 1).contiguous()
+    P = torch.softmax(sigma * (q @ kh.transpose(1, 2)), dim=-1)
+    P = torch.nn.functional.pad(P, (0, n_pages * page_tokens - N)).unflatten(-1, (n_pages, page_tokens)).sum(-1)
+    for width in widths:
+        pages, _ = paged.qwm_paged8_select(rows, bounds, table.expand(M, -1).contiguous(), i32([N] * M),
+                                           torch.arange(M + 1, dtype=torch.int32, device=K.device), page_tokens, width, sink=1)
+        held = torch.gather(P, 2, pages.transpose(0, 1).long().clamp(min=0)) * (pages.transpose(0, 1) >= 0)
+        res[f"weight_in_{width}_pages"] = float(held.sum(-1).mean())
+    return res
 
 
 def compare(K, V, q, sigma: float, kh, vh, Lq) -> dict:
@@ -123,6 +154,7 @@ def run(workload: str, heads=None, rows: int = 256, n_chunks=None, device=None) 
         out["encodings"][f"{assign}{'+psac' if psac else ''}"] = res
         ctx.close()
     out["paged_int4"] = measure_paged(K, V, q, 1.0 / np.sqrt(d))
+    out["paged_e4m3"] = measure_paged8(K, V, q, 1.0 / np.sqrt(d))
     return out
 
 

@@ -546,10 +546,13 @@ size_t qwm_paged_attend_workspace_bytes(int32_t head_dim);
 int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new);
 
 /* ------------------------------------------------------------------------
- * The paged 8-bit cache: the paged cache above with 8 bits a channel, for
- * layers or models that 4 bits disturb, and attention over selected pages for
- * streams too long to read at every step.  qwm_paged_plan, qwm_paged_release
- * and qwm_qk_norm_rope serve both; in every layer a step is then
+ * The paged 8-bit cache: the paged cache above with 8 bits a channel, and
+ * attention over selected pages for streams too long to read at every step.
+ * e4m3 is off by at most 2^-4 of each value where 4 bits are off by up to 1/30 of
+ * their group's range: a third of the error in values and in most keys; keys with
+ * a few channels far above the others keep the error of 4 bits in their products,
+ * since those groups have a zero point and e4m3 has not.  qwm_paged_plan,
+ * qwm_paged_release and qwm_qk_norm_rope serve both; in every layer a step is then
  *   qwm_paged8_append   quantisation of the new keys and values into pages;
  *   qwm_paged8_attend   attention of the new rows over their requests' pages;
  * or, where a step is to read only some of the pages,
@@ -624,10 +627,11 @@ typedef struct {
 qwm_status qwm_paged8_read(const qwm_paged8_read_args* a, void* stream);
 
 /* Attention of the rows of a step over their requests' pages, as
- * qwm_paged_attend: the same arguments, results, kernels (1 float32 on the CUDA
- * cores, 2 mma.sync for few rows, 3 tcgen05) and choice among them; what it says
- * of hidden tokens, rows that see nothing, NaN in q, large logits and waits
- * holds here too.
+ * qwm_paged_attend: the same arguments, results, kernels and choice among them;
+ * what it says of hidden tokens, rows that see nothing, NaN in q, large logits and
+ * waits holds here too.  One difference: float32 runs on kernel 2, with q and the
+ * weights as two float16 terms each (22 of 24 bits; keys and values are exact), and
+ * on kernel 1 where that is asked for.
  * table_heads: 1, or kv_heads for a table of its own for every key/value head,
  * block_table [requests][kv_heads][max_blocks], as qwm_paged8_select writes
  * them: each lists the pages that its head reads, and kv_len, positions and the
@@ -680,7 +684,9 @@ qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* stream);
  *   len_out[b]      tokens in them: kv_len[b] less those of the pages left out
  * A request without rows gets no pages and length 0.  So does one whose own
  * step's pages are more than `width`, which sets QWM_DEV_CAPACITY.  Page ids out of
- * range, and bounds that are NaN, come last.  max_new as in qwm_paged8_bounds. */
+ * range, and bounds that are NaN, come last.  When a bounded device wait runs out,
+ * which no input makes it do, QWM_DEV_TIMEOUT is set and the scored pages may be
+ * any of the request's. */
 typedef struct {
   qwm_rows q;                    /* [rows][heads][d] dtype                      */
   const void* bounds;            /* 16-byte aligned                             */

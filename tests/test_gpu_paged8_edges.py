@@ -244,3 +244,21 @@ def test_selections_do_not_depend_on_the_run(paged, cached, new, d):  # noqa: F8
                 noise = torch.tanh(noise @ noise)
         got, _ = paged.qwm_paged8_select(q, bnd, *step, 16, 30, sink=1)
         assert np.array_equal(host(got), want), i
+
+
+def test_diagnostics_of_the_8_bit_cache(paged):  # noqa: F811
+    """Errors of the read-back values against the oracle's encoding, and the weight
+    in the selected pages: all of it in all pages, a share of it in fewer."""
+    from bit_kv_cache_qwm_gb300 import diagnostics
+    r = np.random.default_rng(11)
+    H, N, d, page = 2, 333, 64, 32
+    K, V = (r.standard_normal((H, N, d)).astype(np.float32) for _ in range(2))
+    q = r.standard_normal((H, 5, d)).astype(np.float32)
+    got = diagnostics.measure_paged8(dev(K), dev(V), dev(q), d ** -0.5, page_tokens=page, widths=(3, 11))
+    _, kh, vh = P8.append(np.full((11, H, P8.block_bytes(d, page)), 255, np.uint8), K.transpose(1, 0, 2), V.transpose(1, 0, 2),
+                          np.arange(11)[None], [N], [0, N], page)
+    for key, a, b in (("key_rel_error", kh, K), ("value_rel_error", vh, V)):
+        b = b.transpose(1, 0, 2)
+        assert got[key] == pytest.approx(np.linalg.norm(a - b) / np.linalg.norm(b), rel=1e-4)
+    # three pages (the last holds 13 tokens) are 77 of 333 tokens: no even share is known beforehand
+    assert got["weight_in_11_pages"] == pytest.approx(1.0, abs=1e-5) and 0 < got["weight_in_3_pages"] < 1
