@@ -78,61 +78,75 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return s != s ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Row r of a request and head (a query head of a token; lanes 4 g .. 4 g + 3 share
-// one, d/4 channels each) as whole numbers: the MMA operands of x^+ and of x^-, and
-// the row's unit (NaN where there is no such row: no maximum takes it).
+// A query row as whole numbers (four lanes share a row, d/4 channels each; `src`: the
+// lane's first, nullptr for a row of zeros) and its unit.  A number y comes as the
+// float kWhole + y, whose low bits it is.
 // The definition divides once a channel.  Here a product with 1/unit, off by less
-// than 2^-15 (127 times 2^-22), gives the same whole number unless it comes within
-// 10^-4 of a tie, where the warp divides after all.
+// than 2 10^-5 (127 times 2^-23, and the quotient's own rounding), gives the same
+// whole number unless it comes within 3 10^-5 of a tie, where the warp divides after
+// all.  The largest quotient is 127 but for its rounding, so none passes 127.
+constexpr float kWhole = 12582912.f;   // 1.5 2^23: a sum with it is rounded to the nearest even
+
 template <int D, class T>
-__device__ __forceinline__ float quantise_row(const qwm_paged8_select_args& a, const Pages& p, int h, int group, int64_t r, int64_t rows,
-                                              uint4 (&w)[D / 16]) {
-  constexpr int C = D / 4, KS = D / 16;
-  const int c = threadIdx.x & 3;
+__device__ __forceinline__ float whole_row(const T* src, float2 (&v)[D / 8]) {
+  constexpr int C = D / 4;
   float x[C];
-  const int64_t tok = r / group;
-  if (r < rows) {
-    load_row(static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride + 16 * c, x);
+  if (src) {
+    load_row(src, x);
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i) x[i] = 0.f;
   }
-  uint32_t bits = 0;
+  float top = 0.f;
+  float2 sum = make_float2(0.f, 0.f);   // NaN where a channel is NaN or infinite
 #pragma unroll
-  for (int i = 0; i < C; ++i) bits = max(bits, __float_as_uint(x[i]) & 0x7fffffffu);
-  if (__any_sync(0xffffffffu, bits >= 0x7f800000u)) {   // NaN or infinite
-    bits = 0;
+  for (int i = 0; i < C; i += 2) {
+    top = fmaxf(fmaxf(top, fabsf(x[i])), fabsf(x[i + 1]));
+    sum = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(0.f, 0.f), sum);
+  }
+  if (__any_sync(0xffffffffu, !(sum.x + sum.y == 0.f))) {
+    top = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -3.402823466e38f), 3.402823466e38f) : 0.f;
-      bits = max(bits, __float_as_uint(x[i]) & 0x7fffffffu);
+      top = fmaxf(top, fabsf(x[i]));
     }
   }
-  float top = __uint_as_float(bits);
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const bool some = top >= 7.888609052e-31f;   // 2^-100
   const float u = some ? __fdiv_rn(top, 127.f) : 0.f, inv = some ? __frcp_rn(u) : 0.f;
-  const float round = 12582912.f;   // 1.5 2^23: adding it rounds to the nearest even
-  float far = 0.f, y[C];
+  float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const float q = x[i] * inv;
-    y[i] = __fsub_rn(__fadd_rn(q, round), round);
-    far = fmaxf(far, fabsf(q - y[i]));
+  for (int i = 0; i < C / 2; ++i) {
+    const float2 q = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(inv, inv));
+    v[i] = __fadd2_rn(q, make_float2(kWhole, kWhole));
+    const float2 d = __fadd2_rn(q, __fadd2_rn(make_float2(kWhole, kWhole), make_float2(-v[i].x, -v[i].y)));
+    far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
   }
-  if (__any_sync(0xffffffffu, far > 0.4999f)) {
+  if (__any_sync(0xffffffffu, far > 0.49997f)) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) y[i] = some ? rintf(__fdiv_rn(x[i], u)) : 0.f;
+    for (int i = 0; i < C; ++i) ((i & 1) ? v[i >> 1].y : v[i >> 1].x) = kWhole + (some ? rintf(__fdiv_rn(x[i], u)) : 0.f);
   }
+  return u;
+}
+
+// Row r of a request and head (a query head of a token) as MMA operands of x^+ and
+// of x^-, and the row's unit (NaN where there is no such row: no maximum takes it).
+template <int D, class T>
+__device__ __forceinline__ float row_operands(const qwm_paged8_select_args& a, const Pages& p, int h, int group, int64_t r, int64_t rows,
+                                              uint4 (&w)[D / 16]) {
+  const int64_t tok = r / group;
+  const T* src = static_cast<const T*>(a.q.ptr) + (p.row0 + tok) * a.q.row_stride + (h * group + r - tok * group) * a.q.head_stride +
+                 16 * (threadIdx.x & 3);
+  float2 v[D / 8];
+  const float u = whole_row<D, T>(r < rows ? src : nullptr, v);
   const __half2 zero = __float2half2_rn(0.f);
+  const float2 less = make_float2(-kWhole, -kWhole);
 #pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    __half2 v[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      v[k] = __floats2half2_rn(fminf(fmaxf(y[4 * i + 2 * k], -127.f), 127.f), fminf(fmaxf(y[4 * i + 2 * k + 1], -127.f), 127.f));
-    w[i] = make_uint4(h2u(__hmax2(v[0], zero)), h2u(__hmax2(v[1], zero)), h2u(__hmin2(v[0], zero)), h2u(__hmin2(v[1], zero)));
+  for (int i = 0; i < D / 16; ++i) {
+    const __half2 v0 = __float22half2_rn(__fadd2_rn(v[2 * i], less)), v1 = __float22half2_rn(__fadd2_rn(v[2 * i + 1], less));
+    w[i] = make_uint4(h2u(__hmax2(v0, zero)), h2u(__hmax2(v1, zero)), h2u(__hmin2(v0, zero)), h2u(__hmin2(v1, zero)));
   }
   return r < rows ? u : __int_as_float(0x7fffffff);
 }
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
     Tile<D> next;
     fetch(next, 0);
     uint4 w[KS];
-    const float u = quantise_row<D, T>(a, p, h, group, r0 + g, rows, w);
+    const float u = row_operands<D, T>(a, p, h, group, r0 + g, rows, w);
     const float u0 = __shfl_sync(0xffffffffu, u, 8 * c), u1 = __shfl_sync(0xffffffffu, u, 8 * c + 4);
     for (int i = 0; i < mine; ++i) {
       const Tile<D> t = next;
@@ -256,22 +270,56 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
 
 // ---- many rows: drafts, prompts and chunks
 //
-// The same products on the 5th-generation tensor cores: M = 128 pages (thread =
-// page = TMEM lane, so that a page's maximum over the rows stays in its thread),
-// N = up to 128 rows, K = 2 d.  A CTA keeps 128 rows of one request and head as an
-// operand and goes through the pages: while tile t is multiplied, warps 8-15 turn the
-// bounds of tile t + 1 into the other operand and warps 0-7 take the maxima of tile
-// t - 1 (four the first 64 rows, four the others) into the keys, by atomicMax, whose
-// order does not matter.
-// Bound by the tensor pipe (1.3K cycles a tile at d = 128) behind the 128 rows'
-// conversion.  On mma.sync, with the rows' operands shared by the eight warps of a
-// CTA, the chunk of 4,680 rows and 24 heads over 767 pages took 250 us.
-constexpr int kManyNt = 512, kRowsTile = 128, kPagesTile = 128;
+// First every row of q becomes whole numbers in int8 with its unit (and the keys are
+// cleared): a row is used by every tile of pages.
+constexpr int kRowsNt = 256;
+
+template <int D, class T>
+__global__ void __launch_bounds__(kRowsNt) paged8_rows_kernel(const qwm_paged8_select_args a, uint8_t* whole_rows, float* units,
+                                                              int64_t n_keys) {
+  wait_for_kernel_ahead();
+  const int64_t at = (int64_t)blockIdx.x * kRowsNt + threadIdx.x, rows = a.rows * a.heads;
+  for (int64_t i = at; i < n_keys; i += (int64_t)gridDim.x * kRowsNt) static_cast<uint32_t*>(a.workspace)[i] = 0;
+  const int64_t r = at >> 2, t = r >> 31 ? r / a.heads : (uint32_t)r / (uint32_t)a.heads;
+  const int c = threadIdx.x & 3;
+  if ((at & ~(int64_t)31) >= 4 * rows) return;
+  float2 v[D / 8];
+  const float u = whole_row<D, T>(r < rows ? static_cast<const T*>(a.q.ptr) + t * a.q.row_stride + (r - t * a.heads) * a.q.head_stride + 16 * c
+                                           : nullptr, v);
+  if (r >= rows) return;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = v[8 * i + 2 * k], y = v[8 * i + 2 * k + 1];
+      w[k] = __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                         __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
+    }
+    *reinterpret_cast<uint4*>(whole_rows + r * D + 64 * i + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (c == 0) units[r] = u;
+}
+
+// Then the products on the 5th-generation tensor cores: M = 128 pages (thread = page =
+// TMEM lane, so that a page's maximum over the rows stays in its thread), N = up to
+// 128 rows, K = 2 d.  A CTA keeps a tile of pages as the operand in TMEM and goes
+// through its rows: while one tile of rows is multiplied, warps 8-15 turn the next
+// one's bytes into the operand in shared memory, and warps 0-7 take the maxima of the
+// one before (four its first 64 rows, four the others) into the keys, by atomicMax,
+// whose order does not matter.
+// The chunk of 4,680 rows and 24 heads over 767 pages: 51 us, 1.3 a step, and 18 for
+// the rows' kernel.  Bound by the three parts' hand-over once a step (51 us without
+// the MMAs, half a microsecond of each step, are 44, without the maxima 40, without
+// the rows' conversion 44).  On mma.sync 250 us, with the pages streamed past a tile of
+// rows and both converted in the kernel 113.
+constexpr int kManyNt = 512, kTile = 128;
+constexpr uint32_t kColPages = 256;
 
 template <int D>
 struct Lay {
-  static constexpr int op = 128 * 2 * D * 2;   // 128 rows or pages of 2 d float16
-  static constexpr int bytes = 3 * op + 1024;  // the rows, two of pages, and room to align
+  static constexpr int op = kTile * 2 * D * 2;   // 128 rows of x^+ and x^- in float16
+  static constexpr int bytes = 2 * op + 1024;    // two, and room to align
 };
 
 // byte offset of 8 channels (chunk) of a row in an operand of SW128 atoms of 64 elements
@@ -279,24 +327,29 @@ __device__ __forceinline__ int op_off(int row, int chunk) {
   return (chunk >> 3) * 16384 + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-template <int D, class T>
-__global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm_paged8_select_args a, int shift, int64_t wait_cycles) {
+template <int D>
+__global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm_paged8_select_args a, int shift, const uint8_t* whole_rows,
+                                                                       const float* units, int page_parts, uint32_t group_mul,
+                                                                       uint32_t group_shift, int64_t wait_cycles) {
   using namespace tcx;
-  constexpr int KS = D / 16;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = sm_raw + ((1024 - (su32(sm_raw) & 1023)) & 1023);
-  __shared__ __align__(8) uint64_t done[2], drained;     // a tile complete, by its parity; nothing left in the pipe
-  __shared__ __align__(16) float unit_row[kRowsTile];   // NaN: no such row
-  __shared__ float unit_page[4][kPagesTile];            // by v mod 4: v + 1 is written while v - 1 is read
-  __shared__ uint32_t tmem_sh;
+  __shared__ __align__(8) uint64_t done[2], drained;       // a step complete, by its parity; nothing left in the pipe
+  // by step mod 4 and page tile mod 4: those of step s + 1 are written while s - 1 is read
+  __shared__ __align__(16) float unit_row[4][kTile];       // NaN: no such row
+  __shared__ float unit_page[4][kTile];
+  __shared__ uint32_t tmem_sh, nowhere;
   __shared__ volatile int abort_sh, late_sh;
-  __shared__ uint32_t nowhere;
   wait_for_kernel_ahead();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z, group = a.heads / a.kv_heads;
   const Pages p = load_pages(a, shift, b);
-  const int64_t rows = (int64_t)(p.n - p.first) * group;
-  if (p.first >= p.n || p.count <= a.width || p.tail == 0 || (int64_t)blockIdx.x * kRowsTile >= rows) return;
+  if (p.first >= p.n || p.count <= a.width) return;
+  // this CTA's tiles: pages p0, p0 + page_parts, ..., rows r0, r0 + row_parts, ...
+  const int rows = (p.n - p.first) * group, row_tiles = (rows + kTile - 1) / kTile, page_tiles = (p.tail + kTile - 1) / kTile;
+  const int row_parts = (int)gridDim.x / page_parts, p0 = (int)blockIdx.x % page_parts, r0 = (int)blockIdx.x / page_parts;
+  if (p0 >= page_tiles || r0 >= row_tiles) return;
+  const int nr = (row_tiles - r0 + row_parts - 1) / row_parts, np = (page_tiles - p0 + page_parts - 1) / page_parts, steps = nr * np;
   if (tid == 0) {
     abort_sh = late_sh = 0, nowhere = 0;
     bar_init(&done[0], 1);
@@ -305,7 +358,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(su32(&tmem_sh)));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&tmem_sh)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
@@ -313,131 +366,150 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   fence_after();
   const uint32_t tmem = tmem_sh;
   uint32_t* status = a.status ? a.status : &nowhere;
-  uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
-  const int tiles = (p.tail + kPagesTile - 1) / kPagesTile;
-  uint8_t* pages_at = sm + Lay<D>::op;
+  // both roles take the same steps and meet before them and at the end of each
+  auto meet = []() { asm volatile("bar.sync 1, %0;" ::"n"(kManyNt) : "memory"); };
+  auto complete = [&](int s) { return warp_all(bar_wait(&done[s & 1], (s >> 1) & 1, &abort_sh, status, wait_cycles)); };
 
-  // Tiles are counted on (v) over the rows' tiles: operands, accumulators and barriers
-  // go by the parity of that, barriers' phases by half of it.
-  // A tile's bounds, 16 pages a warp: a load takes 64 bytes of eight pages, and the
-  // eight lanes of a store phase have two pages, whose swizzles differ.  The pages'
-  // ids are loaded two tiles ahead, the bounds one.
-  uint4 raw[2][D / 32];
-  float unit = 0.f;
-  int id = 0, ahead = 0;   // the tile whose ids are on their way
-  auto look = [&]() {
-    id = page_id(a, b, ahead * kPagesTile + 16 * (warp & 7) + (lane & 15), p.tail);
-    if (++ahead == tiles) ahead = 0;   // the next rows' first tile
-  };
-  auto fetch = [&]() {
-    const int at = max(id, 0);
-    unit = load_global(reinterpret_cast<const float*>((const uint8_t*)a.bounds + ((int64_t)at * a.kv_heads + h) * (2 * D + 16) + 2 * D));
-    if (id < 0) unit = __int_as_float(0x7fffffff);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint8_t* src = (const uint8_t*)a.bounds +
-                           ((int64_t)__shfl_sync(0xffffffffu, at, 8 * k + g) * a.kv_heads + h) * (2 * D + 16) + 16 * c;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) raw[k][i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
-    }
-    look();
-  };
-  auto convert = [&](int v) {
-    const int w = warp & 7;
-    if (lane < 16) unit_page[v & 3][16 * w + lane] = unit;
-    uint8_t* to = pages_at + (v & 1) * Lay<D>::op;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = raw[k][i];
-        uint32_t f[8];
-        whole(u.x, &f[0], &f[1]);
-        whole(u.y, &f[2], &f[3]);
-        whole(u.z, &f[4], &f[5]);
-        whole(u.w, &f[6], &f[7]);
-        const int row = 16 * w + 8 * k + g, chunk = 2 * (c + 4 * i);
-        *reinterpret_cast<uint4*>(to + op_off(row, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<uint4*>(to + op_off(row, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
-      }
-    fence_async_smem();
-    fetch();
-  };
   if (warp >= 8) {
-    look();
+    // ---- the operands.  Rows: 16 a warp; a load takes 64 bytes of eight rows, and the
+    // eight lanes of a store phase have two rows, whose swizzles differ.
+    const int w = warp - 8;
+    uint4 raw[2][D / 64];
+    float unit = 0.f;
+    int ri = 0;             // the row tile on its way
+    auto fetch = [&]() {
+      const int base = (r0 + ri * row_parts) * kTile + 16 * w;
+      auto at = [&](int r) {   // of a row of the request and head, in the caller's order
+        const int tok = (int)(((uint64_t)(uint32_t)r * group_mul) >> group_shift);
+        return (int64_t)(p.row0 + tok) * a.heads + h * group + r - tok * group;
+      };
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = base + 8 * k + g;
+        const uint8_t* src = whole_rows + at(min(r, rows - 1)) * D + 16 * c;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) raw[k][i] = load_global(reinterpret_cast<const uint4*>(src + 64 * i));
+      }
+      const int r = base + (lane & 15);
+      unit = load_global(units + at(min(r, rows - 1)));
+      if (r >= rows) unit = __int_as_float(0x7fffffff);
+      if (++ri == nr) ri = 0;
+    };
+    auto expand = [&](int s) {
+      if (lane < 16) unit_row[s & 3][16 * w + lane] = unit;
+      uint8_t* to = sm + (s & 1) * Lay<D>::op;
+      const __half2 zero = __float2half2_rn(0.f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const uint32_t u[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
+          const int row = 16 * w + 8 * k + g;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t f[4];
+            whole(u[2 * e], &f[0], &f[1]);
+            whole(u[2 * e + 1], &f[2], &f[3]);
+            const int chunk = 2 * (c + 4 * i) + e;
+            *reinterpret_cast<uint4*>(to + op_off(row, chunk)) = make_uint4(h2u(__hmax2(u2h(f[0]), zero)), h2u(__hmax2(u2h(f[1]), zero)),
+                                                                            h2u(__hmax2(u2h(f[2]), zero)), h2u(__hmax2(u2h(f[3]), zero)));
+            *reinterpret_cast<uint4*>(to + op_off(row, D / 8 + chunk)) = make_uint4(h2u(__hmin2(u2h(f[0]), zero)), h2u(__hmin2(u2h(f[1]), zero)),
+                                                                                    h2u(__hmin2(u2h(f[2]), zero)), h2u(__hmin2(u2h(f[3]), zero)));
+          }
+        }
+      fence_async_smem();
+      fetch();
+    };
+    // Pages: warps 8-11, a thread a page = a TMEM lane, 64 bounds at a time
+    auto pages = [&](int pi) {
+      if (w < 4) {
+        const int page = 32 * w + lane, id = page_id(a, b, (p0 + pi * page_parts) * kTile + page, p.tail);
+        const uint8_t* src = (const uint8_t*)a.bounds + ((int64_t)max(id, 0) * a.kv_heads + h) * (2 * D + 16);
+        const uint32_t to = tmem + ((uint32_t)(32 * w) << 16) + kColPages;
+        __syncwarp();   // the stores below are the warp's
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t f[32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 u = load_global(reinterpret_cast<const uint4*>(src + 64 * i) + q);
+            whole(u.x, &f[8 * q], &f[8 * q + 1]);
+            whole(u.y, &f[8 * q + 2], &f[8 * q + 3]);
+            whole(u.z, &f[8 * q + 4], &f[8 * q + 5]);
+            whole(u.w, &f[8 * q + 6], &f[8 * q + 7]);
+          }
+          tmem_st32(to + 32 * i, f);
+        }
+        unit_page[pi & 3][page] = id < 0 ? __int_as_float(0x7fffffff) : load_global(reinterpret_cast<const float*>(src + 2 * D));
+        tmem_wait_st();
+        fence_before();
+      }
+    };
     fetch();
-  }
-  // the largest score of each page of tile t over half of the rows
-  auto reduce = [&](int t, int v, int n, bool ok) {
-    const int page = tid & 127, i0 = 64 * (warp >> 2);
-    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (v & 1);
-    const float2 up = make_float2(unit_page[v & 3][page], unit_page[v & 3][page]);
-    float best = -INFINITY;
-#pragma unroll 1
-    for (int i = i0; i < min(n, i0 + 64); i += 32) {
-      uint32_t s[32];
-      tmem_ld32(at + i, s);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        const float4 u = *reinterpret_cast<const float4*>(&unit_row[i + k]);
-        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), up), make_float2(u.x, u.y));
-        const float2 y = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), up), make_float2(u.z, u.w));
-        best = max3f(max3f(best, x.x, x.y), y.x, y.y);
+    pages(0);
+    expand(0);
+    meet();
+    for (int s = 0, pi = 0, left = nr; s <= steps; ++s) {
+      if (s > 0) complete(s - 1);
+      if (s + 1 < steps) {
+        if (--left == 0) {   // the next step is the next page tile's first
+          left = nr;
+          complete(s);       // reads this one's operand
+          fence_after();
+          pages(++pi);
+        }
+        expand(s + 1);
       }
+      meet();
     }
-    const int j = t * kPagesTile + page;
-    if (ok && j < p.tail && i0 < n) atomicMax(keys + j, key_of(best));
-    fence_before();
-  };
-
-  int v0 = 0;   // tiles of the rows before
-  for (int64_t r0 = (int64_t)blockIdx.x * kRowsTile; r0 < rows; r0 += (int64_t)gridDim.x * kRowsTile, v0 += tiles) {
-    const int n = (int)min((rows - r0 + 31) & ~(int64_t)31, (int64_t)kRowsTile);
-#pragma unroll 1
-    for (int y = 8 * warp; y < n; y += 8 * (kManyNt / 32)) {
-      uint4 w[KS];
-      const float x = quantise_row<D, T>(a, p, h, group, r0 + y + g, rows, w);
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
-        const int chunk = (i >> 1) * 8 + 2 * c + (i & 1);
-        *reinterpret_cast<uint4*>(sm + op_off(y + g, chunk)) = make_uint4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
-        *reinterpret_cast<uint4*>(sm + op_off(y + g, D / 8 + chunk)) = make_uint4(w[2 * i].z, w[2 * i].w, w[2 * i + 1].z, w[2 * i + 1].w);
-      }
-      if (c == 0) unit_row[y + g] = x;
-    }
-    fence_async_smem();
-    if (warp >= 8) convert(v0);
-    __syncthreads();
+  } else {
+    // ---- products and maxima
+    uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
+    const int page = tid & (kTile - 1), i0 = 64 * (warp >> 2);
+    // rows of the operand of row tile i, in 32s
+    auto width = [&](int i) { return min((rows - (r0 + i * row_parts) * kTile + 31) & ~31, kTile); };
+    meet();
     fence_after();
-    for (int t = 0; t <= tiles; ++t) {
-      const int v = v0 + t;
-      if (t < tiles && warp == 0) {
+    for (int s = 0, ri = 0, pi = 0, before = 0, pi_before = 0; s <= steps; ++s) {
+      if (s < steps && warp == 0) {
         const bool go = !__any_sync(0xffffffffu, abort_sh != 0);
         if (go && elect_one()) {
-          const uint32_t idesc = (1u << 4) | ((uint32_t)(n / 8) << 17) | (8u << 24);
-          const uint32_t pa = su32(pages_at + (v & 1) * Lay<D>::op), ra = su32(sm);
+          const uint32_t idesc = (1u << 4) | ((uint32_t)(width(ri) / 8) << 17) | (8u << 24);
+          const uint32_t ra = su32(sm + (s & 1) * Lay<D>::op);
 #pragma unroll
-          for (int k = 0; k < 2 * D / 16; ++k) {
-            const uint32_t ko = (k >> 2) * 16384 + (k & 3) * 32;
-            mma_ss(tmem + 128u * (v & 1), desc_sw128(pa + ko), desc_sw128(ra + ko), idesc, k > 0);
-          }
-          commit(&done[v & 1]);
+          for (int k = 0; k < 2 * D / 16; ++k)
+            mma_ts(tmem + 128u * (s & 1), tmem + kColPages + 8 * k, desc_sw128(ra + (k >> 2) * 16384 + (k & 3) * 32), idesc, k > 0);
+          commit(&done[s & 1]);
         }
         __syncwarp();
       }
-      // tile t - 1 complete: its products are there, its operand is free
-      bool ok = true;
-      if (t > 0) {
-        ok = warp_all(bar_wait(&done[(v - 1) & 1], ((v - 1) >> 1) & 1, &abort_sh, status, wait_cycles));
+      if (s > 0) {
+        // the largest score of each page over half of the rows of step s - 1
+        const bool ok = complete(s - 1);
         fence_after();
+        const int v = s - 1, n = min(width(before), i0 + 64), j = (p0 + pi_before * page_parts) * kTile + page;
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (v & 1);
+        const float2 up = make_float2(unit_page[pi_before & 3][page], unit_page[pi_before & 3][page]);
+        float best = -INFINITY;
+#pragma unroll 1
+        for (int i = i0; i < n; i += 32) {
+          uint32_t x[32];
+          tmem_ld32(at + i, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(&unit_row[v & 3][i + k]);
+            const float2 y = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), up), make_float2(r.x, r.y));
+            const float2 z = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), up), make_float2(r.z, r.w));
+            best = max3f(max3f(best, y.x, y.y), z.x, z.y);
+          }
+        }
+        if (ok && j < p.tail && i0 < n) atomicMax(keys + j, key_of(best));
+        fence_before();
       }
-      if (warp >= 8) {
-        if (t + 1 < tiles) convert(v + 1);
-      } else if (t > 0) {
-        reduce(t - 1, v - 1, n, ok);
-      }
-      __syncthreads();
+      before = ri, pi_before = pi;
+      if (++ri == nr) ri = 0, ++pi;
+      meet();
       fence_after();
     }
   }
@@ -450,22 +522,28 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D, class T>
-cudaError_t launch_many(const qwm_paged8_select_args& a, int shift, dim3 grid, cudaStream_t st) {
+template <int D>
+cudaError_t launch_many(const qwm_paged8_select_args& a, int shift, const uint8_t* whole_rows, const float* units, cudaStream_t st) {
   static SmemLimit limit;
+  const int64_t pairs = (int64_t)a.requests * a.kv_heads, want = (sm_count() + pairs - 1) / pairs;   // CTAs for each
+  const int64_t pages = ((int64_t)a.max_blocks + kTile - 1) / kTile, parts = want < pages ? want : pages;
+  // of rows only where the pages are too few, by the rows of an average request
+  const int64_t rows = (a.rows * (a.heads / a.kv_heads) / a.requests + kTile - 1) / kTile, more = (want + parts - 1) / parts;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3((unsigned)(parts * (more < rows ? more : rows < 1 ? 1 : rows)), (unsigned)a.kv_heads, (unsigned)a.requests);
   cfg.blockDim = dim3(kManyNt, 1, 1);
   cfg.dynamicSmemBytes = Lay<D>::bytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {early_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launched(launch_smem(limit, cfg.dynamicSmemBytes, paged8_score_many_kernel<D, T>, cfg, a, shift,
-                              injected_wait_cycles(tcx::kWaitCycles)));
+  uint32_t mul, by;
+  fast_division(a.heads / a.kv_heads, &mul, &by);
+  return launched(launch_smem(limit, cfg.dynamicSmemBytes, paged8_score_many_kernel<D>, cfg, a, shift, whole_rows, units, (int)parts, mul,
+                              by, injected_wait_cycles(tcx::kWaitCycles)));
 }
 
 // ---- the choice
@@ -662,14 +740,15 @@ cudaError_t launch_select8(const qwm_paged8_select_args& a, int shift, cudaStrea
                        : (bf ? paged8_score_few_kernel<64, __nv_bfloat16> : paged8_score_few_kernel<64, float>);
       e = launch_early(kern, g, kFewNt, 0, st, a, shift, tiles);
     } else {
-      e = cudaMemsetAsync(a.workspace, 0, (size_t)pairs * a.max_blocks * 4, st);
-      if (e != cudaSuccess) return launched(e);
-      // a CTA for every 128 rows of a request of average length, up to eight an SM
-      const int64_t each = (a.rows * (a.heads / a.kv_heads) / a.requests + kRowsTile - 1) / kRowsTile, most = (8 * sms + pairs - 1) / pairs;
-      dim3 g = grid;
-      g.x = (unsigned)(each < 1 ? 1 : each < most ? each : most);
-      e = wide ? (bf ? launch_many<128, __nv_bfloat16>(a, shift, g, st) : launch_many<128, float>(a, shift, g, st))
-               : (bf ? launch_many<64, __nv_bfloat16>(a, shift, g, st) : launch_many<64, float>(a, shift, g, st));
+      // behind the keys: the rows' units, then the rows
+      float* units = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + select8_keys(a.requests, a.kv_heads, a.max_blocks));
+      uint8_t* rows = reinterpret_cast<uint8_t*>(units) + select8_units(a.rows, a.heads);
+      auto kern = wide ? (bf ? paged8_rows_kernel<128, __nv_bfloat16> : paged8_rows_kernel<128, float>)
+                       : (bf ? paged8_rows_kernel<64, __nv_bfloat16> : paged8_rows_kernel<64, float>);
+      const int64_t ctas = (4 * a.rows * a.heads + kRowsNt - 1) / kRowsNt;
+      e = launch_early(kern, dim3((unsigned)ctas, 1, 1), kRowsNt, 0, st, a, rows, units, pairs * a.max_blocks);
+      if (e != cudaSuccess) return e;
+      e = wide ? launch_many<128>(a, shift, rows, units, st) : launch_many<64>(a, shift, rows, units, st);
     }
     if (e != cudaSuccess) return e;
   }

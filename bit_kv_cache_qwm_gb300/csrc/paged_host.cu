@@ -323,8 +323,10 @@ extern "C" qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* s
   return cuda_status(launch_bounds8(*a, page_shift(a->page_tokens), S(stream)));
 }
 
-extern "C" size_t qwm_paged8_select_workspace_bytes(int32_t requests, int32_t kv_heads, int32_t max_blocks) {
-  return requests < 1 || kv_heads < 1 || max_blocks < 1 ? 0 : (size_t)requests * kv_heads * max_blocks * 4;
+extern "C" size_t qwm_paged8_select_workspace_bytes(int64_t rows, int32_t heads, int32_t head_dim, int32_t requests, int32_t kv_heads,
+                                                    int32_t max_blocks) {
+  if (rows < 0 || rows > kInt || heads < 1 || !dim_ok(head_dim) || requests < 0 || kv_heads < 1 || max_blocks < 1) return 0;
+  return select8_keys(requests, kv_heads, max_blocks) + select8_units(rows, heads) + (size_t)(rows * heads) * head_dim;
 }
 
 extern "C" qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* stream) {
@@ -334,11 +336,13 @@ extern "C" qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* s
   const qwm_status s = step_status(*a);
   if (s == QWM_ERR_INVALID_ARG || a->heads % a->kv_heads) return QWM_ERR_INVALID_ARG;
   if (s != QWM_OK || a->requests == 0) return s;
-  if (a->kv_heads > 65535 || a->rows * (a->heads / a->kv_heads) > kHalf) return QWM_ERR_UNSUPPORTED;
+  if (a->kv_heads > 65535 || a->rows * (a->heads / a->kv_heads) > kHalf || a->rows * a->heads > (int64_t)1 << 36)
+    return QWM_ERR_UNSUPPORTED;
   if ((a->rows > 0 && !rows_ok(a->q, a->rows, a->heads, a->head_dim, esize(a->dtype), false)) || !a->bounds ||
       !aligned(a->bounds, 16) || !a->pages || !a->len_out || a->len_out == a->kv_len || !words(a->pages, a->len_out) ||
       !a->workspace || !aligned(a->workspace, 256) ||
-      a->workspace_bytes < qwm_paged8_select_workspace_bytes(a->requests, a->kv_heads, a->max_blocks) || !step_pointers_ok(*a))
+      a->workspace_bytes < qwm_paged8_select_workspace_bytes(a->rows, a->heads, a->head_dim, a->requests, a->kv_heads, a->max_blocks) ||
+      !step_pointers_ok(*a))
     return QWM_ERR_INVALID_ARG;
   if (fault_injected("launch")) return QWM_ERR_CUDA;
   NvtxRange range("qwm_paged8_select");

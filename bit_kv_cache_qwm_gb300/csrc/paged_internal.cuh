@@ -20,6 +20,10 @@ constexpr int kScaleSlots = 16, kScaleLow = -15, kScaleHigh = 7;
 constexpr float kClamp8 = 57344.f;   // 448 2^kScaleHigh
 inline __host__ __device__ int block8_bytes(int d, int page) { return 2 * page * d + (page >= 64 ? page / 4 : 16); }
 
+// A selection's workspace: keys of all pages, and of many rows their units and bytes.
+inline size_t select8_keys(int64_t requests, int64_t kv_heads, int64_t max_blocks) { return ((size_t)(requests * kv_heads * max_blocks) * 4 + 255) & ~(size_t)255; }
+inline size_t select8_units(int64_t rows, int64_t heads) { return ((size_t)(rows * heads) * 4 + 255) & ~(size_t)255; }
+
 // two e4m3 codes (the lower or the upper half of x) as float16, exact; 64 a clock
 // and SM, a third of the instructions of moving the bits into place
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {

@@ -131,7 +131,7 @@ def lib() -> ctypes.CDLL:
     L.qwm_paged8_attend_workspace_bytes.restype = ctypes.c_size_t
     L.qwm_paged8_attend_workspace_bytes.argtypes = [I32]
     L.qwm_paged8_select_workspace_bytes.restype = ctypes.c_size_t
-    L.qwm_paged8_select_workspace_bytes.argtypes = [I32, I32, I32]
+    L.qwm_paged8_select_workspace_bytes.argtypes = [I64, I32, I32, I32, I32, I32]
     L.qwm_paged_attend_kernel_for.restype = I32
     L.qwm_paged_attend_kernel_for.argtypes = [I32, I32, I32, I64]
     L.qwm_attend_kernel_for.restype = I32

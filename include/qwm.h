@@ -705,8 +705,9 @@ typedef struct {
 } qwm_paged8_select_args;
 qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* stream);
 
-/* Bytes of workspace of a selection over this many requests, heads and pages. */
-size_t qwm_paged8_select_workspace_bytes(int32_t requests, int32_t kv_heads, int32_t max_blocks);
+/* Bytes of workspace of a selection of these sizes (0 for sizes out of range). */
+size_t qwm_paged8_select_workspace_bytes(int64_t rows, int32_t heads, int32_t head_dim, int32_t requests, int32_t kv_heads,
+                                         int32_t max_blocks);
 
 #ifdef __cplusplus
 }

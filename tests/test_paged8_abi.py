@@ -112,14 +112,17 @@ def test_bounds_refusals(paged, kw, status):
     ({}, 6), (dict(rows=0), 6), (dict(rows=-1), 1), (dict(rows=1 << 31), 1), (dict(rows=1 << 30, heads=4), 2), (dict(dtype=2), 1),
     (dict(q=(0, 256, 128)), 1), (dict(q=(FAKE + 2, 256, 128)), 1), (dict(q=(FAKE, 257, 128)), 1), (dict(bounds=0), 1),
     (dict(bounds=FAKE + 8), 1), (dict(pages=0), 1), (dict(pages=FAKE + 1), 1), (dict(out=0), 1), (dict(out=FAKE), 1),
-    (dict(out=FAKE + 2), 1), (dict(ws=0), 1), (dict(ws=FAKE + 16), 1), (dict(ws_bytes=95), 1), (dict(ws_bytes=96), 6),
+    (dict(out=FAKE + 2), 1), (dict(ws=0), 1), (dict(ws=FAKE + 16), 1), (dict(ws_bytes=256 + 256 + 1023), 1), (dict(ws_bytes=256 + 256 + 1024), 6),
     (dict(heads=5), 1), (dict(heads=0), 1), (dict(width=0), 1), (dict(sink=-1), 1), (dict(sink=1 << 30, width=1 << 30), 6)])
 def test_select_refusals(paged, kw, status):
     a = dict(q=(FAKE, 256, 128), bounds=FAKE, table=FAKE, lens=FAKE, cu=FAKE, pages=FAKE, out=2 * FAKE, status=0, ws=FAKE,
              ws_bytes=1 << 40, rows=4, n_pages=3, dtype=1, d=128, heads=2, hk=2, page=16, requests=3, max_blocks=4, width=2, sink=0)
     a.update(kw)
     assert paged.lib().qwm_paged8_select(paged._SELECT8.pack(*a["q"], *list(a.values())[1:]), None) == status
-    assert paged.lib().qwm_paged8_select_workspace_bytes(3, 2, 4) == 96
+    # keys, the rows' units, the rows
+    f = paged.lib().qwm_paged8_select_workspace_bytes
+    assert f(4, 2, 128, 3, 2, 4) == 256 + 256 + 1024 and f(0, 5, 64, 10, 5, 1000) == 200192
+    assert f(-1, 2, 128, 3, 2, 4) == f(4, 0, 128, 3, 2, 4) == f(4, 2, 96, 3, 2, 4) == f(4, 2, 128, 3, 0, 4) == f(4, 2, 128, 3, 2, 0) == 0
 
 
 def attend_args(paged, **kw):
@@ -146,7 +149,7 @@ def test_null_arguments(paged):
     L = paged.lib()
     for fn in (L.qwm_paged8_append, L.qwm_paged8_read, L.qwm_paged8_attend, L.qwm_paged8_bounds, L.qwm_paged8_select):
         assert fn(None, None) == 1
-    assert L.qwm_paged8_attend_workspace_bytes(96) == 0 and L.qwm_paged8_select_workspace_bytes(0, 1, 1) == 0
+    assert L.qwm_paged8_attend_workspace_bytes(96) == 0 and L.qwm_paged8_select_workspace_bytes(1, 1, 64, 0, 1, 1) == 256 + 64
 
 
 def test_the_binding_refuses_host_tensors_and_wrong_shapes(paged):
