@@ -15,6 +15,7 @@ struct Steps {
   uint32_t* status;
   int64_t rows;        // of the caller's tensors; -1: there are none
   int32_t n_pages, requests, max_blocks, shift;
+  bool by_row;         // units are rows
 };
 
 // Request b: its rows row0 ... are the tokens first ... n - 1.
@@ -46,14 +47,18 @@ __device__ __forceinline__ Step load_step(const Steps& s, int b) {
 
 // Work is dealt out by blocks of 16 slots: request b takes the units from
 // cu[b] / 16 + 2 b up to the next one's, no fewer than the blocks that its rows
-// can lie in.  The request of a unit, found by a whole warp, 32 guesses at a
-// time, whatever the values in cu.
+// can lie in; or, where that makes fewer (single tokens), a unit is a row and the
+// first row in a block has it.  The request of a unit, found by a whole warp, 32
+// guesses at a time, whatever the values in cu.
 __device__ __forceinline__ int unit_of(const Steps& s, int b) {
-  const int most = (int)s.rows;
-  return min(max(load_cu(s, b), 0), most) / kScaleSlots + 2 * b;
+  const int most = (int)s.rows, row = min(max(load_cu(s, b), 0), most);
+  return s.by_row ? row : row / kScaleSlots + 2 * b;
 }
 __device__ __forceinline__ int find_request(const Steps& s, int unit) {
   const int lane = threadIdx.x & 31;
+  // a token for every request: 8,192 appends 86 us, 143 with blocks as units and the
+  // search
+  if (s.by_row && unit < s.requests && load_cu(s, unit) == unit && load_cu(s, unit + 1) > unit) return unit;
   int lo = 0, span = s.requests;
   while (span > 1) {
     const int step = (span + 31) / 32, at = lane * step;
@@ -78,8 +83,15 @@ __device__ __forceinline__ Block find_block(const Steps& s, int unit) {
   Block x;
   const int b = find_request(s, unit);
   x.s = load_step(s, b);
-  const int64_t n0 = ((int64_t)(x.s.first >> 4) + unit - unit_of(s, b)) * kScaleSlots;
-  x.any = n0 < x.s.n && x.s.first < x.s.n;
+  int64_t n0;
+  if (s.by_row) {
+    const int64_t n = (int64_t)x.s.first + unit - x.s.row0;   // the row's token
+    n0 = n & ~(int64_t)(kScaleSlots - 1);
+    x.any = n >= x.s.first && n < x.s.n && (n == n0 || n == x.s.first);
+  } else {
+    n0 = ((int64_t)(x.s.first >> 4) + unit - unit_of(s, b)) * kScaleSlots;
+    x.any = n0 < x.s.n && x.s.first < x.s.n;
+  }
   x.n0 = x.any ? (int)n0 : 0;
   x.lo = max(x.s.first - x.n0, 0), x.hi = min(x.s.n - x.n0, kScaleSlots);
   x.at = x.n0 & ((1 << s.shift) - 1);
@@ -88,10 +100,11 @@ __device__ __forceinline__ Block find_block(const Steps& s, int unit) {
   x.known = x.page >= 0 && x.page < s.n_pages;
   return x;
 }
-// what the calls report of the requests, by the threads of one CTA
+// what the calls report of the requests
 __device__ __forceinline__ void check_requests(const Steps& s) {
-  for (int b = threadIdx.x; b < s.requests; b += blockDim.x)
-    if (!load_step(s, b).good) flag(s.status, QWM_DEV_BOUNDS);
+  if (blockIdx.y) return;
+  for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < s.requests; b += (int64_t)gridDim.x * blockDim.x)
+    if (!load_step(s, (int)b).good) flag(s.status, QWM_DEV_BOUNDS);
 }
 
 constexpr int kNt = 256, kWarps = kNt / 32;
@@ -188,14 +201,14 @@ __device__ __forceinline__ Raw<T> decode8(uint2 code, __half2 scale) {
 // and the codes go out as the rows came in.  Where the block holds earlier tokens
 // and the scale grows, their codes are moved first.
 // Bound by HBM (2 or 4 bytes a channel in, 1 out, 2 or 4 more for x_hat) in a
-// chunk, by the chain of loads (rows' request, page, scale) in a step of single
-// tokens.
+// chunk: 4,680 rows of 24 heads, d = 128, bf16 with x_hat, 24.8 us (5.8 TB/s); by the
+// chain of loads (lengths, page, rows and scale) in a step of single tokens: 4.0 us.
 template <int D, class T>
 __global__ void __launch_bounds__(kNt) paged8_append_kernel(const qwm_paged8_append_args a, const Steps s) {
   constexpr int L = D / 8, RS = 32 / L, NP = kScaleSlots / RS;
   wait_for_kernel_ahead();
   const int lane = threadIdx.x & 31, job = blockIdx.y * kWarps + (threadIdx.x >> 5), h = job >> 1, half = job & 1;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_requests(s);
+  check_requests(s);
   if (h >= a.kv_heads) return;
   const Block b = find_block(s, blockIdx.x);
   if (!b.any) return;
@@ -285,13 +298,14 @@ __global__ void __launch_bounds__(kNt) paged8_append_kernel(const qwm_paged8_app
 }
 
 // The same walk the other way: a warp reads the block of 16 slots of one head, of
-// K or of V.  Bound by HBM (1 byte a channel in, 2 or 4 out).
+// K or of V.  Bound by HBM (1 byte a channel in, 2 or 4 out): 98,280 tokens of 8
+// heads, d = 128, to bf16 91 us (6.6 TB/s).
 template <int D, class T>
 __global__ void __launch_bounds__(kNt) paged8_read_kernel(const qwm_paged8_read_args a, const Steps s) {
   constexpr int L = D / 8, RS = 32 / L, NP = kScaleSlots / RS;
   wait_for_kernel_ahead();
   const int lane = threadIdx.x & 31, job = blockIdx.y * kWarps + (threadIdx.x >> 5), h = job >> 1, half = job & 1;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_requests(s);
+  check_requests(s);
   if (h >= a.kv_heads) return;
   const Block b = find_block(s, blockIdx.x);
   if (!b.any) return;
@@ -315,8 +329,10 @@ __global__ void __launch_bounds__(kNt) paged8_read_kernel(const qwm_paged8_read_
 }
 
 // A CTA takes a page and a head: a warp its blocks of 16 slots in turn, a lane 16
-// channels of every second (d = 64: fourth) row; maxima and minima in float16,
-// exact.  Bound by the chain of loads; the keys of a step's pages are few.
+// channels of every fourth (d = 64: eighth) row; maxima and minima in float16,
+// exact.  Bound by the chain of loads; the keys of a step's pages are few: 3 us for 48
+// single tokens, 7 for the 38 pages of a chunk.  (A warp a page and head where pages
+// have up to 64 tokens takes 5 for the single tokens: 16 divisions a lane.)
 constexpr int kBoundsNt = 128;
 
 template <int D>
@@ -400,12 +416,14 @@ __global__ void __launch_bounds__(kBoundsNt) paged8_bounds_kernel(const qwm_page
 
 template <class A>
 Steps steps_of(const A& a, int64_t rows, int shift) {
-  return Steps{a.block_table, a.kv_len, a.cu_rows, a.status, rows, (int32_t)a.n_pages, a.requests, a.max_blocks, shift};
+  return Steps{a.block_table, a.kv_len, a.cu_rows, a.status, rows, (int32_t)a.n_pages, a.requests, a.max_blocks, shift,
+               rows >= 0 && rows <= rows / kScaleSlots + 2 * (int64_t)a.requests};
 }
 
 template <class A>
 dim3 unit_grid(const A& a) {
-  return dim3((unsigned)(a.rows / kScaleSlots + 2 * (int64_t)a.requests), (unsigned)((2 * a.kv_heads + kWarps - 1) / kWarps), 1);
+  const int64_t blocks = a.rows / kScaleSlots + 2 * (int64_t)a.requests;
+  return dim3((unsigned)(a.rows < blocks ? a.rows : blocks), (unsigned)((2 * a.kv_heads + kWarps - 1) / kWarps), 1);
 }
 
 }  // namespace

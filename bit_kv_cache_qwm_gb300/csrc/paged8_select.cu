@@ -206,8 +206,9 @@ __device__ __forceinline__ void take(float* best, const float* s, const float* t
 //
 // A warp has 8 rows in its registers and goes through tiles of 16 pages, the next
 // tile's bounds on their way; their ids come first, together.  More rows take
-// another walk each 8.  Bound by latency (rows, ids, bounds) where a warp has one
-// or two tiles, else by the bounds' way from HBM.
+// another walk each 8.  Bound by latency (lengths, ids, bounds, each waits for the one
+// before, and the rows' conversion): 48 requests of 515 pages on average 17 to 20 us,
+// one of 5,850 pages 10.
 constexpr int kFewNt = 128, kFewWarps = kFewNt / 32, kMostTiles = 8;
 
 template <int D, class T>
@@ -552,8 +553,8 @@ cudaError_t launch_many(const qwm_paged8_select_args& a, int shift, const uint8_
 // counted from the highest bit in which the keys differ, so that a digit's counts
 // spread); once no more than kFew are left in question, a thread each counts those
 // ahead of its own instead.  Then every thread writes those of its range of pages.
-// Keys stay in registers where E a thread are enough, else they are read again for
-// every step.  Bound by the latency of its barriers.
+// Keys stay in registers where kE a thread are enough, else they are read again for
+// every step.  Bound by the latency of its barriers: 6 to 8 us.
 constexpr int kE = 8, kFew = 128;
 
 // exclusive sum of x over the CTA

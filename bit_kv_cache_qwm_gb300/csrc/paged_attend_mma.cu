@@ -41,6 +41,17 @@
 // arithmetic 84; 40% fewer float16 instructions in the conversions were no faster.
 // One request of 98,280 tokens (40 heads over 8) takes 35 us, 8 to 10 of them
 // the start, the first ids and copies, and the join.
+//
+// 8 bits (E4m3): codes become float16 by a conversion of two, exact; K's scale of 16
+// tokens is behind the product, one multiply a logit, V's in the operand.  Half the
+// instructions a byte, so the pages' way from HBM is the bound: that batch takes 143
+// us (5.9 TB/s in all; reads of blocks of 4,112 bytes in random order reach 6.1 TB/s
+// with 64 KB in flight an SM and 6.5 to 6.7 with 128), that request 42.
+//
+// float32 (8 bits alone, whose keys and values float16 holds): q and P as two
+// float16 terms each, so two MMAs for one, and a step's 16 tokens of O summed apart.
+// Three windowed requests (30 to 260 rows, 8 heads over 4, d = 64) 25 us, on the CUDA
+// cores 48; 2,048 rows over 10,240 tokens 412 us (d = 128: 820), 1,206 (2,293) there.
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 

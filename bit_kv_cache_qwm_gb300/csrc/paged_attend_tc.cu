@@ -59,6 +59,11 @@
 // registers); with the producers loading the queries 1.55, the prompts 0.51.
 // What an item weighs in tiles when work is dealt out (kItem): the prompts took
 // 0.57 ms at 0, 0.45 at 3, 0.42 at 4 to 6 (then 0.41 in all).
+//
+// 8 bits (E4m3) differ in the producers alone: codes are converted two at a time and
+// multiplied by their block's scale, both exact.  The first case 1.51 ms back to back
+// and 1.35 after a pause; four prompts of 900 to 4,096 tokens with 0 to 4,000 cached
+// 0.365 ms (0.80 PFLOP/s).
 #include "paged_internal.cuh"
 #include "tcgen05_util.cuh"
 
@@ -241,8 +246,8 @@ struct Packed<D, Int4> {
 
 // 8 bits: a warp's 32 tokens are two blocks of 16 slots, each on one page with one
 // scale.  Lane = 16-byte pieces lane % 4 (and + 4) of rows lane / 4 + 8 k: a load
-// takes half of eight rows, eight lines instead of 32 with a token a thread (the
-// chunk below 2.0 ms), and the eight lanes of a store phase have two rows, whose
+// takes half of eight rows, eight lines instead of 32 with a token a thread (which
+// took 1.99 ms for the first case above), and the eight lanes of a store phase have two rows, whose
 // swizzles differ in their lowest bit.
 template <>
 struct Lookup<E4m3> {

@@ -161,7 +161,8 @@ def test_bad_pages_lengths_and_offsets_are_passed_over(paged):
         assert int(status.item()) & BOUNDS
 
 
-@pytest.mark.parametrize("d,page,dtype", [(128, 16, "bf16"), (64, 64, "f32"), (128, 256, "bf16")])
+@pytest.mark.parametrize("d,page,dtype", [(128, 16, "bf16"), (64, 64, "f32"), (128, 256, "bf16"), (64, 128, "bf16"), (128, 64, "bf16"),
+                                          (64, 32, "bf16")])
 @pytest.mark.parametrize("max_new", [None, 1, 0, 10 ** 6])
 def test_bounds_match_the_oracle(paged, d, page, dtype, max_new):
     B = Batch8(6, [0, 70, 15, 300, 64], [0, 1, 2, 300, 90], 2, 2, d, page, dtype)

@@ -146,6 +146,23 @@ def test_a_row_of_length_one_and_queries_before_the_first_token(paged):  # noqa:
     assert np.array_equal(host(rk[3, 1]), P8.gather(B.pool, B.table[0], 1, 1, 128, 16)[0][0])
 
 
+def test_more_rows_than_tokens_among_single_tokens(paged):  # noqa: F811
+    """The same where the calls go row by row."""
+    B = Batch8(14, [0, 5, 40, 31], [1, 1, 2, 1], 4, 2, 64, 16, "f32")
+    cu = np.array([0, 3, 4, 6, 7], np.int32)                      # request 0 has one token and three rows
+    table, lens = B.table, B.kv_len
+    r = np.random.default_rng(1)
+    k, v = r.standard_normal((2, 7, 2, 64)).astype(np.float32)
+    want, kh, vh = P8.append(B.pool, k, v, table, lens, cu, 16)
+    pool, status = dev(B.pool), i32([0])
+    hat = torch.full((7, 2, 64), 9.0, device="cuda")
+    paged.qwm_paged8_append(dev(k), dev(v), pool, dev(table), dev(lens), dev(cu), k_hat=hat, status=status)
+    assert np.array_equal(host(pool), want) and int(status.item()) == 8
+    assert np.array_equal(host(hat), np.where(np.isnan(kh), 9.0, kh))
+    _, rv = paged.qwm_paged8_read(pool, dev(table), dev(lens), dev(cu), 7, 64, dtype=torch.float32)
+    assert np.array_equal(host(rv), np.where(np.isnan(vh), 0.0, vh))
+
+
 @pytest.mark.parametrize("kernel", [1, 2, 3])
 def test_all_pages_selected_is_the_whole_attention(paged, kernel):  # noqa: F811
     B = Batch8(5, [500, 33, 1200], [3, 40, 1], 8, 2, 128, 32, "bf16")
