@@ -542,7 +542,8 @@ qwm_status qwm_paged_attend(const qwm_paged_attend_args* a, void* stream);
  * 41 MB at 128 channels, of which a step of single tokens uses 4. */
 size_t qwm_paged_attend_workspace_bytes(int32_t head_dim);
 
-/* The kernel (1 to 3) that the automatic choice runs. */
+/* The kernel (1 to 3) that the automatic choice runs (qwm_paged8_attend: 2 for
+ * float32, else the same). */
 int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int32_t kv_heads, int64_t max_new);
 
 /* ------------------------------------------------------------------------
