@@ -56,9 +56,6 @@ __device__ __forceinline__ int unit_of(const Steps& s, int b) {
 }
 __device__ __forceinline__ int find_request(const Steps& s, int unit) {
   const int lane = threadIdx.x & 31;
-  // a token for every request: 8,192 appends 86 us, 143 with blocks as units and the
-  // search
-  if (s.by_row && unit < s.requests && load_cu(s, unit) == unit && load_cu(s, unit + 1) > unit) return unit;
   int lo = 0, span = s.requests;
   while (span > 1) {
     const int step = (span + 31) / 32, at = lane * step;
@@ -81,8 +78,18 @@ struct Block {
 };
 __device__ __forceinline__ Block find_block(const Steps& s, int unit) {
   Block x;
-  const int b = find_request(s, unit);
-  x.s = load_step(s, b);
+  // a token for every request (8,192 appends 80 us, 143 with blocks as units and the
+  // search), else the search
+  int b = unit;
+  bool guess = false;
+  if (s.by_row && unit < s.requests) {
+    x.s = load_step(s, b);
+    guess = x.s.row0 == unit && x.s.first < x.s.n;
+  }
+  if (!guess) {
+    b = find_request(s, unit);
+    x.s = load_step(s, b);
+  }
   int64_t n0;
   if (s.by_row) {
     const int64_t n = (int64_t)x.s.first + unit - x.s.row0;   // the row's token

@@ -222,9 +222,16 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
   // the step's own pages, and all where all are kept, need no score
   if (p.first >= p.n || p.count <= a.width || j0 >= p.tail) return;
   const int mine = min(tiles, (p.tail - j0 + 15) / 16);
-  int ids[kMostTiles / 2];
+  int ids[kMostTiles / 2];   // loaded together, then looked at
+  const int32_t* table = a.block_table + (int64_t)b * a.max_blocks + j0 + lane;
 #pragma unroll
-  for (int i = 0; i < kMostTiles / 2; ++i) ids[i] = 2 * i < mine ? page_id(a, b, j0 + 32 * i + lane, p.tail) : -1;
+  for (int i = 0; i < kMostTiles / 2; ++i) ids[i] = j0 + 32 * i + lane < p.tail ? load_global(table + 32 * i) : -1;
+#pragma unroll
+  for (int i = 0; i < kMostTiles / 2; ++i)
+    if (ids[i] < 0 || ids[i] >= a.n_pages) {
+      if (2 * i < mine && j0 + 32 * i + lane < p.tail && (lane < 16 || 2 * i + 1 < mine)) flag(a.status, QWM_DEV_BOUNDS);
+      ids[i] = -1;
+    }
   uint32_t* keys = static_cast<uint32_t*>(a.workspace) + ((int64_t)b * a.kv_heads + h) * a.max_blocks;
   const int64_t rows = (int64_t)(p.n - p.first) * group;
   auto fetch = [&](Tile<D>& t, int i) {
