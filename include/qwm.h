@@ -683,11 +683,11 @@ qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* stream);
  * roundings to int8.
  *   pages[b][h][i]  the page ids, in the order of the request; -1 behind them
  *   len_out[b]      tokens in them: kv_len[b] less those of the pages left out
- * A request without rows gets no pages and length 0.  So does one whose own
- * step's pages are more than `width`, which sets QWM_DEV_CAPACITY.  Page ids out of
- * range, and bounds that are NaN, come last.  When a bounded device wait runs out,
- * which no input makes it do, QWM_DEV_TIMEOUT is set and the scored pages may be
- * any of the request's. */
+ * Neither overlaps the inputs or the other.  A request without rows gets no pages
+ * and length 0.  So does one whose own step's pages are more than `width`, which
+ * sets QWM_DEV_CAPACITY.  Page ids out of range, and bounds that are NaN, come
+ * last.  When a bounded device wait runs out, which no input makes it do,
+ * QWM_DEV_TIMEOUT is set and the scored pages may be any of the request's. */
 typedef struct {
   qwm_rows q;                    /* [rows][heads][d] dtype                      */
   const void* bounds;            /* 16-byte aligned                             */

@@ -237,6 +237,28 @@ def test_calls_on_a_side_stream(paged):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_a_selection_into_its_own_inputs(paged):  # noqa: F811
+    """pages and lens in the memory of the table, the lengths, the first rows or one
+    another are refused; neighbours of them in one allocation are not."""
+    B = Batch8(3, [200], [1], 2, 1, 64, 16, "bf16")
+    q, bnd = dev(B.q, "bf16"), dev(all_bounds(B))
+    n = B.table.shape[1]
+    mem = torch.zeros(2 * n + 8, dtype=torch.int32, device="cuda")
+    table, lens, cu = mem[:n].view(1, n), mem[n:n + 1], mem[n + 1:n + 3]
+    table.copy_(dev(B.table)), lens.copy_(dev(B.kv_len)), cu.copy_(dev(B.cu))
+    want, want_len = paged.qwm_paged8_select(q, bnd, table, lens, cu, 16, 4)
+    before = mem.clone()
+    free = mem[n + 3:]
+    for kw in (dict(pages=mem[:4].view(1, 1, 4)), dict(pages=mem[n - 1:n + 3].view(1, 1, 4)),
+               dict(pages=mem[n + 2:n + 6].view(1, 1, 4)), dict(lens=lens), dict(lens=mem[3:4]), dict(lens=cu[1:]),
+               dict(pages=free[:4].view(1, 1, 4), lens=free[3:4])):
+        with pytest.raises(ValueError, match="memory of its own"):
+            paged.qwm_paged8_select(q, bnd, table, lens, cu, 16, 4, **kw)
+    assert torch.equal(mem, before)
+    got, got_len = paged.qwm_paged8_select(q, bnd, table, lens, cu, 16, 4, pages=free[:4].view(1, 1, 4), lens=free[4:5])
+    assert torch.equal(got, want) and torch.equal(got_len, want_len) and torch.equal(mem[:n + 3], before[:n + 3])
+
+
 @pytest.mark.parametrize("dtype,kernel", [("bf16", 1), ("bf16", 2), ("bf16", 3), ("f32", 1), ("f32", 2)])
 def test_results_do_not_depend_on_the_run(paged, dtype, kernel):  # noqa: F811
     B = Batch8(9, [5000, 10, 300], [9, 2, 40], 8, 2, 64, 32, dtype)
