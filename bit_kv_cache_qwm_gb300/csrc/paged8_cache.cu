@@ -97,7 +97,8 @@ __device__ __forceinline__ Block find_block(const Steps& s, int unit) {
     x.any = n >= x.s.first && n < x.s.n && (n == n0 || n == x.s.first);
   } else {
     n0 = ((int64_t)(x.s.first >> 4) + unit - unit_of(s, b)) * kScaleSlots;
-    x.any = n0 < x.s.n && x.s.first < x.s.n;
+    // units ahead of the first request's, in a slice of a step, are no request's
+    x.any = n0 < x.s.n && n0 + kScaleSlots > x.s.first && x.s.first < x.s.n;
   }
   x.n0 = x.any ? (int)n0 : 0;
   x.lo = max(x.s.first - x.n0, 0), x.hi = min(x.s.n - x.n0, kScaleSlots);

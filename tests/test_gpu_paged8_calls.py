@@ -1,0 +1,46 @@
+"""The 8-bit cache's calls as their documentation allows them and no other test makes
+them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged8_oracle as P8
+from paged8_cases import Batch8
+from test_gpu_paged8_cache import before, dev, host, paged  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ a step in slices
+@pytest.mark.parametrize("cached,new,cuts", [([100, 3, 40], [30, 40, 1], (0, 1, 2, 3)), ([3, 70], [33, 50], (0, 1, 2)),
+                                             ([0, 0, 5, 16], [100, 20, 17, 60], (0, 1, 3, 4)), ([20] * 6, [1, 1, 1, 1, 60, 2], (0, 4, 6))])
+@pytest.mark.parametrize("freed", [False, True])
+def test_append_and_read_of_a_step_in_slices(paged, cached, new, cuts, freed):  # noqa: F811
+    """cu_rows[a: b + 1] of a step begin behind the first row: the rows ahead belong
+    to no request of the call.  Nothing is reported, no byte but the step's blocks
+    changes, and pages ahead of those may have been given up (-1 in the tables)."""
+    B = Batch8(21, cached, new, 2, 2, 64, 16, "f32")
+    k, v = (B.rows_of(x, cached, new) for x in (B.k, B.v))
+    pool0 = before(B)
+    want, kh, vh = P8.append(pool0, k, v, B.table, B.kv_len, B.cu, 16)
+    table = B.table.copy()
+    if freed:
+        for b, c in enumerate(cached):
+            table[b, :c // 16] = -1
+    pool, lens, cu, t = dev(pool0), dev(B.kv_len), dev(B.cu), dev(table)
+    status = i32([0])
+    hats = [torch.full((B.rows, 2, 64), 9.0, device="cuda") for _ in range(4)]
+    for a, b in zip(cuts[:-1], cuts[1:]):
+        step = t[a:b].contiguous(), lens[a:b], cu[a:b + 1]
+        paged.qwm_paged8_append(dev(k), dev(v), pool, *step, k_hat=hats[0], v_hat=hats[1], status=status)
+        assert int(status.item()) == 0, (a, b)
+        paged.qwm_paged8_read(pool, *step, B.rows, 64, dtype=torch.float32, k_out=hats[2], v_out=hats[3], status=status)
+        assert int(status.item()) == 0, (a, b)
+        assert bool((hats[2][int(B.cu[b]):] == 9.0).all())
+    assert np.array_equal(host(pool), want)
+    for got, x in zip(hats, (kh, vh, kh, vh)):
+        assert np.array_equal(host(got), x)
