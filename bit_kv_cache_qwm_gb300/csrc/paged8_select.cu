@@ -78,6 +78,11 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return s != s ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Where maxima over scores start, and what those of a page without bounds stay: NaN,
+// which no maximum takes and whose key is below that of -infinity, the score that an
+// infinite query can have on every page.
+__device__ __forceinline__ float no_score() { return __int_as_float(0x7fffffff); }
+
 // A query row as whole numbers (four lanes share a row, d/4 channels each; `src`: the
 // lane's first, nullptr for a row of zeros) and its unit.  A number y comes as the
 // float kWhole + y, whose low bits it is.
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kFewNt) paged8_score_few_kernel(const qwm_page
         Tile<D>::operand(t.low, k, f);
         mma(v, f, w[k].z, w[k].w);
       }
-      float best[2] = {-INFINITY, -INFINITY};
+      float best[2] = {no_score(), no_score()};
       take(best, s, v, t.unit, u0, u1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(kManyNt, 1) paged8_score_many_kernel(const qwm
         const int v = s - 1, n = min(width(before), i0 + 64), j = (p0 + pi_before * page_parts) * kTile + page;
         const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (v & 1);
         const float2 up = make_float2(unit_page[pi_before & 3][page], unit_page[pi_before & 3][page]);
-        float best = -INFINITY;
+        float best = no_score();
 #pragma unroll 1
         for (int i = i0; i < n; i += 32) {
           uint32_t x[32];

@@ -174,13 +174,14 @@ def bounds(pool, old, table, kv_len, cu, page: int, d: int):
 
 
 def scores(q, bnd, ids, d: int):
-    """[pages] float32: the scores of pages `ids` of one head (bnd [pages, bytes]) for query rows q [m, d]."""
+    """[pages] float32: the scores of pages `ids` of one head (bnd [pages, bytes]) for query rows q [m, d]; NaN
+    where the id is out of range or the bounds are NaN."""
     q = np.asarray(q, f32)
     q = np.clip(np.where(np.isnan(q), f32(0), q), -np.finfo(f32).max, np.finfo(f32).max)
     top = np.abs(q).max(1, keepdims=True)
     unit = np.where(top >= f32(2.0 ** -100), top / f32(127), f32(0)).astype(f32)
     x = np.where(unit > 0, np.clip(np.rint(q / np.where(unit > 0, unit, f32(1))), -127, 127), 0).astype(np.int64)
-    out = np.full(len(ids), -np.inf, f32)
+    out = np.full(len(ids), np.nan, f32)
     for i, pg in enumerate(ids):
         if not 0 <= pg < bnd.shape[0]:
             continue
@@ -208,7 +209,7 @@ def select(q, bnd, table, kv_len, cu, page: int, width: int, sink: int, d: int):
             own = list(range(tail, count))
             first = list(range(min(sink, tail, kept - len(own))))
             rest = [j for j in range(len(first), tail)]
-            rest.sort(key=lambda j: (-s[j], j))
+            rest.sort(key=lambda j: (bool(np.isnan(s[j])), 0 if np.isnan(s[j]) else -s[j], j))
             take = sorted(own + first + rest[: kept - len(own) - len(first)])
             pages[b, h, :kept] = table[b, take]
     return pages, lens

@@ -6,7 +6,7 @@ import torch
 
 from oracle import paged8_oracle as P8
 from paged8_cases import Batch8
-from test_gpu_paged8_cache import before, dev, host, paged  # noqa: F401
+from test_gpu_paged8_cache import BOUNDS, before, dev, host, paged  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,31 @@ def test_append_and_read_of_a_step_in_slices(paged, cached, new, cuts, freed):  
     assert np.array_equal(host(pool), want)
     for got, x in zip(hats, (kh, vh, kh, vh)):
         assert np.array_equal(host(got), x)
+
+
+# ------------------------------------------------------------------ scores without a finite value
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_without_bounds_come_behind_scores_of_minus_infinity(paged, rows, d):  # noqa: F811
+    """Infinite queries against keys of the other sign score -inf on every page; pages
+    out of range and bounds that are NaN still come last, in few rows and in many."""
+    page, count, hk = 16, 300, 2
+    bnd = np.zeros((count, hk, 2 * d + 16), np.uint8)
+    bnd[..., :d], bnd[..., d:2 * d] = 120, 90
+    bnd[..., 2 * d:2 * d + 4] = np.array([0.5], np.float32).view(np.uint8)
+    table = np.random.default_rng(3).permutation(count).astype(np.int32)[None]
+    none = [2, 5, 140, 141]
+    bnd[table[0, none[0]], :, 2 * d:2 * d + 4] = np.array([np.nan], np.float32).view(np.uint8)
+    table[0, none[1]], table[0, none[2]] = -1, count
+    bnd[table[0, none[3]], :, 2 * d:2 * d + 4] = np.array([np.nan], np.float32).view(np.uint8)
+    q = np.full((rows, 2 * hk, d), -np.inf, np.float32)
+    lens, cu = np.array([count * page], np.int32), np.array([0, rows], np.int32)
+    own = count - (count * page - rows) // page
+    rest = [j for j in range(count - own) if j not in none]
+    status = i32([0])
+    for width in (own + 1, own + 7, own + len(rest), own + len(rest) + 2):
+        got, _ = paged.qwm_paged8_select(dev(q), dev(bnd), dev(table), dev(lens), dev(cu), page, width, status=status)
+        take = sorted((rest + none)[:width - own]) + list(range(count - own, count))
+        assert np.array_equal(host(got)[0], np.tile(table[0, take], (hk, 1))), width
+        assert np.array_equal(host(got), P8.select(q, bnd, table, lens, cu, page, width, 0, d)[0])
+    assert int(status.item()) == BOUNDS
