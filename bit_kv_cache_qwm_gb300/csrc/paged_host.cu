@@ -276,6 +276,10 @@ qwm_status step_status(const A& a) {
     return QWM_ERR_UNSUPPORTED;
   return QWM_OK;
 }
+// whether n words at p and m words at q share none
+bool apart(const int32_t* p, int64_t n, const int32_t* q, int64_t m) {
+  return (uintptr_t)p + 4 * n <= (uintptr_t)q || (uintptr_t)q + 4 * m <= (uintptr_t)p;
+}
 template <class A>
 bool step_pointers_ok(const A& a) {
   return a.block_table && a.kv_len && a.cu_rows && words(a.block_table, a.kv_len, a.cu_rows, a.status);
@@ -339,7 +343,8 @@ extern "C" qwm_status qwm_paged8_select(const qwm_paged8_select_args* a, void* s
   if (a->kv_heads > 65535 || a->rows * (a->heads / a->kv_heads) > kHalf || a->rows * a->heads > (int64_t)1 << 36)
     return QWM_ERR_UNSUPPORTED;
   if ((a->rows > 0 && !rows_ok(a->q, a->rows, a->heads, a->head_dim, esize(a->dtype), false)) || !a->bounds ||
-      !aligned(a->bounds, 16) || !a->pages || !a->len_out || a->len_out == a->kv_len || !words(a->pages, a->len_out) ||
+      !aligned(a->bounds, 16) || !a->pages || !a->len_out ||
+      !apart(a->len_out, a->requests, a->kv_len, a->requests) || !apart(a->len_out, a->requests, a->cu_rows, a->requests + 1) || !words(a->pages, a->len_out) ||
       !a->workspace || !aligned(a->workspace, 256) ||
       a->workspace_bytes < qwm_paged8_select_workspace_bytes(a->rows, a->heads, a->head_dim, a->requests, a->kv_heads, a->max_blocks) ||
       !step_pointers_ok(*a))

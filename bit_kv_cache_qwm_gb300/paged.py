@@ -415,8 +415,10 @@ def _apart(out, name: str, *inputs):
     """Refuses an output of 4-byte elements that shares memory with the others."""
     lo, hi = out.data_ptr(), out.data_ptr() + 4 * out.numel()
     for x in inputs:
-        if lo < x.data_ptr() + 4 * x.numel() and x.data_ptr() < hi:
-            raise ValueError(f"{name}: memory of its own is expected, apart from the inputs' and the other output's")
+        if x is not None and x.numel() and lo < hi:
+            size = x.element_size() * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride())))
+            if lo < x.data_ptr() + size and x.data_ptr() < hi:
+                raise ValueError(f"{name}: memory of its own is expected, apart from the inputs' and the other output's")
 
 
 def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -525,7 +527,7 @@ def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.
     reads this step: those of the step's own tokens, the first `sink`, and the ones
     with the highest scores, bounds of the products of the queries q [rows, heads,
     d] with the keys in them.  pages and lens, where given, share no memory with
-    the inputs.  Returns (pages int32 [requests, kv_heads, width],
+    the inputs or each other (refused).  Returns (pages int32 [requests, kv_heads, width],
     lens int32 [requests]), the block_table and kv_len of a qwm_paged8_attend."""
     qr = _rows(q, "q")
     dt, dev = q.dtype, q.get_device()
@@ -545,7 +547,7 @@ def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.
         lens = torch.empty_like(kv_len)
     out = _array(pages, "pages", _I32, (B, hk, width), dev), _array(lens, "lens", _I32, (B,), dev)
     for x, name in given:
-        _apart(x, name, block_table, kv_len, cu_rows, *((pages,) if x is lens else ()))
+        _apart(x, name, q, bounds, block_table, kv_len, cu_rows, status, *((pages,) if x is lens else ()))
     # qwm_paged8_select_workspace_bytes
     n_ws = (4 * B * hk * blocks + 255 & -256) + (4 * T * hq + 255 & -256) + T * hq * d
     ws = torch.empty(n_ws or 1, dtype=_U8, device=device)

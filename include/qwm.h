@@ -683,7 +683,9 @@ qwm_status qwm_paged8_bounds(const qwm_paged8_bounds_args* a, void* stream);
  * roundings to int8.
  *   pages[b][h][i]  the page ids, in the order of the request; -1 behind them
  *   len_out[b]      tokens in them: kv_len[b] less those of the pages left out
- * Neither overlaps the inputs or the other.  A request without rows gets no pages
+ * Neither overlaps the inputs, the workspace or the other: the caller sees to it
+ * (of all these only len_out is compared, with kv_len and cu_rows; the Python
+ * binding compares the rest).  A request without rows gets no pages
  * and length 0.  So does one whose own step's pages are more than `width`, which
  * sets QWM_DEV_CAPACITY.  Page ids out of range, and bounds that are NaN, come
  * last.  When a bounded device wait runs out, which no input makes it do,
@@ -695,7 +697,7 @@ typedef struct {
   const int32_t* kv_len;         /* [requests]                                  */
   const int32_t* cu_rows;        /* [requests + 1]                              */
   int32_t* pages;                /* [requests][kv_heads][width]                 */
-  int32_t* len_out;              /* [requests]; not kv_len                      */
+  int32_t* len_out;              /* [requests]; not in kv_len or cu_rows        */
   uint32_t* status;              /* or NULL                                     */
   void* workspace;               /* 256-byte aligned                            */
   size_t workspace_bytes;        /* >= qwm_paged8_select_workspace_bytes        */

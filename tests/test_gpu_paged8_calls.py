@@ -6,7 +6,7 @@ import torch
 
 from oracle import paged8_oracle as P8
 from paged8_cases import Batch8
-from test_gpu_paged8_cache import BOUNDS, before, dev, host, paged  # noqa: F401
+from test_gpu_paged8_cache import BOUNDS, all_bounds, before, dev, host, paged  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,29 @@ def test_pages_without_bounds_come_behind_scores_of_minus_infinity(paged, rows, 
         assert np.array_equal(host(got)[0], np.tile(table[0, take], (hk, 1))), width
         assert np.array_equal(host(got), P8.select(q, bnd, table, lens, cu, page, width, 0, d)[0])
     assert int(status.item()) == BOUNDS
+
+
+# ------------------------------------------------------------------ outputs in other tensors' memory
+def test_a_selection_into_its_queries_bounds_or_status(paged):  # noqa: F811
+    """pages and lens in the memory of q, of the bounds or of the status word are
+    refused; neighbours of them in one allocation are not."""
+    B = Batch8(3, [200], [2], 2, 1, 64, 16, "f32")
+    step = dev(B.table), dev(B.kv_len), dev(B.cu)
+    bnd = all_bounds(B)
+    n_q, n_b = B.q.size, bnd.size // 4
+    mem = torch.zeros(n_q + n_b + 4 + 8, dtype=torch.int32, device="cuda")
+    q, status = mem[:n_q].view(torch.float32).view(B.q.shape), mem[n_q + n_b: n_q + n_b + 1]
+    bounds = mem[n_q: n_q + n_b].view(torch.uint8).view(bnd.shape)
+    q.copy_(dev(B.q)), bounds.copy_(dev(bnd))
+    want, want_len = paged.qwm_paged8_select(q, bounds, *step, 16, 4, status=status)
+    saved = mem.clone()
+    at = lambda i, m: mem[i: i + m]  # noqa: E731
+    for kw in (dict(pages=at(0, 4).view(1, 1, 4)), dict(pages=at(n_q - 1, 4).view(1, 1, 4)), dict(pages=at(n_q + n_b - 1, 4).view(1, 1, 4)),
+               dict(pages=at(n_q + n_b - 3, 4).view(1, 1, 4)), dict(pages=at(n_q + n_b, 4).view(1, 1, 4)), dict(lens=at(n_q - 1, 1)),
+               dict(lens=at(n_q, 1)), dict(lens=at(n_q + n_b, 1))):
+        with pytest.raises(ValueError, match="memory of its own"):
+            paged.qwm_paged8_select(q, bounds, *step, 16, 4, status=status, **kw)
+    assert torch.equal(mem, saved)
+    got, got_len = paged.qwm_paged8_select(q, bounds, *step, 16, 4, status=status, pages=at(n_q + n_b + 4, 4).view(1, 1, 4),
+                                           lens=at(n_q + n_b + 1, 1))
+    assert torch.equal(got, want) and torch.equal(got_len, want_len) and torch.equal(mem[:n_q + n_b + 1], saved[:n_q + n_b + 1])

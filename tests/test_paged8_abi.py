@@ -125,6 +125,14 @@ def test_select_refusals(paged, kw, status):
     assert f(-1, 2, 128, 3, 2, 4) == f(4, 0, 128, 3, 2, 4) == f(4, 2, 96, 3, 2, 4) == f(4, 2, 128, 3, 0, 4) == f(4, 2, 128, 3, 2, 0) == 0
 
 
+@pytest.mark.parametrize("out,lens,cu,status", [(0, 4, 32, 1), (4, 0, 32, 1), (8, 0, 32, 1), (12, 0, 32, 6), (0, 12, 32, 6), (32, 0, 32, 1),
+                                                (44, 0, 32, 1), (48, 0, 32, 6), (20, 0, 32, 6), (24, 0, 32, 1)])
+def test_select_refuses_lengths_in_its_lengths_or_first_rows(paged, out, lens, cu, status):
+    """len_out [3] anywhere in kv_len [3] or cu_rows [4], not beside them."""
+    a = [FAKE, 256, 128, FAKE, 3 * FAKE, FAKE + lens, FAKE + cu, 4 * FAKE, FAKE + out, 0, 5 * FAKE, 1 << 40, 4, 3, 1, 128, 2, 2, 16, 3, 4, 2, 0]
+    assert paged.lib().qwm_paged8_select(paged._SELECT8.pack(*a), None) == status
+
+
 def attend_args(paged, **kw):
     a = dict(q=(FAKE, 768, 128), out=(FAKE, 768, 128), lse=0, pool=FAKE, table=FAKE, lens=FAKE, cu=FAKE, status=0, ws=FAKE,
              ws_bytes=1 << 40, rows=10, n_pages=5, max_new=4, dtype=1, d=128, hq=6, hk=2, page=16, requests=3, max_blocks=4,
