@@ -421,6 +421,13 @@ def _apart(out, name: str, *inputs):
                 raise ValueError(f"{name}: memory of its own is expected, apart from the inputs' and the other output's")
 
 
+def _differ(what: str, *pairs):
+    """Refuses tensors of `pairs` (as _rows gives them) that begin at one address."""
+    for x, y in pairs:
+        if x[0] and x[0] == y[0]:
+            raise ValueError(f"{what}: tensors apart from each other are expected")
+
+
 def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
                       cu_rows: torch.Tensor, k_hat: Optional[torch.Tensor] = None, v_hat: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None):
@@ -428,7 +435,8 @@ def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, bloc
     cu_rows as qwm_paged_plan returns them) to 8 bits into its requests' pages:
     e4m3 codes, and a power of two as scale for every 16 slots and head, which
     grows with larger tokens.  k_hat, v_hat receive the values that the stored
-    bytes stand for; rows behind the last request are left as they were in them."""
+    bytes stand for; rows behind the last request are left as they were in them.
+    They share no memory with the inputs or each other."""
     kr = _rows(k, "k")
     shape, dt, dev = k.shape, k.dtype, k.get_device()
     T, hk, d = shape
@@ -436,6 +444,7 @@ def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, bloc
     at, n_pages, _, page = _pool8(pool, d, dev, hk)
     kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", dt, dev, shape)
     vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", dt, dev, shape)
+    _differ("k_hat, v_hat", (kh, vh), (kh, vr), (vh, kr))
     step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_append,
          _APPEND8.pack(*kr, *vr, *kh, *vh, at, *step, _status(status, dev), T, n_pages, _DTYPES[dt], d, hk, page, B, width),
@@ -449,7 +458,7 @@ def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch
     cu_rows[b] + i is the i-th of the last cu_rows[b + 1] - cu_rows[b] of the
     first kv_len[b] tokens of request b.  Returns (k_out, v_out), new tensors of
     `dtype` where none are given; rows behind the last request are left as they
-    were."""
+    were.  They share no memory with each other."""
     dev = pool.get_device() if isinstance(pool, _Tensor) else -1
     at, n_pages, hk, page = _pool8(pool, head_dim, dev)
     if dtype not in _DTYPES:
@@ -461,6 +470,7 @@ def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch
     if v_out is None:
         v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
     vr = _rows(v_out, "v_out", dtype, dev, shape)
+    _differ("k_out, v_out", (kr, vr))
     step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_read,
          _READ8.pack(*kr, *vr, at, *step, _status(status, dev), rows, n_pages, _DTYPES[dtype], head_dim, hk, page, B, width),

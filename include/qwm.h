@@ -613,7 +613,7 @@ qwm_status qwm_paged8_append(const qwm_paged8_append_args* a, void* stream);
 /* The values code x scale of the tokens of a step, or of any tokens: the last
  * cu_rows[b + 1] - cu_rows[b] of the first kv_len[b] of request b.  Exact in
  * either dtype.  Rows outside cu_rows[0 .. requests] are left as they were, rows
- * passed over become 0. */
+ * passed over become 0.  k and v do not overlap. */
 typedef struct {
   qwm_rows k, v;                 /* outputs [rows][kv_heads][d]                 */
   const void* pool;              /* 16-byte aligned                             */

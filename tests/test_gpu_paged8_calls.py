@@ -98,3 +98,24 @@ def test_a_selection_into_its_queries_bounds_or_status(paged):  # noqa: F811
     got, got_len = paged.qwm_paged8_select(q, bounds, *step, 16, 4, status=status, pages=at(n_q + n_b + 4, 4).view(1, 1, 4),
                                            lens=at(n_q + n_b + 1, 1))
     assert torch.equal(got, want) and torch.equal(got_len, want_len) and torch.equal(mem[:n_q + n_b + 1], saved[:n_q + n_b + 1])
+
+
+def test_two_outputs_in_one_tensor(paged):  # noqa: F811
+    """Values into the keys' tensor, or the stored values of one into the other's
+    input, are refused; two slices of one tensor are not."""
+    B = Batch8(4, [20], [30], 2, 2, 64, 16, "f32")
+    step, pool = (dev(B.table), dev(B.kv_len), dev(B.cu)), dev(B.pool)
+    k, v = dev(B.rows_of(B.k, [20], [30])), dev(B.rows_of(B.v, [20], [30]))
+    both = torch.zeros((30, 4, 64), device="cuda")
+    saved = pool.clone()
+    for call in (lambda: paged.qwm_paged8_read(pool, *step, 30, 64, dtype=torch.float32, k_out=both[:, :2], v_out=both[:, :2]),
+                 lambda: paged.qwm_paged8_append(k, v, pool, *step, k_hat=both[:, :2], v_hat=both[:, :2]),
+                 lambda: paged.qwm_paged8_append(k, v, pool, *step, k_hat=v), lambda: paged.qwm_paged8_append(k, v, pool, *step, v_hat=k)):
+        with pytest.raises(ValueError, match="apart"):
+            call()
+    assert torch.equal(pool, saved) and bool((both == 0).all())
+    paged.qwm_paged8_read(pool, *step, 30, 64, dtype=torch.float32, k_out=both[:, :2], v_out=both[:, 2:])
+    rk, rv = paged.qwm_paged8_read(pool, *step, 30, 64, dtype=torch.float32)
+    assert torch.equal(both, torch.cat([rk, rv], 1))
+    none = torch.empty((0, 2, 64), device="cuda")
+    paged.qwm_paged8_read(pool, step[0], step[1], i32([0, 0]), 0, 64, dtype=torch.float32, k_out=none, v_out=none)
