@@ -92,9 +92,14 @@ def measure_paged8(K, V, q, sigma: float, page_tokens: int = 64, widths=(16, 64)
     rows = q.float().transpose(0, 1).contiguous()
     P = torch.softmax(sigma * (q @ kh.transpose(1, 2)), dim=-1)
     P = torch.nn.functional.pad(P, (0, n_pages * page_tokens - N)).unflatten(-1, (n_pages, page_tokens)).sum(-1)
+    most = 8192                                                # requests of a call
     for width in widths:
-        pages, _ = paged.qwm_paged8_select(rows, bounds, table.expand(M, -1).contiguous(), i32([N] * M),
-                                           torch.arange(M + 1, dtype=torch.int32, device=K.device), page_tokens, width, sink=1)
+        parts = []
+        for at in range(0, max(M, 1), most):
+            m = min(most, M - at)
+            parts.append(paged.qwm_paged8_select(rows[at: at + m], bounds, table.expand(m, -1).contiguous(), i32([N] * m),
+                                                 torch.arange(m + 1, dtype=torch.int32, device=K.device), page_tokens, width, sink=1)[0])
+        pages = torch.cat(parts)
         held = torch.gather(P, 2, pages.transpose(0, 1).long().clamp(min=0)) * (pages.transpose(0, 1) >= 0)
         res[f"weight_in_{width}_pages"] = float(held.sum(-1).mean())
     return res

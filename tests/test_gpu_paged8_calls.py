@@ -119,3 +119,17 @@ def test_two_outputs_in_one_tensor(paged):  # noqa: F811
     assert torch.equal(both, torch.cat([rk, rv], 1))
     none = torch.empty((0, 2, 64), device="cuda")
     paged.qwm_paged8_read(pool, step[0], step[1], i32([0, 0]), 0, 64, dtype=torch.float32, k_out=none, v_out=none)
+
+
+def test_diagnostics_of_more_rows_than_requests_of_a_call(paged):  # noqa: F811
+    """Every query is a request of its own there, and a call takes 8,192."""
+    from bit_kv_cache_qwm_gb300 import diagnostics
+    r = np.random.default_rng(11)
+    K, V = (dev(r.standard_normal((1, 200, 64)).astype(np.float32)) for _ in range(2))
+    q = dev(r.standard_normal((1, 8200, 64)).astype(np.float32))
+    args = dict(page_tokens=16, widths=(3,))
+    key = "weight_in_3_pages"
+    got = diagnostics.measure_paged8(K, V, q, 0.125, **args)
+    parts = [diagnostics.measure_paged8(K, V, q[:, a:b].contiguous(), 0.125, **args)[key] for a, b in ((0, 4100), (4100, 8200))]
+    # float32 means of 4,100 and 8,200 values in (0, 1)
+    assert got[key] == pytest.approx(sum(parts) / 2, rel=1e-5)
