@@ -451,7 +451,8 @@ cudaError_t launch_read8(const qwm_paged8_read_args& a, int shift, cudaStream_t 
 }
 
 cudaError_t launch_bounds8(const qwm_paged8_bounds_args& a, int shift, cudaStream_t st) {
-  const int64_t page = (int64_t)1 << shift, most = a.max_new < 1 ? 1 : a.max_new;
+  // no more rows than the tables hold, which also keeps the sum below in range
+  const int64_t page = (int64_t)1 << shift, all = a.max_blocks * page, most = a.max_new < 1 ? 1 : a.max_new < all ? a.max_new : all;
   int64_t pages = (most + page - 2) / page + 1;   // that so many rows can lie in
   pages = pages < a.max_blocks ? pages : a.max_blocks;
   const dim3 grid((unsigned)pages, (unsigned)a.kv_heads, (unsigned)a.requests);

@@ -133,3 +133,12 @@ def test_diagnostics_of_more_rows_than_requests_of_a_call(paged):  # noqa: F811
     parts = [diagnostics.measure_paged8(K, V, q[:, a:b].contiguous(), 0.125, **args)[key] for a, b in ((0, 4100), (4100, 8200))]
     # float32 means of 4,100 and 8,200 values in (0, 1)
     assert got[key] == pytest.approx(sum(parts) / 2, rel=1e-5)
+
+
+@pytest.mark.parametrize("max_new", [0, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+def test_bounds_with_any_hint(paged, max_new):  # noqa: F811
+    B = Batch8(5, [100, 3], [300, 20], 2, 2, 64, 16, "f32")
+    old = np.zeros((B.empty.shape[0], 2, 144), np.uint8)
+    got = dev(old)
+    paged.qwm_paged8_bounds(dev(B.pool), got, dev(B.table), dev(B.kv_len), dev(B.cu), max_new=max_new)
+    assert np.array_equal(host(got), P8.bounds(B.pool, old, B.table, B.kv_len, B.cu, 16, 64))
