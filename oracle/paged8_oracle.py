@@ -182,13 +182,13 @@ def scores(q, bnd, ids, d: int):
     unit = np.where(top >= f32(2.0 ** -100), top / f32(127), f32(0)).astype(f32)
     x = np.where(unit > 0, np.clip(np.rint(q / np.where(unit > 0, unit, f32(1))), -127, 127), 0).astype(np.int64)
     out = np.full(len(ids), np.nan, f32)
-    for i, pg in enumerate(ids):
-        if not 0 <= pg < bnd.shape[0]:
-            continue
-        high, low = (bnd[pg, z * d: (z + 1) * d].view(np.int8).astype(np.int64) for z in (0, 1))
-        S = np.where(x >= 0, x * high, x * low).sum(1)
-        with np.errstate(over="ignore"):
-            out[i] = ((S.astype(f32) * bnd[pg, 2 * d: 2 * d + 4].view(f32)[0]) * unit[:, 0]).max()
+    ids = np.asarray(ids)
+    known = (ids >= 0) & (ids < bnd.shape[0])
+    b = bnd[ids[known]]
+    high, low = (np.ascontiguousarray(b[:, z * d: (z + 1) * d]).view(np.int8).astype(np.float64) for z in (0, 1))
+    S = np.maximum(x, 0) @ high.T + np.minimum(x, 0) @ low.T       # whole numbers below 2^24: exact
+    with np.errstate(over="ignore"):
+        out[known] = ((S.astype(f32) * np.ascontiguousarray(b[:, 2 * d: 2 * d + 4]).view(f32)[:, 0]) * unit).max(0)
     return out
 
 

@@ -142,3 +142,119 @@ def test_bounds_with_any_hint(paged, max_new):  # noqa: F811
     got = dev(old)
     paged.qwm_paged8_bounds(dev(B.pool), got, dev(B.table), dev(B.kv_len), dev(B.cu), max_new=max_new)
     assert np.array_equal(host(got), P8.bounds(B.pool, old, B.table, B.kv_len, B.cu, 16, 64))
+
+
+# ------------------------------------------------------------------ many rows over many pages
+def walk(pages, rows, group, requests, kv_heads, page_slots):
+    """(row tiles, page tiles) that a CTA of the scores of many rows goes through for
+    requests of `pages` earlier pages and `rows` rows: tiles of 128 of either,
+    page tiles dealt to as many CTAs as there are SMs for each request and head."""
+    want = -(-torch.cuda.get_device_properties(0).multi_processor_count // (requests * kv_heads))
+    parts = min(want, -(-page_slots // 128))
+    assert parts == want     # so the rows of a request are not split
+    return [(-(-r * group // 128), -(-(-(-p // 128)) // parts)) for p, r in zip(pages, rows)]
+
+
+def long_tables(seed, count, new, heads, kv_heads, d, page, odd=False):
+    """A step over `count` pages of each request with random bounds, no pool behind
+    them; `odd`: with the queries, bounds and ids that a score has rules for."""
+    r = np.random.default_rng(seed)
+    n_pages = sum(count)
+    bnd = np.zeros((n_pages, kv_heads, 2 * d + 16), np.uint8)
+    x = np.sort(r.integers(-127, 128, (n_pages, kv_heads, 2, d)), axis=2)[:, :, ::-1]
+    bnd[..., :2 * d] = x.reshape(n_pages, kv_heads, 2 * d).astype(np.int8).view(np.uint8)
+    bnd[..., 2 * d:2 * d + 4] = np.exp(r.standard_normal((n_pages, kv_heads, 1))).astype(np.float32).view(np.uint8)
+    order = r.permutation(n_pages).astype(np.int32)
+    table = np.full((len(count), max(count)), -1, np.int32)
+    at = 0
+    for b, m in enumerate(count):
+        table[b, :m] = order[at:at + m]
+        at += m
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    lens = np.array([m * page - int(r.integers(0, page)) for m in count], np.int32)
+    q = r.standard_normal((int(cu[-1]), heads, d)).astype(np.float32)
+    if odd:
+        for b, m in enumerate(count):
+            for j in r.choice(m, m // 6, replace=False):        # in every tile of pages
+                table[b, j] = r.choice([-1, n_pages, 2 ** 31 - 1, -5])
+            for j in r.choice(m, m // 6, replace=False):
+                if 0 <= table[b, j] < n_pages:
+                    bnd[table[b, j], :, 2 * d:2 * d + 4] = np.array([r.choice([np.nan, 0.0, 1e-30])], np.float32).view(np.uint8)
+            same = [j for j in r.choice(m, m // 3, replace=False) if 0 <= table[b, j] < n_pages]
+            bnd[table[b, same]] = bnd[table[b, same[0]]]        # equal scores
+        for i in range(q.shape[0]):
+            h, kind = int(r.integers(heads)), i % 7
+            if kind == 0:
+                q[i, h, :4] = np.nan, 3.0, -np.inf, np.inf
+            elif kind == 1:
+                q[i] = np.nan
+            elif kind == 2:
+                q[i, h] = 0.0
+            elif kind == 3:
+                q[i] *= np.float32(1e-38)
+            elif kind == 4:
+                q[i, h] = np.float32(2.0 ** -101)
+            elif kind == 5:
+                q[i] = np.float32(2.0 ** -100) * np.sign(q[i])
+    return bnd, table, lens, cu, q
+
+
+STEP = [800, 1700, 790, 1000, 129, 385, 1650, 641], [60, 40, 110, 330, 70, 0, 135, 5]     # pages, rows of eight requests
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("odd", [False, True])
+def test_scores_of_many_rows_over_several_tiles_of_pages(paged, d, odd):  # noqa: F811
+    """A CTA goes on to another tile of pages, behind one, two and more tiles of
+    rows; its steps, and its tiles of pages, come round the four places that it
+    keeps for each."""
+    count, new = STEP
+    heads, kv_heads, page, group = 16, 8, 16, 2
+    bnd, table, lens, cu, q = long_tables(30 + d, count, new, heads, kv_heads, d, page, odd)
+    walks = walk([(n - m) // page for n, m in zip(lens, new)], new, group, len(count), kv_heads, table.shape[1])
+    assert {nr for nr, pages in walks if pages > 1} >= {1, 2, 3, 6} and {nr for nr, pages in walks if pages > 4} >= {1, 3}
+    assert sum(new) * group > 8 * len(count)       # not the scores of few rows
+    status = i32([0])
+    for width, sink in ((40, 1), (300, 0)):
+        with np.errstate(invalid="ignore", over="ignore"):
+            want, wl = P8.select(q, bnd, table, lens, cu, page, width, sink, d)
+        for _ in range(10):
+            got, gl = paged.qwm_paged8_select(dev(q), dev(bnd), dev(table), dev(lens), dev(cu), page, width, sink=sink, status=status)
+            assert np.array_equal(host(gl), wl) and np.array_equal(host(got), want)
+    assert int(status.item()) == (BOUNDS if odd else 0)
+
+
+@pytest.mark.parametrize("limit", [0, 300, 3000, 30000])
+def test_a_wait_that_runs_out_over_several_tiles_of_pages(paged, monkeypatch, limit):  # noqa: F811
+    """As in the test of waits for one tile: the call ends, names pages of the
+    request, reports what ran out, and the next one is whole again."""
+    count, new = STEP
+    bnd, table, lens, cu, q = long_tables(40, count, new, 16, 8, 64, 16)
+    args = dev(q), dev(bnd), dev(table), dev(lens), dev(cu), 16, 40
+    status = i32([0])
+    want, wl = paged.qwm_paged8_select(*args, status=status)
+    assert int(status.item()) == 0
+    monkeypatch.setenv("QWM_FAULT_INJECT", f"wait={limit}")
+    got, gl = paged.qwm_paged8_select(*args, status=status)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("QWM_FAULT_INJECT")
+    bits = int(status.item())
+    assert bits in (0, 4) and torch.equal(gl, wl)
+    for b in range(len(count)):
+        for h in range(8):
+            ids = [x for x in host(got)[b, h].tolist() if x >= 0]
+            assert len(ids) == len(set(ids)) == (40 if new[b] else 0) and set(ids) <= set(table[b].tolist())
+    if bits == 0:
+        assert torch.equal(got, want)
+    status.zero_()
+    assert torch.equal(paged.qwm_paged8_select(*args, status=status)[0], want) and int(status.item()) == 0
+
+
+def test_a_prompt_among_single_tokens(paged):  # noqa: F811
+    """63 single tokens and a prompt that together count as few rows."""
+    count, new = [20 + 3 * b for b in range(63)] + [400], [1] * 63 + [449]
+    bnd, table, lens, cu, q = long_tables(50, count, new, 1, 1, 64, 16)
+    assert sum(new) <= 8 * len(new)
+    want, wl = P8.select(q, bnd, table, lens, cu, 16, 31, 1, 64)
+    got, gl = paged.qwm_paged8_select(dev(q), dev(bnd), dev(table), dev(lens), dev(cu), 16, 31, sink=1)
+    assert np.array_equal(host(gl), wl) and np.array_equal(host(got), want)
