@@ -209,8 +209,9 @@ __device__ __forceinline__ Raw<T> decode8(uint2 code, __half2 scale) {
 // and the codes go out as the rows came in.  Where the block holds earlier tokens
 // and the scale grows, their codes are moved first.
 // Bound by HBM (2 or 4 bytes a channel in, 1 out, 2 or 4 more for x_hat) in a
-// chunk: 4,680 rows of 24 heads, d = 128, bf16 with x_hat, 24.8 us (5.8 TB/s); by the
-// chain of loads (lengths, page, rows and scale) in a step of single tokens: 3.5 us.
+// chunk: 4,680 rows of 24 heads, d = 128, with x_hat, in bf16 24.9 us (5.8 TB/s), in
+// float32 44 us (5.9 TB/s); by the chain of loads (lengths, page, rows and scale) in a
+// step of single tokens: 2.8 us for 48 rows of 8 heads, one call behind another.
 template <int D, class T>
 __global__ void __launch_bounds__(kNt) paged8_append_kernel(const qwm_paged8_append_args a, const Steps s) {
   constexpr int L = D / 8, RS = 32 / L, NP = kScaleSlots / RS;

@@ -178,7 +178,7 @@ extern "C" int32_t qwm_paged_attend_kernel_for(int32_t dtype, int32_t heads, int
 namespace {
 // Either cache's attention; table_heads: tables a request has.
 qwm_status attend(const qwm_paged_attend_args* a, int bits, int table_heads, const char* name, void* stream) {
-  if ( !dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 ||
+  if (!dtype_ok(a->dtype) || a->rows < 0 || a->rows > kInt || a->heads < 1 || a->heads > 65536 ||
       a->kv_heads < 1 || a->kv_heads > a->heads || a->heads % a->kv_heads || a->requests < 0 || a->max_blocks < 1 ||
       a->n_pages < 1 || a->n_pages > kInt || a->window < 0 || (a->window > 0 && !a->causal) || a->max_new < 0 ||
       a->kernel < 0 || a->kernel > 3 || !(fabsf(a->scale) < INFINITY))

@@ -350,7 +350,8 @@ def qwm_paged_attend(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Ten
 
 
 def paged_attend_kernel_for(dtype: torch.dtype, heads: int, kv_heads: int, max_new: int) -> int:
-    """The attention kernel (PAGED_SIMT, PAGED_MMA or PAGED_TC) of the automatic choice."""
+    """The attention kernel (PAGED_SIMT, PAGED_MMA or PAGED_TC) of the automatic choice
+    for 4 bits; for 8 bits too, but that float32 runs on PAGED_MMA there."""
     return int(lib().qwm_paged_attend_kernel_for(_DTYPES[dtype], heads, kv_heads, max_new))
 
 
@@ -537,8 +538,11 @@ def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.
     reads this step: those of the step's own tokens, the first `sink`, and the ones
     with the highest scores, bounds of the products of the queries q [rows, heads,
     d] with the keys in them.  pages and lens, where given, share no memory with
-    the inputs or each other (refused).  Returns (pages int32 [requests, kv_heads, width],
-    lens int32 [requests]), the block_table and kv_len of a qwm_paged8_attend."""
+    the inputs or each other (refused).  Single tokens and prompts in one step are
+    better two calls, on slices as for qwm_paged_attend and, for single tokens that
+    come first, on q[:rows] of theirs: the kernels are chosen by the mean rows of a
+    request.  Returns (pages int32 [requests, kv_heads, width], lens int32 [requests]),
+    the block_table and kv_len of a qwm_paged8_attend."""
     qr = _rows(q, "q")
     dt, dev = q.dtype, q.get_device()
     T, hq, d = q.shape
