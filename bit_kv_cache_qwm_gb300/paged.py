@@ -445,7 +445,8 @@ def qwm_paged8_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, bloc
     at, n_pages, _, page = _pool8(pool, d, dev, hk)
     kh = (0, 0, 0) if k_hat is None else _rows(k_hat, "k_hat", dt, dev, shape)
     vh = (0, 0, 0) if v_hat is None else _rows(v_hat, "v_hat", dt, dev, shape)
-    _differ("k_hat, v_hat", (kh, vh), (kh, vr), (vh, kr))
+    if T:
+        _differ("k_hat, v_hat", (kh, vh), (kh, vr), (vh, kr))
     step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_append,
          _APPEND8.pack(*kr, *vr, *kh, *vh, at, *step, _status(status, dev), T, n_pages, _DTYPES[dt], d, hk, page, B, width),
@@ -471,7 +472,8 @@ def qwm_paged8_read(pool: torch.Tensor, block_table: torch.Tensor, kv_len: torch
     if v_out is None:
         v_out = torch.empty_like(k_out, memory_format=torch.contiguous_format)
     vr = _rows(v_out, "v_out", dtype, dev, shape)
-    _differ("k_out, v_out", (kr, vr))
+    if rows:
+        _differ("k_out, v_out", (kr, vr))
     step, B, width, _ = _step8(block_table, kv_len, cu_rows, dev)
     _run(lib().qwm_paged8_read,
          _READ8.pack(*kr, *vr, at, *step, _status(status, dev), rows, n_pages, _DTYPES[dtype], head_dim, hk, page, B, width),

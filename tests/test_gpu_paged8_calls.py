@@ -117,8 +117,9 @@ def test_two_outputs_in_one_tensor(paged):  # noqa: F811
     paged.qwm_paged8_read(pool, *step, 30, 64, dtype=torch.float32, k_out=both[:, :2], v_out=both[:, 2:])
     rk, rv = paged.qwm_paged8_read(pool, *step, 30, 64, dtype=torch.float32)
     assert torch.equal(both, torch.cat([rk, rv], 1))
-    none = torch.empty((0, 2, 64), device="cuda")
-    paged.qwm_paged8_read(pool, step[0], step[1], i32([0, 0]), 0, 64, dtype=torch.float32, k_out=none, v_out=none)
+    for none in (torch.empty((0, 2, 64), device="cuda"), both[:0, :2]):
+        paged.qwm_paged8_read(pool, step[0], step[1], i32([0, 0]), 0, 64, dtype=torch.float32, k_out=none, v_out=none)
+        paged.qwm_paged8_append(k[:0], v[:0], pool, step[0], step[1], i32([0, 0]), k_hat=none, v_hat=none)
 
 
 def test_diagnostics_of_more_rows_than_requests_of_a_call(paged):  # noqa: F811
