@@ -562,12 +562,13 @@ def qwm_paged8_select(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.
     if lens is None:
         lens = torch.empty_like(kv_len)
     out = _array(pages, "pages", _I32, (B, hk, width), dev), _array(lens, "lens", _I32, (B,), dev)
+    st = _status(status, dev)
     for x, name in given:
         _apart(x, name, q, bounds, block_table, kv_len, cu_rows, status, *((pages,) if x is lens else ()))
     # qwm_paged8_select_workspace_bytes
     n_ws = (4 * B * hk * blocks + 255 & -256) + (4 * T * hq + 255 & -256) + T * hq * d
     ws = torch.empty(n_ws or 1, dtype=_U8, device=device)
     _run(lib().qwm_paged8_select,
-         _SELECT8.pack(*qr, at, *step, *out, _status(status, dev), ws.data_ptr(), n_ws, T, n_pages, _DTYPES[dt], d, hq, hk,
+         _SELECT8.pack(*qr, at, *step, *out, st, ws.data_ptr(), n_ws, T, n_pages, _DTYPES[dt], d, hq, hk,
                        page_tokens, B, blocks, min(width, _INT_MAX), min(sink, _INT_MAX)), "qwm_paged8_select", dev)
     return pages, lens
